@@ -4,14 +4,15 @@ Three operators over rows of C channels (the last axis of a channels-last tensor
 
   layer norm      y = (x - mean) * rstd * gamma + beta, mean and rstd = 1/sqrt(var + eps) of the
                   row; backward: dx, dgamma, dbeta.
-  dropout         y = keep ? x / (1 - p) : 0, keep from a counter-based generator.
+  dropout         y = keep ? x / (1 - q) : 0, keep from a counter-based generator; q is p
+                  rounded to a multiple of 2^-16, so that the expected value is kept exactly.
   add layer norm  z = res + dropout(x), y = layer_norm(z): the end of one residual branch and
                   the norm in front of the next; backward: dx, dres, dgamma, dbeta.
 
 The generator is Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
-easy as 1, 2, 3", 2011): element i of the tensor in row-major order takes word i % 4 of the
-block with the 128-bit counter (i // 4, offset) and the 64-bit key seed, and is kept where that
-word is at least floor(p * 2^32).
+easy as 1, 2, 3", 2011): element i of the tensor in row-major order takes the 16-bit value
+i % 8 (of each word the low half first) of the block with the 128-bit counter (i // 8, offset)
+and the 64-bit key seed, and is kept where that value is at least q * 2^16.
 
 `run` computes these with elementary torch operations in fp32 (`own` false) or through the
 framework's entry points (`own` true).
@@ -93,10 +94,10 @@ def draw(rng):
 def work(case):
     """Every input read once, every output written once; operations a value cannot do without
     (sums, differences, products; a draw of the generator is 10 rounds of 2 products and 4
-    exclusive-ors or additions for 4 values)."""
+    exclusive-ors for 8 values)."""
     op, rows, C = case["op"], case["rows"], case["C"]
     n, e, w = rows * C, BYTES[case["dtype"]], BYTES[case["wide"]]
-    rng = 15 * n if case["p"] else 0
+    rng = 7.5 * n if case["p"] else 0
     stats = 0 if case["serve"] else 8 * rows
     if op == "ln_fwd":
         return {"bytes": n * (w + e) + 8 * C + stats, "flops": 8 * n}
@@ -149,7 +150,7 @@ def prepare(case, seed):
 # ------------------------------------------------------------------------- plain form
 
 def _philox(groups, seed, offset):
-    """Words 0..3 of the blocks with counters (0..groups-1, offset): groups x 4 of int64."""
+    """The 16-bit values of the blocks with counters (0..groups-1, offset): groups x 8 of int64."""
     m32 = 0xFFFFFFFF
     i = torch.arange(groups, device="cuda", dtype=torch.int64)
     c0, c1 = i & m32, i >> 32
@@ -160,16 +161,17 @@ def _philox(groups, seed, offset):
         c0, c1, c2, c3 = (((b >> 32) & m32) ^ c1 ^ k0, b & m32,
                           ((a >> 32) & m32) ^ c3 ^ k1, a & m32)
         k0, k1 = (k0 + 0x9E3779B9) & m32, (k1 + 0xBB67AE85) & m32
-    return torch.stack((c0, c1, c2, c3), 1)
+    words = torch.stack((c0, c1, c2, c3), 1)
+    return torch.stack((words & 0xFFFF, words >> 16), 2)
 
 
 def _dropout(x, p, seed, offset):
     if p == 0.0:
         return x
     n = x.numel()
-    words = _philox((n + 3) // 4, seed, offset).reshape(-1)[:n].reshape(x.shape)
-    keep = words >= int(p * 4294967296.0)
-    return torch.where(keep, x * (1.0 / (1.0 - p)), torch.zeros_like(x))
+    values = _philox((n + 7) // 8, seed, offset).reshape(-1)[:n].reshape(x.shape)
+    dropped = math.floor(p * 65536 + 0.5)
+    return torch.where(values >= dropped, x * (65536 / (65536 - dropped)), torch.zeros_like(x))
 
 
 def _norm(x, gamma, beta):
@@ -250,7 +252,7 @@ def run(state):
 
 def _kept(first, count, p, seed, offset):
     """Which of the elements first .. first+count-1 are kept (numpy, 64-bit integers)."""
-    g0, g1 = first // 4, (first + count + 3) // 4
+    g0, g1 = first // 8, (first + count + 7) // 8
     m, sh = np.uint64(0xFFFFFFFF), np.uint64(32)
     block = np.arange(g0, g1, dtype=np.uint64)
     x = [block & m, block >> sh, np.full_like(block, offset & 0xFFFFFFFF),
@@ -260,9 +262,9 @@ def _kept(first, count, p, seed, offset):
         k1 = np.uint64((seed // 2 ** 32 + r * 0xBB67AE85) % 2 ** 32)
         u, v = x[0] * np.uint64(0xD2511F53), x[2] * np.uint64(0xCD9E8D57)
         x = [(v >> sh) ^ x[1] ^ k0, v & m, (u >> sh) ^ x[3] ^ k1, u & m]
-    words = np.stack(x, -1).reshape(-1)
-    at = first - 4 * g0
-    return words[at:at + count] >= np.uint64(math.floor(p * 2 ** 32))
+    halves = np.stack(x, -1).astype("<u4").view("<u2").reshape(-1)
+    at = first - 8 * g0
+    return halves[at:at + count] >= round(p * 2 ** 16)
 
 
 def exact(case, seed):
@@ -289,7 +291,7 @@ def exact(case, seed):
             if p == 0.0:
                 return v
             keep = _kept(r * C, n * C, p, s["seed"], s["offset"]).reshape(n, C)
-            return np.where(keep, v / (1.0 - p), 0.0)
+            return np.where(keep, v / (1.0 - round(p * 2 ** 16) / 2 ** 16), 0.0)
 
         if op.startswith("dropout"):
             put("y", drop(t["x"]))
