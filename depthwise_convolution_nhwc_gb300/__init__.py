@@ -12,6 +12,9 @@ Layouts ("Flash-DWC: Making Depthwise Convolution Compute-Efficient on GPUs", §
 ``x``/``dx`` are N x H x W x C, ``y``/``dy`` are N x OH x OW x C, ``w``/``dw`` are
 FH x FW x C, all contiguous.  Inputs are fp32, bf16 or fp16 (one dtype per call); outputs
 are always fp32.
+
+Layer norm, dropout and their residual form over the same channels-last rows
+(``include/dwc_norm.h``) are in ``norm.py`` and re-exported here.
 """
 from __future__ import annotations
 
@@ -36,7 +39,10 @@ EXPORTS = ("dwc_fwd", "dwc_fwd_ex", "dwc_fwd_bn_act", "dwc_bwd_data", "dwc_bwd_d
            "dwc_device_status", "dwc_set_wait_limit_ns", "dwc_fma_rate_probe",
            "dwc_status_string", "dwc_version", "dwc_path", "dwc_kernel_launches",
            "dwc_testing_stall_next_row_launch", "dwc_testing_prefer_family",
-           "dwc_testing_tc_row_pairs")
+           "dwc_testing_tc_row_pairs",
+           "dwc_layer_norm_fwd", "dwc_layer_norm_bwd_workspace_size", "dwc_layer_norm_bwd",
+           "dwc_dropout_fwd", "dwc_dropout_bwd", "dwc_add_layer_norm_fwd",
+           "dwc_add_layer_norm_bwd")
 FMA_KINDS = {"ffma": 0, "ffma2": 1, "hfma2": 2, "bf16x2": 3}  # dwc_fma_rate_probe kinds
 
 _lock = threading.Lock()
@@ -105,6 +111,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.dwc_testing_prefer_family.restype = i
         lib.dwc_testing_tc_row_pairs.argtypes = [i]
         lib.dwc_testing_tc_row_pairs.restype = i
+        ll, ull = ctypes.c_longlong, ctypes.c_ulonglong
+        params, rng = [vp, vp, i, ctypes.c_float], [ctypes.c_double, ull, ull, vp]
+        lib.dwc_layer_norm_fwd.argtypes = [vp, ll] + params + [vp, vp, vp, ll, i, i, i, vp]
+        lib.dwc_layer_norm_bwd_workspace_size.argtypes = [ll, i]
+        lib.dwc_layer_norm_bwd_workspace_size.restype = sz
+        lib.dwc_layer_norm_bwd.argtypes = [vp, ll, vp, ll, vp, vp, vp, i, vp, vp, vp, ll, i, i, i, vp, sz, vp]
+        for f in (lib.dwc_dropout_fwd, lib.dwc_dropout_bwd):
+            f.argtypes = [vp, ll, vp, ll, i] + rng + [i, vp]
+        lib.dwc_add_layer_norm_fwd.argtypes = ([vp, ll, vp, ll] + rng + params +
+                                               [vp, vp, vp, vp, ll, i, i, i, vp])
+        lib.dwc_add_layer_norm_bwd.argtypes = ([vp, ll, vp, ll, vp, ll, vp, vp, vp, i] + rng +
+                                               [vp, vp, vp, vp, ll, i, i, i, vp, sz, vp])
+        for f in (lib.dwc_layer_norm_fwd, lib.dwc_layer_norm_bwd, lib.dwc_dropout_fwd, lib.dwc_dropout_bwd,
+                  lib.dwc_add_layer_norm_fwd, lib.dwc_add_layer_norm_bwd):
+            f.restype = i
         if path is None:
             _lib = lib
         return lib
@@ -316,7 +337,11 @@ def kernel_launches(pass_: str, N, H, W, C, FH, FW, stride, pad, dtype_code) -> 
     return int(load_library().dwc_kernel_launches(p, N, H, W, C, FH, FW, stride, pad, dtype_code))
 
 
+from .norm import (add_layer_norm_bwd, add_layer_norm_fwd, dropout_bwd, dropout_fwd,  # noqa: E402
+                   layer_norm_bwd, layer_norm_fwd)
+
 __all__ = ["build", "load_library", "fwd", "fwd_bn_act", "bwd_data", "bwd_filter",
            "bwd_filter_workspace_size", "device_status", "set_wait_limit_ns", "fma_rate_probe",
            "path", "kernel_launches", "status_string", "DwcError", "EXPORTS", "FMA_KINDS",
-           "LIB_PATH"]
+           "LIB_PATH", "layer_norm_fwd", "layer_norm_bwd", "dropout_fwd", "dropout_bwd",
+           "add_layer_norm_fwd", "add_layer_norm_bwd"]

@@ -1,0 +1,87 @@
+// dwc_norm_host.h -- host-side interface between the C ABI of the norm and dropout operators
+// and their kernel launchers.
+//
+// All three operators are written over a stream tensor (layer norm's x, the residual sum z) and
+// a branch tensor (layer norm's y, the residual form's x and y); the pairs of types are equal,
+// or an fp32 stream with a 16-bit branch.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "dwc_host.h"
+
+namespace dwc {
+
+// Counter-based dropout: 16-bit draws below `threshold` are dropped (0: no dropout, 65536: all).
+struct Dropout {
+    uint32_t threshold = 0;
+    float scale = 1.f;              // 65536 / (65536 - threshold)
+    uint32_t k0 = 0, k1 = 0;        // the seed's words
+    uint64_t offset = 0;
+    const unsigned long long* step = nullptr;
+};
+
+// z = stream (+ dropout(branch)), y = layer_norm(z).
+struct NormFwd {
+    const void* in;                 // rows x C of the stream type, row stride ld_in
+    const void* x;                  // the branch (row stride ld_x), or null: plain layer norm
+    void* z;                        // sum, stream type (with a branch only)
+    void* y;                        // branch type
+    float* mean;                    // may be null
+    float* rstd;                    // may be null
+    const void* gamma;              // may be null
+    const void* beta;               // may be null
+    int param_type;
+    float eps;
+    long long rows, ld_in, ld_x;
+    int C;
+    int stream_type, branch_type;
+    Dropout drop;
+    cudaStream_t stream;
+};
+
+// g = dz + layer_norm_bwd(dy; z): d_stream = g, d_branch = dropout map of g.
+struct NormBwd {
+    const void* dy;                 // branch type, row stride ld_dy
+    const void* dz;                 // stream type, row stride ld_dz, or null
+    const void* z;                  // stream type, row stride ld_z
+    const float* mean;
+    const float* rstd;
+    const void* gamma;              // may be null
+    int param_type;
+    void* d_stream;                 // stream type
+    void* d_branch;                 // branch type, or null
+    float* dgamma;                  // may be null
+    float* dbeta;                   // may be null
+    float* partial;                 // workspace (with a parameter gradient only)
+    long long rows, ld_dy, ld_dz, ld_z;
+    int C;
+    int stream_type, branch_type;
+    Dropout drop;
+    cudaStream_t stream;
+};
+
+struct DropoutCall {
+    const void* x;
+    void* y;
+    long long rows, ld_x;
+    int C;
+    int type;
+    Dropout drop;
+    cudaStream_t stream;
+};
+
+// General kernels: any row stride, alignment and channel count.
+cudaError_t launch_norm_fwd_general(const NormFwd& p);
+cudaError_t launch_norm_bwd_general(const NormBwd& p);
+cudaError_t launch_dropout_general(const DropoutCall& p);
+
+// Rows of partial parameter gradients (2 x C floats each) that a backward pass may write.
+int norm_bwd_partials(long long rows, int C);
+// dgamma / dbeta = the sum of `count` partial rows [dgamma | dbeta], in a fixed order.
+cudaError_t launch_norm_param_sum(const float* partial, int count, int C, float* dgamma,
+                                  float* dbeta, cudaStream_t stream);
+
+}  // namespace dwc
