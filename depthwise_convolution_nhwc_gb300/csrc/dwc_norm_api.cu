@@ -62,6 +62,43 @@ dwc_status_t map_cuda(cudaError_t err) {
     return DWC_ERR_CUDA;
 }
 
+// Whether a tensor's rows start at the same element of a vector of 8 as dense rows from an aligned
+// base do (one row: any stride).
+bool lines_up(const void* t, int bytes, long long ld, long long rows, int C) {
+    return t == nullptr || (!misaligned(t, 8 * static_cast<size_t>(bytes)) && (rows == 1 || (ld - C) % 8 == 0));
+}
+
+#define DWC_BY_PAIR(fn, p)                                                                 \
+    if ((p).stream_type == kF32) {                                                         \
+        if ((p).branch_type == kF32) return fn##_f32(p);                                   \
+        return (p).branch_type == kBF16 ? fn##_f32_bf16(p) : fn##_f32_f16(p);              \
+    }                                                                                      \
+    return (p).stream_type == kBF16 ? fn##_bf16(p) : fn##_f16(p);
+
+cudaError_t fwd_rows(const NormFwd& p) { DWC_BY_PAIR(launch_norm_fwd, p) }
+cudaError_t bwd_rows(const NormBwd& p) { DWC_BY_PAIR(launch_norm_bwd, p) }
+
+cudaError_t launch_fwd(const NormFwd& p) {
+    const int ws = elem_bytes(p.stream_type), wb = elem_bytes(p.branch_type);
+    if (lines_up(p.in, ws, p.ld_in, p.rows, p.C) && lines_up(p.x, wb, p.ld_x, p.rows, p.C) &&
+        lines_up(p.z, ws, p.C, p.rows, p.C) && lines_up(p.y, wb, p.C, p.rows, p.C)) {
+        const cudaError_t err = fwd_rows(p);
+        if (err != cudaErrorNotSupported) return err;
+    }
+    return launch_norm_fwd_general(p);
+}
+
+cudaError_t launch_bwd(const NormBwd& p) {
+    const int ws = elem_bytes(p.stream_type), wb = elem_bytes(p.branch_type);
+    if (lines_up(p.dy, wb, p.ld_dy, p.rows, p.C) && lines_up(p.dz, ws, p.ld_dz, p.rows, p.C) &&
+        lines_up(p.z, ws, p.ld_z, p.rows, p.C) && lines_up(p.d_stream, ws, p.C, p.rows, p.C) &&
+        lines_up(p.d_branch, wb, p.C, p.rows, p.C)) {
+        const cudaError_t err = bwd_rows(p);
+        if (err != cudaErrorNotSupported) return err;
+    }
+    return launch_norm_bwd_general(p);
+}
+
 dwc_status_t norm_fwd(NormFwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_type, dwc_dtype_t param_dtype) {
     if (!valid_pair(stream_type, branch_type) || !known(param_dtype)) return DWC_ERR_INVALID_ARG;
     if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return DWC_ERR_INVALID_ARG;
@@ -83,7 +120,7 @@ dwc_status_t norm_fwd(NormFwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_ty
     p.stream_type = stream_type;
     p.branch_type = branch_type;
     p.param_type = param_dtype;
-    return map_cuda(launch_norm_fwd_general(p));
+    return map_cuda(launch_fwd(p));
 }
 
 dwc_status_t norm_bwd(NormBwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_type, dwc_dtype_t param_dtype,
@@ -120,7 +157,7 @@ dwc_status_t norm_bwd(NormBwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_ty
     p.stream_type = stream_type;
     p.branch_type = branch_type;
     p.param_type = param_dtype;
-    return map_cuda(launch_norm_bwd_general(p));
+    return map_cuda(launch_bwd(p));
 }
 
 dwc_status_t dropout(const void* x, long long ldx, void* y, long long rows, int C, double p,

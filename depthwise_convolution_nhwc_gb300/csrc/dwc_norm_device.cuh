@@ -1,6 +1,8 @@
 // dwc_norm_device.cuh -- device-side parts shared by the norm and dropout kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "dwc_device.cuh"
 #include "dwc_norm_host.h"
 
@@ -68,6 +70,110 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     return v;
+}
+
+// ---- vectors of 8 elements ---------------------------------------------------------------
+// 16 bytes of a 16-bit type, 32 bytes of fp32 (one 256-bit access, new with sm_100; two 16-byte
+// ones would each touch half of every sector).
+template <typename T>
+struct Vec8 {  // 16-bit types
+    uint4 u;
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void set(int j, T v) { reinterpret_cast<T*>(&u)[j] = v; }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                f[2 * k] = __uint_as_float(w[k] << 16);
+                f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            } else {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                f[2 * k] = t.x;
+                f[2 * k + 1] = t.y;
+            }
+        }
+    }
+    __device__ static __forceinline__ void store(T* p, const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 t = make_float2(f[2 * k], f[2 * k + 1]);
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 h = __float22bfloat162_rn(t);
+                w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __float22half2_rn(t);
+                w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <>
+struct Vec8<float> {
+    float v[8];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+    __device__ __forceinline__ void load(const float* p) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "l"(p)
+                     : "memory");
+    }
+    __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[j];
+    }
+    __device__ static __forceinline__ void store(float* p, const float (&f)[8]) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]),
+                     "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+    }
+};
+
+// Elements col .. col + 7 of a row of C, col a vector boundary of the address that may lie before
+// the row's start or reach past its end: only the row's own elements are touched, the others
+// read as 0.
+__device__ __forceinline__ bool inside(int col, int C) { return col >= 0 && col + 8 <= C; }
+
+template <typename T>
+__device__ __forceinline__ void load_row8(Vec8<T>& v, const T* row, int col, int C) {
+    if (inside(col, C)) {
+        v.load(row + col);
+    } else {
+        v.zero();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (static_cast<unsigned>(col + j) < static_cast<unsigned>(C)) v.set(j, row[col + j]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row8(T* row, const float (&f)[8], int col, int C) {
+    if (inside(col, C)) {
+        Vec8<T>::store(row + col, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (static_cast<unsigned>(col + j) < static_cast<unsigned>(C)) store_out(row + col + j, f[j]);
+    }
+}
+
+// The dropout of 8 consecutive elements whose first index is 8 * block.
+__device__ __forceinline__ void drop8(const DropState& d, float (&f)[8], uint64_t block) {
+    const uint4 b = d.draw(block);
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = d.apply(f[2 * k], w[k] & 0xffffu);
+        f[2 * k + 1] = d.apply(f[2 * k + 1], w[k] >> 16);
+    }
 }
 
 }  // namespace dwc

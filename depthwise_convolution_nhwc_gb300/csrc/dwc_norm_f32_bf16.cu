@@ -1,0 +1,11 @@
+// dwc_norm_f32_bf16.cu -- layer norm rows kernels for an fp32 stream with bf16 branches.
+#include "dwc_norm_rows.cuh"
+
+namespace dwc {
+
+cudaError_t launch_norm_fwd_f32_bf16(const NormFwd& p) {
+    return p.x != nullptr ? norm::fwd_rows<float, __nv_bfloat16, true>(p) : norm::fwd_rows<float, __nv_bfloat16, false>(p);
+}
+cudaError_t launch_norm_bwd_f32_bf16(const NormBwd& p) { return norm::bwd_rows<float, __nv_bfloat16>(p); }
+
+}  // namespace dwc

@@ -78,6 +78,18 @@ cudaError_t launch_norm_fwd_general(const NormFwd& p);
 cudaError_t launch_norm_bwd_general(const NormBwd& p);
 cudaError_t launch_dropout_general(const DropoutCall& p);
 
+// Rows in registers (aligned tensors, up to 16384 channels, see norm_rows_serve), one file per
+// pair of types; cudaErrorNotSupported beyond that.
+#define DWC_NORM_PAIR(name)                           \
+    cudaError_t launch_norm_fwd_##name(const NormFwd& p); \
+    cudaError_t launch_norm_bwd_##name(const NormBwd& p);
+DWC_NORM_PAIR(f32)
+DWC_NORM_PAIR(bf16)
+DWC_NORM_PAIR(f16)
+DWC_NORM_PAIR(f32_bf16)
+DWC_NORM_PAIR(f32_f16)
+#undef DWC_NORM_PAIR
+
 // Rows of partial parameter gradients (2 x C floats each) that a backward pass may write.
 int norm_bwd_partials(long long rows, int C);
 // dgamma / dbeta = the sum of `count` partial rows [dgamma | dbeta], in a fixed order.

@@ -89,10 +89,12 @@ def check_add(s, wide, narrow, p, seed=11, offset=3, dz=True, inplace=False):
     within(z.reshape(-1, C), zsum, 1.01 * (e_z + ref.U[wide] * np.abs(zsum)) + ref.TINY[wide], "z")
     want = ref.layer_norm(zsum, gn, bn, EPS)
     bound = ref.layer_norm_bound(zsum, gn, bn, EPS, narrow, e_z)
-    within(y.reshape(-1, C), want[0], bound[0], "y")
+    want_y, bound_y = want[0], bound[0]
+    within(y.reshape(-1, C), want_y, bound_y, "y")
     within(mean.reshape(-1), want[1], bound[1], "mean")
     within(rstd.reshape(-1), want[2], bound[2], "rstd")
-    y2, z2 = dwc.add_layer_norm_fwd(s["x"], s["z"], s["gamma"], s["beta"], EPS, p, seed, offset)
+    # (a dense copy, as above: another row stride may take another kernel and order of sums)
+    y2, z2 = dwc.add_layer_norm_fwd(s["x"], s["z"].clone(), s["gamma"], s["beta"], EPS, p, seed, offset)
     assert torch.equal(y, y2) and torch.equal(z, z2)
 
     zd, m, r = d(z).reshape(-1, C), d(mean).reshape(-1), d(rstd).reshape(-1)
@@ -100,6 +102,10 @@ def check_add(s, wide, narrow, p, seed=11, offset=3, dz=True, inplace=False):
     e_g, e_gamma, e_beta = ref.layer_norm_bwd_bound(dy, zd, m, r, gn, "f32", dzn if dz else None)
     if dz:
         g = g + dzn
+    if not s["z"].is_contiguous():
+        y2, z2 = dwc.add_layer_norm_fwd(s["x"], s["z"], s["gamma"], s["beta"], EPS, p, seed, offset)
+        within(y2.reshape(-1, C), want_y, bound_y, "y of a strided stream")
+        assert torch.equal(z, z2)
     got = dwc.add_layer_norm_bwd(s["dy"], z, mean, rstd, s["gamma"], s["dz"] if dz else None, p, seed, offset)
     within(got[1].reshape(-1, C), g, 1.01 * (e_g + ref.U[wide] * np.abs(g)) + ref.TINY[wide], "dres")
     dx = ref.dropout(g, p, seed, offset)
@@ -199,7 +205,8 @@ def test_outputs_stay_inside_their_rows():
             out = buf[lead:lead + 5 * C].view(5, C)
             x = torch.randn(5, C, device="cuda").bfloat16()
             dwc.layer_norm_fwd(x, out=out)
-            assert torch.equal(out, dwc.layer_norm_fwd(x)), (C, lead)
+            within(out, ref.layer_norm(d(x), 1.0, 0.0, EPS)[0], ref.layer_norm_bound(d(x), 1.0, 0.0, EPS, "bf16")[0],
+                   (C, lead))
             dwc.dropout_fwd(x, 0.5, 1, out=out)
             assert torch.equal(out, dwc.dropout_fwd(x, 0.5, 1)), (C, lead)
             assert bool((buf[:lead] == 7).all()) and bool((buf[lead + 5 * C:] == 7).all()), (C, lead)
