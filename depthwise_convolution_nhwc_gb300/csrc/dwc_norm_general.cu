@@ -205,10 +205,11 @@ cudaError_t dropout_t(const DropoutCall& p) {
 
 }  // namespace
 
-// Partial rows: two CTAs per SM, and at most 2^25 columns in all (256 MB) for very wide rows.
+// Partial rows: four CTAs per SM for short rows, two for long ones, and at most 2^25 columns in
+// all (256 MB) for very wide rows.
 int norm_bwd_partials(long long rows, int C) {
     const long long by_size = std::max<long long>(1, (1LL << 25) / C);
-    return static_cast<int>(std::min({rows, 2LL * device_info().sm_count, by_size}));
+    return static_cast<int>(std::min({rows, (C <= 1024 ? 4LL : 2LL) * device_info().sm_count, by_size}));
 }
 
 #define DWC_BY_PAIR(fn, p)                                                                        \
