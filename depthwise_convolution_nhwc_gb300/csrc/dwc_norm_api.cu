@@ -180,6 +180,10 @@ dwc_status_t dropout(const void* x, long long ldx, void* y, long long rows, int 
     c.C = C;
     c.type = dtype;
     c.stream = stream;
+    if ((ldx == C || rows == 1) && !misaligned(x, 8 * bytes) && !misaligned(y, 8 * bytes)) {
+        const cudaError_t err = launch_dropout_vec(c);
+        if (err != cudaErrorNotSupported) return map_cuda(err);
+    }
     return map_cuda(launch_dropout_general(c));
 }
 

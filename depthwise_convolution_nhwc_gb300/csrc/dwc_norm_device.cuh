@@ -74,37 +74,33 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // ---- vectors of 8 elements ---------------------------------------------------------------
 // 16 bytes of a 16-bit type, 32 bytes of fp32 (one 256-bit access, new with sm_100; two 16-byte
-// ones would each touch half of every sector).
+// ones would each touch half of every sector).  In registers: four fp32 pairs, for the packed
+// fp32x2 arithmetic.
 template <typename T>
 struct Vec8 {  // 16-bit types
     uint4 u;
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void set(int j, T v) { reinterpret_cast<T*>(&u)[j] = v; }
-    __device__ __forceinline__ void widen(float (&f)[8]) const {
+    __device__ __forceinline__ void widen(float2 (&f)[4]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                f[2 * k] = __uint_as_float(w[k] << 16);
-                f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            } else {
-                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                f[2 * k] = t.x;
-                f[2 * k + 1] = t.y;
-            }
+            if constexpr (std::is_same<T, __nv_bfloat16>::value)
+                f[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+            else
+                f[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
         }
     }
-    __device__ static __forceinline__ void store(T* p, const float (&f)[8]) {
+    __device__ static __forceinline__ void store(T* p, const float2 (&f)[4]) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float2 t = make_float2(f[2 * k], f[2 * k + 1]);
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                const __nv_bfloat162 h = __float22bfloat162_rn(t);
+                const __nv_bfloat162 h = __float22bfloat162_rn(f[k]);
                 w[k] = *reinterpret_cast<const uint32_t*>(&h);
             } else {
-                const __half2 h = __float22half2_rn(t);
+                const __half2 h = __float22half2_rn(f[k]);
                 w[k] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
@@ -126,53 +122,55 @@ struct Vec8<float> {
                      : "memory");
     }
     __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
-    __device__ __forceinline__ void widen(float (&f)[8]) const {
+    __device__ __forceinline__ void widen(float2 (&f)[4]) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = v[j];
+        for (int k = 0; k < 4; ++k) f[k] = make_float2(v[2 * k], v[2 * k + 1]);
     }
-    __device__ static __forceinline__ void store(float* p, const float (&f)[8]) {
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]),
-                     "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+    __device__ static __forceinline__ void store(float* p, const float2 (&f)[4]) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0].x), "f"(f[0].y),
+                     "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
                      : "memory");
     }
 };
 
-// Elements col .. col + 7 of a row of C, col a vector boundary of the address that may lie before
-// the row's start or reach past its end: only the row's own elements are touched, the others
-// read as 0.
-__device__ __forceinline__ bool inside(int col, int C) { return col >= 0 && col + 8 <= C; }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-template <typename T>
-__device__ __forceinline__ void load_row8(Vec8<T>& v, const T* row, int col, int C) {
-    if (inside(col, C)) {
-        v.load(row + col);
-    } else {
-        v.zero();
+// Whether elements col .. col + 7 all belong to a row of C; where a row does not start at a
+// vector boundary its first and last vector hang over (col may be negative).
+__device__ __forceinline__ bool inside(int col, int C) { return col >= 0 && col + 8 <= C; }
+__device__ __forceinline__ bool in_row(int c, int C) { return static_cast<unsigned>(c) < static_cast<unsigned>(C); }
+
+// Elements beside the row are set to 0.
+__device__ __forceinline__ void mask8(float2 (&f)[4], int col, int C) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (static_cast<unsigned>(col + j) < static_cast<unsigned>(C)) v.set(j, row[col + j]);
+    for (int k = 0; k < 4; ++k) {
+        if (!in_row(col + 2 * k, C)) f[k].x = 0.f;
+        if (!in_row(col + 2 * k + 1, C)) f[k].y = 0.f;
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_row8(T* row, const float (&f)[8], int col, int C) {
-    if (inside(col, C)) {
+// Store of a vector: only the row's own elements.
+template <bool kAligned, typename T>
+__device__ __forceinline__ void store_row8(T* row, const float2 (&f)[4], int col, int C) {
+    if (kAligned || inside(col, C)) {
         Vec8<T>::store(row + col, f);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (static_cast<unsigned>(col + j) < static_cast<unsigned>(C)) store_out(row + col + j, f[j]);
+        for (int k = 0; k < 4; ++k) {
+            if (in_row(col + 2 * k, C)) store_out(row + col + 2 * k, f[k].x);
+            if (in_row(col + 2 * k + 1, C)) store_out(row + col + 2 * k + 1, f[k].y);
+        }
     }
 }
 
 // The dropout of 8 consecutive elements whose first index is 8 * block.
-__device__ __forceinline__ void drop8(const DropState& d, float (&f)[8], uint64_t block) {
+__device__ __forceinline__ void drop8(const DropState& d, float2 (&f)[4], uint64_t block) {
     const uint4 b = d.draw(block);
     const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        f[2 * k] = d.apply(f[2 * k], w[k] & 0xffffu);
-        f[2 * k + 1] = d.apply(f[2 * k + 1], w[k] >> 16);
+        f[k].x = d.apply(f[k].x, w[k] & 0xffffu);
+        f[k].y = d.apply(f[k].y, w[k] >> 16);
     }
 }
 

@@ -145,28 +145,38 @@ __global__ void __launch_bounds__(kThreads) dropout_general_kernel(DropoutCall p
     }
 }
 
-// Column sums of the partial rows: 32 columns per CTA, a warp takes every kWarps-th row, the
-// warps' sums are added in order.
-__global__ void __launch_bounds__(kThreads) norm_param_sum_kernel(const float* __restrict__ part, int count, int C,
-                                                                  float* dgamma, float* dbeta) {
-    __shared__ float sums[kWarps][32];
+// Column sums of the partial rows: a CTA takes 32 columns, its 32 warps every 32nd row each (all
+// their loads in flight: the kernel is bound by their latency), and warp w adds the 32 warps'
+// sums of column w.  A fixed order, whatever the timing.
+constexpr int kSumThreads = 1024;
+
+__global__ void __launch_bounds__(kSumThreads) norm_param_sum_kernel(const float* __restrict__ part, int count, int C,
+                                                                     float* dgamma, float* dbeta) {
+    __shared__ float sums[32][33];
     pdl_trigger();
-    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long j = static_cast<long long>(blockIdx.x) * 32 + lane;
+    const size_t step = static_cast<size_t>(2) * C;
     float s = 0.f;
+    pdl_wait();
     if (j < 2LL * C) {
-#pragma unroll 8
-        for (int k = warp; k < count; k += kWarps) s += part[static_cast<size_t>(k) * 2 * C + j];
+        const float* from = part + j;
+        int k = warp;
+        for (; k + 96 < count; k += 128) {
+            float t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = from[(k + 32 * i) * step];
+            s += (t[0] + t[1]) + (t[2] + t[3]);
+        }
+        for (; k < count; k += 32) s += from[k * step];
     }
     sums[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || j >= 2LL * C) return;
-    s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sums[w][lane];
-    float* out = j < C ? dgamma : dbeta;
-    if (out != nullptr) out[j < C ? j : j - C] = s;
+    s = warp_sum(sums[lane][warp]);
+    const long long o = static_cast<long long>(blockIdx.x) * 32 + warp;
+    if (lane != 0 || o >= 2LL * C) return;
+    float* out = o < C ? dgamma : dbeta;
+    if (out != nullptr) out[o < C ? o : o - C] = s;
 }
 
 template <typename TS, typename TB, bool kAdd>
@@ -233,7 +243,7 @@ cudaError_t launch_dropout_general(const DropoutCall& p) {
 cudaError_t launch_norm_param_sum(const float* partial, int count, int C, float* dgamma, float* dbeta,
                                   cudaStream_t stream) {
     const unsigned blocks = static_cast<unsigned>((2LL * C + 31) / 32);
-    return launch_pdl(norm_param_sum_kernel, dim3(blocks), dim3(kThreads), 0, stream, partial, count, C, dgamma,
+    return launch_pdl(norm_param_sum_kernel, dim3(blocks), dim3(kSumThreads), 0, stream, partial, count, C, dgamma,
                       dbeta);
 }
 

@@ -78,7 +78,10 @@ cudaError_t launch_norm_fwd_general(const NormFwd& p);
 cudaError_t launch_norm_bwd_general(const NormBwd& p);
 cudaError_t launch_dropout_general(const DropoutCall& p);
 
-// Rows in registers (aligned tensors, up to 16384 channels, see norm_rows_serve), one file per
+// Dropout of dense rows from bases aligned to 8 elements.
+cudaError_t launch_dropout_vec(const DropoutCall& p);
+
+// Rows in registers (aligned tensors, up to 16384 channels), one file per
 // pair of types; cudaErrorNotSupported beyond that.
 #define DWC_NORM_PAIR(name)                           \
     cudaError_t launch_norm_fwd_##name(const NormFwd& p); \
