@@ -33,10 +33,11 @@ __device__ __forceinline__ uint4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_
 // Dropout as a kernel holds it: the counter's high words are the call's offset plus the step
 // that the caller may keep on the device.
 struct DropState {
-    uint32_t threshold, k0, k1, o0, o1;
+    uint32_t threshold, below, k0, k1, o0, o1;
     float scale;
     __device__ __forceinline__ void init(const Dropout& d) {
         threshold = d.threshold;
+        below = (d.threshold << 16) - 1u;   // (65536 gives 2^32 - 1: nothing lies above it)
         k0 = d.k0;
         k1 = d.k1;
         scale = d.scale;
@@ -48,13 +49,14 @@ struct DropState {
     __device__ __forceinline__ uint4 draw(uint64_t block) const {
         return philox4x32_10(static_cast<uint32_t>(block), static_cast<uint32_t>(block >> 32), o0, o1, k0, k1);
     }
-    // one value; the comparison selects, so a dropped infinity or NaN gives 0
-    __device__ __forceinline__ float apply(float v, uint32_t h) const { return h >= threshold ? v * scale : 0.f; }
+    // one value and its draw in the high half of `h` (h >> 16 >= threshold, threshold > 0); the
+    // comparison selects, so a dropped infinity or NaN gives 0
+    __device__ __forceinline__ float apply(float v, uint32_t h) const { return h > below ? v * scale : 0.f; }
     __device__ __forceinline__ float one(float v, uint64_t i) const {
         const uint4 b = draw(i >> 3);
         const uint32_t j = static_cast<uint32_t>(i) & 7u;
         const uint32_t w = j < 4 ? (j < 2 ? b.x : b.y) : (j < 6 ? b.z : b.w);
-        return apply(v, (j & 1u) ? w >> 16 : w & 0xffffu);
+        return apply(v, (j & 1u) ? w : w << 16);
     }
 };
 
@@ -169,8 +171,8 @@ __device__ __forceinline__ void drop8(const DropState& d, float2 (&f)[4], uint64
     const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        f[k].x = d.apply(f[k].x, w[k] & 0xffffu);
-        f[k].y = d.apply(f[k].y, w[k] >> 16);
+        f[k].x = d.apply(f[k].x, w[k] << 16);
+        f[k].y = d.apply(f[k].y, w[k]);
     }
 }
 

@@ -6,6 +6,9 @@ namespace dwc {
 cudaError_t launch_norm_fwd_f32_bf16(const NormFwd& p) {
     return p.x != nullptr ? norm::fwd_rows<float, __nv_bfloat16, true>(p) : norm::fwd_rows<float, __nv_bfloat16, false>(p);
 }
-cudaError_t launch_norm_bwd_f32_bf16(const NormBwd& p) { return norm::bwd_rows<float, __nv_bfloat16>(p); }
+cudaError_t launch_norm_bwd_f32_bf16(const NormBwd& p) {
+    const bool add = p.dz != nullptr || p.d_branch != nullptr;
+    return add ? norm::bwd_rows<float, __nv_bfloat16, true>(p) : norm::bwd_rows<float, __nv_bfloat16, false>(p);
+}
 
 }  // namespace dwc

@@ -6,6 +6,9 @@ namespace dwc {
 cudaError_t launch_norm_fwd_f32_f16(const NormFwd& p) {
     return p.x != nullptr ? norm::fwd_rows<float, __half, true>(p) : norm::fwd_rows<float, __half, false>(p);
 }
-cudaError_t launch_norm_bwd_f32_f16(const NormBwd& p) { return norm::bwd_rows<float, __half>(p); }
+cudaError_t launch_norm_bwd_f32_f16(const NormBwd& p) {
+    const bool add = p.dz != nullptr || p.d_branch != nullptr;
+    return add ? norm::bwd_rows<float, __half, true>(p) : norm::bwd_rows<float, __half, false>(p);
+}
 
 }  // namespace dwc

@@ -257,11 +257,13 @@ __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta) norm_fwd_rows_kern
 // Each thread holds 8 elements of every vector slot; a slot is one 16-byte granule of a 16-bit
 // type or two of fp32.  For fp32 the lanes of a warp copy consecutive granules (whole sectors)
 // and the two halves of a vector land in two planes, where both are read without bank
-// conflicts.  Granules that hang over the row's ends are copied whole while they stay inside the
-// tensor (the reader masks the neighbouring rows' elements); at the tensor's very end single
-// elements are stored instead.
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+// conflicts.  Vectors past the row's end are filled with zeros (a copy of no bytes), so the
+// arithmetic needs no branches.  Granules that hang over the row's ends are copied whole while
+// they stay inside the tensor (the reader masks the neighbouring rows' elements); at the
+// tensor's very end single elements are stored instead.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool some) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(some ? 16 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -270,9 +272,9 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 template <bool kAligned, typename T>
 __device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, int C, int room) {
     constexpr int n = 16 / sizeof(T);
-    if (col >= C) return;
-    if (kAligned || col + n <= room) {
-        copy16(dst, row + col);
+    const bool some = col < C;
+    if (kAligned || !some || col + n <= room) {
+        copy16(dst, row + (some ? col : 0), some);
     } else {
         T* to = reinterpret_cast<T*>(dst);
 #pragma unroll
@@ -317,17 +319,30 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Sums of two values over a group of GW lanes with one exchange and log2(GW) - 1 steps (half the
+// lanes carry one value, half the other): lanes 0 .. GW/2 - 1 return the first, the others the
+// second.
+template <int GW>
+__device__ __forceinline__ float pair_sum(float a, float b, int lane) {
+    const bool upper = (lane & (GW / 2)) != 0;
+    float v = upper ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, upper ? a : b, GW / 2);
+#pragma unroll
+    for (int m = GW / 4; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
 // Each thread keeps the sums of dy * xhat and dy of its columns in registers over all rows of its
 // group; at the end the groups of a CTA are added in order and the CTA writes one row of partial
 // sums.  The sums take the registers, so the rows wait in shared memory, S of them per group, and
 // are read twice there (before and after the row's two means are known).  G == 0: groups of
 // `group_threads` threads, several to a CTA where they are short: one CTA per SM, so that there
-// are few rows of partial sums.
-template <typename TS, typename TB, bool kAligned, int G, int NV, int S>
+// are few rows of partial sums.  kAdd: the residual form (dz, a branch gradient, dropout).
+template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int S>
 __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, bwd_min_ctas(G, NV))
 norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     extern __shared__ __align__(16) float smem[];
-    __shared__ float2 merge[2][kMaxCta / 32];
+    __shared__ __align__(16) float merge[2][2][kMaxCta / 32];
     constexpr bool kCta = G == 0;                  // several warps serve a row
     constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
     constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // planes of a slot
@@ -343,7 +358,8 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     const int C = p.C;
     const int shift = kAligned ? 0 : static_cast<int>((static_cast<long long>(group) * C) & 7);
     const float inv = 1.f / static_cast<float>(C);
-    const bool has_dz = p.dz != nullptr;
+    const bool has_dz = kAdd && p.dz != nullptr;
+    const bool has_branch = kAdd && p.d_branch != nullptr;
     // this thread's granules: stage, then slot (dy, z, dz of each vector), then plane
     const int z_at = NV * kBranch, dz_at = z_at + NV * kStream;
     const int stage_granules = (dz_at + (has_dz ? NV * kStream : 0)) * threads;
@@ -351,7 +367,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     pdl_trigger();
     pdl_wait();
     DropState drop;
-    drop.init(p.drop);
+    if (kAdd) drop.init(p.drop);
 
     auto fetch = [&](int stage, long long r) {
         if (r < p.rows) {
@@ -360,13 +376,18 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             uint4* to = mine + stage * stage_granules;
             const TB* dy = static_cast<const TB*>(p.dy) + r * p.ld_dy;
             const TS* z = static_cast<const TS*>(p.z) + r * p.ld_z;
-            const TS* dz = static_cast<const TS*>(p.dz) + r * p.ld_dz;
+            const TS* dz = has_dz ? static_cast<const TS*>(p.dz) + r * p.ld_dz : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = (k * width + lane) * 8 - shift;
                 copy_slot<kAligned, TB, GW>(to + k * kBranch * threads, threads, dy, sub, col, C, room);
                 copy_slot<kAligned, TS, GW>(to + (z_at + k * kStream) * threads, threads, z, sub, col, C, room);
-                if (has_dz) copy_slot<kAligned, TS, GW>(to + (dz_at + k * kStream) * threads, threads, dz, sub, col, C, room);
+            }
+            if (has_dz) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    copy_slot<kAligned, TS, GW>(to + (dz_at + k * kStream) * threads, threads, dz, sub,
+                                                (k * width + lane) * 8 - shift, C, room);
             }
         }
         copy_commit();
@@ -374,25 +395,33 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * groups);
 
+    // gamma: registers for one vector a lane, else the caller's array (aligned fp32) or a copy
+    // along the shifted vectors, read per use
     float2 gam[4];
-    ParamSource gsrc;
+    const float* gsrc = static_cast<const float*>(p.gamma);
+    int last = C - 8;                               // the last whole vector there
     if constexpr (NV == 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int c = lane * 8 + 2 * k - shift;
             gam[k] = make_float2(shifted_param(p.gamma, p.param_type, c, C, 1.f), shifted_param(p.gamma, p.param_type, c + 1, C, 1.f));
         }
-    } else {
-        gsrc.present = staged || p.gamma != nullptr;
-        gsrc.p = static_cast<const float*>(p.gamma);
-        if (staged) {
-            const int span = width * NV * 8;
-            float* g = smem + S * stage_granules * 4 + local * span;
-            for (int i = lane; i < span; i += width) g[i] = shifted_param(p.gamma, p.param_type, i - shift, C, 1.f);
-            gsrc.p = g;
-            if (kCta) group_barrier(1 + local, width); else __syncwarp();
-        }
+    } else if (staged) {
+        const int span = width * NV * 8;
+        float* g = smem + S * stage_granules * 4 + local * span;
+        for (int i = lane; i < span; i += width) g[i] = shifted_param(p.gamma, p.param_type, i - shift, C, 1.f);
+        gsrc = g;
+        last = span - 8;
+        if (kCta) group_barrier(1 + local, width); else __syncwarp();
     }
+    auto gamma_of = [&](int k) {
+        if constexpr (NV > 1) {
+            const float* g = gsrc + min((k * width + lane) * 8, last);
+            const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
+            gam[0] = make_float2(a.x, a.y), gam[1] = make_float2(a.z, a.w);
+            gam[2] = make_float2(b.x, b.y), gam[3] = make_float2(b.z, b.w);
+        }
+    };
     float2 sum_g[NV][4], sum_b[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -420,15 +449,16 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
         if (live) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int at = (k * width + lane) * 8, col = at - shift;
-                if (col >= C) continue;
-                if constexpr (NV > 1) gsrc.get(gam, at, 1.f);
                 float2 f[4], x[4];
                 read_slot<TB>(f, from + k * kBranch * threads, threads);
                 read_slot<TS>(x, from + (z_at + k * kStream) * threads, threads);
-                if (!kAligned && !inside(col, C)) {
-                    mask8(f, col, C);
-                    mask8(x, col, C);
+                gamma_of(k);
+                if constexpr (!kAligned) {
+                    const int col = (k * width + lane) * 8 - shift;
+                    if (!inside(col, C)) {
+                        mask8(f, col, C);
+                        mask8(x, col, C);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -441,28 +471,34 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
                 }
             }
         }
-        float2 s = make_float2(group_sum<GW>(s1.x + s1.y), group_sum<GW>(s2.x + s2.y));
-        if (kCta) {
-            if ((threadIdx.x & 31) == 0) merge[parity][threadIdx.x >> 5] = s;
+        const float half_sum = pair_sum<GW>(s1.x + s1.y, s2.x + s2.y, sub);
+        float2 s;
+        if constexpr (kCta) {
+            if ((sub & 15) == 0) merge[parity][sub >> 4][threadIdx.x >> 5] = half_sum;
             group_barrier(1 + local, width);
             s = make_float2(0.f, 0.f);
-            for (int w = 0; w < (width >> 5); ++w) {
-                s.x += merge[parity][first_warp + w].x;
-                s.y += merge[parity][first_warp + w].y;
+#pragma unroll 4
+            for (int w = first_warp; w < first_warp + (width >> 5); ++w) {
+                s.x += merge[parity][0][w];
+                s.y += merge[parity][1][w];
             }
             parity ^= 1;
+        } else {
+            s.x = __shfl_sync(0xffffffffu, half_sum, 0, GW);
+            s.y = __shfl_sync(0xffffffffu, half_sum, GW / 2, GW);
         }
         // dx = rstd (a - c1 - xhat c2) = rstd a - k1 - (x - mean) k2
         const float k1 = rstd * s.x * inv, k2 = rstd * rstd * s.y * inv;
         if (live) {
+            TS* ds = static_cast<TS*>(p.d_stream) + r * C;
+            TB* db = has_branch ? static_cast<TB*>(p.d_branch) + r * C : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int at = (k * width + lane) * 8, col = at - shift;
-                if (col >= C) continue;
-                if constexpr (NV > 1) gsrc.get(gam, at, 1.f);
+                const int col = (k * width + lane) * 8 - shift;
                 float2 f[4], x[4], g[4];
                 read_slot<TB>(f, from + k * kBranch * threads, threads);
                 read_slot<TS>(x, from + (z_at + k * kStream) * threads, threads);
+                gamma_of(k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 a = __ffma2_rn(__fmul2_rn(f[j], gam[j]), both(rstd), both(-k1));
@@ -473,10 +509,12 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], x[j]);
                 }
-                store_row8<kAligned>(static_cast<TS*>(p.d_stream) + r * C, g, col, C);
-                if (p.d_branch != nullptr) {
-                    if (drop.threshold != 0) drop8(drop, g, static_cast<uint64_t>(r * C + col) >> 3);
-                    store_row8<kAligned>(static_cast<TB*>(p.d_branch) + r * C, g, col, C);
+                if (col < C) {
+                    store_row8<kAligned>(ds, g, col, C);
+                    if (has_branch) {
+                        if (drop.threshold != 0) drop8(drop, g, static_cast<uint64_t>(r * C + col) >> 3);
+                        store_row8<kAligned>(db, g, col, C);
+                    }
                 }
             }
         }
@@ -493,12 +531,22 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     for (int k = 0; k < NV; ++k) {
         const int col = (k * width + lane) * 8 - shift;
         float* to = combine ? smem + local * 2 * C : part;   // the groups' sums, [group][2][C]
+        if (kAligned) {
+            if (col >= C) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = col + j;
-            if (!in_row(c, C)) continue;
-            to[c] = j & 1 ? sum_g[k][j / 2].y : sum_g[k][j / 2].x;
-            to[C + c] = j & 1 ? sum_b[k][j / 2].y : sum_b[k][j / 2].x;
+            for (int j = 0; j < 4; j += 2) {
+                const float2 *g = &sum_g[k][j], *b = &sum_b[k][j];
+                *reinterpret_cast<float4*>(to + col + 2 * j) = make_float4(g[0].x, g[0].y, g[1].x, g[1].y);
+                *reinterpret_cast<float4*>(to + C + col + 2 * j) = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = col + j;
+                if (!in_row(c, C)) continue;
+                to[c] = j & 1 ? sum_g[k][j / 2].y : sum_g[k][j / 2].x;
+                to[C + c] = j & 1 ? sum_b[k][j / 2].y : sum_b[k][j / 2].x;
+            }
         }
     }
     if (!combine) return;
@@ -553,18 +601,23 @@ cudaError_t fwd_launch(const NormFwd& p, int vectors) {
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes, p.stream, p, staged);
 }
 
-template <typename TS, typename TB, bool kAligned, int G, int NV, int S>
+// Bytes a thread's vector slots take per stage.
+template <typename TS, typename TB>
+size_t slot_bytes(const NormBwd& p) {
+    return 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
+}
+
+template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int S>
 cudaError_t bwd_launch(const NormBwd& p, int vectors) {
-    auto kern = norm_bwd_rows_kernel<TS, TB, kAligned, G, NV, S>;
+    auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, S>;
     const int width = G > 0 ? G : (vectors + NV * 32 - 1) / (NV * 32) * 32;
     const int per_cta = G > 0 ? kWarpCta / G : static_cast<int>(std::min<long long>(kMaxCta / width, (p.rows + 7) / 8));
     const int threads = width * per_cta;
-    const int staged = NV > 1 && !params_line_up(p.gamma, nullptr, p.param_type, p.C);
-    const size_t per_thread = S * 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1)) + (staged ? 8 * sizeof(float) : 0);
-    size_t bytes = per_thread * NV * threads;
+    const int staged = NV > 1 && (p.gamma == nullptr || !params_line_up(p.gamma, nullptr, p.param_type, p.C));
+    size_t bytes = (S * slot_bytes<TS, TB>(p) + (staged ? 8 * sizeof(float) : 0)) * NV * threads;
     if (per_cta > 1 && p.partial != nullptr)
         bytes = std::max(bytes, static_cast<size_t>(per_cta) * 2 * p.C * sizeof(float));
-    if (bytes > kDynamicSmem) return cudaErrorNotSupported;   // (fp32 rows near 16384 with all three tensors)
+    if (bytes > kDynamicSmem) return cudaErrorNotSupported;
     static KernelFacts facts;
     cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
@@ -593,21 +646,24 @@ cudaError_t fwd_rows(const NormFwd& p) {
     return p.C % 8 == 0 ? fwd_rows_a<TS, TB, kAdd, true>(p) : fwd_rows_a<TS, TB, kAdd, false>(p);
 }
 
-template <typename TS, typename TB, bool kAligned>
+template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t bwd_rows_a(const NormBwd& p) {
     const int v = row_vectors(p.C);
-    if (v <= 8) return bwd_launch<TS, TB, kAligned, 8, 1, 2>(p, v);
-    if (v <= 16) return bwd_launch<TS, TB, kAligned, 16, 1, 2>(p, v);
-    if (v <= 32) return bwd_launch<TS, TB, kAligned, 32, 1, 2>(p, v);
-    if (v <= 64) return bwd_launch<TS, TB, kAligned, 32, 2, 2>(p, v);
-    if (v <= 128) return bwd_launch<TS, TB, kAligned, 32, 4, 1>(p, v);
-    if (v <= kMaxCta * kRowVecs) return bwd_launch<TS, TB, kAligned, 0, kRowVecs, 1>(p, v);
-    return cudaErrorNotSupported;
+    if (v <= 8) return bwd_launch<TS, TB, kAdd, kAligned, 8, 1, 2>(p, v);
+    if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, 16, 1, 2>(p, v);
+    if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, 32, 1, 2>(p, v);
+    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2>(p, v);
+    if (v <= 128) return bwd_launch<TS, TB, kAdd, kAligned, 32, 4, 1>(p, v);
+    if (v > kMaxCta * kRowVecs) return cudaErrorNotSupported;
+    // two rows per group in shared memory where they fit, else one (and not even one of the widest
+    // fp32 rows with all three tensors and staged parameters)
+    const cudaError_t err = bwd_launch<TS, TB, kAdd, kAligned, 0, kRowVecs, 2>(p, v);
+    return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, 0, kRowVecs, 1>(p, v);
 }
 
-template <typename TS, typename TB>
+template <typename TS, typename TB, bool kAdd>
 cudaError_t bwd_rows(const NormBwd& p) {
-    return p.C % 8 == 0 ? bwd_rows_a<TS, TB, true>(p) : bwd_rows_a<TS, TB, false>(p);
+    return p.C % 8 == 0 ? bwd_rows_a<TS, TB, kAdd, true>(p) : bwd_rows_a<TS, TB, kAdd, false>(p);
 }
 
 }  // namespace norm
