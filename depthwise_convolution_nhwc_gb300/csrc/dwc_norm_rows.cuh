@@ -311,7 +311,7 @@ __device__ __forceinline__ void read_slot(float2 (&f)[4], const uint4* slot, int
 }
 
 // CTAs per SM that the register budget allows: 80 registers a thread for one vector, 128 for 2 and
-// 4, of which 16 a vector hold the gradient sums.
+// 4, of which 16 a vector hold the gradient sums and 8 gamma.
 constexpr int bwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2; }
 
 // Barrier of one group of `threads` threads (a multiple of 32) of the CTA.
@@ -319,31 +319,42 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sums of two values over a group of GW lanes with one exchange and log2(GW) - 1 steps (half the
-// lanes carry one value, half the other): lanes 0 .. GW/2 - 1 return the first, the others the
-// second.
-template <int GW>
-__device__ __forceinline__ float pair_sum(float a, float b, int lane) {
-    const bool upper = (lane & (GW / 2)) != 0;
-    float v = upper ? b : a;
-    v += __shfl_xor_sync(0xffffffffu, upper ? a : b, GW / 2);
+// Sums of 2 R values over the GW lanes of a group, R = 1 or 2: the lanes part the values among
+// themselves (halves, then quarters), so that log2(GW) steps serve all.  Lanes lane / (GW / 2R) == q
+// return sum q of v[0], v[1], ...
+template <int GW, int R>
+__device__ __forceinline__ float parted_sum(const float (&v)[2 * R], int lane) {
+    float a = v[0], b = v[1];
+    int m = GW / 2;
+    if constexpr (R == 2) {
+        const bool upper = (lane & m) != 0;
+        const float c = upper ? v[0] : v[2], d = upper ? v[1] : v[3];
+        a = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, c, m);
+        b = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, d, m);
+        m /= 2;
+    }
+    const bool upper = (lane & m) != 0;
+    float t = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, m);
 #pragma unroll
-    for (int m = GW / 4; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
+    for (m /= 2; m > 0; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+    return t;
 }
 
 // Each thread keeps the sums of dy * xhat and dy of its columns in registers over all rows of its
 // group; at the end the groups of a CTA are added in order and the CTA writes one row of partial
-// sums.  The sums take the registers, so the rows wait in shared memory, S of them per group, and
-// are read twice there (before and after the row's two means are known).  G == 0: groups of
-// `group_threads` threads, several to a CTA where they are short: one CTA per SM, so that there
-// are few rows of partial sums.  kAdd: the residual form (dz, a branch gradient, dropout).
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int S>
+// sums.  The sums (and gamma, up to two vectors a thread) take the registers, so the rows wait in
+// shared memory, S times R rows per group, and are read twice there (before and after a row's
+// two means are known).  R rows go through together: one reduction and one barrier for both,
+// and two independent chains of latencies.  G == 0: groups of `group_threads` threads, several
+// to a CTA where they are short: one CTA per SM, so that there are few rows of partial sums.
+// kAdd: the residual form (dz, a branch gradient, dropout).
+template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
 __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, bwd_min_ctas(G, NV))
 norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     extern __shared__ __align__(16) float smem[];
-    __shared__ __align__(16) float merge[2][2][kMaxCta / 32];
+    __shared__ float merge[2][2 * R][kMaxCta / 32];
     constexpr bool kCta = G == 0;                  // several warps serve a row
+    constexpr bool kHeld = NV <= 2;                // gamma stays in registers
     constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
     constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // planes of a slot
     const int threads = kCta ? blockDim.x : kWarpCta;
@@ -352,7 +363,6 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     const int lane = threadIdx.x - local * width;
     const int sub = threadIdx.x % GW;
     const int per_cta = threads / width;
-    const int first_warp = local * width / 32;
     const int groups = gridDim.x * per_cta;
     const int group = blockIdx.x * per_cta + local;
     const int C = p.C;
@@ -360,20 +370,23 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     const float inv = 1.f / static_cast<float>(C);
     const bool has_dz = kAdd && p.dz != nullptr;
     const bool has_branch = kAdd && p.d_branch != nullptr;
-    // this thread's granules: stage, then slot (dy, z, dz of each vector), then plane
+    // this thread's granules: stage, row, then slot (dy, z, dz of each vector), then plane
     const int z_at = NV * kBranch, dz_at = z_at + NV * kStream;
-    const int stage_granules = (dz_at + (has_dz ? NV * kStream : 0)) * threads;
+    const int row_granules = (dz_at + (has_dz ? NV * kStream : 0)) * threads;
     uint4* mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;
     pdl_trigger();
     pdl_wait();
     DropState drop;
     if (kAdd) drop.init(p.drop);
 
-    auto fetch = [&](int stage, long long r) {
-        if (r < p.rows) {
+    auto fetch = [&](int stage, long long r0) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long r = r0 + static_cast<long long>(u) * groups;
+            if (r >= p.rows) continue;
             // elements from the row's start to the tensor's end, at least
             const int room = kAligned ? 0 : static_cast<int>(min((p.rows - r) * C, 1LL << 30));
-            uint4* to = mine + stage * stage_granules;
+            uint4* to = mine + (stage * R + u) * row_granules;
             const TB* dy = static_cast<const TB*>(p.dy) + r * p.ld_dy;
             const TS* z = static_cast<const TS*>(p.z) + r * p.ld_z;
             const TS* dz = has_dz ? static_cast<const TS*>(p.dz) + r * p.ld_dz : nullptr;
@@ -393,33 +406,39 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
         copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * groups);
+    for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
 
-    // gamma: registers for one vector a lane, else the caller's array (aligned fp32) or a copy
-    // along the shifted vectors, read per use
-    float2 gam[4];
+    // gamma: registers for one or two vectors a thread, else the caller's array (aligned fp32) or a
+    // copy along the shifted vectors, read per use
+    float2 gam[kHeld ? NV : 1][4];
     const float* gsrc = static_cast<const float*>(p.gamma);
     int last = C - 8;                               // the last whole vector there
-    if constexpr (NV == 1) {
+    if constexpr (kHeld) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = lane * 8 + 2 * k - shift;
-            gam[k] = make_float2(shifted_param(p.gamma, p.param_type, c, C, 1.f), shifted_param(p.gamma, p.param_type, c + 1, C, 1.f));
-        }
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = (k * width + lane) * 8 + 2 * j - shift;
+                gam[k][j] = make_float2(shifted_param(p.gamma, p.param_type, c, C, 1.f),
+                                        shifted_param(p.gamma, p.param_type, c + 1, C, 1.f));
+            }
     } else if (staged) {
         const int span = width * NV * 8;
-        float* g = smem + S * stage_granules * 4 + local * span;
+        float* g = smem + S * R * row_granules * 4 + local * span;
         for (int i = lane; i < span; i += width) g[i] = shifted_param(p.gamma, p.param_type, i - shift, C, 1.f);
         gsrc = g;
         last = span - 8;
         if (kCta) group_barrier(1 + local, width); else __syncwarp();
     }
-    auto gamma_of = [&](int k) {
-        if constexpr (NV > 1) {
+    auto gamma_of = [&](int k) -> const float2(&)[4] {
+        if constexpr (kHeld) {
+            return gam[k];
+        } else {
             const float* g = gsrc + min((k * width + lane) * 8, last);
             const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
-            gam[0] = make_float2(a.x, a.y), gam[1] = make_float2(a.z, a.w);
-            gam[2] = make_float2(b.x, b.y), gam[3] = make_float2(b.z, b.w);
+            gam[0][0] = make_float2(a.x, a.y), gam[0][1] = make_float2(a.z, a.w);
+            gam[0][2] = make_float2(b.x, b.y), gam[0][3] = make_float2(b.z, b.w);
+            return gam[0];
         }
     };
     float2 sum_g[NV][4], sum_b[NV][4];
@@ -428,84 +447,102 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum_g[k][j] = sum_b[k][j] = both(0.f);
     int parity = 0, stage = 0;
-    float next_mean = 0.f, next_rstd = 0.f;
-    if (group < p.rows) {
-        next_mean = p.mean[group];
-        next_rstd = p.rstd[group];
-    }
-
-    const int in_warp = kCta ? 0 : local % (32 / GW);
-    for (long long r = group; r - in_warp < p.rows; r += groups) {
-        const bool live = r < p.rows;
-        const float mean = next_mean, rstd = next_rstd;
-        if (r + groups < p.rows) {
-            next_mean = p.mean[r + groups];
-            next_rstd = p.rstd[r + groups];
+    float next_mean[R], next_rstd[R];
+    auto fetch_stats = [&](long long r0) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long r = r0 + static_cast<long long>(u) * groups;
+            next_mean[u] = r < p.rows ? p.mean[r] : 0.f;
+            next_rstd[u] = r < p.rows ? p.rstd[r] : 0.f;
         }
+    };
+    fetch_stats(group);
+
+    const long long step = static_cast<long long>(R) * groups;
+    const int in_warp = kCta ? 0 : local % (32 / GW);
+    for (long long r0 = group; r0 - in_warp < p.rows; r0 += step) {
+        float mean[R], rstd[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            mean[u] = next_mean[u];
+            rstd[u] = next_rstd[u];
+        }
+        fetch_stats(r0 + step);
         copy_wait<S - 1>();
         __syncwarp();
-        const uint4* from = mine + stage * stage_granules;
-        float2 s1 = both(0.f), s2 = both(0.f);
-        if (live) {
+        const uint4* from = mine + stage * R * row_granules;
+        float s[2 * R];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float2 f[4], x[4];
-                read_slot<TB>(f, from + k * kBranch * threads, threads);
-                read_slot<TS>(x, from + (z_at + k * kStream) * threads, threads);
-                gamma_of(k);
-                if constexpr (!kAligned) {
-                    const int col = (k * width + lane) * 8 - shift;
-                    if (!inside(col, C)) {
-                        mask8(f, col, C);
-                        mask8(x, col, C);
+        for (int u = 0; u < R; ++u) {
+            float2 s1 = both(0.f), s2 = both(0.f);
+            // (no barrier and no shuffle in here: a warp's groups may enter apart)
+            if (r0 + static_cast<long long>(u) * groups < p.rows) {
+                const uint4* row = from + u * row_granules;
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float2 f[4], x[4];
+                    read_slot<TB>(f, row + k * kBranch * threads, threads);
+                    read_slot<TS>(x, row + (z_at + k * kStream) * threads, threads);
+                    const float2(&gk)[4] = gamma_of(k);
+                    if constexpr (!kAligned) {
+                        const int col = (k * width + lane) * 8 - shift;
+                        if (!inside(col, C)) {
+                            mask8(f, col, C);
+                            mask8(x, col, C);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 xhat = __fmul2_rn(__fadd2_rn(x[j], both(-mean[u])), both(rstd[u]));
+                        const float2 a = __fmul2_rn(f[j], gk[j]);
+                        s1 = __fadd2_rn(s1, a);
+                        s2 = __ffma2_rn(a, xhat, s2);
+                        sum_g[k][j] = __ffma2_rn(f[j], xhat, sum_g[k][j]);
+                        sum_b[k][j] = __fadd2_rn(sum_b[k][j], f[j]);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 xhat = __fmul2_rn(__fadd2_rn(x[j], both(-mean)), both(rstd));
-                    const float2 a = __fmul2_rn(f[j], gam[j]);
-                    s1 = __fadd2_rn(s1, a);
-                    s2 = __ffma2_rn(a, xhat, s2);
-                    sum_g[k][j] = __ffma2_rn(f[j], xhat, sum_g[k][j]);
-                    sum_b[k][j] = __fadd2_rn(sum_b[k][j], f[j]);
-                }
             }
+            s[2 * u] = s1.x + s1.y;
+            s[2 * u + 1] = s2.x + s2.y;
         }
-        const float half_sum = pair_sum<GW>(s1.x + s1.y, s2.x + s2.y, sub);
-        float2 s;
+        constexpr int kPart = GW / (2 * R);   // lanes that hold one of the sums
+        float t = parted_sum<GW, R>(s, sub);
         if constexpr (kCta) {
-            if ((sub & 15) == 0) merge[parity][sub >> 4][threadIdx.x >> 5] = half_sum;
+            // the warps' sums: lane l of every warp takes sum l / kPart of warps l % kPart, ...
+            if (sub % kPart == 0) merge[parity][sub / kPart][threadIdx.x >> 5] = t;
             group_barrier(1 + local, width);
-            s = make_float2(0.f, 0.f);
-#pragma unroll 4
-            for (int w = first_warp; w < first_warp + (width >> 5); ++w) {
-                s.x += merge[parity][0][w];
-                s.y += merge[parity][1][w];
-            }
+            const int warps = width >> 5, first = local * warps;
+            t = 0.f;
+            for (int w = sub % kPart; w < warps; w += kPart) t += merge[parity][sub / kPart][first + w];
+#pragma unroll
+            for (int m = kPart / 2; m > 0; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
             parity ^= 1;
-        } else {
-            s.x = __shfl_sync(0xffffffffu, half_sum, 0, GW);
-            s.y = __shfl_sync(0xffffffffu, half_sum, GW / 2, GW);
         }
-        // dx = rstd (a - c1 - xhat c2) = rstd a - k1 - (x - mean) k2
-        const float k1 = rstd * s.x * inv, k2 = rstd * rstd * s.y * inv;
-        if (live) {
+#pragma unroll
+        for (int q = 0; q < 2 * R; ++q) s[q] = __shfl_sync(0xffffffffu, t, q * kPart, GW);
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long r = r0 + static_cast<long long>(u) * groups;
+            if (r >= p.rows) continue;        // (no barrier and no shuffle below)
+            // dx = rstd (a - c1 - xhat c2) = rstd a - k1 - (x - mean) k2
+            const float k1 = rstd[u] * s[2 * u] * inv, k2 = rstd[u] * rstd[u] * s[2 * u + 1] * inv;
+            const uint4* row = from + u * row_granules;
             TS* ds = static_cast<TS*>(p.d_stream) + r * C;
             TB* db = has_branch ? static_cast<TB*>(p.d_branch) + r * C : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = (k * width + lane) * 8 - shift;
                 float2 f[4], x[4], g[4];
-                read_slot<TB>(f, from + k * kBranch * threads, threads);
-                read_slot<TS>(x, from + (z_at + k * kStream) * threads, threads);
-                gamma_of(k);
+                read_slot<TB>(f, row + k * kBranch * threads, threads);
+                read_slot<TS>(x, row + (z_at + k * kStream) * threads, threads);
+                const float2(&gk)[4] = gamma_of(k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 a = __ffma2_rn(__fmul2_rn(f[j], gam[j]), both(rstd), both(-k1));
-                    g[j] = __ffma2_rn(__fadd2_rn(x[j], both(-mean)), both(-k2), a);
+                    const float2 a = __ffma2_rn(__fmul2_rn(f[j], gk[j]), both(rstd[u]), both(-k1));
+                    g[j] = __ffma2_rn(__fadd2_rn(x[j], both(-mean[u])), both(-k2), a);
                 }
                 if (has_dz) {
-                    read_slot<TS>(x, from + (dz_at + k * kStream) * threads, threads);
+                    read_slot<TS>(x, row + (dz_at + k * kStream) * threads, threads);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], x[j]);
                 }
@@ -519,7 +556,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             }
         }
         __syncwarp();   // all lanes have read the stage
-        fetch(stage, r + static_cast<long long>(S) * groups);
+        fetch(stage, r0 + S * step);
         if (++stage == S) stage = 0;
     }
     copy_wait<0>();
@@ -601,20 +638,25 @@ cudaError_t fwd_launch(const NormFwd& p, int vectors) {
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes, p.stream, p, staged);
 }
 
+// Groups of `width` threads in a CTA: several only once there is a row for every SM.
+inline int row_groups(long long rows, int width) {
+    return static_cast<int>(std::max(1LL, std::min<long long>(kMaxCta / width, rows / device_info().sm_count)));
+}
+
 // Bytes a thread's vector slots take per stage.
 template <typename TS, typename TB>
 size_t slot_bytes(const NormBwd& p) {
     return 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
 }
 
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int S>
+template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
 cudaError_t bwd_launch(const NormBwd& p, int vectors) {
-    auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, S>;
+    auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, R, S>;
     const int width = G > 0 ? G : (vectors + NV * 32 - 1) / (NV * 32) * 32;
-    const int per_cta = G > 0 ? kWarpCta / G : static_cast<int>(std::min<long long>(kMaxCta / width, (p.rows + 7) / 8));
+    const int per_cta = G > 0 ? kWarpCta / G : row_groups(p.rows, width);
     const int threads = width * per_cta;
-    const int staged = NV > 1 && (p.gamma == nullptr || !params_line_up(p.gamma, nullptr, p.param_type, p.C));
-    size_t bytes = (S * slot_bytes<TS, TB>(p) + (staged ? 8 * sizeof(float) : 0)) * NV * threads;
+    const int staged = NV > 2 && (p.gamma == nullptr || !params_line_up(p.gamma, nullptr, p.param_type, p.C));
+    size_t bytes = (S * R * slot_bytes<TS, TB>(p) + (staged ? 8 * sizeof(float) : 0)) * NV * threads;
     if (per_cta > 1 && p.partial != nullptr)
         bytes = std::max(bytes, static_cast<size_t>(per_cta) * 2 * p.C * sizeof(float));
     if (bytes > kDynamicSmem) return cudaErrorNotSupported;
@@ -649,16 +691,20 @@ cudaError_t fwd_rows(const NormFwd& p) {
 template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t bwd_rows_a(const NormBwd& p) {
     const int v = row_vectors(p.C);
-    if (v <= 8) return bwd_launch<TS, TB, kAdd, kAligned, 8, 1, 2>(p, v);
-    if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, 16, 1, 2>(p, v);
-    if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, 32, 1, 2>(p, v);
-    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2>(p, v);
-    if (v <= 128) return bwd_launch<TS, TB, kAdd, kAligned, 32, 4, 1>(p, v);
-    if (v > kMaxCta * kRowVecs) return cudaErrorNotSupported;
-    // two rows per group in shared memory where they fit, else one (and not even one of the widest
-    // fp32 rows with all three tensors and staged parameters)
-    const cudaError_t err = bwd_launch<TS, TB, kAdd, kAligned, 0, kRowVecs, 2>(p, v);
-    return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, 0, kRowVecs, 1>(p, v);
+    if (v <= 8) return bwd_launch<TS, TB, kAdd, kAligned, 8, 1, 2, 1>(p, v);
+    if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, 16, 1, 2, 1>(p, v);
+    if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, 32, 1, 2, 1>(p, v);
+    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2, 1>(p, v);
+    // two stages of two rows where they fit in shared memory, else one (of one row for the widest,
+    // and not even that for fp32 rows near 16384 with all three tensors and staged parameters)
+    cudaError_t err = cudaErrorNotSupported;
+    if (v <= kMaxCta * 2) {
+        err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 2>(p, v);
+        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 1>(p, v);
+    } else if (v <= kMaxCta * 4) {
+        err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
+    }
+    return err;
 }
 
 template <typename TS, typename TB, bool kAdd>
