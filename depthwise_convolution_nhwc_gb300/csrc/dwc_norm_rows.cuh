@@ -254,10 +254,12 @@ __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta) norm_fwd_rows_kern
 // ------------------------------------------------------------------------------ backward
 
 // Asynchronous copies of one row's tensors into the thread group's own part of shared memory.
-// Each thread holds 8 elements of every vector slot; a slot is one 16-byte granule of a 16-bit
-// type or two of fp32.  For fp32 the lanes of a warp copy consecutive granules (whole sectors)
-// and the two halves of a vector land in two planes, where both are read without bank
-// conflicts.  Vectors past the row's end are filled with zeros (a copy of no bytes), so the
+// Each thread holds 8 elements of every vector slot: one 16-byte granule of a 16-bit type or two of
+// fp32, of which the lanes of a warp copy consecutive ones (whole sectors).  A warp's granules stay
+// in the tensor's order, so each copy fills 512 contiguous bytes; the fp32 reads then meet in
+// banks two by two, which costs little: with the halves of the vectors parted into two planes
+// (no conflicts) the copies themselves were the limit, 238 us instead of 185 for 16384 x 4096 with
+// an fp32 stream.  Vectors past the row's end are filled with zeros (a copy of no bytes), so the
 // arithmetic needs no branches.  Granules that hang over the row's ends are copied whole while
 // they stay inside the tensor (the reader masks the neighbouring rows' elements); at the
 // tensor's very end single elements are stored instead.
@@ -283,28 +285,27 @@ __device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, 
     }
 }
 
-// One vector slot of the lanes of a (sub-)warp of GW lanes: `slot` is the thread's own granule of
-// the slot's first plane, `col` its first element, `plane` granules lie between two planes.
+// One vector slot of the lanes of a (sub-)warp of GW lanes: `slot` is the thread's own first granule,
+// `col` its first element.
 template <bool kAligned, typename T, int GW>
-__device__ __forceinline__ void copy_slot(uint4* slot, int plane, const T* row, int lane, int col, int C, int room) {
+__device__ __forceinline__ void copy_slot(uint4* slot, const T* row, int lane, int col, int C, int room) {
     if constexpr (sizeof(T) == 2) {
         copy_granule<kAligned>(slot, row, col, C, room);
     } else {
-        uint4* base = slot - lane + (lane & 1) * plane + (lane >> 1);
         const int first = col - 4 * lane;       // this lane's granule of the group's 2 * GW
-        copy_granule<kAligned>(base, row, first, C, room);
-        copy_granule<kAligned>(base + GW / 2, row, first + 4 * GW, C, room);
+        copy_granule<kAligned>(slot - lane, row, first, C, room);
+        copy_granule<kAligned>(slot - lane + GW, row, first + 4 * GW, C, room);
     }
 }
 
 template <typename T>
-__device__ __forceinline__ void read_slot(float2 (&f)[4], const uint4* slot, int plane) {
+__device__ __forceinline__ void read_slot(float2 (&f)[4], const uint4* slot) {
     if constexpr (sizeof(T) == 2) {
         Vec8<T> v;
         v.u = *slot;
         v.widen(f);
     } else {
-        const float4 a = *reinterpret_cast<const float4*>(slot), b = *reinterpret_cast<const float4*>(slot + plane);
+        const float4 a = reinterpret_cast<const float4*>(slot)[0], b = reinterpret_cast<const float4*>(slot)[1];
         f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
         f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
     }
@@ -356,7 +357,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     constexpr bool kCta = G == 0;                  // several warps serve a row
     constexpr bool kHeld = NV <= 2;                // gamma stays in registers
     constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
-    constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // planes of a slot
+    constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // granules of a slot
     const int threads = kCta ? blockDim.x : kWarpCta;
     const int width = kCta ? group_threads : G;
     const int local = threadIdx.x / width;         // group within the CTA
@@ -370,10 +371,11 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     const float inv = 1.f / static_cast<float>(C);
     const bool has_dz = kAdd && p.dz != nullptr;
     const bool has_branch = kAdd && p.d_branch != nullptr;
-    // this thread's granules: stage, row, then slot (dy, z, dz of each vector), then plane
-    const int z_at = NV * kBranch, dz_at = z_at + NV * kStream;
-    const int row_granules = (dz_at + (has_dz ? NV * kStream : 0)) * threads;
-    uint4* mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+    // shared memory: stage, row, then slot (dy, z, dz of each vector), then thread
+    const int z_at = NV * kBranch * threads, dz_at = z_at + NV * kStream * threads;
+    const int row_granules = dz_at + (has_dz ? NV * kStream * threads : 0);
+    uint4* const slots = reinterpret_cast<uint4*>(smem);
+    const int mine_b = threadIdx.x * kBranch, mine_s = threadIdx.x * kStream;   // this thread's granules of a slot
     pdl_trigger();
     pdl_wait();
     DropState drop;
@@ -386,20 +388,20 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             if (r >= p.rows) continue;
             // elements from the row's start to the tensor's end, at least
             const int room = kAligned ? 0 : static_cast<int>(min((p.rows - r) * C, 1LL << 30));
-            uint4* to = mine + (stage * R + u) * row_granules;
+            uint4* to = slots + (stage * R + u) * row_granules;
             const TB* dy = static_cast<const TB*>(p.dy) + r * p.ld_dy;
             const TS* z = static_cast<const TS*>(p.z) + r * p.ld_z;
             const TS* dz = has_dz ? static_cast<const TS*>(p.dz) + r * p.ld_dz : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = (k * width + lane) * 8 - shift;
-                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads, threads, dy, sub, col, C, room);
-                copy_slot<kAligned, TS, GW>(to + (z_at + k * kStream) * threads, threads, z, sub, col, C, room);
+                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, col, C, room);
+                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, col, C, room);
             }
             if (has_dz) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
-                    copy_slot<kAligned, TS, GW>(to + (dz_at + k * kStream) * threads, threads, dz, sub,
+                    copy_slot<kAligned, TS, GW>(to + dz_at + k * kStream * threads + mine_s, dz, sub,
                                                 (k * width + lane) * 8 - shift, C, room);
             }
         }
@@ -470,7 +472,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
         fetch_stats(r0 + step);
         copy_wait<S - 1>();
         __syncwarp();
-        const uint4* from = mine + stage * R * row_granules;
+        const uint4* from = slots + stage * R * row_granules;
         float s[2 * R];
 #pragma unroll
         for (int u = 0; u < R; ++u) {
@@ -481,8 +483,8 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     float2 f[4], x[4];
-                    read_slot<TB>(f, row + k * kBranch * threads, threads);
-                    read_slot<TS>(x, row + (z_at + k * kStream) * threads, threads);
+                    read_slot<TB>(f, row + k * kBranch * threads + mine_b);
+                    read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
                     const float2(&gk)[4] = gamma_of(k);
                     if constexpr (!kAligned) {
                         const int col = (k * width + lane) * 8 - shift;
@@ -533,8 +535,8 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             for (int k = 0; k < NV; ++k) {
                 const int col = (k * width + lane) * 8 - shift;
                 float2 f[4], x[4], g[4];
-                read_slot<TB>(f, row + k * kBranch * threads, threads);
-                read_slot<TS>(x, row + (z_at + k * kStream) * threads, threads);
+                read_slot<TB>(f, row + k * kBranch * threads + mine_b);
+                read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
                 const float2(&gk)[4] = gamma_of(k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -542,7 +544,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
                     g[j] = __ffma2_rn(__fadd2_rn(x[j], both(-mean[u])), both(-k2), a);
                 }
                 if (has_dz) {
-                    read_slot<TS>(x, row + (dz_at + k * kStream) * threads, threads);
+                    read_slot<TS>(x, row + dz_at + k * kStream * threads + mine_s);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], x[j]);
                 }
@@ -700,7 +702,7 @@ cudaError_t bwd_rows_a(const NormBwd& p) {
     cudaError_t err = cudaErrorNotSupported;
     if (v <= kMaxCta * 2) {
         err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 2>(p, v);
-        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 1>(p, v);
+        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 1, 2>(p, v);
     } else if (v <= kMaxCta * 4) {
         err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
     }
