@@ -26,16 +26,26 @@ import functools
 
 import torch
 
-from . import _call, load_library
+from . import DwcError, load_library
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_F32 = torch.float32
+
+# The current stream's handle without building a Stream object (a microsecond of a small call).
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+@functools.lru_cache(maxsize=None)
+def _fn(name: str):
+    return getattr(load_library(), name)
 
 
 def _code(dtype) -> int:
-    try:
-        return _CODE[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {dtype} (fp32, bf16 or fp16)") from None
+    code = _CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (fp32, bf16 or fp16)")
+    return code
 
 
 def _stride(t, what: str) -> int:
@@ -61,214 +71,230 @@ def _stride(t, what: str) -> int:
 
 
 def _rows(t, what: str):
-    """(rows, C, row stride) of a tensor on a CUDA device."""
-    if not t.is_cuda:
+    """(shape, device index, channels, row stride) of a tensor on a CUDA device."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device (no CPU fallback)")
-    if t.dim() < 1 or t.shape[-1] < 1:
+    shape = t.shape
+    if not shape or shape[-1] < 1:
         raise ValueError(f"{what} must be [..., C] with at least one channel")
-    C = t.shape[-1]
-    return t.numel() // C, C, _stride(t, what)
+    return shape, dev, shape[-1], shape[-1] if t.is_contiguous() else _stride(t, what)
 
 
-def _like(t, x, dtype, what: str) -> int:
-    """Row stride of a second tensor of x's shape."""
-    if t.shape != x.shape or t.dtype != dtype or t.device != x.device:
-        raise ValueError(f"{what} must be a {tuple(x.shape)} {dtype} tensor on {x.device} "
+def _like(t, shape, dev, dtype, what: str) -> int:
+    """Row stride of a second tensor of that shape (dtype None: any)."""
+    if t.shape != shape or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be a {tuple(shape)} {dtype or ''} tensor on cuda:{dev} "
                          f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
-    return _stride(t, what)
+    return shape[-1] if t.is_contiguous() else _stride(t, what)
 
 
-def _out(t, shape, dtype, x, what: str):
-    """A dense output: the caller's, checked, or a new one."""
+def _out(t, like, dtype, what: str):
+    """A dense output of `like`'s shape: the caller's, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=x.device)
-    if t.shape != shape or t.dtype != dtype or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {x.device} "
+        if like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)
+        return torch.empty(like.shape, dtype=dtype, device=like.device)
+    if t.shape != like.shape or t.dtype != dtype or t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(like.shape)} {dtype} tensor on {like.device} "
                          f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
     return t
 
 
-def _param(t, C: int, x, what: str):
-    """(pointer, type code) of gamma or beta."""
-    if t is None:
-        return None, None
-    if t.dim() != 1 or t.shape[0] != C or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"{what} must hold {C} values on {x.device} (got {tuple(t.shape)} on {t.device})")
-    return t.data_ptr(), _code(t.dtype)
+def _param(t, C: int, dev: int, what: str) -> int:
+    """Pointer of gamma or beta."""
+    if t.numel() != C or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must hold {C} values on cuda:{dev} (got {tuple(t.shape)} on {t.device})")
+    return t.data_ptr()
 
 
-def _params(gamma, beta, C: int, x):
-    g, gt = _param(gamma, C, x, "gamma")
-    b, bt = _param(beta, C, x, "beta")
-    if gt is not None and bt is not None and gt != bt:
+def _params(gamma, beta, C: int, dev: int):
+    """(gamma's pointer, beta's, their type code)."""
+    g = None if gamma is None else _param(gamma, C, dev, "gamma")
+    b = None if beta is None else _param(beta, C, dev, "beta")
+    if gamma is None:
+        return g, b, 0 if beta is None else _code(beta.dtype)
+    if beta is not None and beta.dtype != gamma.dtype:
         raise ValueError("gamma and beta must have one dtype")
-    return g, b, gt if gt is not None else (bt or 0)
+    return g, b, _code(gamma.dtype)
 
 
-def _stat(t, x, what: str) -> int:
-    if t.shape != x.shape[:-1] or t.dtype != torch.float32 or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {tuple(x.shape[:-1])} fp32 tensor on {x.device} "
+def _stat(t, lead, dev: int, what: str) -> int:
+    if t.shape != lead or t.dtype != _F32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(lead)} fp32 tensor on cuda:{dev} "
                          f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
     return t.data_ptr()
 
 
-def _random(p, seed, offset, x):
+_M64 = 2 ** 64 - 1
+
+
+def _random(p, seed, offset, dev: int):
     """(p, seed, offset, step pointer) of a dropout."""
     p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1] (got {p})")
     if isinstance(offset, torch.Tensor):
-        if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != x.device:
+        if offset.dtype != torch.int64 or offset.numel() != 1 or offset.get_device() != dev:
             raise ValueError("an offset on the device must be one int64 value on the tensors' device")
-        return p, int(seed) & (2 ** 64 - 1), 0, offset.data_ptr()
-    return p, int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1), None
+        return p, int(seed) & _M64, 0, offset.data_ptr()
+    return p, int(seed) & _M64, int(offset) & _M64, None
 
 
-def _run(x, fn: str, *args) -> None:
-    """The library call on the current stream of x's device, with that device current."""
-    dev = x.get_device()
+def _run(dev: int, name: str, *args) -> None:
+    """The library call on the current stream of device `dev`, with that device current."""
     if dev == torch.cuda.current_device():
-        _call(fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+        code = _fn(name)(*args, _stream_handle(dev))
     else:
         with torch.cuda.device(dev):
-            _call(fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+            code = _fn(name)(*args, _stream_handle(dev))
+    if code != 0:
+        raise DwcError(name, code)
 
 
-def _on_stream(f):
-    """``stream``: run the call, its allocations included, on that stream."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        tensors = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)]
-        for t in tensors:
-            if t.is_cuda and t.device != stream.device:
-                raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
-        with torch.cuda.stream(stream):
-            out = f(*args, **kw)
-        for t in tensors:
-            if t.is_cuda:
-                t.record_stream(stream)
-        return out
-    return call
+def _on(stream, f, *args):
+    """The call f(*args), its allocations included, on `stream`."""
+    tensors = [t for t in args if isinstance(t, torch.Tensor) and t.is_cuda]
+    for t in tensors:
+        if t.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+    with torch.cuda.stream(stream):
+        out = f(*args)
+    for t in tensors:
+        t.record_stream(stream)
+    return out
 
 
-@_on_stream
 def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, out=None, out_dtype=None,
-                   stats: bool = False):
+                   stats: bool = False, stream=None):
     """y = (x - mean) * rstd * gamma + beta over the last axis; y, or (y, mean, rstd) with
     ``stats`` (fp32, what the backward pass needs).  y has x's dtype, or ``out_dtype`` (``out``'s):
     a 16-bit type for fp32 x.  gamma and beta: C values of one dtype each, or None."""
-    rows, C, ld = _rows(x, "x")
-    od = out_dtype or (x.dtype if out is None else out.dtype)
-    g, b, pt = _params(gamma, beta, C, x)
-    y = _out(out, x.shape, od, x, "out")
-    mean = rstd = None
-    if stats:
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) for _ in range(2))
-    _run(x, "dwc_layer_norm_fwd", x.data_ptr(), ld, g, b, pt, eps, y.data_ptr(),
-         mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, rows, C,
-         _code(x.dtype), _code(od))
-    return (y, mean, rstd) if stats else y
+    if stream is not None:
+        return _on(stream, layer_norm_fwd, x, gamma, beta, eps, out, out_dtype, stats)
+    shape, dev, C, ld = _rows(x, "x")
+    dtype = x.dtype
+    od = out_dtype or (dtype if out is None else out.dtype)
+    g, b, pt = _params(gamma, beta, C, dev)
+    y = _out(out, x, od, "out")
+    if not stats:
+        _run(dev, "dwc_layer_norm_fwd", x.data_ptr(), ld, g, b, pt, eps, y.data_ptr(), None, None,
+             x.numel() // C, C, _code(dtype), _code(od))
+        return y
+    mean = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _run(dev, "dwc_layer_norm_fwd", x.data_ptr(), ld, g, b, pt, eps, y.data_ptr(), mean.data_ptr(),
+         rstd.data_ptr(), x.numel() // C, C, _code(dtype), _code(od))
+    return y, mean, rstd
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(device: int, rows: int, C: int) -> int:
-    with torch.cuda.device(device):
-        return int(load_library().dwc_layer_norm_bwd_workspace_size(rows, C))
+def _workspace_bytes(dev: int, rows: int, C: int) -> int:
+    with torch.cuda.device(dev):
+        return int(_fn("dwc_layer_norm_bwd_workspace_size")(rows, C))
 
 
-def _param_grads(x, rows: int, C: int, wanted: bool):
-    """(dgamma, dbeta, workspace) of a backward pass."""
-    if not wanted:
-        return None, None, None
-    grads = torch.empty((2, C), dtype=torch.float32, device=x.device)
-    ws = torch.empty(_workspace_bytes(x.get_device(), rows, C), dtype=torch.uint8, device=x.device)
-    return grads[0], grads[1], ws
+def _param_grads(x, dev: int, rows: int, C: int):
+    """(dgamma, dbeta, workspace) of a backward pass.  The workspace comes from PyTorch's allocator
+    call by call, so it belongs to the call's stream (or graph) and to no other."""
+    dgamma = torch.empty(C, dtype=_F32, device=x.device)
+    return dgamma, torch.empty_like(dgamma), torch.empty(_workspace_bytes(dev, rows, C), dtype=torch.uint8,
+                                                         device=x.device)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-@_on_stream
-def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = True):
+def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = True, stream=None):
     """(dx, dgamma, dbeta) of ``layer_norm_fwd`` from dy, its x and its statistics: dx in x's
     dtype, dgamma and dbeta fp32 (None without ``param_grads``)."""
-    rows, C, ld = _rows(x, "x")
-    lddy = _like(dy, x, dy.dtype, "dy")
-    g, _, pt = _params(gamma, None, C, x)
-    m, r = _stat(mean, x, "mean"), _stat(rstd, x, "rstd")
-    dx = _out(out, x.shape, x.dtype, x, "out")
-    dgamma, dbeta, ws = _param_grads(x, rows, C, param_grads)
-    _run(x, "dwc_layer_norm_bwd", dy.data_ptr(), lddy, x.data_ptr(), ld, m, r, g, pt, dx.data_ptr(),
-         _ptr(dgamma), _ptr(dbeta), rows, C, _code(x.dtype), _code(dy.dtype), _ptr(ws),
-         0 if ws is None else ws.numel())
+    if stream is not None:
+        return _on(stream, layer_norm_bwd, dy, x, mean, rstd, gamma, out, param_grads)
+    shape, dev, C, ld = _rows(x, "x")
+    rows, dtype, lead = x.numel() // C, x.dtype, shape[:-1]
+    lddy = _like(dy, shape, dev, None, "dy")
+    g, _, pt = _params(gamma, None, C, dev)
+    m, r = _stat(mean, lead, dev, "mean"), _stat(rstd, lead, dev, "rstd")
+    dx = _out(out, x, dtype, "out")
+    dgamma = dbeta = dg = db = w = None
+    n = 0
+    if param_grads:
+        dgamma, dbeta, ws = _param_grads(x, dev, rows, C)
+        dg, db, w, n = dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel()
+    _run(dev, "dwc_layer_norm_bwd", dy.data_ptr(), lddy, x.data_ptr(), ld, m, r, g, pt, dx.data_ptr(), dg, db,
+         rows, C, _code(dtype), _code(dy.dtype), w, n)
     return dx, dgamma, dbeta
 
 
-def _dropout(fn, x, p, seed, offset, out, what):
-    rows, C, ld = _rows(x, what)
-    p, seed, offset, step = _random(p, seed, offset, x)
-    y = _out(out, x.shape, x.dtype, x, "out")
-    _run(x, fn, x.data_ptr(), ld, y.data_ptr(), rows, C, p, seed, offset, step, _code(x.dtype))
+def _dropout(name, x, p, seed, offset, out, what):
+    _, dev, C, ld = _rows(x, what)
+    p, seed, offset, step = _random(p, seed, offset, dev)
+    dtype = x.dtype
+    y = _out(out, x, dtype, "out")
+    _run(dev, name, x.data_ptr(), ld, y.data_ptr(), x.numel() // C, C, p, seed, offset, step, _code(dtype))
     return y
 
 
-@_on_stream
-def dropout_fwd(x, p: float, seed: int, offset=0, out=None):
+def dropout_fwd(x, p: float, seed: int, offset=0, out=None, stream=None):
     """x / (1 - q) where kept, 0 where dropped, with probability q = p to the nearest 2^-16;
     ``out`` may be x."""
+    if stream is not None:
+        return _on(stream, dropout_fwd, x, p, seed, offset, out)
     return _dropout("dwc_dropout_fwd", x, p, seed, offset, out, "x")
 
 
-@_on_stream
-def dropout_bwd(dy, p: float, seed: int, offset=0, out=None):
+def dropout_bwd(dy, p: float, seed: int, offset=0, out=None, stream=None):
     """dx of ``dropout_fwd`` with the same p, seed and offset; ``out`` may be dy."""
+    if stream is not None:
+        return _on(stream, dropout_bwd, dy, p, seed, offset, out)
     return _dropout("dwc_dropout_bwd", dy, p, seed, offset, out, "dy")
 
 
-@_on_stream
 def add_layer_norm_fwd(x, res, gamma=None, beta=None, eps: float = 1e-5, p: float = 0.0, seed: int = 0,
-                       offset=0, out=None, z=None, stats: bool = False):
+                       offset=0, out=None, z=None, stats: bool = False, stream=None):
     """z = res + dropout(x), y = layer_norm(z) in one pass; (y, z), or (y, z, mean, rstd) with
     ``stats``.  y has x's dtype, z has res's: the same, or fp32 with a 16-bit x.  ``z`` may be
     res (an update of the residual stream in place)."""
-    rows, C, ldx = _rows(x, "x")
-    ldr = _like(res, x, res.dtype, "res")
-    p, seed, offset, step = _random(p, seed, offset, x)
-    g, b, pt = _params(gamma, beta, C, x)
-    y = _out(out, x.shape, x.dtype, x, "out")
-    z = _out(z, x.shape, res.dtype, x, "z")
-    mean = rstd = None
+    if stream is not None:
+        return _on(stream, add_layer_norm_fwd, x, res, gamma, beta, eps, p, seed, offset, out, z, stats)
+    shape, dev, C, ldx = _rows(x, "x")
+    ldr = _like(res, shape, dev, None, "res")
+    p, seed, offset, step = _random(p, seed, offset, dev)
+    g, b, pt = _params(gamma, beta, C, dev)
+    dtype, rdtype = x.dtype, res.dtype
+    y = _out(out, x, dtype, "out")
+    z = _out(z, res, rdtype, "z")
+    mean = rstd = m = r = None
     if stats:
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) for _ in range(2))
-    _run(x, "dwc_add_layer_norm_fwd", x.data_ptr(), ldx, res.data_ptr(), ldr, p, seed, offset, step, g, b, pt,
-         eps, z.data_ptr(), y.data_ptr(), mean.data_ptr() if stats else None,
-         rstd.data_ptr() if stats else None, rows, C, _code(x.dtype), _code(res.dtype))
+        mean = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+        rstd = torch.empty_like(mean)
+        m, r = mean.data_ptr(), rstd.data_ptr()
+    _run(dev, "dwc_add_layer_norm_fwd", x.data_ptr(), ldx, res.data_ptr(), ldr, p, seed, offset, step, g, b, pt,
+         eps, z.data_ptr(), y.data_ptr(), m, r, x.numel() // C, C, _code(dtype), _code(rdtype))
     return (y, z, mean, rstd) if stats else (y, z)
 
 
-@_on_stream
 def add_layer_norm_bwd(dy, z, mean, rstd, gamma=None, dz=None, p: float = 0.0, seed: int = 0, offset=0,
-                       param_grads: bool = True):
+                       param_grads: bool = True, stream=None):
     """(dx, dres, dgamma, dbeta) of ``add_layer_norm_fwd``: dres = dz + layer_norm_bwd(dy) in z's
     dtype, dx = the dropout map of dres in dy's.  ``dz``: the gradient that reaches z from the rest
     of the residual stream (None: zero).  Without dropout and with one dtype dx is dres."""
-    rows, C, ldz = _rows(z, "z")
-    lddy = _like(dy, z, dy.dtype, "dy")
-    lddz = C if dz is None else _like(dz, z, z.dtype, "dz")
-    p, seed, offset, step = _random(p, seed, offset, z)
-    g, _, pt = _params(gamma, None, C, z)
-    m, r = _stat(mean, z, "mean"), _stat(rstd, z, "rstd")
-    dres = torch.empty(z.shape, dtype=z.dtype, device=z.device)
-    dx = dres
-    if p != 0.0 or dy.dtype != z.dtype:
-        dx = torch.empty(z.shape, dtype=dy.dtype, device=z.device)
-    dgamma, dbeta, ws = _param_grads(z, rows, C, param_grads)
-    _run(z, "dwc_add_layer_norm_bwd", dy.data_ptr(), lddy, _ptr(dz), lddz, z.data_ptr(), ldz, m, r, g, pt, p,
-         seed, offset, step, None if dx is dres else dx.data_ptr(), dres.data_ptr(), _ptr(dgamma), _ptr(dbeta),
-         rows, C, _code(dy.dtype), _code(z.dtype), _ptr(ws), 0 if ws is None else ws.numel())
+    if stream is not None:
+        return _on(stream, add_layer_norm_bwd, dy, z, mean, rstd, gamma, dz, p, seed, offset, param_grads)
+    shape, dev, C, ldz = _rows(z, "z")
+    rows, zdtype, lead, dtype = z.numel() // C, z.dtype, shape[:-1], dy.dtype
+    lddy = _like(dy, shape, dev, None, "dy")
+    lddz = C if dz is None else _like(dz, shape, dev, zdtype, "dz")
+    p, seed, offset, step = _random(p, seed, offset, dev)
+    g, _, pt = _params(gamma, None, C, dev)
+    m, r = _stat(mean, lead, dev, "mean"), _stat(rstd, lead, dev, "rstd")
+    dres = _out(None, z, zdtype, "dres")
+    dx = dres if p == 0.0 and dtype == zdtype else _out(None, dy, dtype, "dx")
+    dgamma = dbeta = dg = db = w = None
+    n = 0
+    if param_grads:
+        dgamma, dbeta, ws = _param_grads(z, dev, rows, C)
+        dg, db, w, n = dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel()
+    _run(dev, "dwc_add_layer_norm_bwd", dy.data_ptr(), lddy, None if dz is None else dz.data_ptr(), lddz,
+         z.data_ptr(), ldz, m, r, g, pt, p, seed, offset, step, None if dx is dres else dx.data_ptr(),
+         dres.data_ptr(), dg, db, rows, C, _code(dtype), _code(zdtype), w, n)
     return dx, dres, dgamma, dbeta
 
 
