@@ -3,8 +3,9 @@
 //
 // Both passes are bound by memory: a row is read once, reduced in registers or shared memory and
 // written once, 8 elements per access.  A group of threads serves one row:
-//   rows of up to 8, 16 and 32 vectors: G = 8, 16, 32 lanes, one vector each; up to 64 and 128
-//   vectors: a warp with 2 and 4; longer rows (up to 4 vectors x 512 threads): several warps.
+//   rows of up to 8, 16 and 32 vectors: G = 8, 16, 32 lanes, one vector each; up to 64 vectors: a
+//   warp with 2; longer rows: several warps, 2 vectors a thread and above 1024 vectors 4 (up to
+//   512 threads).
 //
 // Alignment.  A dense row of C channels starts (row * C) mod 8 elements past a vector boundary, and
 // so does every tensor of the call if its base is aligned and its row stride is congruent to C
@@ -22,7 +23,6 @@
 namespace dwc {
 namespace norm {
 
-constexpr int kRowVecs = 4;              // vectors per thread where several warps serve a row
 constexpr int kWarpCta = 256;            // threads of a CTA whose warps or lane groups serve rows
 constexpr int kMaxCta = 512;             // threads of a CTA otherwise: 128 registers each
 constexpr int kDynamicSmem = 225 * 1024;
@@ -34,19 +34,10 @@ inline int row_vectors(int C) {
     return (C + (8 - g) + 7) / 8;
 }
 
-// Sum over the G lanes of a group.
-template <int G>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int m = G / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
-}
-
-// Elements that warp `warp` of a group of `threads` threads holds of a row.
-__device__ __forceinline__ int warp_columns(int warp, int threads, int shift, int C) {
+// Elements that warp `warp` of a group of `threads` threads with `vecs` vectors each holds of a row.
+__device__ __forceinline__ int warp_columns(int warp, int threads, int vecs, int shift, int C) {
     int n = 0;
-#pragma unroll
-    for (int k = 0; k < kRowVecs; ++k) {
+    for (int k = 0; k < vecs; ++k) {
         const int lo = max(0, (k * threads + warp * 32) * 8 - shift);
         const int hi = min(C, (k * threads + warp * 32 + 32) * 8 - shift);
         n += max(0, hi - lo);
@@ -54,204 +45,53 @@ __device__ __forceinline__ int warp_columns(int warp, int threads, int shift, in
     return n;
 }
 
-// Where a group finds 8 consecutive parameters in fp32: the caller's own fp32 array where the
-// vectors line up with it, else a copy in shared memory laid out along the group's shifted
-// vectors (written once per group, read for every row).
-struct ParamSource {
-    const float* p = nullptr;            // indexed by column + shift
-    bool present = false;
-    __device__ __forceinline__ void get(float2 (&f)[4], int at, float absent) const {
-        if (!present) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = both(absent);
-            return;
-        }
-        const float4 a = *reinterpret_cast<const float4*>(p + at), b = *reinterpret_cast<const float4*>(p + at + 4);
-        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
-        f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
-    }
-};
-
 __device__ __forceinline__ float shifted_param(const void* p, int type, int c, int C, float absent) {
     return in_row(c, C) ? load_param(p, type, c, absent) : 0.f;
 }
 
-// ------------------------------------------------------------------------------- forward
-//
-// Row statistics: each warp (or lane group) takes the mean of its own elements, then the sum of
-// squares about it, and the warps of a group are merged by their counts (Chan, Golub and LeVeque,
-// "Updating formulae and a pairwise algorithm for computing sample variances", 1979): one
-// barrier per row, and no cancellation however far the mean lies from zero.
-
-// Elements col .. col + 7: a whole vector where it lies within [low, room) of the row's start (the
-// tensor's extent: neighbouring rows' elements are masked after), else the row's own elements.
-template <bool kAligned, typename T>
-__device__ __forceinline__ void load_row8(Vec8<T>& v, const T* row, int col, int C, int low, int room) {
-    if (kAligned || (col >= low && col + 8 <= room)) {
-        v.load(row + col);
-    } else {
-        v.zero();
+// Gamma or beta of a thread's vectors.  Up to two vectors a thread they stay in registers; beyond
+// that they are read per use, from the caller's array where that is fp32 and lines up with the
+// vectors, else from a copy in shared memory laid out along the group's shifted vectors.
+template <int NV>
+struct Params {
+    static constexpr bool kHeld = NV <= 2;
+    float2 f[kHeld ? NV : 1][4];
+    const float* from;
+    int last;                             // the last vector that may be read there
+    __device__ __forceinline__ void hold(const void* p, int type, int C, int lane, int width, int shift, float absent) {
+        if constexpr (kHeld) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (in_row(col + j, C)) v.set(j, row[col + j]);
-    }
-}
-
-// G > 0: lanes of a row's group, NV vectors a lane, U rows at a time (their loads in flight
-// together); G == 0: the CTA serves a row.  `staged`: parameters go through shared memory.
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int U>
-__global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta) norm_fwd_rows_kernel(NormFwd p, int staged) {
-    extern __shared__ __align__(16) float smem[];
-    __shared__ float2 merge[2][32];
-    constexpr bool kCta = G == 0;
-    constexpr int GW = kCta ? 32 : G;                              // lanes that reduce by shuffles
-    const int width = kCta ? blockDim.x : G;                       // threads of a group
-    const int lane = kCta ? threadIdx.x : threadIdx.x % GW;
-    const int local = kCta ? 0 : threadIdx.x / GW;                 // group within the CTA
-    const int per_cta = kCta ? 1 : kWarpCta / GW;
-    const int groups = gridDim.x * per_cta;
-    const int group = blockIdx.x * per_cta + local;
-    const int C = p.C;
-    const int shift = kAligned ? 0 : static_cast<int>((static_cast<long long>(group) * C) & 7);
-    const float inv = 1.f / static_cast<float>(C);
-    // (an update in place overwrites the neighbouring rows: then only the row's own elements are read)
-    const bool whole = !kAdd || p.z != p.in;
-    const int low = whole ? -8 : 0;
-    pdl_trigger();
-    pdl_wait();
-    DropState drop;
-    if (kAdd) drop.init(p.drop);
-
-    // parameters: registers for one vector a lane, else read (or staged) per use
-    float2 gam[4], bet[4];
-    ParamSource gsrc, bsrc;
-    if constexpr (NV == 1) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = lane * 8 + 2 * k - shift;
-            gam[k] = make_float2(shifted_param(p.gamma, p.param_type, c, C, 1.f), shifted_param(p.gamma, p.param_type, c + 1, C, 1.f));
-            bet[k] = make_float2(shifted_param(p.beta, p.param_type, c, C, 0.f), shifted_param(p.beta, p.param_type, c + 1, C, 0.f));
-        }
-    } else {
-        gsrc.present = staged || p.gamma != nullptr;
-        bsrc.present = staged || p.beta != nullptr;
-        gsrc.p = static_cast<const float*>(p.gamma);
-        bsrc.p = static_cast<const float*>(p.beta);
-        if (staged) {
-            const int span = width * NV * 8;
-            float* g = smem + local * 2 * span;
-            for (int i = lane; i < span; i += width) {
-                g[i] = shifted_param(p.gamma, p.param_type, i - shift, C, 1.f);
-                g[span + i] = shifted_param(p.beta, p.param_type, i - shift, C, 0.f);
-            }
-            gsrc.p = g;
-            bsrc.p = g + span;
-            if (kCta) __syncthreads(); else __syncwarp();
-        }
-    }
-    // elements of this thread's warp or group, and (lane l) of warp l of the CTA
-    const int mine = kCta ? warp_columns(threadIdx.x >> 5, width, shift, C) : C;
-    const int peer = kCta && (threadIdx.x & 31) < (width >> 5) ? warp_columns(threadIdx.x & 31, width, shift, C) : 0;
-    const float mine_inv = mine > 0 ? 1.f / static_cast<float>(mine) : 0.f;
-    int parity = 0;
-
-    // (the lane groups of a warp stay together: the warp goes on while its first group has a row)
-    const int in_warp = kCta ? 0 : local % (32 / GW);
-    for (long long r0 = group; r0 - in_warp < p.rows; r0 += static_cast<long long>(groups) * U) {
-        Vec8<TS> raw[U][NV];
-        Vec8<TB> branch[kAdd ? U : 1][kAdd ? NV : 1];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long r = r0 + static_cast<long long>(u) * groups;
-            // elements from the row's start to the tensor's end, at least
-            const int room = kAligned ? 0 : whole ? static_cast<int>(min((p.rows - r) * C, 1LL << 30)) : C;
-            const TS* in = static_cast<const TS*>(p.in) + r * p.ld_in;
-            const TB* x = static_cast<const TB*>(p.x) + r * p.ld_x;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
-                raw[u][k].zero();
-                if constexpr (kAdd) branch[u][k].zero();
-                if (r < p.rows && col < C) {
-                    load_row8<kAligned>(raw[u][k], in, col, C, low, room);
-                    if constexpr (kAdd) load_row8<kAligned>(branch[u][k], x, col, C, low, room);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long r = r0 + static_cast<long long>(u) * groups;
-            const bool live = r < p.rows;
-            float2 v[NV][4], s2 = both(0.f);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
-                raw[u][k].widen(v[k]);
-                if constexpr (kAdd) {
-                    float2 b[4];
-                    branch[u][k].widen(b);
-                    if (drop.threshold != 0 && live && col < C)
-                        drop8(drop, b, static_cast<uint64_t>(r * C + col) >> 3);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[k][j] = __fadd2_rn(v[k][j], b[j]);
-                    if (live && col < C) store_row8<kAligned>(static_cast<TS*>(p.z) + r * C, v[k], col, C);
-                }
-                if (!kAligned && !inside(col, C)) mask8(v[k], col, C);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s2 = __fadd2_rn(s2, v[k][j]);
-            }
-            float mean = group_sum<GW>(s2.x + s2.y) * mine_inv;
-            float2 q2 = both(0.f);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
-                if (col >= C) continue;
-                float2 d[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = __fadd2_rn(v[k][j], both(-mean));
-                if (!kAligned && !inside(col, C)) mask8(d, col, C);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q2 = __ffma2_rn(d[j], d[j], q2);
-            }
-            float q = group_sum<GW>(q2.x + q2.y);
-            if (kCta) {
-                const int w = threadIdx.x & 31;
-                if (w == 0) merge[parity][threadIdx.x >> 5] = make_float2(mean, q);
-                __syncthreads();
-                const float2 m = w < (width >> 5) ? merge[parity][w] : make_float2(0.f, 0.f);
-                parity ^= 1;
-                const float n = static_cast<float>(peer);
-                mean = warp_sum(n * m.x) * inv;
-                const float d = m.x - mean;
-                q = warp_sum(peer > 0 ? fmaf(n * d, d, m.y) : 0.f);
-            }
-            const float rstd = 1.f / sqrtf(q * inv + p.eps);
-            if (!live) continue;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int at = (k * width + lane) * 8, col = at - shift;
-                if (col >= C) continue;
-                if constexpr (NV > 1) {
-                    gsrc.get(gam, at, 1.f);
-                    bsrc.get(bet, at, 0.f);
-                }
-                float2 y[4];
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 xhat = __fmul2_rn(__fadd2_rn(v[k][j], both(-mean)), both(rstd));
-                    y[j] = __ffma2_rn(xhat, gam[j], bet[j]);
+                    const int c = (k * width + lane) * 8 + 2 * j - shift;
+                    f[k][j] = make_float2(shifted_param(p, type, c, C, absent), shifted_param(p, type, c + 1, C, absent));
                 }
-                store_row8<kAligned>(static_cast<TB*>(p.y) + r * C, y, col, C);
-            }
-            if (lane == 0) {
-                if (p.mean != nullptr) p.mean[r] = mean;
-                if (p.rstd != nullptr) p.rstd[r] = rstd;
-            }
+        } else {
+            from = static_cast<const float*>(p);
+            last = C - 8;
         }
     }
-}
-
-// ------------------------------------------------------------------------------ backward
+    // (the caller synchronises the group before the first use)
+    __device__ __forceinline__ void stage(float* to, const void* p, int type, int C, int lane, int width, int shift,
+                                          float absent) {
+        const int span = width * NV * 8;
+        for (int i = lane; i < span; i += width) to[i] = shifted_param(p, type, i - shift, C, absent);
+        from = to;
+        last = span - 8;
+    }
+    __device__ __forceinline__ const float2 (&get(int at, int k))[4] {
+        if constexpr (kHeld) {
+            return f[k];
+        } else {
+            const float* g = from + min(at, last);
+            const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
+            f[0][0] = make_float2(a.x, a.y), f[0][1] = make_float2(a.z, a.w);
+            f[0][2] = make_float2(b.x, b.y), f[0][3] = make_float2(b.z, b.w);
+            return f[0];
+        }
+    }
+};
 
 // Asynchronous copies of one row's tensors into the thread group's own part of shared memory.
 // Each thread holds 8 elements of every vector slot: one 16-byte granule of a 16-bit type or two of
@@ -261,8 +101,8 @@ __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta) norm_fwd_rows_kern
 // (no conflicts) the copies themselves were the limit, 238 us instead of 185 for 16384 x 4096 with
 // an fp32 stream.  Vectors past the row's end are filled with zeros (a copy of no bytes), so the
 // arithmetic needs no branches.  Granules that hang over the row's ends are copied whole while
-// they stay inside the tensor (the reader masks the neighbouring rows' elements); at the
-// tensor's very end single elements are stored instead.
+// they stay within [low, room) of the row's start, the tensor's extent (the reader masks the
+// neighbouring rows' elements); beyond it, at the tensor's very end, single elements are stored.
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool some) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(some ? 16 : 0)
                  : "memory");
@@ -272,10 +112,10 @@ template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <bool kAligned, typename T>
-__device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, int C, int room) {
+__device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, int C, int low, int room) {
     constexpr int n = 16 / sizeof(T);
     const bool some = col < C;
-    if (kAligned || !some || col + n <= room) {
+    if (kAligned || !some || (col >= low && col + n <= room)) {
         copy16(dst, row + (some ? col : 0), some);
     } else {
         T* to = reinterpret_cast<T*>(dst);
@@ -288,13 +128,13 @@ __device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, 
 // One vector slot of the lanes of a (sub-)warp of GW lanes: `slot` is the thread's own first granule,
 // `col` its first element.
 template <bool kAligned, typename T, int GW>
-__device__ __forceinline__ void copy_slot(uint4* slot, const T* row, int lane, int col, int C, int room) {
+__device__ __forceinline__ void copy_slot(uint4* slot, const T* row, int lane, int col, int C, int low, int room) {
     if constexpr (sizeof(T) == 2) {
-        copy_granule<kAligned>(slot, row, col, C, room);
+        copy_granule<kAligned>(slot, row, col, C, low, room);
     } else {
         const int first = col - 4 * lane;       // this lane's granule of the group's 2 * GW
-        copy_granule<kAligned>(slot - lane, row, first, C, room);
-        copy_granule<kAligned>(slot - lane + GW, row, first + 4 * GW, C, room);
+        copy_granule<kAligned>(slot - lane, row, first, C, low, room);
+        copy_granule<kAligned>(slot - lane + GW, row, first + 4 * GW, C, low, room);
     }
 }
 
@@ -311,35 +151,240 @@ __device__ __forceinline__ void read_slot(float2 (&f)[4], const uint4* slot) {
     }
 }
 
-// CTAs per SM that the register budget allows: 80 registers a thread for one vector, 128 for 2 and
-// 4, of which 16 a vector hold the gradient sums and 8 gamma.
-constexpr int bwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2; }
-
 // Barrier of one group of `threads` threads (a multiple of 32) of the CTA.
 __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sums of 2 R values over the GW lanes of a group, R = 1 or 2: the lanes part the values among
-// themselves (halves, then quarters), so that log2(GW) steps serve all.  Lanes lane / (GW / 2R) == q
-// return sum q of v[0], v[1], ...
-template <int GW, int R>
-__device__ __forceinline__ float parted_sum(const float (&v)[2 * R], int lane) {
-    float a = v[0], b = v[1];
-    int m = GW / 2;
-    if constexpr (R == 2) {
-        const bool upper = (lane & m) != 0;
-        const float c = upper ? v[0] : v[2], d = upper ? v[1] : v[3];
-        a = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, c, m);
-        b = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, d, m);
-        m /= 2;
-    }
-    const bool upper = (lane & m) != 0;
-    float t = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, m);
+// Sums of N = 1, 2 or 4 values over the GW lanes of a group: the lanes part the values among
+// themselves (halves, then quarters), so that N - 1 + log2(GW / N) exchanges serve all.  Lanes
+// with lane / (GW / N) == q return sum q.
+template <int GW, int N>
+__device__ __forceinline__ float parted_sum(const float (&v)[N], int lane) {
+    static_assert(N == 1 || N == 2 || N == 4, "parts");
+    float t;
+    if constexpr (N == 1) {
+        t = v[0];
+    } else {
+        const bool upper = (lane & (GW / 2)) != 0;
+        float half[N / 2];
 #pragma unroll
-    for (m /= 2; m > 0; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        for (int i = 0; i < N / 2; ++i)
+            half[i] = (upper ? v[N / 2 + i] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[N / 2 + i], GW / 2);
+        if constexpr (N == 2) {
+            t = half[0];
+        } else {
+            const bool odd = (lane & (GW / 4)) != 0;
+            t = (odd ? half[1] : half[0]) + __shfl_xor_sync(0xffffffffu, odd ? half[0] : half[1], GW / 4);
+        }
+    }
+#pragma unroll
+    for (int m = GW / (2 * N); m > 0; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
     return t;
 }
+
+// ------------------------------------------------------------------------------- forward
+
+// CTAs per SM that the register budget allows: 80 registers a thread for one vector, 128 for more.
+constexpr int fwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2; }
+
+// Rows wait in shared memory, S times R of them per group, and R rows go through together (one
+// barrier for both, two independent chains of latencies); their values then stay in registers
+// until y is written.  G == 0: groups of `group_threads` threads, several to a CTA.
+//
+// Row statistics: each warp (or lane group) takes the mean of its own elements, then the sum of
+// squares about it, and the warps of a group are merged by their counts (Chan, Golub and LeVeque,
+// "Updating formulae and a pairwise algorithm for computing sample variances", 1979): one
+// barrier per R rows, and no cancellation however far the mean lies from zero.
+template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
+__global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, fwd_min_ctas(G, NV))
+norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
+    extern __shared__ __align__(16) float smem[];
+    __shared__ float2 merge[2][R][kMaxCta / 32];
+    constexpr bool kCta = G == 0;                  // several warps serve a row
+    constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
+    constexpr int kPart = GW / R;                  // lanes that hold one row's sums
+    constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // granules of a slot
+    const int threads = kCta ? blockDim.x : kWarpCta;
+    const int width = kCta ? group_threads : G;
+    const int local = threadIdx.x / width;         // group within the CTA
+    const int lane = threadIdx.x - local * width;
+    const int sub = threadIdx.x % GW;
+    const int per_cta = threads / width;
+    const int groups = gridDim.x * per_cta;
+    const int group = blockIdx.x * per_cta + local;
+    const int C = p.C;
+    const int shift = kAligned ? 0 : static_cast<int>((static_cast<long long>(group) * C) & 7);
+    const float inv = 1.f / static_cast<float>(C);
+    // (an update in place overwrites the neighbouring rows: then only the row's own elements are read)
+    const bool whole = !kAdd || p.z != p.in;
+    const int low = whole ? -8 : 0;
+    // shared memory: stage, row, then slot (the stream's vectors, the branch's), then thread
+    const int x_at = NV * kStream * threads;
+    const int row_granules = x_at + (kAdd ? NV * kBranch * threads : 0);
+    uint4* const slots = reinterpret_cast<uint4*>(smem);
+    const int mine_b = threadIdx.x * kBranch, mine_s = threadIdx.x * kStream;   // this thread's granules of a slot
+    pdl_trigger();
+    pdl_wait();
+    DropState drop;
+    if (kAdd) drop.init(p.drop);
+
+    auto fetch = [&](int stage, long long r0) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long r = r0 + static_cast<long long>(u) * groups;
+            if (r >= p.rows) continue;
+            // elements from the row's start to the tensor's end, at least
+            const int room = kAligned ? 0 : whole ? static_cast<int>(min((p.rows - r) * C, 1LL << 30)) : C;
+            uint4* to = slots + (stage * R + u) * row_granules;
+            const TS* in = static_cast<const TS*>(p.in) + r * p.ld_in;
+            const TB* x = static_cast<const TB*>(p.x) + r * p.ld_x;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (k * width + lane) * 8 - shift;
+                copy_slot<kAligned, TS, GW>(to + k * kStream * threads + mine_s, in, sub, col, C, low, room);
+                if (kAdd) copy_slot<kAligned, TB, GW>(to + x_at + k * kBranch * threads + mine_b, x, sub, col, C, low, room);
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
+
+    Params<NV> gamma, beta;
+    gamma.hold(p.gamma, p.param_type, C, lane, width, shift, 1.f);
+    beta.hold(p.beta, p.param_type, C, lane, width, shift, 0.f);
+    if (NV > 2 && staged) {
+        float* to = smem + S * R * row_granules * 4 + local * width * NV * 16;
+        gamma.stage(to, p.gamma, p.param_type, C, lane, width, shift, 1.f);
+        beta.stage(to + width * NV * 8, p.beta, p.param_type, C, lane, width, shift, 0.f);
+        if (kCta) group_barrier(1 + local, width); else __syncwarp();
+    }
+    // elements of this thread's warp or group, and of the warp whose sums this lane merges
+    const int warps = width >> 5, first_warp = local * warps;
+    const int mine = kCta ? warp_columns(lane >> 5, width, NV, shift, C) : C;
+    const int peer = kCta && sub % kPart < warps ? warp_columns(sub % kPart, width, NV, shift, C) : 0;
+    const float mine_inv = mine > 0 ? 1.f / static_cast<float>(mine) : 0.f;
+    int parity = 0, stage = 0;
+
+    const long long step = static_cast<long long>(R) * groups;
+    // (the lane groups of a warp stay together: the warp goes on while its first group has a row, and
+    // all its lanes run the loop's barriers and shuffles)
+    const int in_warp = kCta ? 0 : local % (32 / GW);
+    for (long long r0 = group; r0 - in_warp < p.rows; r0 += step) {
+        copy_wait<S - 1>();
+        __syncwarp();
+        const uint4* from = slots + stage * R * row_granules;
+        float2 v[R][NV][4];
+        float s[R], mean[R], rstd[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long r = r0 + static_cast<long long>(u) * groups;
+            const bool live = r < p.rows;
+            const uint4* row = from + u * row_granules;
+            float2 s2 = both(0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (k * width + lane) * 8 - shift;
+                read_slot<TS>(v[u][k], row + k * kStream * threads + mine_s);
+                if constexpr (kAdd) {
+                    float2 b[4];
+                    read_slot<TB>(b, row + x_at + k * kBranch * threads + mine_b);
+                    if (drop.threshold != 0) drop8(drop, b, static_cast<uint64_t>(r * C + col) >> 3);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[u][k][j] = __fadd2_rn(v[u][k][j], b[j]);
+                    if (live && col < C) store_row8<kAligned>(static_cast<TS*>(p.z) + r * C, v[u][k], col, C);
+                }
+                if (!kAligned && !inside(col, C)) mask8(v[u][k], col, C);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s2 = __fadd2_rn(s2, v[u][k][j]);
+            }
+            s[u] = s2.x + s2.y;
+        }
+        // the stage is read: the rows S steps on take it
+        __syncwarp();
+        fetch(stage, r0 + S * step);
+        if (++stage == S) stage = 0;
+
+        float t = parted_sum<GW, R>(s, sub);
+#pragma unroll
+        for (int u = 0; u < R; ++u) mean[u] = __shfl_sync(0xffffffffu, t, u * kPart, GW) * mine_inv;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            float2 q2 = both(0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (k * width + lane) * 8 - shift;
+                float2 d[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = __fadd2_rn(v[u][k][j], both(-mean[u]));
+                if (!inside(col, C)) mask8(d, col, C);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q2 = __ffma2_rn(d[j], d[j], q2);
+            }
+            s[u] = q2.x + q2.y;
+        }
+        t = parted_sum<GW, R>(s, sub);
+        float m = mean[0];
+        if constexpr (R == 2) m = sub < kPart ? mean[0] : mean[1];
+        if constexpr (kCta) {
+            // lane l merges row l / kPart over the group's warps, warp l % kPart
+            if (sub % kPart == 0) merge[parity][sub / kPart][threadIdx.x >> 5] = make_float2(m, t);
+            group_barrier(1 + local, width);
+            const int w = sub % kPart;
+            const float2 e = w < warps ? merge[parity][sub / kPart][first_warp + w] : make_float2(0.f, 0.f);
+            parity ^= 1;
+            const float n = static_cast<float>(peer);
+            m = n * e.x;
+#pragma unroll
+            for (int x = kPart / 2; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+            m *= inv;
+            const float d = e.x - m;
+            t = peer > 0 ? fmaf(n * d, d, e.y) : 0.f;
+#pragma unroll
+            for (int x = kPart / 2; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+        }
+        t = 1.f / sqrtf(t * inv + p.eps);
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            mean[u] = __shfl_sync(0xffffffffu, m, u * kPart, GW);
+            rstd[u] = __shfl_sync(0xffffffffu, t, u * kPart, GW);
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int at = (k * width + lane) * 8, col = at - shift;
+            const float2(&g)[4] = gamma.get(at, k);
+            const float2(&b)[4] = beta.get(at, k);
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                const long long r = r0 + static_cast<long long>(u) * groups;
+                float2 y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 xhat = __fmul2_rn(__fadd2_rn(v[u][k][j], both(-mean[u])), both(rstd[u]));
+                    y[j] = __ffma2_rn(xhat, g[j], b[j]);
+                }
+                if (r < p.rows && col < C) store_row8<kAligned>(static_cast<TB*>(p.y) + r * C, y, col, C);
+            }
+        }
+        if (lane == 0) {
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                const long long r = r0 + static_cast<long long>(u) * groups;
+                if (r >= p.rows) continue;
+                if (p.mean != nullptr) p.mean[r] = mean[u];
+                if (p.rstd != nullptr) p.rstd[r] = rstd[u];
+            }
+        }
+    }
+    copy_wait<0>();
+}
+
+// ------------------------------------------------------------------------------ backward
+
+// CTAs per SM that the register budget allows: 80 registers a thread for one vector, 128 for 2 and
+// 4, of which 16 a vector hold the gradient sums and 8 gamma.
+constexpr int bwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2; }
 
 // Each thread keeps the sums of dy * xhat and dy of its columns in registers over all rows of its
 // group; at the end the groups of a CTA are added in order and the CTA writes one row of partial
@@ -355,7 +400,6 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     extern __shared__ __align__(16) float smem[];
     __shared__ float merge[2][2 * R][kMaxCta / 32];
     constexpr bool kCta = G == 0;                  // several warps serve a row
-    constexpr bool kHeld = NV <= 2;                // gamma stays in registers
     constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
     constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // granules of a slot
     const int threads = kCta ? blockDim.x : kWarpCta;
@@ -395,14 +439,14 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = (k * width + lane) * 8 - shift;
-                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, col, C, room);
-                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, col, C, room);
+                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, col, C, -8, room);
+                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, col, C, -8, room);
             }
             if (has_dz) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
                     copy_slot<kAligned, TS, GW>(to + dz_at + k * kStream * threads + mine_s, dz, sub,
-                                                (k * width + lane) * 8 - shift, C, room);
+                                                (k * width + lane) * 8 - shift, C, -8, room);
             }
         }
         copy_commit();
@@ -410,39 +454,13 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
 
-    // gamma: registers for one or two vectors a thread, else the caller's array (aligned fp32) or a
-    // copy along the shifted vectors, read per use
-    float2 gam[kHeld ? NV : 1][4];
-    const float* gsrc = static_cast<const float*>(p.gamma);
-    int last = C - 8;                               // the last whole vector there
-    if constexpr (kHeld) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = (k * width + lane) * 8 + 2 * j - shift;
-                gam[k][j] = make_float2(shifted_param(p.gamma, p.param_type, c, C, 1.f),
-                                        shifted_param(p.gamma, p.param_type, c + 1, C, 1.f));
-            }
-    } else if (staged) {
-        const int span = width * NV * 8;
-        float* g = smem + S * R * row_granules * 4 + local * span;
-        for (int i = lane; i < span; i += width) g[i] = shifted_param(p.gamma, p.param_type, i - shift, C, 1.f);
-        gsrc = g;
-        last = span - 8;
+    Params<NV> gamma;
+    gamma.hold(p.gamma, p.param_type, C, lane, width, shift, 1.f);
+    if (NV > 2 && staged) {
+        gamma.stage(smem + S * R * row_granules * 4 + local * width * NV * 8, p.gamma, p.param_type, C, lane, width,
+                    shift, 1.f);
         if (kCta) group_barrier(1 + local, width); else __syncwarp();
     }
-    auto gamma_of = [&](int k) -> const float2(&)[4] {
-        if constexpr (kHeld) {
-            return gam[k];
-        } else {
-            const float* g = gsrc + min((k * width + lane) * 8, last);
-            const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
-            gam[0][0] = make_float2(a.x, a.y), gam[0][1] = make_float2(a.z, a.w);
-            gam[0][2] = make_float2(b.x, b.y), gam[0][3] = make_float2(b.z, b.w);
-            return gam[0];
-        }
-    };
     float2 sum_g[NV][4], sum_b[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -485,7 +503,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
                     float2 f[4], x[4];
                     read_slot<TB>(f, row + k * kBranch * threads + mine_b);
                     read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
-                    const float2(&gk)[4] = gamma_of(k);
+                    const float2(&gk)[4] = gamma.get((k * width + lane) * 8, k);
                     if constexpr (!kAligned) {
                         const int col = (k * width + lane) * 8 - shift;
                         if (!inside(col, C)) {
@@ -508,7 +526,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             s[2 * u + 1] = s2.x + s2.y;
         }
         constexpr int kPart = GW / (2 * R);   // lanes that hold one of the sums
-        float t = parted_sum<GW, R>(s, sub);
+        float t = parted_sum<GW, 2 * R>(s, sub);
         if constexpr (kCta) {
             // the warps' sums: lane l of every warp takes sum l / kPart of warps l % kPart, ...
             if (sub % kPart == 0) merge[parity][sub / kPart][threadIdx.x >> 5] = t;
@@ -537,7 +555,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
                 float2 f[4], x[4], g[4];
                 read_slot<TB>(f, row + k * kBranch * threads + mine_b);
                 read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
-                const float2(&gk)[4] = gamma_of(k);
+                const float2(&gk)[4] = gamma.get((k * width + lane) * 8, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 a = __ffma2_rn(__fmul2_rn(f[j], gk[j]), both(rstd[u]), both(-k1));
@@ -626,23 +644,27 @@ inline bool params_line_up(const void* gamma, const void* beta, int type, int C)
            (reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) % 16 == 0;
 }
 
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int U>
+// Groups of `width` threads in a CTA: several only once there is a row for every SM.
+inline int row_groups(long long rows, int width) {
+    return static_cast<int>(std::max(1LL, std::min<long long>(kMaxCta / width, rows / device_info().sm_count)));
+}
+
+template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
 cudaError_t fwd_launch(const NormFwd& p, int vectors) {
-    auto kern = norm_fwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, U>;
-    const int threads = G > 0 ? kWarpCta : (vectors + NV * 32 - 1) / (NV * 32) * 32;
-    const int per_cta = G > 0 ? kWarpCta / G : 1;
-    const int staged = NV > 1 && !params_line_up(p.gamma, p.beta, p.param_type, p.C);
-    const size_t bytes = staged ? static_cast<size_t>(threads) * NV * 8 * 2 * sizeof(float) : 0;
+    auto kern = norm_fwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, R, S>;
+    const int width = G > 0 ? G : (vectors + NV * 32 - 1) / (NV * 32) * 32;
+    const int per_cta = G > 0 ? kWarpCta / G : row_groups(p.rows, width);
+    const int threads = width * per_cta;
+    const int staged = NV > 2 && (p.gamma == nullptr || p.beta == nullptr ||
+                                  !params_line_up(p.gamma, p.beta, p.param_type, p.C));
+    const size_t slot = 8 * (sizeof(TS) + (kAdd ? sizeof(TB) : 0));
+    const size_t bytes = (S * R * slot + (staged ? 16 * sizeof(float) : 0)) * NV * threads;
+    if (bytes > kDynamicSmem) return cudaErrorNotSupported;
     static KernelFacts facts;
     const cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
     const long long grid = persistent_grid((p.rows + per_cta - 1) / per_cta, bytes, threads, facts.registers(kern));
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes, p.stream, p, staged);
-}
-
-// Groups of `width` threads in a CTA: several only once there is a row for every SM.
-inline int row_groups(long long rows, int width) {
-    return static_cast<int>(std::max(1LL, std::min<long long>(kMaxCta / width, rows / device_info().sm_count)));
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes, p.stream, p, staged, width);
 }
 
 // Bytes a thread's vector slots take per stage.
@@ -676,13 +698,21 @@ cudaError_t bwd_launch(const NormBwd& p, int vectors) {
 template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t fwd_rows_a(const NormFwd& p) {
     const int v = row_vectors(p.C);
-    if (v <= 8) return fwd_launch<TS, TB, kAdd, kAligned, 8, 1, 4>(p, v);
-    if (v <= 16) return fwd_launch<TS, TB, kAdd, kAligned, 16, 1, 4>(p, v);
-    if (v <= 32) return fwd_launch<TS, TB, kAdd, kAligned, 32, 1, 4>(p, v);
-    if (v <= 64) return fwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2>(p, v);
-    if (v <= 128) return fwd_launch<TS, TB, kAdd, kAligned, 32, 4, 1>(p, v);
-    if (v <= kMaxCta * kRowVecs) return fwd_launch<TS, TB, kAdd, kAligned, 0, kRowVecs, 1>(p, v);
-    return cudaErrorNotSupported;
+    if (v <= 8) return fwd_launch<TS, TB, kAdd, kAligned, 8, 1, 2, 2>(p, v);
+    if (v <= 16) return fwd_launch<TS, TB, kAdd, kAligned, 16, 1, 2, 2>(p, v);
+    if (v <= 32) return fwd_launch<TS, TB, kAdd, kAligned, 32, 1, 2, 2>(p, v);
+    if (v <= 64) return fwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2, 1>(p, v);
+    // two stages of two rows where they fit in shared memory, else of one row; the widest rows in one
+    // stage (and not at all as fp32 with an fp32 branch and staged parameters)
+    cudaError_t err = cudaErrorNotSupported;
+    if (v <= kMaxCta * 2) {
+        err = fwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 2>(p, v);
+        if (err == cudaErrorNotSupported) err = fwd_launch<TS, TB, kAdd, kAligned, 0, 2, 1, 2>(p, v);
+    } else if (v <= kMaxCta * 4) {
+        err = fwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 2>(p, v);
+        if (err == cudaErrorNotSupported) err = fwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
+    }
+    return err;
 }
 
 template <typename TS, typename TB, bool kAdd>
@@ -704,7 +734,8 @@ cudaError_t bwd_rows_a(const NormBwd& p) {
         err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 2>(p, v);
         if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 1, 2>(p, v);
     } else if (v <= kMaxCta * 4) {
-        err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
+        err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 2>(p, v);
+        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
     }
     return err;
 }
