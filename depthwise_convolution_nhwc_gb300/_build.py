@@ -3,6 +3,9 @@
 Every ``csrc/*.cu`` file is compiled to an object in parallel, then linked into a shared
 library next to this file.  Rebuilds only what changed (sources or headers newer than the
 object).  No CPU fallback exists: importing the binding without this library fails loudly.
+
+``csrc/dwc_norm_py.cpp``, the host path of the norm operators for Python, is compiled beside it with
+the host compiler against the installed PyTorch and linked as the module ``_norm_host``.
 """
 from __future__ import annotations
 
@@ -19,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libdwc_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+HOST_SRC = os.path.join(CSRC, "dwc_norm_py.cpp")
+HOST_PATH = os.path.join(HERE, "_norm_host.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -44,6 +49,40 @@ def _stale(obj: str, src: str, hdr_mtime: float) -> bool:
     return t < os.path.getmtime(src) or t < hdr_mtime
 
 
+def _host_object() -> str:
+    """The host module's object file, one per PyTorch and Python version."""
+    import torch
+    return os.path.join(OBJ_DIR, f"dwc_norm_py-{torch.__version__}-{sys.version_info[0]}{sys.version_info[1]}.o")
+
+
+def _compile_host(obj: str) -> None:
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    r = subprocess.run(cmd + [f"-I{d}" for d in dirs] + ["-c", HOST_SRC, "-o", obj + ".tmp"], capture_output=True,
+                       text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(HOST_SRC)}:\n{r.stderr[-6000:]}")
+    os.replace(obj + ".tmp", obj)
+
+
+def _link_host(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = HOST_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", HERE,
+           f"-l:{LIB_NAME}", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {os.path.basename(HOST_PATH)} failed:\n{r.stderr[-6000:]}")
+    os.replace(tmp, HOST_PATH)
+
+
 def build(verbose: bool = False, jobs: int | None = None, extra_flags=None) -> str:
     """Compile and link the library; returns its path."""
     nvcc = nvcc_path()
@@ -66,11 +105,16 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=None) -> s
         os.replace(o + ".tmp", o)
         return s, r.stderr
 
-    jobs = jobs or min(len(todo), os.cpu_count() or 4) or 1
+    host_obj = _host_object()
+    host_todo = _stale(host_obj, HOST_SRC, hdr_mtime)
+    jobs = jobs or min(len(todo) + host_todo, os.cpu_count() or 4) or 1
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        host = ex.submit(_compile_host, host_obj) if host_todo else None
         for s, log in ex.map(compile_one, todo):
             if verbose and log:
                 sys.stderr.write(f"== {os.path.basename(s)}\n{log}")
+        if host is not None:
+            host.result()
 
     if todo or not os.path.exists(LIB_PATH):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -79,6 +123,8 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=None) -> s
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr[-6000:]}")
         os.replace(tmp, LIB_PATH)
+    if not os.path.exists(HOST_PATH) or os.path.getmtime(HOST_PATH) < os.path.getmtime(host_obj):
+        _link_host(host_obj)
     return LIB_PATH
 
 

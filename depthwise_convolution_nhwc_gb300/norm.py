@@ -22,134 +22,32 @@ the kernel runs, so a captured CUDA graph draws new masks as the program advance
 """
 from __future__ import annotations
 
-import functools
-
 import torch
 
 from . import DwcError, load_library
 
-_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_F32 = torch.float32
-
-# The current stream's handle without building a Stream object (a microsecond of a small call).
-_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_module = None
 
 
-@functools.lru_cache(maxsize=None)
-def _fn(name: str):
-    return getattr(load_library(), name)
-
-
-def _code(dtype) -> int:
-    code = _CODE.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype} (fp32, bf16 or fp16)")
-    return code
+def _host():
+    """The compiled host path (``csrc/dwc_norm_py.cpp``): argument checks, output allocation and the
+    library call of each operator as one C++ function.  An error if it was not built."""
+    global _module
+    if _module is None:
+        load_library()
+        try:
+            from . import _norm_host
+        except ImportError as e:
+            raise RuntimeError("_norm_host.so is missing or does not fit this PyTorch: build it with "
+                               "depthwise_convolution_nhwc_gb300.build()") from e
+        _norm_host.set_error(DwcError)
+        _module = _norm_host
+    return _module
 
 
 def _stride(t, what: str) -> int:
     """Elements between the rows of [..., C]: one stride over all leading axes, adjacent channels."""
-    C = t.shape[-1]
-    if t.is_contiguous():
-        return C
-    ld, span = None, None
-    if C > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what}: channels must be adjacent (stride {t.stride(-1)})")
-    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if n == 1:
-            continue
-        if ld is None:
-            if s < C:
-                raise ValueError(f"{what}: rows overlap (stride {s} between rows of {C})")
-            ld, span = s, n * s
-        elif s != span:
-            raise ValueError(f"{what}: rows must have one stride (got {tuple(t.stride())} for {tuple(t.shape)})")
-        else:
-            span *= n
-    return C if ld is None else ld
-
-
-def _rows(t, what: str):
-    """(shape, device index, channels, row stride) of a tensor on a CUDA device."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device (no CPU fallback)")
-    shape = t.shape
-    if not shape or shape[-1] < 1:
-        raise ValueError(f"{what} must be [..., C] with at least one channel")
-    return shape, dev, shape[-1], shape[-1] if t.is_contiguous() else _stride(t, what)
-
-
-def _like(t, shape, dev, dtype, what: str) -> int:
-    """Row stride of a second tensor of that shape (dtype None: any)."""
-    if t.shape != shape or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what} must be a {tuple(shape)} {dtype or ''} tensor on cuda:{dev} "
-                         f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
-    return shape[-1] if t.is_contiguous() else _stride(t, what)
-
-
-def _out(t, like, dtype, what: str):
-    """A dense output of `like`'s shape: the caller's, checked, or a new one."""
-    if t is None:
-        if like.is_contiguous():
-            return torch.empty_like(like, dtype=dtype)
-        return torch.empty(like.shape, dtype=dtype, device=like.device)
-    if t.shape != like.shape or t.dtype != dtype or t.get_device() != like.get_device() or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {tuple(like.shape)} {dtype} tensor on {like.device} "
-                         f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
-    return t
-
-
-def _param(t, C: int, dev: int, what: str) -> int:
-    """Pointer of gamma or beta."""
-    if t.numel() != C or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what} must hold {C} values on cuda:{dev} (got {tuple(t.shape)} on {t.device})")
-    return t.data_ptr()
-
-
-def _params(gamma, beta, C: int, dev: int):
-    """(gamma's pointer, beta's, their type code)."""
-    g = None if gamma is None else _param(gamma, C, dev, "gamma")
-    b = None if beta is None else _param(beta, C, dev, "beta")
-    if gamma is None:
-        return g, b, 0 if beta is None else _code(beta.dtype)
-    if beta is not None and beta.dtype != gamma.dtype:
-        raise ValueError("gamma and beta must have one dtype")
-    return g, b, _code(gamma.dtype)
-
-
-def _stat(t, lead, dev: int, what: str) -> int:
-    if t.shape != lead or t.dtype != _F32 or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {tuple(lead)} fp32 tensor on cuda:{dev} "
-                         f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
-    return t.data_ptr()
-
-
-_M64 = 2 ** 64 - 1
-
-
-def _random(p, seed, offset, dev: int):
-    """(p, seed, offset, step pointer) of a dropout."""
-    p = float(p)
-    if not 0.0 <= p <= 1.0:
-        raise ValueError(f"p must be in [0, 1] (got {p})")
-    if isinstance(offset, torch.Tensor):
-        if offset.dtype != torch.int64 or offset.numel() != 1 or offset.get_device() != dev:
-            raise ValueError("an offset on the device must be one int64 value on the tensors' device")
-        return p, int(seed) & _M64, 0, offset.data_ptr()
-    return p, int(seed) & _M64, int(offset) & _M64, None
-
-
-def _run(dev: int, name: str, *args) -> None:
-    """The library call on the current stream of device `dev`, with that device current."""
-    if dev == torch.cuda.current_device():
-        code = _fn(name)(*args, _stream_handle(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = _fn(name)(*args, _stream_handle(dev))
-    if code != 0:
-        raise DwcError(name, code)
+    return _host().row_stride(t, what)
 
 
 def _on(stream, f, *args):
@@ -172,34 +70,7 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, out=None, out_dt
     a 16-bit type for fp32 x.  gamma and beta: C values of one dtype each, or None."""
     if stream is not None:
         return _on(stream, layer_norm_fwd, x, gamma, beta, eps, out, out_dtype, stats)
-    shape, dev, C, ld = _rows(x, "x")
-    dtype = x.dtype
-    od = out_dtype or (dtype if out is None else out.dtype)
-    g, b, pt = _params(gamma, beta, C, dev)
-    y = _out(out, x, od, "out")
-    if not stats:
-        _run(dev, "dwc_layer_norm_fwd", x.data_ptr(), ld, g, b, pt, eps, y.data_ptr(), None, None,
-             x.numel() // C, C, _code(dtype), _code(od))
-        return y
-    mean = torch.empty(shape[:-1], dtype=_F32, device=x.device)
-    rstd = torch.empty_like(mean)
-    _run(dev, "dwc_layer_norm_fwd", x.data_ptr(), ld, g, b, pt, eps, y.data_ptr(), mean.data_ptr(),
-         rstd.data_ptr(), x.numel() // C, C, _code(dtype), _code(od))
-    return y, mean, rstd
-
-
-@functools.lru_cache(maxsize=4096)
-def _workspace_bytes(dev: int, rows: int, C: int) -> int:
-    with torch.cuda.device(dev):
-        return int(_fn("dwc_layer_norm_bwd_workspace_size")(rows, C))
-
-
-def _param_grads(x, dev: int, rows: int, C: int):
-    """(dgamma, dbeta, workspace) of a backward pass.  The workspace comes from PyTorch's allocator
-    call by call, so it belongs to the call's stream (or graph) and to no other."""
-    dgamma = torch.empty(C, dtype=_F32, device=x.device)
-    return dgamma, torch.empty_like(dgamma), torch.empty(_workspace_bytes(dev, rows, C), dtype=torch.uint8,
-                                                         device=x.device)
+    return (_module or _host()).layer_norm_fwd(x, gamma, beta, eps, out, out_dtype, bool(stats))
 
 
 def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = True, stream=None):
@@ -207,29 +78,7 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = 
     dtype, dgamma and dbeta fp32 (None without ``param_grads``)."""
     if stream is not None:
         return _on(stream, layer_norm_bwd, dy, x, mean, rstd, gamma, out, param_grads)
-    shape, dev, C, ld = _rows(x, "x")
-    rows, dtype, lead = x.numel() // C, x.dtype, shape[:-1]
-    lddy = _like(dy, shape, dev, None, "dy")
-    g, _, pt = _params(gamma, None, C, dev)
-    m, r = _stat(mean, lead, dev, "mean"), _stat(rstd, lead, dev, "rstd")
-    dx = _out(out, x, dtype, "out")
-    dgamma = dbeta = dg = db = w = None
-    n = 0
-    if param_grads:
-        dgamma, dbeta, ws = _param_grads(x, dev, rows, C)
-        dg, db, w, n = dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel()
-    _run(dev, "dwc_layer_norm_bwd", dy.data_ptr(), lddy, x.data_ptr(), ld, m, r, g, pt, dx.data_ptr(), dg, db,
-         rows, C, _code(dtype), _code(dy.dtype), w, n)
-    return dx, dgamma, dbeta
-
-
-def _dropout(name, x, p, seed, offset, out, what):
-    _, dev, C, ld = _rows(x, what)
-    p, seed, offset, step = _random(p, seed, offset, dev)
-    dtype = x.dtype
-    y = _out(out, x, dtype, "out")
-    _run(dev, name, x.data_ptr(), ld, y.data_ptr(), x.numel() // C, C, p, seed, offset, step, _code(dtype))
-    return y
+    return (_module or _host()).layer_norm_bwd(dy, x, mean, rstd, gamma, out, bool(param_grads))
 
 
 def dropout_fwd(x, p: float, seed: int, offset=0, out=None, stream=None):
@@ -237,14 +86,14 @@ def dropout_fwd(x, p: float, seed: int, offset=0, out=None, stream=None):
     ``out`` may be x."""
     if stream is not None:
         return _on(stream, dropout_fwd, x, p, seed, offset, out)
-    return _dropout("dwc_dropout_fwd", x, p, seed, offset, out, "x")
+    return (_module or _host()).dropout_fwd(x, p, seed, offset, out)
 
 
 def dropout_bwd(dy, p: float, seed: int, offset=0, out=None, stream=None):
     """dx of ``dropout_fwd`` with the same p, seed and offset; ``out`` may be dy."""
     if stream is not None:
         return _on(stream, dropout_bwd, dy, p, seed, offset, out)
-    return _dropout("dwc_dropout_bwd", dy, p, seed, offset, out, "dy")
+    return (_module or _host()).dropout_bwd(dy, p, seed, offset, out)
 
 
 def add_layer_norm_fwd(x, res, gamma=None, beta=None, eps: float = 1e-5, p: float = 0.0, seed: int = 0,
@@ -254,21 +103,7 @@ def add_layer_norm_fwd(x, res, gamma=None, beta=None, eps: float = 1e-5, p: floa
     res (an update of the residual stream in place)."""
     if stream is not None:
         return _on(stream, add_layer_norm_fwd, x, res, gamma, beta, eps, p, seed, offset, out, z, stats)
-    shape, dev, C, ldx = _rows(x, "x")
-    ldr = _like(res, shape, dev, None, "res")
-    p, seed, offset, step = _random(p, seed, offset, dev)
-    g, b, pt = _params(gamma, beta, C, dev)
-    dtype, rdtype = x.dtype, res.dtype
-    y = _out(out, x, dtype, "out")
-    z = _out(z, res, rdtype, "z")
-    mean = rstd = m = r = None
-    if stats:
-        mean = torch.empty(shape[:-1], dtype=_F32, device=x.device)
-        rstd = torch.empty_like(mean)
-        m, r = mean.data_ptr(), rstd.data_ptr()
-    _run(dev, "dwc_add_layer_norm_fwd", x.data_ptr(), ldx, res.data_ptr(), ldr, p, seed, offset, step, g, b, pt,
-         eps, z.data_ptr(), y.data_ptr(), m, r, x.numel() // C, C, _code(dtype), _code(rdtype))
-    return (y, z, mean, rstd) if stats else (y, z)
+    return (_module or _host()).add_layer_norm_fwd(x, res, gamma, beta, eps, p, seed, offset, out, z, bool(stats))
 
 
 def add_layer_norm_bwd(dy, z, mean, rstd, gamma=None, dz=None, p: float = 0.0, seed: int = 0, offset=0,
@@ -278,24 +113,7 @@ def add_layer_norm_bwd(dy, z, mean, rstd, gamma=None, dz=None, p: float = 0.0, s
     of the residual stream (None: zero).  Without dropout and with one dtype dx is dres."""
     if stream is not None:
         return _on(stream, add_layer_norm_bwd, dy, z, mean, rstd, gamma, dz, p, seed, offset, param_grads)
-    shape, dev, C, ldz = _rows(z, "z")
-    rows, zdtype, lead, dtype = z.numel() // C, z.dtype, shape[:-1], dy.dtype
-    lddy = _like(dy, shape, dev, None, "dy")
-    lddz = C if dz is None else _like(dz, shape, dev, zdtype, "dz")
-    p, seed, offset, step = _random(p, seed, offset, dev)
-    g, _, pt = _params(gamma, None, C, dev)
-    m, r = _stat(mean, lead, dev, "mean"), _stat(rstd, lead, dev, "rstd")
-    dres = _out(None, z, zdtype, "dres")
-    dx = dres if p == 0.0 and dtype == zdtype else _out(None, dy, dtype, "dx")
-    dgamma = dbeta = dg = db = w = None
-    n = 0
-    if param_grads:
-        dgamma, dbeta, ws = _param_grads(z, dev, rows, C)
-        dg, db, w, n = dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel()
-    _run(dev, "dwc_add_layer_norm_bwd", dy.data_ptr(), lddy, None if dz is None else dz.data_ptr(), lddz,
-         z.data_ptr(), ldz, m, r, g, pt, p, seed, offset, step, None if dx is dres else dx.data_ptr(),
-         dres.data_ptr(), dg, db, rows, C, _code(dtype), _code(zdtype), w, n)
-    return dx, dres, dgamma, dbeta
+    return (_module or _host()).add_layer_norm_bwd(dy, z, mean, rstd, gamma, dz, p, seed, offset, bool(param_grads))
 
 
 __all__ = ["layer_norm_fwd", "layer_norm_bwd", "dropout_fwd", "dropout_bwd", "add_layer_norm_fwd",
