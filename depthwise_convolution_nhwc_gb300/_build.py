@@ -76,7 +76,7 @@ def _link_host(obj: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = HOST_PATH + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", HERE,
-           f"-l:{LIB_NAME}", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+           f"-l:{LIB_NAME}", "-L", lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {os.path.basename(HOST_PATH)} failed:\n{r.stderr[-6000:]}")

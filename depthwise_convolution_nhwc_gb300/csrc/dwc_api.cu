@@ -130,7 +130,7 @@ int family_preference() { return g_family_pref.load(std::memory_order_relaxed); 
 
 int tc_row_pairs_mode() { return g_tc_pairs.load(std::memory_order_relaxed); }
 
-static unsigned int* status_word() {
+unsigned int* status_word() {
     PerDevice* s = device_state();
     return s ? s->status : nullptr;
 }

@@ -90,6 +90,8 @@ struct GeneralConv {
 // fault-injection flag of the next row-kernel launch (both set through the C ABI).
 unsigned long long wait_limit_ns();
 int take_row_stall();
+// The current device's status word (null if CUDA is unusable).
+unsigned int* status_word();
 
 // Device properties cached per device.
 struct DeviceInfo {

@@ -120,6 +120,8 @@ dwc_status_t norm_fwd(NormFwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_ty
     p.stream_type = stream_type;
     p.branch_type = branch_type;
     p.param_type = param_dtype;
+    p.status = status_word();
+    p.wait_ns = wait_limit_ns();
     return map_cuda(launch_fwd(p));
 }
 
@@ -157,6 +159,8 @@ dwc_status_t norm_bwd(NormBwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_ty
     p.stream_type = stream_type;
     p.branch_type = branch_type;
     p.param_type = param_dtype;
+    p.status = status_word();
+    p.wait_ns = wait_limit_ns();
     return map_cuda(launch_bwd(p));
 }
 

@@ -40,6 +40,8 @@ struct NormFwd {
     int stream_type, branch_type;
     Dropout drop;
     cudaStream_t stream;
+    unsigned int* status = nullptr;   // of the kernels whose waits have a limit
+    unsigned long long wait_ns = 0;   // that limit (0: the default)
 };
 
 // g = dz + layer_norm_bwd(dy; z): d_stream = g, d_branch = dropout map of g.
@@ -61,6 +63,8 @@ struct NormBwd {
     int stream_type, branch_type;
     Dropout drop;
     cudaStream_t stream;
+    unsigned int* status = nullptr;
+    unsigned long long wait_ns = 0;
 };
 
 struct DropoutCall {
@@ -81,7 +85,7 @@ cudaError_t launch_dropout_general(const DropoutCall& p);
 // Dropout of dense rows from bases aligned to 8 elements.
 cudaError_t launch_dropout_vec(const DropoutCall& p);
 
-// Rows in registers (aligned tensors, up to 16384 channels), one file per
+// Rows in registers (aligned tensors, up to 65536 channels), one file per
 // pair of types; cudaErrorNotSupported beyond that.
 #define DWC_NORM_PAIR(name)                           \
     cudaError_t launch_norm_fwd_##name(const NormFwd& p); \

@@ -9,7 +9,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -64,6 +64,12 @@ int64_t row_stride(const Tensor& t, const char* what) {
     return ld < 0 ? C : ld;
 }
 
+// A new dense tensor from PyTorch's allocator (the CUDA backend's own factory: the dispatcher's way
+// to it costs as much again).
+Tensor new_tensor(at::IntArrayRef shape, ScalarType type, const at::Device& device) {
+    return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
+}
+
 // The tensor whose shape, device and channels a call goes by.
 struct Rows {
     const Tensor& t;
@@ -83,7 +89,7 @@ struct Rows {
     }
     // a dense output: the caller's, checked, or a new one
     Tensor out(PyObject* o, ScalarType type, const char* what) const {
-        if (o == Py_None) return at::empty(t.sizes(), t.options().dtype(type).requires_grad(false));
+        if (o == Py_None) return new_tensor(t.sizes(), type, t.device());
         const Tensor& given = tensor(o, what);
         TORCH_CHECK_VALUE(given.sizes() == t.sizes() && given.scalar_type() == type && given.device() == t.device() &&
                               given.is_contiguous(),
@@ -92,7 +98,7 @@ struct Rows {
         return given;
     }
     Tensor stat() const {
-        return at::empty(t.sizes().slice(0, t.dim() - 1), t.options().dtype(at::kFloat).requires_grad(false));
+        return new_tensor(t.sizes().slice(0, t.dim() - 1), at::kFloat, t.device());
     }
     const float* given_stat(PyObject* o, const char* what) const {
         const Tensor& s = tensor(o, what);
@@ -179,11 +185,10 @@ struct ParamGrads {
     size_t bytes = 0;
     ParamGrads(const Rows& x, bool wanted) {
         if (!wanted) return;
-        const auto f32 = x.t.options().dtype(at::kFloat).requires_grad(false);
-        dgamma = at::empty({x.C}, f32);
-        dbeta = at::empty({x.C}, f32);
+        dgamma = new_tensor({x.C}, at::kFloat, x.t.device());
+        dbeta = new_tensor({x.C}, at::kFloat, x.t.device());
         bytes = dwc_layer_norm_bwd_workspace_size(x.rows, static_cast<int>(x.C));
-        ws = at::empty({static_cast<int64_t>(bytes)}, x.t.options().dtype(at::kByte).requires_grad(false));
+        ws = new_tensor({static_cast<int64_t>(bytes)}, at::kByte, x.t.device());
         dg = static_cast<float*>(dgamma.data_ptr());
         db = static_cast<float*>(dbeta.data_ptr());
         w = ws.data_ptr();

@@ -1,11 +1,12 @@
 // dwc_norm_rows.cuh -- layer norm and its residual form, forward and backward, on rows of up to
-// 16384 channels held by a group of threads.
+// 65536 channels.
 //
 // Both passes are bound by memory: a row is read once, reduced in registers or shared memory and
 // written once, 8 elements per access.  A group of threads serves one row:
 //   rows of up to 8, 16 and 32 vectors: G = 8, 16, 32 lanes, one vector each; up to 64 vectors: a
-//   warp with 2; longer rows: several warps, 2 vectors a thread and above 1024 vectors 4 (up to
-//   512 threads).
+//   warp with 2; up to 1024: several warps with 2 vectors a thread (up to 512 threads); beyond
+//   that a cluster of 2, 4 or 8 CTAs, each with a share of the columns, which exchange their sums
+//   through distributed shared memory.
 //
 // Alignment.  A dense row of C channels starts (row * C) mod 8 elements past a vector boundary, and
 // so does every tensor of the call if its base is aligned and its row stride is congruent to C
@@ -17,6 +18,7 @@
 #pragma once
 
 #include <algorithm>
+#include <climits>
 
 #include "dwc_norm_device.cuh"
 
@@ -25,77 +27,113 @@ namespace norm {
 
 constexpr int kWarpCta = 256;            // threads of a CTA whose warps or lane groups serve rows
 constexpr int kMaxCta = 512;             // threads of a CTA otherwise: 128 registers each
-constexpr int kDynamicSmem = 225 * 1024;
+constexpr size_t kDynamicSmem = 220 * 1024;   // of 227 KB, beside the exchanges' static arrays
 
 // Vectors that the longest-shifted row of C channels touches.
 inline int row_vectors(int C) {
     int g = 8;                            // gcd(C, 8): the shifts are its multiples
     while (C % g != 0) g /= 2;
-    return (C + (8 - g) + 7) / 8;
-}
-
-// Elements that warp `warp` of a group of `threads` threads with `vecs` vectors each holds of a row.
-__device__ __forceinline__ int warp_columns(int warp, int threads, int vecs, int shift, int C) {
-    int n = 0;
-    for (int k = 0; k < vecs; ++k) {
-        const int lo = max(0, (k * threads + warp * 32) * 8 - shift);
-        const int hi = min(C, (k * threads + warp * 32 + 32) * 8 - shift);
-        n += max(0, hi - lo);
-    }
-    return n;
+    return static_cast<int>((static_cast<long long>(C) + (8 - g) + 7) / 8);
 }
 
 __device__ __forceinline__ float shifted_param(const void* p, int type, int c, int C, float absent) {
     return in_row(c, C) ? load_param(p, type, c, absent) : 0.f;
 }
 
-// Gamma or beta of a thread's vectors.  Up to two vectors a thread they stay in registers; beyond
-// that they are read per use, from the caller's array where that is fp32 and lines up with the
-// vectors, else from a copy in shared memory laid out along the group's shifted vectors.
-template <int NV>
-struct Params {
-    static constexpr bool kHeld = NV <= 2;
-    float2 f[kHeld ? NV : 1][4];
-    const float* from;
-    int last;                             // the last vector that may be read there
-    __device__ __forceinline__ void hold(const void* p, int type, int C, int lane, int width, int shift, float absent) {
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = (k * width + lane) * 8 + 2 * j - shift;
-                    f[k][j] = make_float2(shifted_param(p, type, c, C, absent), shifted_param(p, type, c + 1, C, absent));
-                }
-        } else {
-            from = static_cast<const float*>(p);
-            last = C - 8;
-        }
-    }
-    // (the caller synchronises the group before the first use)
-    __device__ __forceinline__ void stage(float* to, const void* p, int type, int C, int lane, int width, int shift,
-                                          float absent) {
-        const int span = width * NV * 8;
-        for (int i = lane; i < span; i += width) to[i] = shifted_param(p, type, i - shift, C, absent);
-        from = to;
-        last = span - 8;
-    }
-    __device__ __forceinline__ const float2 (&get(int at, int k))[4] {
-        if constexpr (kHeld) {
-            return f[k];
-        } else {
-            const float* g = from + min(at, last);
-            const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
-            f[0][0] = make_float2(a.x, a.y), f[0][1] = make_float2(a.z, a.w);
-            f[0][2] = make_float2(b.x, b.y), f[0][3] = make_float2(b.z, b.w);
-            return f[0];
-        }
-    }
+// Where a thread's vectors lie: vector k of the thread begins at column first + 8 * (k * width +
+// lane) and is the thread's if that is below `end`.  `first` is the CTA's first column (minus the
+// row's shift), so a CTA of a cluster has the columns max(0, first) .. end - 1.
+struct Columns {
+    int first, end, width, lane;
+    __device__ __forceinline__ int of(int k) const { return first + (k * width + lane) * 8; }
 };
+
+// Elements of a row that warp `warp` of the group holds.
+template <int NV>
+__device__ __forceinline__ int warp_columns(const Columns& at, int warp) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int lo = at.first + (k * at.width + warp * 32) * 8;
+        n += max(0, min(at.end, lo + 32 * 8) - max(0, lo));
+    }
+    return n;
+}
+
+// Gamma or beta of a thread's vectors, in registers.
+template <int NV>
+__device__ __forceinline__ void load_params(float2 (&f)[NV][4], const void* p, int type, int C, const Columns& at, float absent) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = at.of(k) + 2 * j;
+            f[k][j] = make_float2(shifted_param(p, type, c, C, absent), shifted_param(p, type, c + 1, C, absent));
+        }
+}
+
+// ---- sums of several warps or CTAs ---------------------------------------------------------
+constexpr int kWarps = kMaxCta / 32;         // entries of one CTA in an exchange
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Barrier of all threads of the cluster; shared memory written before it, the other CTAs' too, is
+// visible after it.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// *p = v in the shared memory of CTA `rank` of the cluster (ordered by cluster_barrier()).
+__device__ __forceinline__ void store_remote(float* p, float v, uint32_t rank) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_addr(p)),
+        "r"(rank), "f"(v)
+        : "memory");
+}
+// The same counted on that CTA's mbarrier: what a cluster exchanges per row.  (A cluster barrier in
+// its place waits for the CTA's stores to global memory as well: 132 against 110 us for bf16
+// 4096 x 16384 forward, before the number of clusters was set right, now 66.)
+__device__ __forceinline__ void send_remote(float* p, float v, uint64_t* bar, uint32_t rank) {
+    asm volatile(
+        "{\n\t.reg .b32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %3, [b];\n\t}" ::"r"(smem_addr(p)),
+        "r"(smem_addr(bar)), "r"(rank), "r"(__float_as_uint(v))
+        : "memory");
+}
+// Wait for a phase of the exchange, no longer than the limit: then the status word says so and the
+// kernel goes on (with wrong sums) to its end.
+__device__ __forceinline__ void await_exchange(uint64_t* bar, uint32_t phase, unsigned long long limit_ns, unsigned int* status) {
+    const unsigned long long limit = limit_ns != 0 ? limit_ns : kWaitLimitNs, t0 = global_ns();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(phase)
+            : "memory");
+        if (done) return;
+        if (global_ns() - t0 > limit) break;
+    }
+    record_status(status, DWC_DEVSTAT_TIMEOUT);
+}
+// A warp's value to the place in the exchange where its row's threads find it.
+template <bool kCluster>
+__device__ __forceinline__ void publish(float* p, float v, uint64_t* bar, int cluster) {
+    if constexpr (!kCluster) {
+        *p = v;
+    } else {
+        for (int q = 0; q < cluster; ++q) send_remote(p, v, bar, q);
+    }
+}
 
 // Asynchronous copies of one row's tensors into the thread group's own part of shared memory.
 // Each thread holds 8 elements of every vector slot: one 16-byte granule of a 16-bit type or two of
-// fp32, of which the lanes of a warp copy consecutive ones (whole sectors).  A warp's granules stay
+// fp32, of which the lanes of a warp copy consecutive ones (whole sectors; `lane` counts them).  A warp's granules stay
 // in the tensor's order, so each copy fills 512 contiguous bytes; the fp32 reads then meet in
 // banks two by two, which costs little: with the halves of the vectors parted into two planes
 // (no conflicts) the copies themselves were the limit, 238 us instead of 185 for 16384 x 4096 with
@@ -112,9 +150,9 @@ template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <bool kAligned, typename T>
-__device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, int C, int low, int room) {
+__device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, int end, int C, int low, int room) {
     constexpr int n = 16 / sizeof(T);
-    const bool some = col < C;
+    const bool some = col < end;
     if (kAligned || !some || (col >= low && col + n <= room)) {
         copy16(dst, row + (some ? col : 0), some);
     } else {
@@ -128,13 +166,13 @@ __device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, 
 // One vector slot of the lanes of a (sub-)warp of GW lanes: `slot` is the thread's own first granule,
 // `col` its first element.
 template <bool kAligned, typename T, int GW>
-__device__ __forceinline__ void copy_slot(uint4* slot, const T* row, int lane, int col, int C, int low, int room) {
+__device__ __forceinline__ void copy_slot(uint4* slot, const T* row, int lane, int col, int end, int C, int low, int room) {
     if constexpr (sizeof(T) == 2) {
-        copy_granule<kAligned>(slot, row, col, C, low, room);
+        copy_granule<kAligned>(slot, row, col, end, C, low, room);
     } else {
         const int first = col - 4 * lane;       // this lane's granule of the group's 2 * GW
-        copy_granule<kAligned>(slot - lane, row, first, C, low, room);
-        copy_granule<kAligned>(slot - lane + GW, row, first + 4 * GW, C, low, room);
+        copy_granule<kAligned>(slot - lane, row, first, end, C, low, room);
+        copy_granule<kAligned>(slot - lane + GW, row, first + 4 * GW, end, C, low, room);
     }
 }
 
@@ -196,11 +234,13 @@ constexpr int fwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2;
 // squares about it, and the warps of a group are merged by their counts (Chan, Golub and LeVeque,
 // "Updating formulae and a pairwise algorithm for computing sample variances", 1979): one
 // barrier per R rows, and no cancellation however far the mean lies from zero.
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
+template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, fwd_min_ctas(G, NV))
-norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
+norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vectors) {
+    const int cluster = kCluster ? cluster_ctas : 1;
     extern __shared__ __align__(16) float smem[];
-    __shared__ float2 merge[2][R][kMaxCta / 32];
+    __shared__ float exchange[2][R][2][kWarps * (kCluster ? kMaxCluster : 1)], counts[kWarps * (kCluster ? kMaxCluster : 1)];
+    __shared__ uint64_t arrived[2];
     constexpr bool kCta = G == 0;                  // several warps serve a row
     constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
     constexpr int kPart = GW / R;                  // lanes that hold one row's sums
@@ -211,10 +251,13 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
     const int lane = threadIdx.x - local * width;
     const int sub = threadIdx.x % GW;
     const int per_cta = threads / width;
-    const int groups = gridDim.x * per_cta;
-    const int group = blockIdx.x * per_cta + local;
+    const int groups = gridDim.x / cluster * per_cta;
+    const int group = blockIdx.x / cluster * per_cta + local;
+    const int rank = kCluster ? cluster_rank() : 0;
     const int C = p.C;
     const int shift = kAligned ? 0 : static_cast<int>((static_cast<long long>(group) * C) & 7);
+    const int first = rank * cta_vectors * 8 - shift;
+    const Columns at{first, min(C, first + cta_vectors * 8), width, lane};
     const float inv = 1.f / static_cast<float>(C);
     // (an update in place overwrites the neighbouring rows: then only the row's own elements are read)
     const bool whole = !kAdd || p.z != p.in;
@@ -225,6 +268,14 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
     uint4* const slots = reinterpret_cast<uint4*>(smem);
     const int mine_b = threadIdx.x * kBranch, mine_s = threadIdx.x * kStream;   // this thread's granules of a slot
     pdl_trigger();
+    if (kCluster) {
+        if (threadIdx.x == 0) {
+            mbar_init(&arrived[0], 1);
+            mbar_init(&arrived[1], 1);
+            fence_barrier_init();
+        }
+        cluster_barrier();   // every CTA of the cluster is ready before any writes to it
+    }
     pdl_wait();
     DropState drop;
     if (kAdd) drop.init(p.drop);
@@ -241,9 +292,10 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
             const TB* x = static_cast<const TB*>(p.x) + r * p.ld_x;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
-                copy_slot<kAligned, TS, GW>(to + k * kStream * threads + mine_s, in, sub, col, C, low, room);
-                if (kAdd) copy_slot<kAligned, TB, GW>(to + x_at + k * kBranch * threads + mine_b, x, sub, col, C, low, room);
+                copy_slot<kAligned, TS, GW>(to + k * kStream * threads + mine_s, in, sub, at.of(k), at.end, C, low, room);
+                if (kAdd)
+                    copy_slot<kAligned, TB, GW>(to + x_at + k * kBranch * threads + mine_b, x, sub, at.of(k), at.end, C, low,
+                                                room);
             }
         }
         copy_commit();
@@ -251,21 +303,32 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
 
-    Params<NV> gamma, beta;
-    gamma.hold(p.gamma, p.param_type, C, lane, width, shift, 1.f);
-    beta.hold(p.beta, p.param_type, C, lane, width, shift, 0.f);
-    if (NV > 2 && staged) {
-        float* to = smem + S * R * row_granules * 4 + local * width * NV * 16;
-        gamma.stage(to, p.gamma, p.param_type, C, lane, width, shift, 1.f);
-        beta.stage(to + width * NV * 8, p.beta, p.param_type, C, lane, width, shift, 0.f);
-        if (kCta) group_barrier(1 + local, width); else __syncwarp();
+    float2 gamma[NV][4], beta[NV][4];
+    load_params(gamma, p.gamma, p.param_type, C, at, 1.f);
+    load_params(beta, p.beta, p.param_type, C, at, 0.f);
+    // elements of this thread's warp (or group) in a row; its place in the exchange, and the places
+    // that one row's sums come from
+    const int warps = width >> 5;
+    const int place = kCluster ? rank * kWarps + (lane >> 5) : threadIdx.x >> 5;
+    const int from_place = local * warps, places = cluster * kWarps;
+    int mine = C;
+    float peer = 0.f;              // elements of the warp whose sums this lane merges (one CTA to a row)
+    if constexpr (kCta) {
+        mine = warp_columns<NV>(at, lane >> 5);
+        const int w = sub % kPart;
+        if (w < warps) peer = static_cast<float>(warp_columns<NV>(at, w));
+        if (kCluster) {
+            // (places of warps that do not exist count nothing)
+            for (int i = threadIdx.x; i < cluster * kWarps; i += threads) counts[i] = 0.f;
+            cluster_barrier();
+            if (sub == 0)
+                for (int q = 0; q < cluster; ++q) store_remote(&counts[place], static_cast<float>(mine), q);
+            cluster_barrier();
+        }
     }
-    // elements of this thread's warp or group, and of the warp whose sums this lane merges
-    const int warps = width >> 5, first_warp = local * warps;
-    const int mine = kCta ? warp_columns(lane >> 5, width, NV, shift, C) : C;
-    const int peer = kCta && sub % kPart < warps ? warp_columns(sub % kPart, width, NV, shift, C) : 0;
     const float mine_inv = mine > 0 ? 1.f / static_cast<float>(mine) : 0.f;
     int parity = 0, stage = 0;
+    uint32_t phase = 0;                 // of the exchange barrier that is next in use
 
     const long long step = static_cast<long long>(R) * groups;
     // (the lane groups of a warp stay together: the warp goes on while its first group has a row, and
@@ -285,7 +348,7 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
             float2 s2 = both(0.f);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
+                const int col = at.of(k);
                 read_slot<TS>(v[u][k], row + k * kStream * threads + mine_s);
                 if constexpr (kAdd) {
                     float2 b[4];
@@ -293,7 +356,7 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
                     if (drop.threshold != 0) drop8(drop, b, static_cast<uint64_t>(r * C + col) >> 3);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[u][k][j] = __fadd2_rn(v[u][k][j], b[j]);
-                    if (live && col < C) store_row8<kAligned>(static_cast<TS*>(p.z) + r * C, v[u][k], col, C);
+                    if (live && col < at.end) store_row8<kAligned>(static_cast<TS*>(p.z) + r * C, v[u][k], col, C);
                 }
                 if (!kAligned && !inside(col, C)) mask8(v[u][k], col, C);
 #pragma unroll
@@ -314,11 +377,11 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
             float2 q2 = both(0.f);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
+                const int col = at.of(k);
                 float2 d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = __fadd2_rn(v[u][k][j], both(-mean[u]));
-                if (!inside(col, C)) mask8(d, col, C);
+                if (col >= at.end || !inside(col, C)) mask8(d, col, col >= at.end ? 0 : C);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q2 = __ffma2_rn(d[j], d[j], q2);
             }
@@ -328,21 +391,43 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
         float m = mean[0];
         if constexpr (R == 2) m = sub < kPart ? mean[0] : mean[1];
         if constexpr (kCta) {
-            // lane l merges row l / kPart over the group's warps, warp l % kPart
-            if (sub % kPart == 0) merge[parity][sub / kPart][threadIdx.x >> 5] = make_float2(m, t);
-            group_barrier(1 + local, width);
-            const int w = sub % kPart;
-            const float2 e = w < warps ? merge[parity][sub / kPart][first_warp + w] : make_float2(0.f, 0.f);
-            parity ^= 1;
-            const float n = static_cast<float>(peer);
-            m = n * e.x;
+            // the part of a warp that holds row u's sums merges that row over the warps (and CTAs)
+            float(&e)[2][kWarps * (kCluster ? kMaxCluster : 1)] = exchange[parity][sub / kPart];
+            if (kCluster && threadIdx.x == 0)
+                mbar_arrive_expect_tx(&arrived[parity], R * 2 * sizeof(float) * warps * cluster);
+            if (sub % kPart == 0) {
+                publish<kCluster>(&e[0][place], m, &arrived[parity], cluster);
+                publish<kCluster>(&e[1][place], t, &arrived[parity], cluster);
+            }
+            if constexpr (!kCluster) {
+                group_barrier(1 + local, width);
+                const int w = sub % kPart;
+                const float em = w < warps ? e[0][from_place + w] : 0.f, eq = w < warps ? e[1][from_place + w] : 0.f;
+                m = peer * em;
 #pragma unroll
-            for (int x = kPart / 2; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
-            m *= inv;
-            const float d = e.x - m;
-            t = peer > 0 ? fmaf(n * d, d, e.y) : 0.f;
+                for (int x = kPart / 2; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+                m *= inv;
+                const float d = em - m;
+                t = peer > 0.f ? fmaf(peer * d, d, eq) : 0.f;
+            } else {
+                await_exchange(&arrived[parity], phase, p.wait_ns, p.status);
+                m = 0.f;
+                for (int w = sub % kPart; w < places; w += kPart)
+                    if (counts[w] > 0.f) m = fmaf(counts[w], e[0][w], m);
+#pragma unroll
+                for (int x = kPart / 2; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+                m *= inv;
+                t = 0.f;
+                for (int w = sub % kPart; w < places; w += kPart)
+                    if (counts[w] > 0.f) {
+                        const float d = e[0][w] - m;
+                        t += fmaf(counts[w] * d, d, e[1][w]);
+                    }
+            }
 #pragma unroll
             for (int x = kPart / 2; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+            phase ^= parity;                // both barriers have been used once: their next phase
+            parity ^= 1;
         }
         t = 1.f / sqrtf(t * inv + p.eps);
 #pragma unroll
@@ -351,54 +436,70 @@ norm_fwd_rows_kernel(NormFwd p, int staged, int group_threads) {
             rstd[u] = __shfl_sync(0xffffffffu, t, u * kPart, GW);
         }
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int at = (k * width + lane) * 8, col = at - shift;
-            const float2(&g)[4] = gamma.get(at, k);
-            const float2(&b)[4] = beta.get(at, k);
+        for (int u = 0; u < R; ++u) {
+            const long long r = r0 + static_cast<long long>(u) * groups;
+            if (r >= p.rows) continue;     // (no barrier and no shuffle below)
 #pragma unroll
-            for (int u = 0; u < R; ++u) {
-                const long long r = r0 + static_cast<long long>(u) * groups;
+            for (int k = 0; k < NV; ++k) {
                 float2 y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 xhat = __fmul2_rn(__fadd2_rn(v[u][k][j], both(-mean[u])), both(rstd[u]));
-                    y[j] = __ffma2_rn(xhat, g[j], b[j]);
+                    y[j] = __ffma2_rn(xhat, gamma[k][j], beta[k][j]);
                 }
-                if (r < p.rows && col < C) store_row8<kAligned>(static_cast<TB*>(p.y) + r * C, y, col, C);
+                if (at.of(k) < at.end) store_row8<kAligned>(static_cast<TB*>(p.y) + r * C, y, at.of(k), C);
             }
-        }
-        if (lane == 0) {
-#pragma unroll
-            for (int u = 0; u < R; ++u) {
-                const long long r = r0 + static_cast<long long>(u) * groups;
-                if (r >= p.rows) continue;
+            if (lane == 0 && rank == 0) {
                 if (p.mean != nullptr) p.mean[r] = mean[u];
                 if (p.rstd != nullptr) p.rstd[r] = rstd[u];
             }
         }
     }
     copy_wait<0>();
+    if (kCluster) cluster_barrier();   // (also where a wait gave up: nothing is on its way to a CTA that has ended)
 }
 
 // ------------------------------------------------------------------------------ backward
 
-// CTAs per SM that the register budget allows: 80 registers a thread for one vector, 128 for 2 and
-// 4, of which 16 a vector hold the gradient sums and 8 gamma.
+// CTAs per SM that the register budget allows: 80 registers a thread for one vector, 128 for 2, of
+// which 16 a vector hold the gradient sums and 8 gamma.
 constexpr int bwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2; }
+
+// A thread's sums of its columns (null: not wanted).
+template <bool kAligned, int NV>
+__device__ __forceinline__ void store_sums(float* to, const float2 (&f)[NV][4], const Columns& at, int C) {
+    if (to == nullptr) return;
+    const bool vec = kAligned && reinterpret_cast<uintptr_t>(to) % 16 == 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int col = at.of(k);
+        if (col >= at.end) continue;
+        if (vec) {
+            *reinterpret_cast<float4*>(to + col) = make_float4(f[k][0].x, f[k][0].y, f[k][1].x, f[k][1].y);
+            *reinterpret_cast<float4*>(to + col + 4) = make_float4(f[k][2].x, f[k][2].y, f[k][3].x, f[k][3].y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (in_row(col + j, C)) to[col + j] = j & 1 ? f[k][j / 2].y : f[k][j / 2].x;
+        }
+    }
+}
 
 // Each thread keeps the sums of dy * xhat and dy of its columns in registers over all rows of its
 // group; at the end the groups of a CTA are added in order and the CTA writes one row of partial
-// sums.  The sums (and gamma, up to two vectors a thread) take the registers, so the rows wait in
+// sums.  The sums and gamma take the registers, so the rows wait in
 // shared memory, S times R rows per group, and are read twice there (before and after a row's
 // two means are known).  R rows go through together: one reduction and one barrier for both,
 // and two independent chains of latencies.  G == 0: groups of `group_threads` threads, several
 // to a CTA where they are short: one CTA per SM, so that there are few rows of partial sums.
 // kAdd: the residual form (dz, a branch gradient, dropout).
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
+template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 __global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, bwd_min_ctas(G, NV))
-norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
+norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vectors) {
+    const int cluster = kCluster ? cluster_ctas : 1;
     extern __shared__ __align__(16) float smem[];
-    __shared__ float merge[2][2 * R][kMaxCta / 32];
+    __shared__ float exchange[2][2 * R][kWarps * (kCluster ? kMaxCluster : 1)];
+    __shared__ uint64_t arrived[2];
     constexpr bool kCta = G == 0;                  // several warps serve a row
     constexpr int GW = kCta ? 32 : G;              // lanes whose vectors are adjacent
     constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // granules of a slot
@@ -408,10 +509,13 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     const int lane = threadIdx.x - local * width;
     const int sub = threadIdx.x % GW;
     const int per_cta = threads / width;
-    const int groups = gridDim.x * per_cta;
-    const int group = blockIdx.x * per_cta + local;
+    const int groups = gridDim.x / cluster * per_cta;
+    const int group = blockIdx.x / cluster * per_cta + local;
+    const int rank = kCluster ? cluster_rank() : 0;
     const int C = p.C;
     const int shift = kAligned ? 0 : static_cast<int>((static_cast<long long>(group) * C) & 7);
+    const int first = rank * cta_vectors * 8 - shift;
+    const Columns at{first, min(C, first + cta_vectors * 8), width, lane};
     const float inv = 1.f / static_cast<float>(C);
     const bool has_dz = kAdd && p.dz != nullptr;
     const bool has_branch = kAdd && p.d_branch != nullptr;
@@ -421,6 +525,14 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
     uint4* const slots = reinterpret_cast<uint4*>(smem);
     const int mine_b = threadIdx.x * kBranch, mine_s = threadIdx.x * kStream;   // this thread's granules of a slot
     pdl_trigger();
+    if (kCluster) {
+        if (threadIdx.x == 0) {
+            mbar_init(&arrived[0], 1);
+            mbar_init(&arrived[1], 1);
+            fence_barrier_init();
+        }
+        cluster_barrier();   // every CTA of the cluster is ready before any writes to it
+    }
     pdl_wait();
     DropState drop;
     if (kAdd) drop.init(p.drop);
@@ -438,15 +550,14 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             const TS* dz = has_dz ? static_cast<const TS*>(p.dz) + r * p.ld_dz : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
-                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, col, C, -8, room);
-                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, col, C, -8, room);
+                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, at.of(k), at.end, C, -8, room);
+                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, at.of(k), at.end, C, -8, room);
             }
             if (has_dz) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
-                    copy_slot<kAligned, TS, GW>(to + dz_at + k * kStream * threads + mine_s, dz, sub,
-                                                (k * width + lane) * 8 - shift, C, -8, room);
+                    copy_slot<kAligned, TS, GW>(to + dz_at + k * kStream * threads + mine_s, dz, sub, at.of(k), at.end, C, -8,
+                                                room);
             }
         }
         copy_commit();
@@ -454,19 +565,19 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
 
-    Params<NV> gamma;
-    gamma.hold(p.gamma, p.param_type, C, lane, width, shift, 1.f);
-    if (NV > 2 && staged) {
-        gamma.stage(smem + S * R * row_granules * 4 + local * width * NV * 8, p.gamma, p.param_type, C, lane, width,
-                    shift, 1.f);
-        if (kCta) group_barrier(1 + local, width); else __syncwarp();
-    }
+    float2 gamma[NV][4];
+    load_params(gamma, p.gamma, p.param_type, C, at, 1.f);
     float2 sum_g[NV][4], sum_b[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum_g[k][j] = sum_b[k][j] = both(0.f);
+    // the warp's place in the exchange, and the places that one row's sums come from
+    const int warps = width >> 5;
+    const int place = kCluster ? rank * kWarps + (lane >> 5) : threadIdx.x >> 5;
+    const int from_place = local * warps;
     int parity = 0, stage = 0;
+    uint32_t phase = 0;                 // of the exchange barrier that is next in use
     float next_mean[R], next_rstd[R];
     auto fetch_stats = [&](long long r0) {
 #pragma unroll
@@ -503,18 +614,14 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
                     float2 f[4], x[4];
                     read_slot<TB>(f, row + k * kBranch * threads + mine_b);
                     read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
-                    const float2(&gk)[4] = gamma.get((k * width + lane) * 8, k);
-                    if constexpr (!kAligned) {
-                        const int col = (k * width + lane) * 8 - shift;
-                        if (!inside(col, C)) {
-                            mask8(f, col, C);
-                            mask8(x, col, C);
-                        }
+                    if (!kAligned && !inside(at.of(k), C)) {
+                        mask8(f, at.of(k), C);
+                        mask8(x, at.of(k), C);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 xhat = __fmul2_rn(__fadd2_rn(x[j], both(-mean[u])), both(rstd[u]));
-                        const float2 a = __fmul2_rn(f[j], gk[j]);
+                        const float2 a = __fmul2_rn(f[j], gamma[k][j]);
                         s1 = __fadd2_rn(s1, a);
                         s2 = __ffma2_rn(a, xhat, s2);
                         sum_g[k][j] = __ffma2_rn(f[j], xhat, sum_g[k][j]);
@@ -528,14 +635,23 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
         constexpr int kPart = GW / (2 * R);   // lanes that hold one of the sums
         float t = parted_sum<GW, 2 * R>(s, sub);
         if constexpr (kCta) {
-            // the warps' sums: lane l of every warp takes sum l / kPart of warps l % kPart, ...
-            if (sub % kPart == 0) merge[parity][sub / kPart][threadIdx.x >> 5] = t;
-            group_barrier(1 + local, width);
-            const int warps = width >> 5, first = local * warps;
+            // the part of a warp that holds sum q adds it up over the warps (and CTAs)
+            float(&e)[kWarps * (kCluster ? kMaxCluster : 1)] = exchange[parity][sub / kPart];
+            if (kCluster && threadIdx.x == 0)
+                mbar_arrive_expect_tx(&arrived[parity], 2 * R * sizeof(float) * warps * cluster);
+            if (sub % kPart == 0) publish<kCluster>(&e[place], t, &arrived[parity], cluster);
             t = 0.f;
-            for (int w = sub % kPart; w < warps; w += kPart) t += merge[parity][sub / kPart][first + w];
+            if constexpr (!kCluster) {
+                group_barrier(1 + local, width);
+                for (int w = sub % kPart; w < warps; w += kPart) t += e[from_place + w];
+            } else {
+                await_exchange(&arrived[parity], phase, p.wait_ns, p.status);
+                for (int w = sub % kPart; w < cluster * kWarps; w += kPart)
+                    if (w % kWarps < warps) t += e[w];
+            }
 #pragma unroll
             for (int m = kPart / 2; m > 0; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+            phase ^= parity;                // both barriers have been used once: their next phase
             parity ^= 1;
         }
 #pragma unroll
@@ -551,14 +667,13 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
             TB* db = has_branch ? static_cast<TB*>(p.d_branch) + r * C : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * width + lane) * 8 - shift;
+                const int col = at.of(k);
                 float2 f[4], x[4], g[4];
                 read_slot<TB>(f, row + k * kBranch * threads + mine_b);
                 read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
-                const float2(&gk)[4] = gamma.get((k * width + lane) * 8, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 a = __ffma2_rn(__fmul2_rn(f[j], gk[j]), both(rstd[u]), both(-k1));
+                    const float2 a = __ffma2_rn(__fmul2_rn(f[j], gamma[k][j]), both(rstd[u]), both(-k1));
                     g[j] = __ffma2_rn(__fadd2_rn(x[j], both(-mean[u])), both(-k2), a);
                 }
                 if (has_dz) {
@@ -566,7 +681,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], x[j]);
                 }
-                if (col < C) {
+                if (col < at.end) {
                     store_row8<kAligned>(ds, g, col, C);
                     if (has_branch) {
                         if (drop.threshold != 0) drop8(drop, g, static_cast<uint64_t>(r * C + col) >> 3);
@@ -580,38 +695,28 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
         if (++stage == S) stage = 0;
     }
     copy_wait<0>();
-    if (p.partial == nullptr) return;
-    float* part = p.partial + static_cast<size_t>(blockIdx.x) * 2 * C;
-    const bool combine = per_cta > 1;
-    if (combine) __syncthreads();   // no group reads its rows or parameters any more
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int col = (k * width + lane) * 8 - shift;
-        float* to = combine ? smem + local * 2 * C : part;   // the groups' sums, [group][2][C]
-        if (kAligned) {
-            if (col >= C) continue;
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const float2 *g = &sum_g[k][j], *b = &sum_b[k][j];
-                *reinterpret_cast<float4*>(to + col + 2 * j) = make_float4(g[0].x, g[0].y, g[1].x, g[1].y);
-                *reinterpret_cast<float4*>(to + C + col + 2 * j) = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = col + j;
-                if (!in_row(c, C)) continue;
-                to[c] = j & 1 ? sum_g[k][j / 2].y : sum_g[k][j / 2].x;
-                to[C + c] = j & 1 ? sum_b[k][j / 2].y : sum_b[k][j / 2].x;
-            }
-        }
+    if (kCluster) cluster_barrier();   // (also where a wait gave up: nothing is on its way to a CTA that has ended)
+    if (p.dgamma == nullptr && p.dbeta == nullptr) return;
+    // a lone CTA (or cluster) has the whole sums, others write a row of partial ones
+    const bool alone = gridDim.x == cluster;
+    float* part = alone ? nullptr : p.partial + static_cast<size_t>(blockIdx.x / cluster) * 2 * C;
+    float *to_g = alone ? p.dgamma : part, *to_b = alone ? p.dbeta : part + C;
+    if (per_cta == 1) {
+        // (one group: its threads hold each column once)
+        store_sums<kAligned, NV>(to_g, sum_g, at, C);
+        store_sums<kAligned, NV>(to_b, sum_b, at, C);
+        return;
     }
-    if (!combine) return;
+    __syncthreads();                 // no group reads its rows any more
+    float* mine_sums = smem + local * 2 * C;   // the groups' sums, [group][2][C]
+    store_sums<kAligned, NV>(mine_sums, sum_g, at, C);
+    store_sums<kAligned, NV>(mine_sums + C, sum_b, at, C);
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * C; i += threads) {
         float t = 0.f;
         for (int g = 0; g < per_cta; ++g) t += smem[g * 2 * C + i];
-        part[i] = t;
+        float* to = i < C ? to_g : to_b;
+        if (to != nullptr) to[i < C ? i : i - C] = t;
     }
 }
 
@@ -621,6 +726,7 @@ norm_bwd_rows_kernel(NormBwd p, int staged, int group_threads) {
 struct KernelFacts {
     DeviceOnce smem;
     std::atomic<int> regs{0};
+    std::atomic<uint64_t> clusters{0};   // shared memory, threads and CTAs of a cluster; how many fit
     template <class K>
     int registers(K kern) {
         int r = regs.load(std::memory_order_relaxed);
@@ -632,87 +738,139 @@ struct KernelFacts {
     }
 };
 
-// CTAs for `want` of them: at most what the SMs hold together, in eights (a group's rows are a
-// multiple of 8 apart, see the head of this file).
-inline long long persistent_grid(long long want, size_t smem, int threads, int regs) {
-    const long long all = static_cast<long long>(device_info().sm_count) * resident_ctas(smem, threads, regs);
-    return std::min(want, std::max(8LL, all / 8 * 8));
+// How the rows of a call are laid over CTAs.
+struct Layout {
+    int width;          // threads of a group
+    int per_cta;        // groups of a CTA
+    int cluster;        // CTAs that share a row
+    int cta_vectors;    // vectors of a row in one of them
+    int threads;        // of a CTA
+};
+
+// G > 0: a row to G lanes.  Else NV vectors a thread: one CTA of up to 512 threads to a row (several
+// groups to a CTA only once there is a row for every SM), or a cluster of 2, 4 or 8 CTAs of up to
+// 256 threads, two of which an SM holds (one works while the other waits for its cluster), and of
+// up to 512 for the longest rows.  No layout: threads = 0.
+inline Layout layout(bool cluster, int G, int NV, long long rows, int vectors) {
+    if (G > 0) return {G, kWarpCta / G, 1, vectors, kWarpCta};
+    Layout l{};
+    l.cluster = cluster ? 2 : 1;
+    while (cluster && l.cluster < kMaxCluster && vectors > l.cluster * NV * kMaxCta / 2) l.cluster *= 2;
+    if (vectors > l.cluster * NV * kMaxCta) return Layout{};
+    l.cta_vectors = (vectors + l.cluster - 1) / l.cluster;
+    l.width = (l.cta_vectors + NV * 32 - 1) / (NV * 32) * 32;
+    l.per_cta = cluster ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(kMaxCta / l.width, rows / device_info().sm_count)));
+    l.threads = l.width * l.per_cta;
+    return l;
 }
 
-inline bool params_line_up(const void* gamma, const void* beta, int type, int C) {
-    return C % 8 == 0 && (type == kF32 || (gamma == nullptr && beta == nullptr)) &&
-           (reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) % 16 == 0;
+// Rows beyond 1024 vectors, 512 threads of two, go to clusters.  (Shorter ones are faster in one CTA:
+// bf16 8192 x 8192 44 against 61 us forward, 70 against 80 backward.)
+constexpr int kCtaVectors = 2 * kMaxCta;
+// Rows that go through the forward pass together where several warps serve a row: two of a 16-bit
+// stream (the arithmetic and the generator need the pairs: bf16 16384 x 4096 with dropout 85 us, 98
+// with one), one of an fp32 stream (twice the bytes, whose copies in flight only get in the way of
+// the stores: fp32 16384 x 4096 87 us, 93 with two).
+template <typename TS>
+constexpr int kFwdRows = sizeof(TS) == 2 ? 2 : 1;
+
+// Rows of a lane group that go through the backward pass together, in two stages: two of a 16-bit
+// stream, one of an fp32 stream or where edges are masked (80 registers hold no more; bf16
+// 524288 x 128: 66 us, 76 with one stage of two rows).
+template <typename TS, bool kAligned>
+constexpr int kBwdLaneRows = sizeof(TS) == 2 && kAligned ? 2 : 1;
+
+template <class P>
+struct RowLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    RowLaunch(const P& p, const Layout& l, size_t smem) {
+        cfg.blockDim = dim3(static_cast<unsigned>(l.threads));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = p.stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(l.cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = l.cluster > 1 ? 2 : 1;
+    }
+};
+
+// CTAs (or clusters) for `want` of them: at most what the GPU holds together, since each takes its
+// share of the rows and a late one would double the time.  Where rows are shifted they come in
+// eights (a group's rows are a multiple of 8 apart, see the head of this file).
+template <class K, class P>
+cudaError_t launch_rows(K kern, KernelFacts& facts, const P& p, const Layout& l, long long want, size_t smem, int* grid) {
+    RowLaunch<P> launch(p, l, smem);
+    long long all;
+    if (l.cluster == 1) {
+        all = static_cast<long long>(device_info().sm_count) * resident_ctas(smem, l.threads, facts.registers(kern));
+    } else {
+        // clusters need their CTAs on one GPC, whose SMs they do not always divide: 4 CTAs, two to an SM,
+        // fit 74 times, not 76
+        const uint64_t key = (static_cast<uint64_t>(smem) << 32 | static_cast<uint64_t>(l.threads) << 20 | l.cluster << 16);
+        uint64_t known = facts.clusters.load(std::memory_order_relaxed);
+        if (known >> 16 != key >> 16) {
+            launch.cfg.gridDim = dim3(static_cast<unsigned>(l.cluster));
+            int n = 0;
+            const cudaError_t err = cudaOccupancyMaxActiveClusters(&n, kern, &launch.cfg);
+            if (err != cudaSuccess) return err;
+            if (n < 1) return cudaErrorNotSupported;
+            known = key | static_cast<uint64_t>(std::min(n, 0xffff));
+            facts.clusters.store(known, std::memory_order_relaxed);
+        }
+        all = static_cast<long long>(known & 0xffff);
+    }
+    if (p.C % 8 != 0) all = std::max(8LL, all / 8 * 8);
+    *grid = static_cast<int>(std::min(want, all));
+    launch.cfg.gridDim = dim3(static_cast<unsigned>(*grid) * static_cast<unsigned>(l.cluster));
+    return cudaLaunchKernelEx(&launch.cfg, kern, p, l.width, l.cluster, l.cta_vectors);
 }
 
-// Groups of `width` threads in a CTA: several only once there is a row for every SM.
-inline int row_groups(long long rows, int width) {
-    return static_cast<int>(std::max(1LL, std::min<long long>(kMaxCta / width, rows / device_info().sm_count)));
-}
-
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
+template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 cudaError_t fwd_launch(const NormFwd& p, int vectors) {
-    auto kern = norm_fwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, R, S>;
-    const int width = G > 0 ? G : (vectors + NV * 32 - 1) / (NV * 32) * 32;
-    const int per_cta = G > 0 ? kWarpCta / G : row_groups(p.rows, width);
-    const int threads = width * per_cta;
-    const int staged = NV > 2 && (p.gamma == nullptr || p.beta == nullptr ||
-                                  !params_line_up(p.gamma, p.beta, p.param_type, p.C));
-    const size_t slot = 8 * (sizeof(TS) + (kAdd ? sizeof(TB) : 0));
-    const size_t bytes = (S * R * slot + (staged ? 16 * sizeof(float) : 0)) * NV * threads;
-    if (bytes > kDynamicSmem) return cudaErrorNotSupported;
+    auto kern = norm_fwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
+    const Layout l = layout(kCluster, G, NV, p.rows, vectors);
+    const size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TS) + (kAdd ? sizeof(TB) : 0));
+    if (l.threads == 0 || bytes > kDynamicSmem) return cudaErrorNotSupported;
     static KernelFacts facts;
     const cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
-    const long long grid = persistent_grid((p.rows + per_cta - 1) / per_cta, bytes, threads, facts.registers(kern));
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes, p.stream, p, staged, width);
+    int grid = 0;
+    return launch_rows(kern, facts, p, l, (p.rows + l.per_cta - 1) / l.per_cta, bytes, &grid);
 }
 
-// Bytes a thread's vector slots take per stage.
-template <typename TS, typename TB>
-size_t slot_bytes(const NormBwd& p) {
-    return 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
-}
-
-template <typename TS, typename TB, bool kAdd, bool kAligned, int G, int NV, int R, int S>
+template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 cudaError_t bwd_launch(const NormBwd& p, int vectors) {
-    auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, G, NV, R, S>;
-    const int width = G > 0 ? G : (vectors + NV * 32 - 1) / (NV * 32) * 32;
-    const int per_cta = G > 0 ? kWarpCta / G : row_groups(p.rows, width);
-    const int threads = width * per_cta;
-    const int staged = NV > 2 && (p.gamma == nullptr || !params_line_up(p.gamma, nullptr, p.param_type, p.C));
-    size_t bytes = (S * R * slot_bytes<TS, TB>(p) + (staged ? 8 * sizeof(float) : 0)) * NV * threads;
-    if (per_cta > 1 && p.partial != nullptr)
-        bytes = std::max(bytes, static_cast<size_t>(per_cta) * 2 * p.C * sizeof(float));
-    if (bytes > kDynamicSmem) return cudaErrorNotSupported;
+    auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
+    const Layout l = layout(kCluster, G, NV, p.rows, vectors);
+    size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
+    if (l.per_cta > 1) bytes = std::max(bytes, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
+    if (l.threads == 0 || bytes > kDynamicSmem) return cudaErrorNotSupported;
     static KernelFacts facts;
     cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
-    long long want = (p.rows + per_cta - 1) / per_cta;
-    if (p.partial != nullptr) want = std::min<long long>(want, norm_bwd_partials(p.rows, p.C));
-    const long long grid = persistent_grid(want, bytes, threads, facts.registers(kern));
-    err = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes, p.stream, p, staged, width);
-    if (err != cudaSuccess || p.partial == nullptr) return err;
-    return launch_norm_param_sum(p.partial, static_cast<int>(grid), p.C, p.dgamma, p.dbeta, p.stream);
+    long long want = (p.rows + l.per_cta - 1) / l.per_cta;
+    const int most = p.partial != nullptr ? norm_bwd_partials(p.rows, p.C) : INT_MAX;
+    if (most < want) want = p.C % 8 != 0 ? std::max(8, most / 8 * 8) : most;   // (eights: see launch_rows)
+    int grid = 0;
+    err = launch_rows(kern, facts, p, l, want, bytes, &grid);
+    if (err != cudaSuccess || p.partial == nullptr || grid == 1) return err;
+    return launch_norm_param_sum(p.partial, grid, p.C, p.dgamma, p.dbeta, p.stream);
 }
 
 template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t fwd_rows_a(const NormFwd& p) {
     const int v = row_vectors(p.C);
-    if (v <= 8) return fwd_launch<TS, TB, kAdd, kAligned, 8, 1, 2, 2>(p, v);
-    if (v <= 16) return fwd_launch<TS, TB, kAdd, kAligned, 16, 1, 2, 2>(p, v);
-    if (v <= 32) return fwd_launch<TS, TB, kAdd, kAligned, 32, 1, 2, 2>(p, v);
-    if (v <= 64) return fwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2, 1>(p, v);
-    // two stages of two rows where they fit in shared memory, else of one row; the widest rows in one
-    // stage (and not at all as fp32 with an fp32 branch and staged parameters)
-    cudaError_t err = cudaErrorNotSupported;
-    if (v <= kMaxCta * 2) {
-        err = fwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 2>(p, v);
-        if (err == cudaErrorNotSupported) err = fwd_launch<TS, TB, kAdd, kAligned, 0, 2, 1, 2>(p, v);
-    } else if (v <= kMaxCta * 4) {
-        err = fwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 2>(p, v);
-        if (err == cudaErrorNotSupported) err = fwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
-    }
-    return err;
+    if (v <= 8) return fwd_launch<TS, TB, kAdd, kAligned, false, 8, 1, 2, 2>(p, v);
+    if (v <= 16) return fwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, 2, 2>(p, v);
+    if (v <= 32) return fwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, 2, 2>(p, v);
+    if (v <= 64) return fwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
+    if (v <= kCtaVectors) return fwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, kFwdRows<TS>, 2>(p, v);
+    return fwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, kFwdRows<TS>, 2>(p, v);
 }
 
 template <typename TS, typename TB, bool kAdd>
@@ -720,24 +878,21 @@ cudaError_t fwd_rows(const NormFwd& p) {
     return p.C % 8 == 0 ? fwd_rows_a<TS, TB, kAdd, true>(p) : fwd_rows_a<TS, TB, kAdd, false>(p);
 }
 
+// Two stages of two rows where they fit in shared memory (bf16 16384 x 4096: 67 us, with one row at
+// a time 76), else of one row.
 template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t bwd_rows_a(const NormBwd& p) {
     const int v = row_vectors(p.C);
-    if (v <= 8) return bwd_launch<TS, TB, kAdd, kAligned, 8, 1, 2, 1>(p, v);
-    if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, 16, 1, 2, 1>(p, v);
-    if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, 32, 1, 2, 1>(p, v);
-    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, 32, 2, 2, 1>(p, v);
-    // two stages of two rows where they fit in shared memory, else one (of one row for the widest,
-    // and not even that for fp32 rows near 16384 with all three tensors and staged parameters)
-    cudaError_t err = cudaErrorNotSupported;
-    if (v <= kMaxCta * 2) {
-        err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 2, 2>(p, v);
-        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 2, 1, 2>(p, v);
-    } else if (v <= kMaxCta * 4) {
-        err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 2>(p, v);
-        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, 0, 4, 1, 1>(p, v);
+    if (v <= 8) return bwd_launch<TS, TB, kAdd, kAligned, false, 8, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
+    if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
+    if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
+    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
+    if (v > kCtaVectors) {
+        const cudaError_t err = bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 2, 2>(p, v);
+        return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 1, 2>(p, v);
     }
-    return err;
+    const cudaError_t err = bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 2, 2>(p, v);
+    return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 1, 2>(p, v);
 }
 
 template <typename TS, typename TB, bool kAdd>
