@@ -151,10 +151,10 @@ __device__ __forceinline__ void mask8(float2 (&f)[4], int col, int C) {
     }
 }
 
-// Store of a vector: only the row's own elements.
-template <bool kAligned, typename T>
-__device__ __forceinline__ void store_row8(T* row, const float2 (&f)[4], int col, int C) {
-    if (kAligned || inside(col, C)) {
+// Store of a vector: only the row's own elements.  `whole`: the warp has no vector that hangs over.
+template <typename T>
+__device__ __forceinline__ void store_row8(T* row, const float2 (&f)[4], int col, int C, bool whole) {
+    if (whole || inside(col, C)) {
         Vec8<T>::store(row + col, f);
     } else {
 #pragma unroll

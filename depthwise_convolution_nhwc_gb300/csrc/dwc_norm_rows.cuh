@@ -26,7 +26,9 @@ namespace dwc {
 namespace norm {
 
 constexpr int kWarpCta = 256;            // threads of a CTA whose warps or lane groups serve rows
-constexpr int kMaxCta = 512;             // threads of a CTA otherwise: 128 registers each
+// Threads of a CTA otherwise: 512 of 128 registers where two rows go through together, 640 of 96
+// where it is one (which serves rows of 4104 to 5120 channels with two groups instead of one).
+constexpr int max_cta(int R) { return R == 2 ? 512 : 640; }
 constexpr size_t kDynamicSmem = 220 * 1024;   // of 227 KB, beside the exchanges' static arrays
 
 // Vectors that the longest-shifted row of C channels touches.
@@ -46,6 +48,21 @@ __device__ __forceinline__ float shifted_param(const void* p, int type, int c, i
 struct Columns {
     int first, end, width, lane;
     __device__ __forceinline__ int of(int k) const { return first + (k * width + lane) * 8; }
+};
+
+// What the warp's lanes have in common about their vectors k (a vote once, a uniform branch per use):
+// `whole`: none of the row's vectors hangs over its ends; `full`: besides, none lies past the end.
+template <int NV, bool kAligned>
+struct Edges {
+    bool whole[NV], full[NV];
+    __device__ __forceinline__ Edges(const Columns& at, int C) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const bool some = at.of(k) < at.end, in = inside(at.of(k), C);
+            whole[k] = kAligned || __all_sync(0xffffffffu, !some || in);
+            full[k] = __all_sync(0xffffffffu, some && in);
+        }
+    }
 };
 
 // Elements of a row that warp `warp` of the group holds.
@@ -73,7 +90,7 @@ __device__ __forceinline__ void load_params(float2 (&f)[NV][4], const void* p, i
 }
 
 // ---- sums of several warps or CTAs ---------------------------------------------------------
-constexpr int kWarps = kMaxCta / 32;         // entries of one CTA in an exchange
+constexpr int kWarps = 20;                   // places of one CTA in an exchange
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -235,7 +252,7 @@ constexpr int fwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2;
 // "Updating formulae and a pairwise algorithm for computing sample variances", 1979): one
 // barrier per R rows, and no cancellation however far the mean lies from zero.
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
-__global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, fwd_min_ctas(G, NV))
+__global__ void __launch_bounds__(G > 0 ? kWarpCta : kCluster ? 512 : max_cta(R), fwd_min_ctas(G, NV))
 norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vectors) {
     const int cluster = kCluster ? cluster_ctas : 1;
     extern __shared__ __align__(16) float smem[];
@@ -303,6 +320,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
 
+    const Edges<NV, kAligned> edges(at, C);
     float2 gamma[NV][4], beta[NV][4];
     load_params(gamma, p.gamma, p.param_type, C, at, 1.f);
     load_params(beta, p.beta, p.param_type, C, at, 0.f);
@@ -356,9 +374,9 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
                     if (drop.threshold != 0) drop8(drop, b, static_cast<uint64_t>(r * C + col) >> 3);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[u][k][j] = __fadd2_rn(v[u][k][j], b[j]);
-                    if (live && col < at.end) store_row8<kAligned>(static_cast<TS*>(p.z) + r * C, v[u][k], col, C);
+                    if (live && col < at.end) store_row8(static_cast<TS*>(p.z) + r * C, v[u][k], col, C, edges.whole[k]);
                 }
-                if (!kAligned && !inside(col, C)) mask8(v[u][k], col, C);
+                if (!edges.whole[k]) mask8(v[u][k], col, C);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s2 = __fadd2_rn(s2, v[u][k][j]);
             }
@@ -381,7 +399,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
                 float2 d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = __fadd2_rn(v[u][k][j], both(-mean[u]));
-                if (col >= at.end || !inside(col, C)) mask8(d, col, col >= at.end ? 0 : C);
+                if (!edges.full[k]) mask8(d, col, col >= at.end ? 0 : C);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q2 = __ffma2_rn(d[j], d[j], q2);
             }
@@ -447,7 +465,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
                     const float2 xhat = __fmul2_rn(__fadd2_rn(v[u][k][j], both(-mean[u])), both(rstd[u]));
                     y[j] = __ffma2_rn(xhat, gamma[k][j], beta[k][j]);
                 }
-                if (at.of(k) < at.end) store_row8<kAligned>(static_cast<TB*>(p.y) + r * C, y, at.of(k), C);
+                if (at.of(k) < at.end) store_row8(static_cast<TB*>(p.y) + r * C, y, at.of(k), C, edges.whole[k]);
             }
             if (lane == 0 && rank == 0) {
                 if (p.mean != nullptr) p.mean[r] = mean[u];
@@ -494,7 +512,7 @@ __device__ __forceinline__ void store_sums(float* to, const float2 (&f)[NV][4], 
 // to a CTA where they are short: one CTA per SM, so that there are few rows of partial sums.
 // kAdd: the residual form (dz, a branch gradient, dropout).
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
-__global__ void __launch_bounds__(G > 0 ? kWarpCta : kMaxCta, bwd_min_ctas(G, NV))
+__global__ void __launch_bounds__(G > 0 ? kWarpCta : kCluster ? 512 : max_cta(R), bwd_min_ctas(G, NV))
 norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vectors) {
     const int cluster = kCluster ? cluster_ctas : 1;
     extern __shared__ __align__(16) float smem[];
@@ -565,6 +583,7 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, group + static_cast<long long>(i) * R * groups);
 
+    const Edges<NV, kAligned> edges(at, C);
     float2 gamma[NV][4];
     load_params(gamma, p.gamma, p.param_type, C, at, 1.f);
     float2 sum_g[NV][4], sum_b[NV][4];
@@ -614,7 +633,7 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
                     float2 f[4], x[4];
                     read_slot<TB>(f, row + k * kBranch * threads + mine_b);
                     read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
-                    if (!kAligned && !inside(at.of(k), C)) {
+                    if (!edges.whole[k]) {
                         mask8(f, at.of(k), C);
                         mask8(x, at.of(k), C);
                     }
@@ -682,10 +701,10 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
                     for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], x[j]);
                 }
                 if (col < at.end) {
-                    store_row8<kAligned>(ds, g, col, C);
+                    store_row8(ds, g, col, C, edges.whole[k]);
                     if (has_branch) {
                         if (drop.threshold != 0) drop8(drop, g, static_cast<uint64_t>(r * C + col) >> 3);
-                        store_row8<kAligned>(db, g, col, C);
+                        store_row8(db, g, col, C, edges.whole[k]);
                     }
                 }
             }
@@ -747,26 +766,33 @@ struct Layout {
     int threads;        // of a CTA
 };
 
-// G > 0: a row to G lanes.  Else NV vectors a thread: one CTA of up to 512 threads to a row (several
+// G > 0: a row to G lanes.  Else NV vectors a thread: one CTA to a row (several
 // groups to a CTA only once there is a row for every SM), or a cluster of 2, 4 or 8 CTAs of up to
 // 256 threads, two of which an SM holds (one works while the other waits for its cluster), and of
 // up to 512 for the longest rows.  No layout: threads = 0.
-inline Layout layout(bool cluster, int G, int NV, long long rows, int vectors) {
+inline Layout layout(bool cluster, int G, int NV, int R, long long rows, int vectors) {
     if (G > 0) return {G, kWarpCta / G, 1, vectors, kWarpCta};
+    const int most = cluster ? 512 : max_cta(R);
     Layout l{};
     l.cluster = cluster ? 2 : 1;
-    while (cluster && l.cluster < kMaxCluster && vectors > l.cluster * NV * kMaxCta / 2) l.cluster *= 2;
-    if (vectors > l.cluster * NV * kMaxCta) return Layout{};
+    while (cluster && l.cluster < kMaxCluster && vectors > l.cluster * NV * most / 2) l.cluster *= 2;
+    if (vectors > l.cluster * NV * most) return Layout{};
     l.cta_vectors = (vectors + l.cluster - 1) / l.cluster;
     l.width = (l.cta_vectors + NV * 32 - 1) / (NV * 32) * 32;
-    l.per_cta = cluster ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(kMaxCta / l.width, rows / device_info().sm_count)));
+    l.per_cta = cluster ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(most / l.width, rows / device_info().sm_count)));
     l.threads = l.width * l.per_cta;
     return l;
 }
 
-// Rows beyond 1024 vectors, 512 threads of two, go to clusters.  (Shorter ones are faster in one CTA:
-// bf16 8192 x 8192 44 against 61 us forward, 70 against 80 backward.)
-constexpr int kCtaVectors = 2 * kMaxCta;
+// Rows that fill no CTA go to clusters.  (Those that do are faster in one: bf16 8192 x 8192 44 against
+// 61 us forward, 70 against 80 backward.)
+inline bool fits_cta(int vectors) { return vectors <= 2 * max_cta(1); }
+// Whether rows of this many vectors go through two at a time: unless one at a time makes so much
+// better use of the threads (bf16 8192 x 5120, groups of 320: XXX).
+inline bool in_pairs(int vectors) {
+    const int width = (vectors + 63) / 64 * 32;
+    return max_cta(2) >= width && max_cta(2) / width * 3 > max_cta(1) / width * 2;
+}
 // Rows that go through the forward pass together where several warps serve a row: two of a 16-bit
 // stream (the arithmetic and the generator need the pairs: bf16 16384 x 4096 with dropout 85 us, 98
 // with one), one of an fp32 stream (twice the bytes, whose copies in flight only get in the way of
@@ -833,7 +859,7 @@ cudaError_t launch_rows(K kern, KernelFacts& facts, const P& p, const Layout& l,
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 cudaError_t fwd_launch(const NormFwd& p, int vectors) {
     auto kern = norm_fwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
-    const Layout l = layout(kCluster, G, NV, p.rows, vectors);
+    const Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
     const size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TS) + (kAdd ? sizeof(TB) : 0));
     if (l.threads == 0 || bytes > kDynamicSmem) return cudaErrorNotSupported;
     static KernelFacts facts;
@@ -846,7 +872,7 @@ cudaError_t fwd_launch(const NormFwd& p, int vectors) {
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 cudaError_t bwd_launch(const NormBwd& p, int vectors) {
     auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
-    const Layout l = layout(kCluster, G, NV, p.rows, vectors);
+    const Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
     size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
     if (l.per_cta > 1) bytes = std::max(bytes, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
     if (l.threads == 0 || bytes > kDynamicSmem) return cudaErrorNotSupported;
@@ -869,8 +895,9 @@ cudaError_t fwd_rows_a(const NormFwd& p) {
     if (v <= 16) return fwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, 2, 2>(p, v);
     if (v <= 32) return fwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, 2, 2>(p, v);
     if (v <= 64) return fwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
-    if (v <= kCtaVectors) return fwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, kFwdRows<TS>, 2>(p, v);
-    return fwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, kFwdRows<TS>, 2>(p, v);
+    if (!fits_cta(v)) return fwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, kFwdRows<TS>, 2>(p, v);
+    if (in_pairs(v)) return fwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, kFwdRows<TS>, 2>(p, v);
+    return fwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 1, 2>(p, v);
 }
 
 template <typename TS, typename TB, bool kAdd>
@@ -887,11 +914,12 @@ cudaError_t bwd_rows_a(const NormBwd& p) {
     if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
     if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
     if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
-    if (v > kCtaVectors) {
-        const cudaError_t err = bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 2, 2>(p, v);
+    cudaError_t err = cudaErrorNotSupported;
+    if (!fits_cta(v)) {
+        err = bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 2, 2>(p, v);
         return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 1, 2>(p, v);
     }
-    const cudaError_t err = bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 2, 2>(p, v);
+    if (in_pairs(v)) err = bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 2, 2>(p, v);
     return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 1, 2>(p, v);
 }
 
