@@ -800,6 +800,13 @@ inline bool in_pairs(int vectors) {
 template <typename TS>
 constexpr int kFwdRows = sizeof(TS) == 2 ? 2 : 1;
 
+// Most shared memory of rows on their way, where one row goes through at a time: above it one stage
+// serves, not two.  (Copies beyond that only crowd the memory system.  Forward, fp32 branch and
+// stream: 8192 x 8192 186 us with two stages of 128 KB in all, 171 with one; fp32 stream with bf16
+// branches, 96 KB: 120 against 127.  Backward, fp32 stream with bf16 branches: 65536 x 1024 188 us with
+// 200 KB, 164 with 100; 16384 x 4096 174 us with 160 KB, 189 with 80.)
+constexpr size_t kFwdFlight = 112 * 1024, kBwdFlight = 176 * 1024;
+
 // Rows of a lane group that go through the backward pass together, in two stages: two of a 16-bit
 // stream, one of an fp32 stream or where edges are masked (80 registers hold no more; bf16
 // 524288 x 128: 66 us, 76 with one stage of two rows).
@@ -861,7 +868,7 @@ cudaError_t fwd_launch(const NormFwd& p, int vectors) {
     auto kern = norm_fwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
     const Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
     const size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TS) + (kAdd ? sizeof(TB) : 0));
-    if (l.threads == 0 || bytes > kDynamicSmem) return cudaErrorNotSupported;
+    if (l.threads == 0 || bytes > (G == 0 && R == 1 && S == 2 ? kFwdFlight : kDynamicSmem)) return cudaErrorNotSupported;
     static KernelFacts facts;
     const cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
@@ -875,7 +882,7 @@ cudaError_t bwd_launch(const NormBwd& p, int vectors) {
     const Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
     size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
     if (l.per_cta > 1) bytes = std::max(bytes, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
-    if (l.threads == 0 || bytes > kDynamicSmem) return cudaErrorNotSupported;
+    if (l.threads == 0 || bytes > (G == 0 && R == 1 && S == 2 ? kBwdFlight : kDynamicSmem)) return cudaErrorNotSupported;
     static KernelFacts facts;
     cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
@@ -888,6 +895,14 @@ cudaError_t bwd_launch(const NormBwd& p, int vectors) {
     return launch_norm_param_sum(p.partial, grid, p.C, p.dgamma, p.dbeta, p.stream);
 }
 
+template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster>
+cudaError_t fwd_rows_c(const NormFwd& p, int v) {
+    if constexpr (kFwdRows<TS> == 2)
+        if (kCluster || in_pairs(v)) return fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
+    const cudaError_t err = fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
+    return err != cudaErrorNotSupported ? err : fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 1>(p, v);
+}
+
 template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t fwd_rows_a(const NormFwd& p) {
     const int v = row_vectors(p.C);
@@ -895,9 +910,7 @@ cudaError_t fwd_rows_a(const NormFwd& p) {
     if (v <= 16) return fwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, 2, 2>(p, v);
     if (v <= 32) return fwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, 2, 2>(p, v);
     if (v <= 64) return fwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
-    if (!fits_cta(v)) return fwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, kFwdRows<TS>, 2>(p, v);
-    if (in_pairs(v)) return fwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, kFwdRows<TS>, 2>(p, v);
-    return fwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 1, 2>(p, v);
+    return fits_cta(v) ? fwd_rows_c<TS, TB, kAdd, kAligned, false>(p, v) : fwd_rows_c<TS, TB, kAdd, kAligned, true>(p, v);
 }
 
 template <typename TS, typename TB, bool kAdd>
@@ -906,7 +919,15 @@ cudaError_t fwd_rows(const NormFwd& p) {
 }
 
 // Two stages of two rows where they fit in shared memory (bf16 16384 x 4096: 67 us, with one row at
-// a time 76), else of one row.
+// a time 76), else of one row, else one stage of one row.
+template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster>
+cudaError_t bwd_rows_c(const NormBwd& p, int v) {
+    cudaError_t err = cudaErrorNotSupported;
+    if (kCluster || in_pairs(v)) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
+    if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
+    return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 1>(p, v);
+}
+
 template <typename TS, typename TB, bool kAdd, bool kAligned>
 cudaError_t bwd_rows_a(const NormBwd& p) {
     const int v = row_vectors(p.C);
@@ -914,13 +935,7 @@ cudaError_t bwd_rows_a(const NormBwd& p) {
     if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
     if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
     if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
-    cudaError_t err = cudaErrorNotSupported;
-    if (!fits_cta(v)) {
-        err = bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 2, 2>(p, v);
-        return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, true, 0, 2, 1, 2>(p, v);
-    }
-    if (in_pairs(v)) err = bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 2, 2>(p, v);
-    return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, false, 0, 2, 1, 2>(p, v);
+    return fits_cta(v) ? bwd_rows_c<TS, TB, kAdd, kAligned, false>(p, v) : bwd_rows_c<TS, TB, kAdd, kAligned, true>(p, v);
 }
 
 template <typename TS, typename TB, bool kAdd>
