@@ -161,14 +161,12 @@ __global__ void __launch_bounds__(kSumThreads) norm_param_sum_kernel(const float
     pdl_wait();
     if (j < 2LL * C) {
         const float* from = part + j;
-        int k = warp;
-        for (; k + 96 < count; k += 128) {
-            float t[4];
+        for (int k = warp; k < count; k += 8 * 32) {
+            float t[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = from[(k + 32 * i) * step];
-            s += (t[0] + t[1]) + (t[2] + t[3]);
+            for (int i = 0; i < 8; ++i) t[i] = k + 32 * i < count ? from[(k + 32 * i) * step] : 0.f;
+            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
         }
-        for (; k < count; k += 32) s += from[k * step];
     }
     sums[warp][lane] = s;
     __syncthreads();

@@ -15,6 +15,18 @@
 // and nothing is).  Groups advance by a multiple of 8 rows, so a group's shift never changes:
 // its columns (parameters, gradient sums) stay its own.  The dropout's blocks of 8 elements
 // coincide with these vectors.
+//
+// Copies.  cp.async of 16 bytes per thread into the thread group's own slots of shared memory, one or two
+// rows ahead: no registers wait for memory, and neither alignment of the row nor a barrier between
+// producer and consumer is needed.  (Rows loaded straight into registers reached 64 % of the
+// bandwidth with bf16, which leaves half the bytes in flight: 61 us forward for 16384 x 4096.)
+//
+// Measured (device time, GB300, of the bytes that must move at 6.79 TB/s): forward bf16 16384 x 4096
+// 43 us (93 %), fp32 16384 x 4096 81 us (98 %), fp32 200704 x 128 35 us (88 %); residual form, fp32
+// stream and bf16 branches with dropout, 16384 x 4096 forward 120 us (99 %), backward 174 to 178 us
+// (90 %); backward bf16 8192 x 4096 40 us (75 %, of which 6 us are the parameter gradients' second
+// kernel), bf16 200704 x 128 30 us (76 %).  Bound by memory from about 100 MB on; below that by the
+// two launches' and the copies' latency, a few microseconds.
 #pragma once
 
 #include <algorithm>
@@ -767,7 +779,7 @@ struct Layout {
 };
 
 // G > 0: a row to G lanes.  Else NV vectors a thread: one CTA to a row (several
-// groups to a CTA only once there is a row for every SM), or a cluster of 2, 4 or 8 CTAs of up to
+// groups to a CTA once there are more rows than SMs), or a cluster of 2, 4 or 8 CTAs of up to
 // 256 threads, two of which an SM holds (one works while the other waits for its cluster), and of
 // up to 512 for the longest rows.  No layout: threads = 0.
 inline Layout layout(bool cluster, int G, int NV, int R, long long rows, int vectors) {
@@ -779,7 +791,11 @@ inline Layout layout(bool cluster, int G, int NV, int R, long long rows, int vec
     if (vectors > l.cluster * NV * most) return Layout{};
     l.cta_vectors = (vectors + l.cluster - 1) / l.cluster;
     l.width = (l.cta_vectors + NV * 32 - 1) / (NV * 32) * 32;
-    l.per_cta = cluster ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(most / l.width, rows / device_info().sm_count)));
+    // as many groups as serve an SM's share of the rows in the fewest rounds, and no more (fp32 3136 x
+    // 1024, all tensors: 7 groups and two stages of shared memory 16 us, 10 groups and one 19)
+    const long long share = (rows + device_info().sm_count - 1) / device_info().sm_count;
+    const long long rounds = (share + most / l.width * R - 1) / (most / l.width * R);
+    l.per_cta = cluster ? 1 : static_cast<int>((share + rounds * R - 1) / (rounds * R));
     l.threads = l.width * l.per_cta;
     return l;
 }
@@ -788,7 +804,8 @@ inline Layout layout(bool cluster, int G, int NV, int R, long long rows, int vec
 // 61 us forward, 70 against 80 backward.)
 inline bool fits_cta(int vectors) { return vectors <= 2 * max_cta(1); }
 // Whether rows of this many vectors go through two at a time: unless one at a time makes so much
-// better use of the threads (bf16 8192 x 5120, groups of 320: XXX).
+// better use of the threads (bf16 8192 x 5003, groups of 320 threads: 50 us forward and 76 backward in
+// pairs, one group to a CTA; 42 and 66 one at a time, two groups).
 inline bool in_pairs(int vectors) {
     const int width = (vectors + 63) / 64 * 32;
     return max_cta(2) >= width && max_cta(2) / width * 3 > max_cta(1) / width * 2;
@@ -859,6 +876,9 @@ cudaError_t launch_rows(K kern, KernelFacts& facts, const P& p, const Layout& l,
     }
     if (p.C % 8 != 0) all = std::max(8LL, all / 8 * 8);
     *grid = static_cast<int>(std::min(want, all));
+    // what the kernels' accesses rest on: a group's rows all have one shift
+    const long long groups = static_cast<long long>(*grid) * l.per_cta;
+    if (p.C % 8 != 0 && groups % 8 != 0 && groups < p.rows) return cudaErrorInvalidConfiguration;
     launch.cfg.gridDim = dim3(static_cast<unsigned>(*grid) * static_cast<unsigned>(l.cluster));
     return cudaLaunchKernelEx(&launch.cfg, kern, p, l.width, l.cluster, l.cta_vectors);
 }
@@ -879,16 +899,26 @@ cudaError_t fwd_launch(const NormFwd& p, int vectors) {
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 cudaError_t bwd_launch(const NormBwd& p, int vectors) {
     auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
-    const Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
-    size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
+    Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
+    const size_t slot = 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
+    // A few rows go through one CTA, up to three to a group: it writes the parameter gradients itself,
+    // and the second kernel that sums partial ones (4 us, as long as three rows) is not needed.
+    const int groups = G > 0 ? l.per_cta : kCluster ? 1 : max_cta(R) / std::max(1, l.width);
+    // (Shifted rows of a group must be a multiple of 8 apart: lane groups are, others come in one go.)
+    const bool one_cta = p.partial != nullptr && !kCluster && p.rows <= (kAligned || G > 0 ? 3LL : 1LL) * groups;
+    if (G == 0 && one_cta) {
+        l.per_cta = static_cast<int>(std::min<long long>(groups, p.rows));
+        l.threads = l.width * l.per_cta;
+    }
+    size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * slot;
     if (l.per_cta > 1) bytes = std::max(bytes, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
     if (l.threads == 0 || bytes > (G == 0 && R == 1 && S == 2 ? kBwdFlight : kDynamicSmem)) return cudaErrorNotSupported;
     static KernelFacts facts;
     cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;
-    long long want = (p.rows + l.per_cta - 1) / l.per_cta;
-    const int most = p.partial != nullptr ? norm_bwd_partials(p.rows, p.C) : INT_MAX;
-    if (most < want) want = p.C % 8 != 0 ? std::max(8, most / 8 * 8) : most;   // (eights: see launch_rows)
+    long long want = one_cta ? 1 : (p.rows + l.per_cta - 1) / l.per_cta;
+    const int parts = p.partial != nullptr ? norm_bwd_partials(p.rows, p.C) : INT_MAX;
+    if (parts < want) want = p.C % 8 != 0 ? std::max(8, parts / 8 * 8) : parts;   // (eights: see launch_rows)
     int grid = 0;
     err = launch_rows(kern, facts, p, l, want, bytes, &grid);
     if (err != cudaSuccess || p.partial == nullptr || grid == 1) return err;
