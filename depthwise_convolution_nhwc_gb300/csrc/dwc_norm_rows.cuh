@@ -132,9 +132,8 @@ __device__ __forceinline__ void send_remote(float* p, float v, uint64_t* bar, ui
         "r"(smem_addr(bar)), "r"(rank), "r"(__float_as_uint(v))
         : "memory");
 }
-// Wait for a phase of the exchange, no longer than the limit: then the status word says so and the
-// kernel goes on (with wrong sums) to its end.
-__device__ __forceinline__ void await_exchange(uint64_t* bar, uint32_t phase, unsigned long long limit_ns, unsigned int* status) {
+// Wait for a phase of the exchange, no longer than the limit; false if it ran out.
+__device__ __forceinline__ bool await_exchange(uint64_t* bar, uint32_t phase, unsigned long long limit_ns, unsigned int* status) {
     const unsigned long long limit = limit_ns != 0 ? limit_ns : kWaitLimitNs, t0 = global_ns();
     for (;;) {
         uint32_t done;
@@ -145,10 +144,20 @@ __device__ __forceinline__ void await_exchange(uint64_t* bar, uint32_t phase, un
             : "=r"(done)
             : "r"(smem_addr(bar)), "r"(phase)
             : "memory");
-        if (done) return;
+        if (done) return true;
         if (global_ns() - t0 > limit) break;
     }
     record_status(status, DWC_DEVSTAT_TIMEOUT);
+    return false;
+}
+// The end of a cluster's kernel.  A thread whose wait ran out (`lost`) has sent and awaited nothing since
+// and goes on with wrong sums; its CTA stays until what was on its way to it must have come.
+__device__ __forceinline__ void leave_cluster(bool lost) {
+    cluster_barrier();
+    if (!lost) return;
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 100000ull) {
+    }
 }
 // A warp's value to the place in the exchange where its row's threads find it.
 template <bool kCluster>
@@ -359,6 +368,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
     const float mine_inv = mine > 0 ? 1.f / static_cast<float>(mine) : 0.f;
     int parity = 0, stage = 0;
     uint32_t phase = 0;                 // of the exchange barrier that is next in use
+    bool lost = false;                  // a wait of this thread ran out
 
     const long long step = static_cast<long long>(R) * groups;
     // (the lane groups of a warp stay together: the warp goes on while its first group has a row, and
@@ -423,9 +433,9 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
         if constexpr (kCta) {
             // the part of a warp that holds row u's sums merges that row over the warps (and CTAs)
             float(&e)[2][kWarps * (kCluster ? kMaxCluster : 1)] = exchange[parity][sub / kPart];
-            if (kCluster && threadIdx.x == 0)
+            if (kCluster && threadIdx.x == 0 && !lost)
                 mbar_arrive_expect_tx(&arrived[parity], R * 2 * sizeof(float) * warps * cluster);
-            if (sub % kPart == 0) {
+            if (sub % kPart == 0 && !lost) {
                 publish<kCluster>(&e[0][place], m, &arrived[parity], cluster);
                 publish<kCluster>(&e[1][place], t, &arrived[parity], cluster);
             }
@@ -440,7 +450,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
                 const float d = em - m;
                 t = peer > 0.f ? fmaf(peer * d, d, eq) : 0.f;
             } else {
-                await_exchange(&arrived[parity], phase, p.wait_ns, p.status);
+                if (!lost) lost = !await_exchange(&arrived[parity], phase, p.wait_ns, p.status);
                 m = 0.f;
                 for (int w = sub % kPart; w < places; w += kPart)
                     if (counts[w] > 0.f) m = fmaf(counts[w], e[0][w], m);
@@ -486,7 +496,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
         }
     }
     copy_wait<0>();
-    if (kCluster) cluster_barrier();   // (also where a wait gave up: nothing is on its way to a CTA that has ended)
+    if (kCluster) leave_cluster(lost);
 }
 
 // ------------------------------------------------------------------------------ backward
@@ -609,6 +619,7 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
     const int from_place = local * warps;
     int parity = 0, stage = 0;
     uint32_t phase = 0;                 // of the exchange barrier that is next in use
+    bool lost = false;                  // a wait of this thread ran out
     float next_mean[R], next_rstd[R];
     auto fetch_stats = [&](long long r0) {
 #pragma unroll
@@ -668,15 +679,15 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
         if constexpr (kCta) {
             // the part of a warp that holds sum q adds it up over the warps (and CTAs)
             float(&e)[kWarps * (kCluster ? kMaxCluster : 1)] = exchange[parity][sub / kPart];
-            if (kCluster && threadIdx.x == 0)
+            if (kCluster && threadIdx.x == 0 && !lost)
                 mbar_arrive_expect_tx(&arrived[parity], 2 * R * sizeof(float) * warps * cluster);
-            if (sub % kPart == 0) publish<kCluster>(&e[place], t, &arrived[parity], cluster);
+            if (sub % kPart == 0 && !lost) publish<kCluster>(&e[place], t, &arrived[parity], cluster);
             t = 0.f;
             if constexpr (!kCluster) {
                 group_barrier(1 + local, width);
                 for (int w = sub % kPart; w < warps; w += kPart) t += e[from_place + w];
             } else {
-                await_exchange(&arrived[parity], phase, p.wait_ns, p.status);
+                if (!lost) lost = !await_exchange(&arrived[parity], phase, p.wait_ns, p.status);
                 for (int w = sub % kPart; w < cluster * kWarps; w += kPart)
                     if (w % kWarps < warps) t += e[w];
             }
@@ -726,7 +737,7 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
         if (++stage == S) stage = 0;
     }
     copy_wait<0>();
-    if (kCluster) cluster_barrier();   // (also where a wait gave up: nothing is on its way to a CTA that has ended)
+    if (kCluster) leave_cluster(lost);
     if (p.dgamma == nullptr && p.dbeta == nullptr) return;
     // a lone CTA (or cluster) has the whole sums, others write a row of partial ones
     const bool alone = gridDim.x == cluster;

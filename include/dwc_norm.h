@@ -20,6 +20,12 @@
  * No call allocates device memory; the backward passes take a caller workspace for the partial
  * sums of the parameter gradients.
  *
+ * Kernels: rows of up to 65536 channels whose tensors are aligned to 8 elements and whose row strides
+ * are congruent to C modulo 8 (dense tensors from aligned bases are, for any C) run on kernels that
+ * read every input once; other views and wider rows run on general kernels (same results within
+ * the rounding of another order of sums, slower).  Rows beyond 10240 channels use clusters of CTAs
+ * whose waits have the limit of dwc_set_wait_limit_ns and report to dwc_device_status.
+ *
  * Dropout: p in [0, 1] is held as q = floor(p * 65536 + 0.5) / 65536 and kept values are scaled
  * by 1 / (1 - q), so the expected value is exact.  Element i of the tensor (i = row * C + channel,
  * whatever the row stride) is kept where h(i) >= q * 65536; h(i) is the 16-bit value i % 8 (of

@@ -21,6 +21,8 @@ EPS = 1e-5
 def _lib():
     dwc.build()
     dwc.load_library()
+    yield
+    assert dwc.device_status() == 0, "a kernel reported a timed-out wait"
 
 
 def d(t):
