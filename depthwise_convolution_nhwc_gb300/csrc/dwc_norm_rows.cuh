@@ -4,7 +4,7 @@
 // Both passes are bound by memory: a row is read once, reduced in registers or shared memory and
 // written once, 8 elements per access.  A group of threads serves one row:
 //   rows of up to 8, 16 and 32 vectors: G = 8, 16, 32 lanes, one vector each; up to 64 vectors: a
-//   warp with 2; up to 1024: several warps with 2 vectors a thread (up to 512 threads); beyond
+//   warp with 2; up to 1280: several warps with 2 vectors a thread (up to 640 threads); beyond
 //   that a cluster of 2, 4 or 8 CTAs, each with a share of the columns, which exchange their sums
 //   through distributed shared memory.
 //
@@ -25,7 +25,7 @@
 // 43 us (93 %), fp32 16384 x 4096 81 us (98 %), fp32 200704 x 128 35 us (88 %); residual form, fp32
 // stream and bf16 branches with dropout, 16384 x 4096 forward 120 us (99 %), backward 174 to 178 us
 // (90 %); backward bf16 8192 x 4096 40 us (75 %, of which 6 us are the parameter gradients' second
-// kernel), bf16 200704 x 128 30 us (76 %).  Bound by memory from about 100 MB on; below that by the
+// kernel), bf16 200704 x 128 29 us (79 %).  Bound by memory from about 100 MB on; below that by the
 // two launches' and the copies' latency, a few microseconds.
 #pragma once
 
@@ -803,7 +803,7 @@ inline Layout layout(bool cluster, int G, int NV, int R, long long rows, int vec
     l.cta_vectors = (vectors + l.cluster - 1) / l.cluster;
     l.width = (l.cta_vectors + NV * 32 - 1) / (NV * 32) * 32;
     // as many groups as serve an SM's share of the rows in the fewest rounds, and no more (fp32 3136 x
-    // 1024, all tensors: 7 groups and two stages of shared memory 16 us, 10 groups and one 19)
+    // 1024, all tensors: 7 groups and two stages of shared memory 17 us, 10 groups and one 19)
     const long long share = (rows + device_info().sm_count - 1) / device_info().sm_count;
     const long long rounds = (share + most / l.width * R - 1) / (most / l.width * R);
     l.per_cta = cluster ? 1 : static_cast<int>((share + rounds * R - 1) / (rounds * R));
@@ -821,13 +821,6 @@ inline bool in_pairs(int vectors) {
     const int width = (vectors + 63) / 64 * 32;
     return max_cta(2) >= width && max_cta(2) / width * 3 > max_cta(1) / width * 2;
 }
-// Rows that go through the forward pass together where several warps serve a row: two of a 16-bit
-// stream (the arithmetic and the generator need the pairs: bf16 16384 x 4096 with dropout 85 us, 98
-// with one), one of an fp32 stream (twice the bytes, whose copies in flight only get in the way of
-// the stores: fp32 16384 x 4096 87 us, 93 with two).
-template <typename TS>
-constexpr int kFwdRows = sizeof(TS) == 2 ? 2 : 1;
-
 // Most shared memory of rows on their way, where one row goes through at a time: above it one stage
 // serves, not two.  (Copies beyond that only crowd the memory system.  Forward, fp32 branch and
 // stream: 8192 x 8192 186 us with two stages of 128 KB in all, 171 with one; fp32 stream with bf16
@@ -936,15 +929,26 @@ cudaError_t bwd_launch(const NormBwd& p, int vectors) {
     return launch_norm_param_sum(p.partial, grid, p.C, p.dgamma, p.dbeta, p.stream);
 }
 
+// Rows of several warps: pairs in two stages for 16-bit streams (the arithmetic and the generator need
+// them: bf16 16384 x 4096 with dropout 85 us, 98 with one row at a time; they always fit), one row at a
+// time in two stages or one for fp32 streams (twice the bytes, and copies in flight beyond them only
+// get in the way of the stores: fp32 16384 x 4096 81 us, 93 in pairs).
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster>
 cudaError_t fwd_rows_c(const NormFwd& p, int v) {
-    // (a cluster's exchange is paid per pair of rows where pairs go through, whatever the type)
-    cudaError_t err = cudaErrorNotSupported;
-    if constexpr (kCluster || kFwdRows<TS> == 2)
-        if (kCluster || in_pairs(v)) err = fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
-    if (err != cudaErrorNotSupported) return err;
-    err = fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
-    return err != cudaErrorNotSupported ? err : fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 1>(p, v);
+    if constexpr (sizeof(TS) == 2) {
+        if constexpr (!kCluster)
+            if (!in_pairs(v)) return fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
+        return fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
+    } else {
+        // (a cluster's exchange is paid per pair of rows where pairs go through: fp32 4096 x 16384 102 us, 127
+        // with one row at a time)
+        if constexpr (kCluster) {
+            const cudaError_t err = fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
+            if (err != cudaErrorNotSupported) return err;
+        }
+        const cudaError_t err = fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
+        return err != cudaErrorNotSupported ? err : fwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 1>(p, v);
+    }
 }
 
 template <typename TS, typename TB, bool kAdd, bool kAligned>
@@ -962,14 +966,16 @@ cudaError_t fwd_rows(const NormFwd& p) {
     return p.C % 8 == 0 ? fwd_rows_a<TS, TB, kAdd, true>(p) : fwd_rows_a<TS, TB, kAdd, false>(p);
 }
 
-// Two stages of two rows where they fit in shared memory (bf16 16384 x 4096: 67 us, with one row at
-// a time 76), else of one row, else one stage of one row.
+// As forward; fp32 rows go in pairs where those fit (bf16 16384 x 4096: 67 us, with one row at a time 76).
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster>
 cudaError_t bwd_rows_c(const NormBwd& p, int v) {
     cudaError_t err = cudaErrorNotSupported;
     if (kCluster || in_pairs(v)) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
-    if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
-    return err != cudaErrorNotSupported ? err : bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 1>(p, v);
+    if constexpr (sizeof(TS) == 4 || !kCluster)
+        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 2>(p, v);
+    if constexpr (sizeof(TS) == 4)
+        if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 1, 1>(p, v);
+    return err;
 }
 
 template <typename TS, typename TB, bool kAdd, bool kAligned>
@@ -978,7 +984,7 @@ cudaError_t bwd_rows_a(const NormBwd& p) {
     if (v <= 8) return bwd_launch<TS, TB, kAdd, kAligned, false, 8, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
     if (v <= 16) return bwd_launch<TS, TB, kAdd, kAligned, false, 16, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
     if (v <= 32) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 1, kBwdLaneRows<TS, kAligned>, 2>(p, v);
-    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 2, 1>(p, v);
+    if (v <= 64) return bwd_launch<TS, TB, kAdd, kAligned, false, 32, 2, 1, 2>(p, v);
     return fits_cta(v) ? bwd_rows_c<TS, TB, kAdd, kAligned, false>(p, v) : bwd_rows_c<TS, TB, kAdd, kAligned, true>(p, v);
 }
 
