@@ -274,7 +274,7 @@ constexpr int fwd_min_ctas(int G, int NV) { return G == 0 ? 1 : NV == 1 ? 3 : 2;
 // barrier per R rows, and no cancellation however far the mean lies from zero.
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 __global__ void __launch_bounds__(G > 0 ? kWarpCta : kCluster ? 512 : max_cta(R), fwd_min_ctas(G, NV))
-norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vectors) {
+norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vectors, int) {
     const int cluster = kCluster ? cluster_ctas : 1;
     extern __shared__ __align__(16) float smem[];
     __shared__ float exchange[2][R][2][kWarps * (kCluster ? kMaxCluster : 1)], counts[kWarps * (kCluster ? kMaxCluster : 1)];
@@ -525,6 +525,54 @@ __device__ __forceinline__ void store_sums(float* to, const float2 (&f)[NV][4], 
     }
 }
 
+// dgamma and dbeta of a call of few rows: each CTA adds up a share of the columns over all rows, whose dy
+// and z are read once more (from L2).  No partial sums, so no second kernel: a launch of the host and
+// some of the GPU's time less (bf16 64 x 4096: 6.1 us and 6.8 call to call, with partial sums 7.9 and
+// 9.1).  32 columns are a chunk; `slots` warps share the rows of one, 8 rows at a time in flight, and a
+// CTA's warps work on warps / slots chunks together.  `red` holds 32 pairs a warp.
+template <typename TS, typename TB>
+__device__ __forceinline__ void column_sums(const NormBwd& p, float2* red, int threads, int slots) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, together = (threads >> 5) / slots;
+    const int chunks = (p.C + 31) / 32, share = (chunks + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int first = min(chunks, static_cast<int>(blockIdx.x) * share), last = min(chunks, first + share);
+    const int slot = warp % slots, mine = warp / slots;
+    for (int k = first; k < last; k += together) {
+        const int c = (k + mine) * 32 + lane;
+        const bool in = mine < together && k + mine < last && c < p.C;
+        float2 s = both(0.f);
+        if (in) {
+            for (long long r0 = slot; r0 < p.rows; r0 += 8 * slots) {
+                float f[8], x[8], m[8], rs[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const long long r = r0 + i * slots;
+                    const bool live = r < p.rows;
+                    f[i] = live ? to_f32(static_cast<const TB*>(p.dy)[r * p.ld_dy + c]) : 0.f;
+                    x[i] = live ? to_f32(static_cast<const TS*>(p.z)[r * p.ld_z + c]) : 0.f;
+                    m[i] = live ? p.mean[r] : 0.f;
+                    rs[i] = live ? p.rstd[r] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s.x = fmaf(f[i], (x[i] - m[i]) * rs[i], s.x);
+                    s.y += f[i];
+                }
+            }
+        }
+        __syncthreads();              // red is free: nothing reads the rows or an earlier result any more
+        red[warp * 32 + lane] = s;
+        __syncthreads();
+        if (slot == 0 && in) {
+            for (int w = 1; w < slots; ++w) {
+                s.x += red[(warp + w) * 32 + lane].x;
+                s.y += red[(warp + w) * 32 + lane].y;
+            }
+            if (p.dgamma != nullptr) p.dgamma[c] = s.x;
+            if (p.dbeta != nullptr) p.dbeta[c] = s.y;
+        }
+    }
+}
+
 // Each thread keeps the sums of dy * xhat and dy of its columns in registers over all rows of its
 // group; at the end the groups of a CTA are added in order and the CTA writes one row of partial
 // sums.  The sums and gamma take the registers, so the rows wait in
@@ -535,7 +583,7 @@ __device__ __forceinline__ void store_sums(float* to, const float2 (&f)[NV][4], 
 // kAdd: the residual form (dz, a branch gradient, dropout).
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
 __global__ void __launch_bounds__(G > 0 ? kWarpCta : kCluster ? 512 : max_cta(R), bwd_min_ctas(G, NV))
-norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vectors) {
+norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vectors, int row_slots) {
     const int cluster = kCluster ? cluster_ctas : 1;
     extern __shared__ __align__(16) float smem[];
     __shared__ float exchange[2][2 * R][kWarps * (kCluster ? kMaxCluster : 1)];
@@ -739,8 +787,13 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
     copy_wait<0>();
     if (kCluster) leave_cluster(lost);
     if (p.dgamma == nullptr && p.dbeta == nullptr) return;
-    // a lone CTA (or cluster) has the whole sums, others write a row of partial ones
+    // a lone CTA (or cluster) has the whole sums, others write a row of partial ones, or where a call of
+    // few rows has no place for them each adds up a share of the columns
     const bool alone = gridDim.x == cluster;
+    if (!alone && p.partial == nullptr) {
+        column_sums<TS, TB>(p, reinterpret_cast<float2*>(smem), threads, row_slots);
+        return;
+    }
     float* part = alone ? nullptr : p.partial + static_cast<size_t>(blockIdx.x / cluster) * 2 * C;
     float *to_g = alone ? p.dgamma : part, *to_b = alone ? p.dbeta : part + C;
     if (per_cta == 1) {
@@ -787,6 +840,7 @@ struct Layout {
     int cluster;        // CTAs that share a row
     int cta_vectors;    // vectors of a row in one of them
     int threads;        // of a CTA
+    int slots = 0;      // warps that share a column's rows (column_sums), 0: partial sums
 };
 
 // G > 0: a row to G lanes.  Else NV vectors a thread: one CTA to a row (several
@@ -827,6 +881,17 @@ inline bool in_pairs(int vectors) {
 // branches, 96 KB: 120 against 127.  Backward, fp32 stream with bf16 branches: 65536 x 1024 188 us with
 // 200 KB, 164 with 100; 16384 x 4096 174 us with 160 KB, 189 with 80.)
 constexpr size_t kFwdFlight = 112 * 1024, kBwdFlight = 176 * 1024;
+
+// Warps that share the rows of a column (column_sums) in a call of `ctas` CTAs of `threads` threads, or 0
+// where that would take more than 4 rounds of loads (about 1 us each; partial sums cost as much and a launch).
+inline int column_slots(long long rows, int C, int threads, long long ctas) {
+    if (rows > 256) return 0;
+    int slots = 1;
+    while (slots * 2 <= threads / 32 && slots * 8 < rows) slots *= 2;
+    const int together = threads / 32 / slots, chunks = (C + 31) / 32;
+    const long long share = (chunks + ctas - 1) / ctas;
+    return (share + together - 1) / together * ((rows + 8 * slots - 1) / (8 * slots)) <= 4 ? slots : 0;
+}
 
 // Rows of a lane group that go through the backward pass together, in two stages: two of a 16-bit
 // stream, one of an fp32 stream or where edges are masked (80 registers hold no more; bf16
@@ -884,7 +949,7 @@ cudaError_t launch_rows(K kern, KernelFacts& facts, const P& p, const Layout& l,
     const long long groups = static_cast<long long>(*grid) * l.per_cta;
     if (p.C % 8 != 0 && groups % 8 != 0 && groups < p.rows) return cudaErrorInvalidConfiguration;
     launch.cfg.gridDim = dim3(static_cast<unsigned>(*grid) * static_cast<unsigned>(l.cluster));
-    return cudaLaunchKernelEx(&launch.cfg, kern, p, l.width, l.cluster, l.cta_vectors);
+    return cudaLaunchKernelEx(&launch.cfg, kern, p, l.width, l.cluster, l.cta_vectors, l.slots);
 }
 
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
@@ -901,22 +966,33 @@ cudaError_t fwd_launch(const NormFwd& p, int vectors) {
 }
 
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>
-cudaError_t bwd_launch(const NormBwd& p, int vectors) {
+cudaError_t bwd_launch(const NormBwd& call, int vectors) {
+    NormBwd p = call;
     auto kern = norm_bwd_rows_kernel<TS, TB, kAdd, kAligned, kCluster, G, NV, R, S>;
     Layout l = layout(kCluster, G, NV, R, p.rows, vectors);
+    if (l.threads == 0) return cudaErrorNotSupported;
     const size_t slot = 8 * (sizeof(TB) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
     // A few rows go through one CTA, up to three to a group: it writes the parameter gradients itself,
     // and the second kernel that sums partial ones (4 us, as long as three rows) is not needed.
-    const int groups = G > 0 ? l.per_cta : kCluster ? 1 : max_cta(R) / std::max(1, l.width);
+    const int groups = G > 0 ? l.per_cta : kCluster ? 1 : max_cta(R) / l.width;
     // (Shifted rows of a group must be a multiple of 8 apart: lane groups are, others come in one go.)
     const bool one_cta = p.partial != nullptr && !kCluster && p.rows <= (kAligned || G > 0 ? 3LL : 1LL) * groups;
-    if (G == 0 && one_cta) {
-        l.per_cta = static_cast<int>(std::min<long long>(groups, p.rows));
-        l.threads = l.width * l.per_cta;
+    if (p.partial != nullptr && !kCluster && !one_cta) {
+        // up to 256 rows: the columns' sums in the same kernel, with more groups to a CTA where that
+        // takes fewer rounds
+        l.slots = column_slots(p.rows, p.C, l.threads, (p.rows + l.per_cta - 1) / l.per_cta);
+        if (G == 0 && l.slots == 0 && p.rows <= 256) {
+            const int most = static_cast<int>(std::min<long long>(groups, p.rows));
+            l.slots = column_slots(p.rows, p.C, l.width * most, (p.rows + most - 1) / most);
+            if (l.slots != 0) l.per_cta = most;
+        }
+        if (l.slots != 0) p.partial = nullptr;
     }
+    if (G == 0 && one_cta) l.per_cta = static_cast<int>(std::min<long long>(groups, p.rows));
+    if (G == 0) l.threads = l.width * l.per_cta;
     size_t bytes = static_cast<size_t>(S * R * NV * l.threads) * slot;
     if (l.per_cta > 1) bytes = std::max(bytes, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
-    if (l.threads == 0 || bytes > (G == 0 && R == 1 && S == 2 ? kBwdFlight : kDynamicSmem)) return cudaErrorNotSupported;
+    if (bytes > (G == 0 && R == 1 && S == 2 ? kBwdFlight : kDynamicSmem)) return cudaErrorNotSupported;
     static KernelFacts facts;
     cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;

@@ -167,6 +167,15 @@ def test_row_counts(rows, C):
     check_add(s, "f32", "bf16", p=0.3)
 
 
+@pytest.mark.parametrize("rows", [11, 31, 32, 64, 100, 255, 256, 257])
+@pytest.mark.parametrize("C", [8, 40, 65, 513, 1000, 4099, 5120, 8200])
+def test_few_rows(rows, C):
+    """Around the rules for calls of few rows: one CTA, columns added up in the row kernel, partial sums."""
+    s = inputs(rows, C, "bf16", "bf16", seed=rows + C)
+    check_ln(s, "bf16", "bf16")
+    check_add(s, "bf16", "bf16", p=0.3, dz=rows % 2 == 0)
+
+
 @pytest.mark.parametrize("gdt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("gamma,beta", [(True, True), (True, False), (False, True), (False, False)])
 @pytest.mark.parametrize("C", [100, 2048])
@@ -403,8 +412,9 @@ def test_back_to_back_calls_see_each_other():
     assert torch.equal(x, y)
 
 
-def test_graph_draws_new_masks_as_its_step_advances():
-    s = inputs(64, 1024, "bf16", "bf16", seed=3)
+@pytest.mark.parametrize("C", [1024, 1001, 12288])
+def test_graph_draws_new_masks_as_its_step_advances(C):
+    s = inputs(64, C, "bf16", "bf16", seed=3)
     step = torch.zeros(1, dtype=torch.int64, device="cuda")
     stats = dwc.layer_norm_fwd(s["z"], stats=True)[1:]
 
