@@ -23,8 +23,8 @@
 //
 // Measured (device time, GB300, of the bytes that must move at 6.79 TB/s): forward bf16 16384 x 4096
 // 43 us (93 %), fp32 16384 x 4096 81 us (98 %), fp32 200704 x 128 35 us (88 %); residual form, fp32
-// stream and bf16 branches with dropout, 16384 x 4096 forward 120 us (99 %), backward 174 to 178 us
-// (90 %); backward bf16 8192 x 4096 40 us (75 %, of which 6 us are the parameter gradients' second
+// stream and bf16 branches with dropout, 16384 x 4096 forward 120 us (99 %), backward 174 us
+// (91 %); backward bf16 8192 x 4096 40 us (75 %, of which 6 us are the parameter gradients' second
 // kernel), bf16 200704 x 128 29 us (79 %).  Bound by memory from about 100 MB on; below that by the
 // two launches' and the copies' latency, a few microseconds.
 #pragma once
@@ -1045,6 +1045,11 @@ cudaError_t fwd_rows(const NormFwd& p) {
 // As forward; fp32 rows go in pairs where those fit (bf16 16384 x 4096: 67 us, with one row at a time 76).
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster>
 cudaError_t bwd_rows_c(const NormBwd& p, int v) {
+    // the residual form on an fp32 stream, where one vector a thread fills most of a CTA: one group to an SM
+    // with three rows on their way, instead of two groups with two each (fp32 stream, bf16 branches:
+    // 16384 x 4096 174 against 180 us, 13107 x 5120 168 against 182; fp32 16384 x 4096 207 against 217)
+    if constexpr (sizeof(TS) == 4 && kAdd && !kCluster)
+        if (v > 480 && v <= max_cta(1)) return bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 1, 1, 3>(p, v);
     cudaError_t err = cudaErrorNotSupported;
     if (kCluster || in_pairs(v)) err = bwd_launch<TS, TB, kAdd, kAligned, kCluster, 0, 2, 2, 2>(p, v);
     if constexpr (sizeof(TS) == 4 || !kCluster)
