@@ -159,6 +159,12 @@ def test_many_rows(rows, C, pair):
     check_add(s, *pair, p=0.1)
 
 
+@pytest.mark.parametrize("p", [1.0, 0.9999, 2.0 ** -16, 2.0 ** -18])
+@pytest.mark.parametrize("C", [40, 1001, 2048])
+def test_extreme_probabilities_of_the_residual_form(C, p):
+    check_add(inputs(37, C, "f32", "f32", seed=C), "f32", "f32", p=p)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 3, 5, 8, 9, 151, 152, 153, 304, 305, 609])
 @pytest.mark.parametrize("C", [72, 1001, 2048])
 def test_row_counts(rows, C):
