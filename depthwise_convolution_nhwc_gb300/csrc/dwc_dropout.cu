@@ -1,4 +1,4 @@
-// dwc_dropout.cu -- dropout of dense tensors, 8 elements per access.
+// dwc_dropout.cu -- dropout of dense tensors and of rows with an aligned stride, 8 elements per access.
 //
 // y = keep ? x * scale : 0, the mask drawn in registers (one Philox block per 8 elements, see
 // dwc_norm_device.cuh).  Bound by memory: x is read once and y written once; the generator's 20
@@ -14,8 +14,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_vec_kernel(const T* x, T* y, long long n, Dropout d) {
+// kStrided: rows of `row_vecs` vectors, ld elements apart in x (dense in y); the vector's place costs a
+// division, which the copies hide.
+template <typename T, bool kStrided>
+__global__ void __launch_bounds__(kThreads) dropout_vec_kernel(const T* x, T* y, long long n, long long ld, int row_vecs,
+                                                               Dropout d) {
     pdl_trigger();
     pdl_wait();
     DropState drop;
@@ -27,7 +30,13 @@ __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(const T* x, T* y,
     for (int k = 0; k < kVecs; ++k) {
         const long long i = first + k * kThreads;
         raw[k].zero();
-        if (i < vecs) raw[k].load(x + 8 * i);
+        if (i >= vecs) continue;
+        if constexpr (kStrided) {
+            const long long r = i / row_vecs;
+            raw[k].load(x + r * ld + 8 * (i - r * row_vecs));
+        } else {
+            raw[k].load(x + 8 * i);
+        }
     }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
@@ -39,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(const T* x, T* y,
         Vec8<T>::store(y + 8 * i, f);
     }
     // the last n % 8 elements
-    if (blockIdx.x == 0 && threadIdx.x < n - 8 * vecs) {
+    if (!kStrided && blockIdx.x == 0 && threadIdx.x < n - 8 * vecs) {
         const long long i = 8 * vecs + threadIdx.x;
         const float v = to_f32(x[i]);
         store_out(y + i, drop.threshold != 0 ? drop.one(v, i) : v);
@@ -51,8 +60,11 @@ cudaError_t dropout_t(const DropoutCall& p) {
     const long long n = p.rows * p.C;
     const long long grid = std::max(1LL, (n / 8 + kThreads * kVecs - 1) / (kThreads * kVecs));
     if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
-    return launch_pdl(dropout_vec_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream,
-                      static_cast<const T*>(p.x), static_cast<T*>(p.y), n, p.drop);
+    const bool strided = p.ld_x != p.C && p.rows > 1;
+    if (strided && p.C % 8 != 0) return cudaErrorNotSupported;
+    return launch_pdl(strided ? dropout_vec_kernel<T, true> : dropout_vec_kernel<T, false>,
+                      dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, static_cast<const T*>(p.x),
+                      static_cast<T*>(p.y), n, p.ld_x, std::max(1, p.C / 8), p.drop);
 }
 
 }  // namespace

@@ -184,7 +184,7 @@ dwc_status_t dropout(const void* x, long long ldx, void* y, long long rows, int 
     c.C = C;
     c.type = dtype;
     c.stream = stream;
-    if ((ldx == C || rows == 1) && !misaligned(x, 8 * bytes) && !misaligned(y, 8 * bytes)) {
+    if (lines_up(x, bytes, ldx, rows, C) && lines_up(y, bytes, C, rows, C)) {
         const cudaError_t err = launch_dropout_vec(c);
         if (err != cudaErrorNotSupported) return map_cuda(err);
     }

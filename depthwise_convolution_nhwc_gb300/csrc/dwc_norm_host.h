@@ -82,7 +82,8 @@ cudaError_t launch_norm_fwd_general(const NormFwd& p);
 cudaError_t launch_norm_bwd_general(const NormBwd& p);
 cudaError_t launch_dropout_general(const DropoutCall& p);
 
-// Dropout of dense rows from bases aligned to 8 elements.
+// Dropout from bases aligned to 8 elements: dense rows, or rows of a multiple of 8 channels whose stride is
+// one too; cudaErrorNotSupported for others.
 cudaError_t launch_dropout_vec(const DropoutCall& p);
 
 // Rows in registers (aligned tensors, up to 65536 channels), one file per

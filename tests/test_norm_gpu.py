@@ -322,6 +322,11 @@ def test_dropout_of_views_counts_logical_elements():
     t = torch.randn(50, 200, device="cuda")
     for v in (t[:, 3:100], t[::2, 8:136], t[:, 7:8]):
         assert torch.equal(dwc.dropout_fwd(v, 0.3, 5), dwc.dropout_fwd(v.contiguous(), 0.3, 5))
+    t = torch.randn(301, 1072, device="cuda")
+    for dt in DT.values():
+        u = t.to(dt)
+        for v in (u[:, :8], u[:, 16:1064], u[3:, 64:128], u[::3, 8:1048], u[7:8, 8:64], u[:, 8:13], u[:, :1071]):
+            assert torch.equal(dwc.dropout_fwd(v, 0.3, 5, 2), dwc.dropout_fwd(v.contiguous(), 0.3, 5, 2))
 
 
 def test_offsets_past_32_bits():
