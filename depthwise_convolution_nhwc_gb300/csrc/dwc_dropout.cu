@@ -15,7 +15,8 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 4;
 
 // kStrided: rows of `row_vecs` vectors, ld elements apart in x (dense in y); the vector's place costs a
-// division, which the copies hide.
+// division, which the copies nearly hide: bf16 8192 x 8192 of 16384 channels takes 54 us, dense 50 us, and
+// the general kernel, one element at a time, 300 us on the strided rows (each with a flushed L2).
 template <typename T, bool kStrided>
 __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(const T* x, T* y, long long n, long long ld, int row_vecs,
                                                                Dropout d) {
