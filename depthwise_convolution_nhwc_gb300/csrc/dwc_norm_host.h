@@ -77,6 +77,12 @@ struct DropoutCall {
     cudaStream_t stream;
 };
 
+// First element, counted from a row's start, that a 16-byte copy of the granule of `n` elements at column `col` names
+// in global memory.  A granule past the row's `end` is a copy of no bytes (zeros), but the copy's address has to
+// be aligned all the same, and the start of a shifted row is not: it names the boundary at or before that start
+// (col is minus the row's shift modulo n, and the tensor's base lies on a boundary).
+constexpr int copy_column(int col, int end, int n) { return col < end ? col : -(-col & (n - 1)); }
+
 // General kernels: any row stride, alignment and channel count.
 cudaError_t launch_norm_fwd_general(const NormFwd& p);
 cudaError_t launch_norm_bwd_general(const NormBwd& p);

@@ -176,7 +176,7 @@ __device__ __forceinline__ void publish(float* p, float v, uint64_t* bar, int cl
 // banks two by two, which costs little: with the halves of the vectors parted into two planes
 // (no conflicts) the copies themselves were the limit, 238 us instead of 185 for 16384 x 4096 with
 // an fp32 stream.  Vectors past the row's end are filled with zeros (a copy of no bytes), so the
-// arithmetic needs no branches.  Granules that hang over the row's ends are copied whole while
+// arithmetic needs no branches (copy_column: what such a copy names).  Granules that hang over the row's ends are copied whole while
 // they stay within [low, room) of the row's start, the tensor's extent (the reader masks the
 // neighbouring rows' elements); beyond it, at the tensor's very end, single elements are stored.
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool some) {
@@ -192,7 +192,7 @@ __device__ __forceinline__ void copy_granule(uint4* dst, const T* row, int col, 
     constexpr int n = 16 / sizeof(T);
     const bool some = col < end;
     if (kAligned || !some || (col >= low && col + n <= room)) {
-        copy16(dst, row + (some ? col : 0), some);
+        copy16(dst, row + (kAligned ? (some ? col : 0) : copy_column(col, end, n)), some);
     } else {
         T* to = reinterpret_cast<T*>(dst);
 #pragma unroll
