@@ -150,12 +150,13 @@ __global__ void general_bwd_filter_kernel(const T* __restrict__ x, const T* __re
 // out[i] = sum_z part[z * count + i].  A block covers 32 consecutive outputs (one per lane,
 // so every slice row is read with coalesced 128-byte loads); warp k sums the contiguous
 // slice range [k*zc, (k+1)*zc) and warp 0 adds the 8 partial sums in warp order.  The order
-// of additions depends only on `slices`, so runs are bit-identical.
+// of additions depends only on `slices`, so runs are bit-identical.  (`part` is not
+// __restrict__: the kernel may start while its data is still being written, so it must not be
+// read as constant data.)
 constexpr int kReduceWarps = 8;
 
 __global__ void __launch_bounds__(kReduceWarps * 32)
-reduce_slices_kernel(const float* __restrict__ part, int slices, size_t count,
-                     float* __restrict__ out) {
+reduce_slices_kernel(const float* part, int slices, size_t count, float* out) {
     pdl_wait();   // the kernel that wrote the slices has finished
     __shared__ float partial[kReduceWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -186,8 +187,7 @@ reduce_slices_kernel(const float* __restrict__ part, int slices, size_t count,
 // output's additions come in the same order as in reduce_slices_kernel, so the two give
 // identical results.
 __global__ void __launch_bounds__(kReduceWarps * 32)
-reduce_slices4_kernel(const float4* __restrict__ part, int slices, size_t count4,
-                      float4* __restrict__ out) {
+reduce_slices4_kernel(const float4* part, int slices, size_t count4, float4* out) {
     pdl_wait();   // the kernel that wrote the slices has finished
     __shared__ float4 partial[kReduceWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) mma_rows_kernel(const MmaAr
         if (cb != loaded_cb) {
             for (int i = tid; i < a.FH * a.FW; i += blockDim.x)
                 *reinterpret_cast<uint4*>(wb + i * kMmaCB) =
-                    __ldg(reinterpret_cast<const uint4*>(Wg + static_cast<size_t>(i) * a.C + c0));
+                    *reinterpret_cast<const uint4*>(Wg + static_cast<size_t>(i) * a.C + c0);
             loaded_cb = cb;
         }
         // input block, transposed to channel-major, zeros outside the image.  Eight
@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) mma_rows_kernel(const MmaAr
                     const int xr = i / a.XC, xc = i - xr * a.XC;
                     const int ih = oh0 - a.pad_h + xr, iw = xc - a.pad_w;
                     if (ih >= 0 && ih < a.H && iw >= 0 && iw < a.W)
-                        v[j] = __ldg(reinterpret_cast<const uint4*>(
-                            X + ((static_cast<size_t>(n) * a.H + ih) * a.W + iw) * a.C + c0));
+                        v[j] = *reinterpret_cast<const uint4*>(
+                            X + ((static_cast<size_t>(n) * a.H + ih) * a.W + iw) * a.C + c0);
                 }
             }
 #pragma unroll

@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) mma_fgrad_kernel(const MmaF
                     const int xr = i / a.XC, xc = i - xr * a.XC;
                     const int ih = oh0 - a.pad + xr, iw = xc - a.pad;
                     if (ih >= 0 && ih < a.H && iw >= 0 && iw < a.W)
-                        v[j] = __ldg(reinterpret_cast<const uint4*>(
-                            X + ((static_cast<size_t>(n) * a.H + ih) * a.W + iw) * a.C + c0));
+                        v[j] = *reinterpret_cast<const uint4*>(
+                            X + ((static_cast<size_t>(n) * a.H + ih) * a.W + iw) * a.C + c0);
                 }
             }
 #pragma unroll
@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) mma_fgrad_kernel(const MmaF
                 if (i < nd) {
                     const int r = i / a.DC, col = i - r * a.DC - 8;
                     if (col >= 0 && col < a.OW)
-                        v[j] = __ldg(reinterpret_cast<const uint4*>(
-                            DY + ((static_cast<size_t>(n) * a.OH + oh0 + r) * a.OW + col) * a.C + c0));
+                        v[j] = *reinterpret_cast<const uint4*>(
+                            DY + ((static_cast<size_t>(n) * a.OH + oh0 + r) * a.OW + col) * a.C + c0);
                 }
             }
 #pragma unroll

@@ -149,10 +149,12 @@ __global__ void __launch_bounds__(kThreads) dropout_general_kernel(DropoutCall p
 // one, 8 loads in flight, and a warp adds the threads' sums of a column.  A fixed order, whatever the
 // timing.  The kernel is bound by the latency of its loads: 8 columns (a sector) to a CTA where there
 // are few of them (bf16 200704 x 128 backward 29.1 us, 30.3 with 32), 32 where that would be more CTAs than two to an SM.
+// (`part` is not __restrict__: that would promise data unchanged for as long as the kernel runs, and the
+// row kernel may still write it when this one starts.)
 constexpr int kSumThreads = 1024;
 
 template <int kWidth>
-__global__ void __launch_bounds__(kSumThreads) norm_param_sum_kernel(const float* __restrict__ part, int count, int C,
+__global__ void __launch_bounds__(kSumThreads) norm_param_sum_kernel(const float* part, int count, int C,
                                                                      float* dgamma, float* dbeta) {
     constexpr int kSlots = kSumThreads / kWidth;
     __shared__ float sums[kSlots][kWidth + 1];
