@@ -36,6 +36,15 @@ dwc_status_t check_tensor(const void* p, long long ld, long long rows, int C, in
     return misaligned(p, bytes) ? DWC_ERR_ALIGNMENT : DWC_OK;
 }
 
+// Whether `out` (dense, `out_type`) is the input `in`.  An update in place reads each element before it is
+// overwritten; another type or row stride would overwrite elements that are still to be read.
+dwc_status_t check_in_place(const void* out, int out_type, const void* in, long long ld, int type, long long rows,
+                            int C, bool& in_place) {
+    if (out == nullptr || out != in || rows == 0) return DWC_OK;
+    in_place = true;
+    return out_type == type && (ld == C || rows == 1) ? DWC_OK : DWC_ERR_INVALID_ARG;
+}
+
 // The first error of a list of checks.
 dwc_status_t first_error(std::initializer_list<dwc_status_t> list) {
     for (dwc_status_t s : list)
@@ -113,9 +122,12 @@ dwc_status_t norm_fwd(NormFwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_ty
     if (st != DWC_OK) return st;
     if (misaligned(p.gamma, wp) || misaligned(p.beta, wp) || misaligned(p.mean, 4) || misaligned(p.rstd, 4))
         return DWC_ERR_ALIGNMENT;
-    // an update in place reads each element before it is overwritten; another row stride would
-    // overwrite rows that are still to be read
-    if (add && p.z == p.in && p.ld_in != p.C && p.rows > 1) return DWC_ERR_INVALID_ARG;
+    const auto over = [&](const void* out, int type) {
+        return first_error({check_in_place(out, type, p.in, p.ld_in, stream_type, p.rows, p.C, p.in_place),
+                            check_in_place(out, type, p.x, p.ld_x, branch_type, p.rows, p.C, p.in_place)});
+    };
+    st = first_error({over(p.y, branch_type), add ? over(p.z, stream_type) : DWC_OK});
+    if (st != DWC_OK) return st;
     if (p.rows == 0) return DWC_OK;
     p.stream_type = stream_type;
     p.branch_type = branch_type;
@@ -141,6 +153,13 @@ dwc_status_t norm_bwd(NormBwd& p, dwc_dtype_t stream_type, dwc_dtype_t branch_ty
     if (misaligned(p.gamma, wp) || misaligned(p.mean, 4) || misaligned(p.rstd, 4) || misaligned(p.dgamma, 4) ||
         misaligned(p.dbeta, 4))
         return DWC_ERR_ALIGNMENT;
+    const auto over = [&](const void* out, int type) {
+        return first_error({check_in_place(out, type, p.dy, p.ld_dy, branch_type, p.rows, p.C, p.in_place),
+                            check_in_place(out, type, p.dz, p.ld_dz, stream_type, p.rows, p.C, p.in_place),
+                            check_in_place(out, type, p.z, p.ld_z, stream_type, p.rows, p.C, p.in_place)});
+    };
+    st = first_error({over(p.d_stream, stream_type), over(p.d_branch, branch_type)});
+    if (st != DWC_OK) return st;
     const bool params = p.dgamma != nullptr || p.dbeta != nullptr;
     if (p.rows == 0) {
         for (float* d : {p.dgamma, p.dbeta}) {
@@ -175,7 +194,9 @@ dwc_status_t dropout(const void* x, long long ldx, void* y, long long rows, int 
     st = first_error({make_dropout(p, seed, offset, step, c.drop), check_tensor(x, ldx, rows, C, bytes, false),
                       check_tensor(y, C, rows, C, bytes, false)});
     if (st != DWC_OK) return st;
-    if (x == y && ldx != C && rows > 1) return DWC_ERR_INVALID_ARG;
+    bool in_place = false;
+    st = check_in_place(y, dtype, x, ldx, dtype, rows, C, in_place);
+    if (st != DWC_OK) return st;
     if (rows == 0) return DWC_OK;
     c.x = x;
     c.y = y;

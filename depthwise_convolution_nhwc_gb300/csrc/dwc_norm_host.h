@@ -40,6 +40,7 @@ struct NormFwd {
     int stream_type, branch_type;
     Dropout drop;
     cudaStream_t stream;
+    bool in_place = false;            // an output is one of the inputs
     unsigned int* status = nullptr;   // of the kernels whose waits have a limit
     unsigned long long wait_ns = 0;   // that limit (0: the default)
 };
@@ -63,6 +64,7 @@ struct NormBwd {
     int stream_type, branch_type;
     Dropout drop;
     cudaStream_t stream;
+    bool in_place = false;            // an output is one of the inputs
     unsigned int* status = nullptr;
     unsigned long long wait_ns = 0;
 };

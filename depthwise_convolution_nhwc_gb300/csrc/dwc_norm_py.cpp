@@ -110,6 +110,26 @@ struct Rows {
     }
 };
 
+// An output given by the caller may be one of the call's inputs, from the same address, dense and of its type
+// (an update in place); it must not overlap inputs or another output in any other way.  `in`: rows of
+// C elements, ld apart.
+void check_apart(const Tensor& out, const char* what, const Tensor& in, int64_t ld, int64_t C, const char* name,
+                 bool may_be = true) {
+    if (out.numel() == 0 || in.numel() == 0) return;
+    const auto o = reinterpret_cast<uintptr_t>(out.data_ptr()), b = reinterpret_cast<uintptr_t>(in.data_ptr());
+    if (may_be && o == b && out.scalar_type() == in.scalar_type() && out.sizes() == in.sizes() && in.is_contiguous()) return;
+    const uintptr_t end = o + out.numel() * out.element_size(), width = C * in.element_size(), step = ld * in.element_size();
+    // the first row that ends past the output's start
+    const uintptr_t row = o < b + width ? 0 : (o - b - width) / step + 1;
+    TORCH_CHECK_VALUE(row >= static_cast<uintptr_t>(in.numel() / C) || b + row * step >= end, what, " overlaps ", name,
+                      may_be ? " (it may be a dense tensor of its dtype itself, but not a part of it)" : "");
+}
+void check_apart(const Tensor& out, const char* what, PyObject* vector, const char* name) {
+    if (!THPVariable_Check(vector)) return;
+    const Tensor& t = THPVariable_Unpack(vector);
+    check_apart(out, what, t, t.numel(), t.numel(), name, false);
+}
+
 // gamma and beta: C values of one type each, or None.
 struct Params {
     const void* p[2] = {nullptr, nullptr};
@@ -251,6 +271,11 @@ PyObject* layer_norm_fwd(PyObject* const* a) {
     const float eps = static_cast<float>(number(a[3]));
     const OnDevice on(x);
     const Tensor y = x.out(a[4], type, "out");
+    if (a[4] != Py_None) {
+        check_apart(y, "out", x.t, x.ld, x.C, "x");
+        check_apart(y, "out", a[1], "gamma");
+        check_apart(y, "out", a[2], "beta");
+    }
     Tensor mean, rstd;
     const bool stats = a[6] == Py_True;
     if (stats) {
@@ -273,6 +298,13 @@ PyObject* layer_norm_bwd(PyObject* const* a) {
     const dwc_dtype_t type = code_of(x.t.scalar_type()), dtype = code_of(dy.scalar_type());
     const OnDevice on(x);
     const Tensor dx = x.out(a[5], x.t.scalar_type(), "out");
+    if (a[5] != Py_None) {
+        check_apart(dx, "out", dy, lddy, x.C, "dy");
+        check_apart(dx, "out", x.t, x.ld, x.C, "x");
+        check_apart(dx, "out", a[2], "mean");
+        check_apart(dx, "out", a[3], "rstd");
+        check_apart(dx, "out", a[4], "gamma");
+    }
     const ParamGrads g(x, a[6] == Py_True);
     check("dwc_layer_norm_bwd",
           dwc_layer_norm_bwd(dy.data_ptr(), lddy, x.t.data_ptr(), x.ld, mean, rstd, w.p[0], w.type, dx.data_ptr(), g.dg,
@@ -289,6 +321,10 @@ PyObject* dropout(PyObject* const* a) {
     const dwc_dtype_t type = code_of(x.t.scalar_type());
     const OnDevice on(x);
     const Tensor y = x.out(a[4], x.t.scalar_type(), "out");
+    if (a[4] != Py_None) {
+        check_apart(y, "out", x.t, x.ld, x.C, what);
+        check_apart(y, "out", a[3], "offset");
+    }
     const auto call = kBackward ? dwc_dropout_bwd : dwc_dropout_fwd;
     check(kBackward ? "dwc_dropout_bwd" : "dwc_dropout_fwd",
           call(x.t.data_ptr(), x.ld, y.data_ptr(), x.rows, static_cast<int>(x.C), rnd.p, rnd.seed, rnd.offset, rnd.step,
@@ -307,6 +343,17 @@ PyObject* add_layer_norm_fwd(PyObject* const* a) {
     const dwc_dtype_t type = code_of(x.t.scalar_type()), wide = code_of(res.scalar_type());
     const OnDevice on(x);
     const Tensor y = x.out(a[8], x.t.scalar_type(), "out"), z = x.out(a[9], res.scalar_type(), "z");
+    for (int i = 8; i <= 9; ++i) {
+        if (a[i] == Py_None) continue;
+        const Tensor& o = i == 8 ? y : z;
+        const char* what = i == 8 ? "out" : "z";
+        check_apart(o, what, x.t, x.ld, x.C, "x");
+        check_apart(o, what, res, ldres, x.C, "res");
+        check_apart(o, what, a[2], "gamma");
+        check_apart(o, what, a[3], "beta");
+        check_apart(o, what, a[7], "offset");
+    }
+    if (a[8] != Py_None && a[9] != Py_None) check_apart(y, "out", z, x.C, x.C, "z", false);
     Tensor mean, rstd;
     const bool stats = a[10] == Py_True;
     if (stats) {

@@ -298,7 +298,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
     const Columns at{first, min(C, first + cta_vectors * 8), width, lane};
     const float inv = 1.f / static_cast<float>(C);
     // (an update in place overwrites the neighbouring rows: then only the row's own elements are read)
-    const bool whole = !kAdd || p.z != p.in;
+    const bool whole = !p.in_place;
     const int low = whole ? -8 : 0;
     // shared memory: stage, row, then slot (the stream's vectors, the branch's), then thread
     const int x_at = NV * kStream * threads;
@@ -607,6 +607,8 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
     const float inv = 1.f / static_cast<float>(C);
     const bool has_dz = kAdd && p.dz != nullptr;
     const bool has_branch = kAdd && p.d_branch != nullptr;
+    const bool whole = !p.in_place;                // (as forward)
+    const int low = whole ? -8 : 0;
     // shared memory: stage, row, then slot (dy, z, dz of each vector), then thread
     const int z_at = NV * kBranch * threads, dz_at = z_at + NV * kStream * threads;
     const int row_granules = dz_at + (has_dz ? NV * kStream * threads : 0);
@@ -631,20 +633,20 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
             const long long r = r0 + static_cast<long long>(u) * groups;
             if (r >= p.rows) continue;
             // elements from the row's start to the tensor's end, at least
-            const int room = kAligned ? 0 : static_cast<int>(min((p.rows - r) * C, 1LL << 30));
+            const int room = kAligned ? 0 : whole ? static_cast<int>(min((p.rows - r) * C, 1LL << 30)) : C;
             uint4* to = slots + (stage * R + u) * row_granules;
             const TB* dy = static_cast<const TB*>(p.dy) + r * p.ld_dy;
             const TS* z = static_cast<const TS*>(p.z) + r * p.ld_z;
             const TS* dz = has_dz ? static_cast<const TS*>(p.dz) + r * p.ld_dz : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, at.of(k), at.end, C, -8, room);
-                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, at.of(k), at.end, C, -8, room);
+                copy_slot<kAligned, TB, GW>(to + k * kBranch * threads + mine_b, dy, sub, at.of(k), at.end, C, low, room);
+                copy_slot<kAligned, TS, GW>(to + z_at + k * kStream * threads + mine_s, z, sub, at.of(k), at.end, C, low, room);
             }
             if (has_dz) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
-                    copy_slot<kAligned, TS, GW>(to + dz_at + k * kStream * threads + mine_s, dz, sub, at.of(k), at.end, C, -8,
+                    copy_slot<kAligned, TS, GW>(to + dz_at + k * kStream * threads + mine_s, dz, sub, at.of(k), at.end, C, low,
                                                 room);
             }
         }
@@ -977,9 +979,9 @@ cudaError_t bwd_launch(const NormBwd& call, int vectors) {
     const int groups = G > 0 ? l.per_cta : kCluster ? 1 : max_cta(R) / l.width;
     // (Shifted rows of a group must be a multiple of 8 apart: lane groups are, others come in one go.)
     const bool one_cta = p.partial != nullptr && !kCluster && p.rows <= (kAligned || G > 0 ? 3LL : 1LL) * groups;
-    if (p.partial != nullptr && !kCluster && !one_cta) {
+    if (p.partial != nullptr && !kCluster && !one_cta && !p.in_place) {
         // up to 256 rows: the columns' sums in the same kernel, with more groups to a CTA where that
-        // takes fewer rounds
+        // takes fewer rounds (not in place: it reads dy and z again, which other CTAs may have overwritten by then)
         l.slots = column_slots(p.rows, p.C, l.threads, (p.rows + l.per_cta - 1) / l.per_cta);
         if (G == 0 && l.slots == 0 && p.rows <= 256) {
             const int most = static_cast<int>(std::min<long long>(groups, p.rows));

@@ -2,7 +2,9 @@
 
 Binding over the C ABI in ``include/dwc_norm.h``.  Tensors are ``[..., C]`` on a CUDA device, fp32,
 bf16 or fp16, with adjacent channels and one stride between rows (a slice of a larger tensor's
-channels or tokens is taken as it is); outputs are dense.  Work runs on the current CUDA stream
+channels or tokens is taken as it is); outputs are dense.  An output that a call is given (``out``, ``z``) may
+be one of its inputs itself, dense and of the output's dtype (an update in place), and must not
+overlap them in any other way (ValueError).  Work runs on the current CUDA stream
 of the tensors' device, or on ``stream``; outputs and workspaces are then allocated for that
 stream and the inputs are recorded on it.  Nothing falls back to the CPU.
 
@@ -82,15 +84,14 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = 
 
 
 def dropout_fwd(x, p: float, seed: int, offset=0, out=None, stream=None):
-    """x / (1 - q) where kept, 0 where dropped, with probability q = p to the nearest 2^-16;
-    ``out`` may be x."""
+    """x / (1 - q) where kept, 0 where dropped, with probability q = p to the nearest 2^-16."""
     if stream is not None:
         return _on(stream, dropout_fwd, x, p, seed, offset, out)
     return (_module or _host()).dropout_fwd(x, p, seed, offset, out)
 
 
 def dropout_bwd(dy, p: float, seed: int, offset=0, out=None, stream=None):
-    """dx of ``dropout_fwd`` with the same p, seed and offset; ``out`` may be dy."""
+    """dx of ``dropout_fwd`` with the same p, seed and offset."""
     if stream is not None:
         return _on(stream, dropout_bwd, dy, p, seed, offset, out)
     return (_module or _host()).dropout_bwd(dy, p, seed, offset, out)
@@ -99,8 +100,8 @@ def dropout_bwd(dy, p: float, seed: int, offset=0, out=None, stream=None):
 def add_layer_norm_fwd(x, res, gamma=None, beta=None, eps: float = 1e-5, p: float = 0.0, seed: int = 0,
                        offset=0, out=None, z=None, stats: bool = False, stream=None):
     """z = res + dropout(x), y = layer_norm(z) in one pass; (y, z), or (y, z, mean, rstd) with
-    ``stats``.  y has x's dtype, z has res's: the same, or fp32 with a 16-bit x.  ``z`` may be
-    res (an update of the residual stream in place)."""
+    ``stats``.  y has x's dtype, z has res's: the same, or fp32 with a 16-bit x.  With z=res the
+    residual stream is updated in place."""
     if stream is not None:
         return _on(stream, add_layer_norm_fwd, x, res, gamma, beta, eps, p, seed, offset, out, z, stats)
     return (_module or _host()).add_layer_norm_fwd(x, res, gamma, beta, eps, p, seed, offset, out, z, bool(stats))

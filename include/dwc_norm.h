@@ -10,12 +10,13 @@
  *
  * Arithmetic is fp32: 16-bit inputs are widened exactly, sums, means, variances and their
  * merges are fp32, 16-bit outputs are rounded to nearest even once, at the store.  The order of
- * every sum is fixed by the shape, the types, the alignment and the number of SMs, so results
- * are bit-identical from run to run (no atomics).
+ * every sum is fixed by the shape, the types, the alignment, whether the call works in place and
+ * the number of SMs, so results are bit-identical from run to run (no atomics).
  *
- * Outputs must not overlap inputs, with two exceptions that allow an update in place: z may be
- * res (ldres == C) in dwc_add_layer_norm_fwd, and y / dx may be x / dy (ld == C) in
- * dwc_dropout_fwd / dwc_dropout_bwd.
+ * In place: an output of rows x C values may be one of the call's inputs of rows x C values, from the same
+ * address, of the same type and with dense rows (z over res, y over x, dx over dy or x, ...); the same
+ * address with another type or row stride is DWC_ERR_INVALID_ARG.  Outputs must not overlap inputs or one
+ * another in any other way.
  *
  * No call allocates device memory; the backward passes take a caller workspace for the partial
  * sums of the parameter gradients.
@@ -99,7 +100,7 @@ dwc_status_t dwc_dropout_bwd(const void* dy, long long lddy, void* dx, long long
  * (statistics and y from the fp32 sum, z rounded once where it is stored).
  *   x : rows x C, dtype, row stride ldx (the branch)   y : rows x C, dtype (out)
  *   res : rows x C, res_dtype, row stride ldres (the residual stream)
- *   z : rows x C, res_dtype (out); may be res itself when ldres == C
+ *   z : rows x C, res_dtype (out); may be res itself (see "In place" above)
  *   res_dtype : dtype, or DWC_F32 (an fp32 stream with 16-bit branches)
  *   p = 0 : no dropout (serving); seed, offset and step are then not used
  * The rest and the errors as dwc_layer_norm_fwd and dwc_dropout_fwd. */
