@@ -10,6 +10,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "dwc_host.h"
 
 namespace dwc {
@@ -84,6 +86,35 @@ struct DropoutCall {
 // be aligned all the same, and the start of a shifted row is not: it names the boundary at or before that start
 // (col is minus the row's shift modulo n, and the tensor's base lies on a boundary).
 constexpr int copy_column(int col, int end, int n) { return col < end ? col : -(-col & (n - 1)); }
+
+// How many clusters of a kernel a device holds together, by device and launch shape, each asked for once
+// (a runtime call of its own).  `ask()` gives the number; none (below 1) is not kept.  No allocation: a kernel
+// has at most 96 shapes (threads in steps of 32 up to 512, clusters of 2, 4 and 8, with and without
+// dz), and what finds no place any more, with many devices, is asked for at every call.
+class ClusterCounts {
+public:
+    template <class Ask>
+    int get(int device, size_t smem, int threads, int cluster, Ask ask) {
+        std::lock_guard<std::mutex> lock(mu_);
+        for (int i = 0; i < count_; ++i) {
+            const Place& k = known_[i];
+            if (k.device == device && k.smem == smem && k.threads == threads && k.cluster == cluster) return k.n;
+        }
+        const int n = ask();
+        if (n >= 1 && count_ < kPlaces) known_[count_++] = {smem, device, threads, cluster, n};
+        return n;
+    }
+
+private:
+    static constexpr int kPlaces = 192;
+    struct Place {
+        size_t smem;
+        int device, threads, cluster, n;
+    };
+    std::mutex mu_;
+    Place known_[kPlaces];
+    int count_ = 0;
+};
 
 // General kernels: any row stride, alignment and channel count.
 cudaError_t launch_norm_fwd_general(const NormFwd& p);

@@ -825,7 +825,7 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
 struct KernelFacts {
     DeviceOnce smem;
     std::atomic<int> regs{0};
-    std::atomic<uint64_t> clusters{0};   // shared memory, threads and CTAs of a cluster; how many fit
+    ClusterCounts clusters;
     template <class K>
     int registers(K kern) {
         int r = regs.load(std::memory_order_relaxed);
@@ -934,18 +934,17 @@ cudaError_t launch_rows(K kern, KernelFacts& facts, const P& p, const Layout& l,
     } else {
         // clusters need their CTAs on one GPC, whose SMs they do not always divide: 4 CTAs, two to an SM,
         // fit 74 times, not 76
-        const uint64_t key = (static_cast<uint64_t>(smem) << 32 | static_cast<uint64_t>(l.threads) << 20 | l.cluster << 16);
-        uint64_t known = facts.clusters.load(std::memory_order_relaxed);
-        if (known >> 16 != key >> 16) {
+        int device = 0;
+        cudaError_t err = cudaGetDevice(&device);
+        if (err != cudaSuccess) return err;
+        all = facts.clusters.get(device, smem, l.threads, l.cluster, [&] {
             launch.cfg.gridDim = dim3(static_cast<unsigned>(l.cluster));
             int n = 0;
-            const cudaError_t err = cudaOccupancyMaxActiveClusters(&n, kern, &launch.cfg);
-            if (err != cudaSuccess) return err;
-            if (n < 1) return cudaErrorNotSupported;
-            known = key | static_cast<uint64_t>(std::min(n, 0xffff));
-            facts.clusters.store(known, std::memory_order_relaxed);
-        }
-        all = static_cast<long long>(known & 0xffff);
+            err = cudaOccupancyMaxActiveClusters(&n, kern, &launch.cfg);
+            return err == cudaSuccess ? n : 0;
+        });
+        if (err != cudaSuccess) return err;
+        if (all < 1) return cudaErrorNotSupported;
     }
     if (p.C % 8 != 0) all = std::max(8LL, all / 8 * 8);
     *grid = static_cast<int>(std::min(want, all));

@@ -11,7 +11,8 @@
  * Arithmetic is fp32: 16-bit inputs are widened exactly, sums, means, variances and their
  * merges are fp32, 16-bit outputs are rounded to nearest even once, at the store.  The order of
  * every sum is fixed by the shape, the types, the alignment, whether the call works in place and
- * the number of SMs, so results are bit-identical from run to run (no atomics).
+ * the number of SMs (beyond 10240 channels: of clusters that the GPU holds), so results are
+ * bit-identical from run to run (no atomics).
  *
  * In place: an output of rows x C values may be one of the call's inputs of rows x C values, from the same
  * address, of the same type and with dense rows (z over res, y over x, dx over dy or x, ...); the same

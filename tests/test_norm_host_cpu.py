@@ -51,3 +51,34 @@ def test_every_copy_names_an_aligned_address_inside_the_tensor(run):
     """)
     copies, empty, bad = map(int, out.split())
     assert copies > empty > 10 ** 6 and bad == 0
+
+
+def test_cluster_counts_are_kept_by_device_and_shape(run):
+    """Shapes that alternate are asked for once each; another device has its own answer; no answer is not kept."""
+    out = run(r"""
+    dwc::ClusterCounts counts;
+    int asked = 0, wrong = 0;
+    for (int i = 0; i < 10; ++i)
+        for (int device = 0; device < 2; ++device)
+            for (int threads = 256; threads <= 512; threads += 32)
+                for (int cluster = 2; cluster <= 8; cluster *= 2) {
+                    const int want = 1000 * device + threads + cluster;
+                    wrong += counts.get(device, 65536, threads, cluster, [&] { ++asked; return want; }) != want;
+                }
+    std::printf("%d %d ", asked, wrong);
+    int failed = 0;
+    for (int i = 0; i < 3; ++i) failed += counts.get(0, 1, 32, 2, [&] { return 0; }) == 0;
+    std::printf("%d %d", failed, counts.get(0, 1, 32, 2, [&] { return 5; }));
+    """)
+    assert out.split() == [str(2 * 9 * 3), "0", "3", "5"]
+
+
+def test_more_shapes_than_places_are_answered_all_the_same(run):
+    out = run(r"""
+    dwc::ClusterCounts counts;
+    int wrong = 0;
+    for (int i = 0; i < 2; ++i)
+        for (int k = 1; k <= 1000; ++k) wrong += counts.get(0, k, 32, 2, [&] { return k; }) != k;
+    std::printf("%d", wrong);
+    """)
+    assert out == "0"
