@@ -113,21 +113,21 @@ struct Rows {
 // An output given by the caller may be one of the call's inputs, from the same address, dense and of its type
 // (an update in place); it must not overlap inputs or another output in any other way.  `in`: rows of
 // C elements, ld apart.
-void check_apart(const Tensor& out, const char* what, const Tensor& in, int64_t ld, int64_t C, const char* name,
-                 bool may_be = true) {
-    if (out.numel() == 0 || in.numel() == 0) return;
+void check_apart(const Tensor& out, const char* what, const Tensor& in, int64_t rows, int64_t C, int64_t ld,
+                 const char* name, bool may_be = true) {
     const auto o = reinterpret_cast<uintptr_t>(out.data_ptr()), b = reinterpret_cast<uintptr_t>(in.data_ptr());
+    const uintptr_t end = o + out.numel() * out.element_size(), size = in.element_size(), width = C * size, step = ld * size;
+    if (o == end || rows == 0 || end <= b || o >= b + (rows - 1) * step + width) return;
     if (may_be && o == b && out.scalar_type() == in.scalar_type() && out.sizes() == in.sizes() && in.is_contiguous()) return;
-    const uintptr_t end = o + out.numel() * out.element_size(), width = C * in.element_size(), step = ld * in.element_size();
     // the first row that ends past the output's start
     const uintptr_t row = o < b + width ? 0 : (o - b - width) / step + 1;
-    TORCH_CHECK_VALUE(row >= static_cast<uintptr_t>(in.numel() / C) || b + row * step >= end, what, " overlaps ", name,
+    TORCH_CHECK_VALUE(b + row * step >= end, what, " overlaps ", name,
                       may_be ? " (it may be a dense tensor of its dtype itself, but not a part of it)" : "");
 }
 void check_apart(const Tensor& out, const char* what, PyObject* vector, const char* name) {
     if (!THPVariable_Check(vector)) return;
     const Tensor& t = THPVariable_Unpack(vector);
-    check_apart(out, what, t, t.numel(), t.numel(), name, false);
+    if (t.numel() > 0) check_apart(out, what, t, 1, t.numel(), t.numel(), name, false);
 }
 
 // gamma and beta: C values of one type each, or None.
@@ -272,7 +272,7 @@ PyObject* layer_norm_fwd(PyObject* const* a) {
     const OnDevice on(x);
     const Tensor y = x.out(a[4], type, "out");
     if (a[4] != Py_None) {
-        check_apart(y, "out", x.t, x.ld, x.C, "x");
+        check_apart(y, "out", x.t, x.rows, x.C, x.ld, "x");
         check_apart(y, "out", a[1], "gamma");
         check_apart(y, "out", a[2], "beta");
     }
@@ -299,8 +299,8 @@ PyObject* layer_norm_bwd(PyObject* const* a) {
     const OnDevice on(x);
     const Tensor dx = x.out(a[5], x.t.scalar_type(), "out");
     if (a[5] != Py_None) {
-        check_apart(dx, "out", dy, lddy, x.C, "dy");
-        check_apart(dx, "out", x.t, x.ld, x.C, "x");
+        check_apart(dx, "out", dy, x.rows, x.C, lddy, "dy");
+        check_apart(dx, "out", x.t, x.rows, x.C, x.ld, "x");
         check_apart(dx, "out", a[2], "mean");
         check_apart(dx, "out", a[3], "rstd");
         check_apart(dx, "out", a[4], "gamma");
@@ -322,7 +322,7 @@ PyObject* dropout(PyObject* const* a) {
     const OnDevice on(x);
     const Tensor y = x.out(a[4], x.t.scalar_type(), "out");
     if (a[4] != Py_None) {
-        check_apart(y, "out", x.t, x.ld, x.C, what);
+        check_apart(y, "out", x.t, x.rows, x.C, x.ld, what);
         check_apart(y, "out", a[3], "offset");
     }
     const auto call = kBackward ? dwc_dropout_bwd : dwc_dropout_fwd;
@@ -347,13 +347,13 @@ PyObject* add_layer_norm_fwd(PyObject* const* a) {
         if (a[i] == Py_None) continue;
         const Tensor& o = i == 8 ? y : z;
         const char* what = i == 8 ? "out" : "z";
-        check_apart(o, what, x.t, x.ld, x.C, "x");
-        check_apart(o, what, res, ldres, x.C, "res");
+        check_apart(o, what, x.t, x.rows, x.C, x.ld, "x");
+        check_apart(o, what, res, x.rows, x.C, ldres, "res");
         check_apart(o, what, a[2], "gamma");
         check_apart(o, what, a[3], "beta");
         check_apart(o, what, a[7], "offset");
     }
-    if (a[8] != Py_None && a[9] != Py_None) check_apart(y, "out", z, x.C, x.C, "z", false);
+    if (a[8] != Py_None && a[9] != Py_None) check_apart(y, "out", z, x.rows, x.C, x.C, "z", false);
     Tensor mean, rstd;
     const bool stats = a[10] == Py_True;
     if (stats) {
