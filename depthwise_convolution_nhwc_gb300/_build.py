@@ -64,11 +64,25 @@ def _compile_host(obj: str) -> None:
             os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    r = subprocess.run(cmd + [f"-I{d}" for d in dirs] + ["-c", HOST_SRC, "-o", obj + ".tmp"], capture_output=True,
-                       text=True)
+    tmp = obj + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + [f"-I{d}" for d in dirs] + ["-c", HOST_SRC, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(HOST_SRC)}:\n{r.stderr[-6000:]}")
-    os.replace(obj + ".tmp", obj)
+    os.replace(tmp, obj)
+
+
+def _host_linked(obj: str) -> bool:
+    """Whether the host module was linked from this object as it is now (objects of several PyTorch
+    versions share one module; which of them it holds is recorded beside them)."""
+    try:
+        with open(_host_record()) as f:
+            return f.read() == os.path.basename(obj) and os.path.getmtime(HOST_PATH) >= os.path.getmtime(obj)
+    except OSError:
+        return False
+
+
+def _host_record() -> str:
+    return os.path.join(OBJ_DIR, "dwc_norm_py.linked")
 
 
 def _link_host(obj: str) -> None:
@@ -123,8 +137,10 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=None) -> s
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr[-6000:]}")
         os.replace(tmp, LIB_PATH)
-    if not os.path.exists(HOST_PATH) or os.path.getmtime(HOST_PATH) < os.path.getmtime(host_obj):
+    if not _host_linked(host_obj):
         _link_host(host_obj)
+        with open(_host_record(), "w") as f:
+            f.write(os.path.basename(host_obj))
     return LIB_PATH
 
 
