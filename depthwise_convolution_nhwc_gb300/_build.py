@@ -5,7 +5,9 @@ library next to this file.  Rebuilds only what changed (sources or headers newer
 object).  No CPU fallback exists: importing the binding without this library fails loudly.
 
 ``csrc/dwc_norm_py.cpp``, the host path of the norm operators for Python, is compiled beside it with
-the host compiler against the installed PyTorch and linked as the module ``_norm_host``.
+the host compiler against the installed PyTorch and linked as the module ``_norm_host``.  Run as a
+script (``python depthwise_convolution_nhwc_gb300/_build.py``) where there is no PyTorch, the build makes the C
+library alone.
 """
 from __future__ import annotations
 
@@ -49,9 +51,12 @@ def _stale(obj: str, src: str, hdr_mtime: float) -> bool:
     return t < os.path.getmtime(src) or t < hdr_mtime
 
 
-def _host_object() -> str:
-    """The host module's object file, one per PyTorch and Python version."""
-    import torch
+def _host_object() -> str | None:
+    """The host module's object file, one per PyTorch and Python version; none without PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     return os.path.join(OBJ_DIR, f"dwc_norm_py-{torch.__version__}-{sys.version_info[0]}{sys.version_info[1]}.o")
 
 
@@ -120,7 +125,7 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=None) -> s
         return s, r.stderr
 
     host_obj = _host_object()
-    host_todo = _stale(host_obj, HOST_SRC, hdr_mtime)
+    host_todo = host_obj is not None and _stale(host_obj, HOST_SRC, hdr_mtime)
     jobs = jobs or min(len(todo) + host_todo, os.cpu_count() or 4) or 1
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         host = ex.submit(_compile_host, host_obj) if host_todo else None
@@ -137,7 +142,7 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=None) -> s
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr[-6000:]}")
         os.replace(tmp, LIB_PATH)
-    if not _host_linked(host_obj):
+    if host_obj is not None and not _host_linked(host_obj):
         _link_host(host_obj)
         with open(_host_record(), "w") as f:
             f.write(os.path.basename(host_obj))

@@ -1,11 +1,14 @@
 """The build's decisions, with compilers replaced by stubs that write text files."""
 import os
 import shutil
+import sys
 import time
 
 import pytest
 
 from depthwise_convolution_nhwc_gb300 import _build
+
+HOST_OBJECT = _build._host_object
 
 
 @pytest.fixture
@@ -79,3 +82,11 @@ def test_nothing_is_done_twice(tree):
     os.utime(_build.HOST_SRC, (now, now))
     _build.build()
     assert calls[3:] == ["compile", "link"]
+
+
+def test_the_library_is_built_without_pytorch(tree, monkeypatch):
+    """The C ABI needs no PyTorch, nor does its build, which then leaves out the host module."""
+    _, calls = tree
+    monkeypatch.setattr(_build, "_host_object", HOST_OBJECT)
+    monkeypatch.setitem(sys.modules, "torch", None)     # `import torch` raises ImportError
+    assert _build.build() == _build.LIB_PATH and calls == []
