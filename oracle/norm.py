@@ -7,7 +7,9 @@ The bounds follow from u = 2^-24 (fp32) and the output type's u_out: a sum of n 
 partial sum is deeper than D additions is off by at most D * u * sum|terms| (first order).  The
 kernels add at most C / 256 + 80 terms one after another along a row (threads of a CTA, then
 lanes, then warps) and at most rows / 64 + 400 down a column (the rows of one CTA, its row
-groups, then the partial sums); each further operation adds one u of its result.
+groups, then the partial sums); each further operation adds one u of its result.  Beyond 10240
+channels a cluster of up to 8 CTAs takes the place of a CTA, of which at least 8 run together: a thread
+adds at most rows / 8 terms and the partial sums 76, which is within rows / 64 + 400 up to 2900 rows.
 """
 from __future__ import annotations
 
