@@ -38,8 +38,8 @@ EXPORTS = ("dwc_fwd", "dwc_fwd_ex", "dwc_fwd_bn_act", "dwc_bwd_data", "dwc_bwd_d
            "dwc_bwd_filter_workspace_size", "dwc_bwd_filter", "dwc_bwd_filter_noalloc",
            "dwc_device_status", "dwc_set_wait_limit_ns", "dwc_fma_rate_probe",
            "dwc_status_string", "dwc_version", "dwc_path", "dwc_kernel_launches",
-           "dwc_testing_stall_next_row_launch", "dwc_testing_prefer_family",
-           "dwc_testing_tc_row_pairs",
+           "dwc_testing_stall_next_row_launch", "dwc_testing_stall_next_norm_cluster",
+           "dwc_testing_prefer_family", "dwc_testing_tc_row_pairs",
            "dwc_layer_norm_fwd", "dwc_layer_norm_bwd_workspace_size", "dwc_layer_norm_bwd",
            "dwc_dropout_fwd", "dwc_dropout_bwd", "dwc_add_layer_norm_fwd",
            "dwc_add_layer_norm_bwd")
@@ -107,6 +107,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.dwc_fma_rate_probe.restype = i
         lib.dwc_testing_stall_next_row_launch.argtypes = []
         lib.dwc_testing_stall_next_row_launch.restype = None
+        lib.dwc_testing_stall_next_norm_cluster.argtypes = []
+        lib.dwc_testing_stall_next_norm_cluster.restype = None
         lib.dwc_testing_prefer_family.argtypes = [i]
         lib.dwc_testing_prefer_family.restype = i
         lib.dwc_testing_tc_row_pairs.argtypes = [i]

@@ -32,6 +32,7 @@ PerDevice g_dev[kMaxDevices];
 std::mutex g_mu;
 std::atomic<unsigned long long> g_wait_limit_ns{0};  // 0: the kernels' default
 std::atomic<int> g_row_stall{0};
+std::atomic<int> g_norm_stall{0};
 std::atomic<int> g_family_pref{0};
 std::atomic<int> g_tc_pairs{0};
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -125,6 +126,8 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t ran
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 
 int take_row_stall() { return g_row_stall.exchange(0, std::memory_order_acq_rel); }
+
+bool take_norm_stall() { return g_norm_stall.exchange(0, std::memory_order_acq_rel) != 0; }
 
 int family_preference() { return g_family_pref.load(std::memory_order_relaxed); }
 
@@ -557,6 +560,8 @@ unsigned long long dwc_set_wait_limit_ns(unsigned long long ns) {
 }
 
 void dwc_testing_stall_next_row_launch(void) { g_row_stall.store(1, std::memory_order_release); }
+
+void dwc_testing_stall_next_norm_cluster(void) { g_norm_stall.store(1, std::memory_order_release); }
 
 int dwc_testing_prefer_family(int family) {
     if (family != 0 && family != kFamilyCudaCore && family != kFamilyTcgen05 &&

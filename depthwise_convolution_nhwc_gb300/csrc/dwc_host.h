@@ -87,9 +87,11 @@ struct GeneralConv {
 };
 
 // Limit of the waits inside kernels launched from now on (nanoseconds), and the one-shot
-// fault-injection flag of the next row-kernel launch (both set through the C ABI).
+// fault-injection flags of the next row-kernel launch and of the next norm launch on clusters (all
+// set through the C ABI).
 unsigned long long wait_limit_ns();
 int take_row_stall();
+bool take_norm_stall();
 // The current device's status word (null if CUDA is unusable).
 unsigned int* status_word();
 

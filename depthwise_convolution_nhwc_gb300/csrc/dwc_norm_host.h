@@ -43,6 +43,7 @@ struct NormFwd {
     Dropout drop;
     cudaStream_t stream;
     bool in_place = false;            // an output is one of the inputs
+    bool stall = false;               // test of the wait limit: each cluster's last CTA sends its sums to nobody
     unsigned int* status = nullptr;   // of the kernels whose waits have a limit
     unsigned long long wait_ns = 0;   // that limit (0: the default)
 };
@@ -67,6 +68,7 @@ struct NormBwd {
     Dropout drop;
     cudaStream_t stream;
     bool in_place = false;            // an output is one of the inputs
+    bool stall = false;               // test of the wait limit: each cluster's last CTA sends its sums to nobody
     unsigned int* status = nullptr;
     unsigned long long wait_ns = 0;
 };

@@ -368,7 +368,7 @@ norm_fwd_rows_kernel(NormFwd p, int group_threads, int cluster_ctas, int cta_vec
     const float mine_inv = mine > 0 ? 1.f / static_cast<float>(mine) : 0.f;
     int parity = 0, stage = 0;
     uint32_t phase = 0;                 // of the exchange barrier that is next in use
-    bool lost = false;                  // a wait of this thread ran out
+    bool lost = kCluster && p.stall && rank == cluster - 1;   // a wait of this thread ran out (or is to)
 
     const long long step = static_cast<long long>(R) * groups;
     // (the lane groups of a warp stay together: the warp goes on while its first group has a row, and
@@ -669,7 +669,7 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
     const int from_place = local * warps;
     int parity = 0, stage = 0;
     uint32_t phase = 0;                 // of the exchange barrier that is next in use
-    bool lost = false;                  // a wait of this thread ran out
+    bool lost = kCluster && p.stall && rank == cluster - 1;   // a wait of this thread ran out (or is to)
     float next_mean[R], next_rstd[R];
     auto fetch_stats = [&](long long r0) {
 #pragma unroll
@@ -952,7 +952,9 @@ cudaError_t launch_rows(K kern, KernelFacts& facts, const P& p, const Layout& l,
     const long long groups = static_cast<long long>(*grid) * l.per_cta;
     if (p.C % 8 != 0 && groups % 8 != 0 && groups < p.rows) return cudaErrorInvalidConfiguration;
     launch.cfg.gridDim = dim3(static_cast<unsigned>(*grid) * static_cast<unsigned>(l.cluster));
-    return cudaLaunchKernelEx(&launch.cfg, kern, p, l.width, l.cluster, l.cta_vectors, l.slots);
+    P args = p;
+    if (l.cluster > 1) args.stall = take_norm_stall();
+    return cudaLaunchKernelEx(&launch.cfg, kern, args, l.width, l.cluster, l.cta_vectors, l.slots);
 }
 
 template <typename TS, typename TB, bool kAdd, bool kAligned, bool kCluster, int G, int NV, int R, int S>

@@ -3,9 +3,9 @@
  * selection for tests that run every kernel on the same shapes.
  *
  * No counterpart in the paper.  The injected failure is made on the host side and involves
- * no GPU fault: a kernel is told not to issue some of its own input copies, so its compute
- * warps wait until their wait limit (dwc_set_wait_limit_ns) runs out, record the timeout in
- * the device status word and end.  No copy is in flight at that point.
+ * no GPU fault: a kernel is told not to issue some of its own input copies (or not to send some
+ * of its own sums), so its compute warps wait until their wait limit (dwc_set_wait_limit_ns) runs
+ * out, record the timeout in the device status word and end.  No copy is in flight at that point.
  */
 #ifndef DWC_GB300_TESTING_H
 #define DWC_GB300_TESTING_H
@@ -22,6 +22,13 @@ extern "C" {
  * request is consumed by that one launch; launches of other kernels leave it pending.  Not
  * for production use. */
 void dwc_testing_stall_next_row_launch(void);
+
+/* In the next norm launch whose rows go to clusters of CTAs (layer norm or its residual form, more
+ * than 10240 channels) the last CTA of each cluster sends its sums to nobody and waits for none.
+ * The other CTAs' waits run out, the outputs are not meaningful and dwc_device_status() then returns
+ * DWC_ERR_TIMEOUT.  Consumed by that one launch; other launches leave it pending.  Not for
+ * production use. */
+void dwc_testing_stall_next_norm_cluster(void);
 
 /* Kernel family for the 16-bit forward / backward-data calls made from now on, where that
  * family can run the shape (else the automatic choice): 0 = automatic (the default),
