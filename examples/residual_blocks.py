@@ -1,4 +1,5 @@
-"""A training loop over depthwise residual blocks, every GPU step from this library:
+"""A training loop over depthwise residual blocks, forward and backward entirely calls of this library
+(the loss and the update of the weights are PyTorch's):
 
     z_0 = dropout(x),  y_0 = norm(z_0);    b_i = dwc(y_i),  z_{i+1} = z_i + dropout(b_i),
     y_{i+1} = norm(z_{i+1})
@@ -71,10 +72,12 @@ def backward(dy, saved, params: Params, p: float, seed: int, step: int):
         grads.w[i] = dwc.bwd_filter(y, db, taps, 1, pad)
         dy = dwc.bwd_data(db, params.w[i], y.shape[1:3], 1, pad, out_dtype=dtype)
     z, mean, rstd, _ = saved[0]
-    dz0, grads.gamma[0], grads.beta[0] = dwc.layer_norm_bwd(dy, z, mean, rstd, params.gamma[0])
-    if dz is not None:
-        dz0 = dz0 + dz
-    return dwc.dropout_bwd(dz0, p, seed, base), grads
+    if dy.dtype == z.dtype:    # z_0 = 0 + dropout(x): the residual form's gradient of its branch is dx
+        dx, _, grads.gamma[0], grads.beta[0] = dwc.add_layer_norm_bwd(dy, z, mean, rstd, params.gamma[0], dz, p, seed, base)
+    else:                      # (that one would be in the branches' type; x is fp32)
+        _, dz, grads.gamma[0], grads.beta[0] = dwc.add_layer_norm_bwd(dy, z, mean, rstd, params.gamma[0], dz)
+        dx = dwc.dropout_bwd(dz, p, seed, base, out=dz)
+    return dx, grads
 
 
 def train_step(x, target, params: Params, p: float, seed: int, step: int, rate: float):
