@@ -752,9 +752,9 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
         for (int u = 0; u < R; ++u) {
             const long long r = r0 + static_cast<long long>(u) * groups;
             if (r >= p.rows) continue;        // (no barrier and no shuffle below)
-            // dx = rstd (a - c1 - xhat c2), xhat before its product with c2 and rstd last: rstd * rstd on the way
-            // would overflow for rows of very little spread (eps = 0) whose dx is finite
-            const float c1 = s[2 * u] * inv, c2 = s[2 * u + 1] * inv;
+            // dx = rstd (a - c1 - xhat c2) = rstd (a - c1 - (x - mean) k2), k2 = rstd c2.  rstd comes last: its square
+            // would overflow for rows of very little spread (eps = 0) whose dx is finite, k2 only where dx does.
+            const float c1 = s[2 * u] * inv, k2 = rstd[u] * (s[2 * u + 1] * inv);
             const uint4* row = from + u * row_granules;
             TS* ds = static_cast<TS*>(p.d_stream) + r * C;
             TB* db = has_branch ? static_cast<TB*>(p.d_branch) + r * C : nullptr;
@@ -766,9 +766,8 @@ norm_bwd_rows_kernel(NormBwd p, int group_threads, int cluster_ctas, int cta_vec
                 read_slot<TS>(x, row + z_at + k * kStream * threads + mine_s);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 xhat = __fmul2_rn(__fadd2_rn(x[j], both(-mean[u])), both(rstd[u]));
                     const float2 a = __ffma2_rn(f[j], gamma[k][j], both(-c1));
-                    g[j] = __fmul2_rn(__ffma2_rn(xhat, both(-c2), a), both(rstd[u]));
+                    g[j] = __fmul2_rn(__ffma2_rn(__fadd2_rn(x[j], both(-mean[u])), both(-k2), a), both(rstd[u]));
                 }
                 if (has_dz) {
                     read_slot<TS>(x, row + dz_at + k * kStream * threads + mine_s);
