@@ -10,8 +10,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Sums of two values over the CTA, for every thread.  `red` holds 2 * kWarps floats and is free
-// for the next call once all threads have left this one twice (the two halves alternate).
+// Sums of two values over the CTA, for every thread.  `red` holds one pair a warp; the first barrier keeps
+// a call's pairs from being written while an earlier call's are still read.
 __device__ __forceinline__ float2 cta_sum(float2 v, float2* red) {
     v.x = warp_sum(v.x);
     v.y = warp_sum(v.y);

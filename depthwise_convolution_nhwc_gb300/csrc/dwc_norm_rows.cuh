@@ -22,10 +22,11 @@
 // bandwidth with bf16, which leaves half the bytes in flight: 61 us forward for 16384 x 4096.)
 //
 // Measured (device time, GB300, of the bytes that must move at 6.79 TB/s): forward bf16 16384 x 4096
-// 43 us (93 %), fp32 16384 x 4096 81 us (98 %), fp32 200704 x 128 35 us (88 %); residual form, fp32
+// 43 us (92 %), fp32 16384 x 4096 81 us (97 %), fp32 200704 x 128 35 us (88 %); residual form, fp32
 // stream and bf16 branches with dropout, 16384 x 4096 forward 120 us (99 %), backward 174 us
-// (91 %); backward bf16 8192 x 4096 40 us (75 %, of which 6 us are the parameter gradients' second
-// kernel), bf16 200704 x 128 29 us (79 %).  Bound by memory from about 100 MB on; below that by the
+// (91 %), bf16 stream 85 us (93 %) and 111 us (89 %); backward bf16 8192 x 4096 40 us (74 %, of which 6 us
+// are the parameter gradients' second kernel), bf16 200704 x 128 29 us (79 %), fp32 x with bf16 dy
+// 16384 x 4096 120 us (82 %).  Bound by memory from about 100 MB on; below that by the
 // two launches' and the copies' latency, a few microseconds.
 #pragma once
 
