@@ -14,7 +14,8 @@ FH x FW x C, all contiguous.  Inputs are fp32, bf16 or fp16 (one dtype per call)
 are always fp32.
 
 Layer norm, dropout and their residual form over the same channels-last rows
-(``include/dwc_norm.h``) are in ``norm.py`` and re-exported here.
+(``include/dwc_norm.h``) are in ``norm.py`` and re-exported here, as are the causal convolution and
+the selective scan along sequences (``include/dwc_seq.h``) of ``seq.py``.
 """
 from __future__ import annotations
 
@@ -42,8 +43,39 @@ EXPORTS = ("dwc_fwd", "dwc_fwd_ex", "dwc_fwd_bn_act", "dwc_bwd_data", "dwc_bwd_d
            "dwc_testing_prefer_family", "dwc_testing_tc_row_pairs",
            "dwc_layer_norm_fwd", "dwc_layer_norm_bwd_workspace_size", "dwc_layer_norm_bwd",
            "dwc_dropout_fwd", "dwc_dropout_bwd", "dwc_add_layer_norm_fwd",
-           "dwc_add_layer_norm_bwd")
+           "dwc_add_layer_norm_bwd", "dwc_block_norm_fwd", "dwc_block_norm_bwd_workspace_size",
+           "dwc_block_norm_bwd", "dwc_causal_conv_fwd", "dwc_causal_conv_bwd_workspace_size",
+           "dwc_causal_conv_bwd", "dwc_causal_conv_step", "dwc_selective_scan_saved_floats",
+           "dwc_selective_scan_fwd_workspace_size", "dwc_selective_scan_bwd_workspace_size",
+           "dwc_selective_scan_fwd", "dwc_selective_scan_bwd", "dwc_selective_scan_step",
+           "dwc_zero_beside_sequences")
 FMA_KINDS = {"ffma": 0, "ffma2": 1, "hfma2": 2, "bf16x2": 3}  # dwc_fma_rate_probe kinds
+
+
+
+class Rows(ctypes.Structure):
+    """dwc_rows_t: a view of positions."""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_longlong), ("row_stride", ctypes.c_longlong)]
+
+
+class Seqs(ctypes.Structure):
+    """dwc_seqs_t."""
+    _fields_ = [("count", ctypes.c_int), ("length", ctypes.c_longlong), ("offsets", ctypes.c_void_p)]
+
+
+class CausalConv(ctypes.Structure):
+    """dwc_causal_conv_t."""
+    _fields_ = [("seqs", Seqs), ("C", ctypes.c_int), ("K", ctypes.c_int), ("act", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("param_dtype", ctypes.c_int), ("x", Rows), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("state", ctypes.c_void_p)]
+
+
+class Scan(ctypes.Structure):
+    """dwc_scan_t."""
+    _fields_ = [("seqs", Seqs), ("C", ctypes.c_int), ("N", ctypes.c_int), ("G", ctypes.c_int), ("softplus", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("u", Rows), ("dt", Rows), ("z", Rows), ("b", Rows), ("c", Rows),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -127,6 +159,30 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                                [vp, vp, vp, vp, ll, i, i, i, vp, sz, vp])
         for f in (lib.dwc_layer_norm_fwd, lib.dwc_layer_norm_bwd, lib.dwc_dropout_fwd, lib.dwc_dropout_bwd,
                   lib.dwc_add_layer_norm_fwd, lib.dwc_add_layer_norm_bwd):
+            f.restype = i
+        act = [vp, ll, i]
+        lib.dwc_block_norm_fwd.argtypes = ([vp, ll, vp, ll] + act + [vp, vp, vp, i, ctypes.c_float, ctypes.c_float] +
+                                           [vp, vp, vp, vp, ll, i, i, i, vp])
+        lib.dwc_block_norm_bwd_workspace_size.argtypes = [ll, i]
+        lib.dwc_block_norm_bwd.argtypes = ([vp, ll] * 4 + act + [vp, vp, vp, vp, vp, i, ctypes.c_float] + [vp] * 6 +
+                                           [ll, i, i, i, vp, sz, vp])
+        conv, scan, rows = (ctypes.POINTER(s) for s in (CausalConv, Scan, Rows))
+        lib.dwc_zero_beside_sequences.argtypes = [ctypes.POINTER(Seqs), ctypes.POINTER(vp), ctypes.POINTER(ll), i, vp]
+        lib.dwc_causal_conv_fwd.argtypes = [conv, vp, vp, vp]
+        lib.dwc_causal_conv_bwd_workspace_size.argtypes = [conv]
+        lib.dwc_causal_conv_bwd.argtypes = [conv, rows] + [vp] * 6 + [sz, vp]
+        lib.dwc_causal_conv_step.argtypes = [conv, vp, ll, vp, vp]
+        for f in (lib.dwc_selective_scan_saved_floats, lib.dwc_selective_scan_fwd_workspace_size,
+                  lib.dwc_selective_scan_bwd_workspace_size):
+            f.argtypes = [scan]
+            f.restype = sz
+        lib.dwc_block_norm_bwd_workspace_size.restype = lib.dwc_causal_conv_bwd_workspace_size.restype = sz
+        lib.dwc_selective_scan_fwd.argtypes = [scan] + [vp] * 5 + [sz, vp]
+        lib.dwc_selective_scan_bwd.argtypes = [scan, rows] + [vp] * 12 + [sz, vp]
+        lib.dwc_selective_scan_step.argtypes = [scan, vp, ll, vp, vp]
+        for f in (lib.dwc_block_norm_fwd, lib.dwc_block_norm_bwd, lib.dwc_zero_beside_sequences, lib.dwc_causal_conv_fwd,
+                  lib.dwc_causal_conv_bwd, lib.dwc_causal_conv_step, lib.dwc_selective_scan_fwd,
+                  lib.dwc_selective_scan_bwd, lib.dwc_selective_scan_step):
             f.restype = i
         if path is None:
             _lib = lib
@@ -339,11 +395,15 @@ def kernel_launches(pass_: str, N, H, W, C, FH, FW, stride, pad, dtype_code) -> 
     return int(load_library().dwc_kernel_launches(p, N, H, W, C, FH, FW, stride, pad, dtype_code))
 
 
-from .norm import (add_layer_norm_bwd, add_layer_norm_fwd, dropout_bwd, dropout_fwd,  # noqa: E402
-                   layer_norm_bwd, layer_norm_fwd)
+from .norm import (add_layer_norm_bwd, add_layer_norm_fwd, block_norm_bwd, block_norm_fwd,  # noqa: E402
+                   dropout_bwd, dropout_fwd, layer_norm_bwd, layer_norm_fwd)
+from .seq import (causal_conv_bwd, causal_conv_fwd, causal_conv_step, selective_scan_bwd,  # noqa: E402
+                  selective_scan_fwd, selective_scan_step)
 
 __all__ = ["build", "load_library", "fwd", "fwd_bn_act", "bwd_data", "bwd_filter",
            "bwd_filter_workspace_size", "device_status", "set_wait_limit_ns", "fma_rate_probe",
            "path", "kernel_launches", "status_string", "DwcError", "EXPORTS", "FMA_KINDS",
            "LIB_PATH", "layer_norm_fwd", "layer_norm_bwd", "dropout_fwd", "dropout_bwd",
-           "add_layer_norm_fwd", "add_layer_norm_bwd"]
+           "add_layer_norm_fwd", "add_layer_norm_bwd", "block_norm_fwd", "block_norm_bwd",
+           "causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "selective_scan_fwd",
+           "selective_scan_bwd", "selective_scan_step"]

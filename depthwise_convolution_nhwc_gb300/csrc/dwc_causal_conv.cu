@@ -1,0 +1,444 @@
+// dwc_causal_conv.cu -- the short causal depthwise convolution along sequences, forward, backward and
+// for single tokens.
+//
+//     pre[t, c] = bias[c] + sum_k w[k, c] x[t - K + 1 + k, c],  y = act(pre)
+//     dpre = dy act'(pre),  dx[t] = sum_k w[k] dpre[t + K - 1 - k],  dw[k] = sum_t dpre[t] x[t - K + 1 + k]
+//
+// Bound by memory: x (and dy) are read once and y (dx) written once.  A thread owns V adjacent
+// channels and walks along a run of positions with the last K inputs in registers; the run's K - 1
+// rows in front (and, backward, behind) are read again from L1 or L2.
+#include <algorithm>
+
+#include "dwc_seq_device.cuh"
+
+namespace dwc {
+namespace {
+
+constexpr int kThreads = 128;
+
+// V values of a row.
+template <typename T, int V>
+__device__ __forceinline__ void get(float (&f)[V], const T* p) {
+    if constexpr (V == 8) {
+        Vec8<T> v;
+        float2 g[4];
+        v.load(p);
+        v.widen(g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = g[j].x;
+            f[2 * j + 1] = g[j].y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = to_f32(p[j]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void put(T* p, const float (&f)[V]) {
+    if constexpr (V == 8) {
+        float2 g[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = make_float2(f[2 * j], f[2 * j + 1]);
+        Vec8<T>::store(p, g);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) store_out(p + j, f[j]);
+    }
+}
+
+// Input at position t of a sequence (negative: from its state).
+template <typename T, int V>
+__device__ __forceinline__ void input(float (&f)[V], const T* x, long long row, const T* state, int C, int K, long long t) {
+    if (t >= 0) {
+        get<T, V>(f, x + t * row);
+    } else if (state != nullptr) {
+        get<T, V>(f, state + (t + K - 1) * C);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = 0.f;
+    }
+}
+
+// KM: taps held in registers; K == KM unless KM is 16, which serves every K up to it.
+template <typename T, int KM, int V>
+__global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p, int columns, int run, int blocks) {
+    pdl_trigger();
+    pdl_wait();
+    const int K = KM == 16 ? p.K : KM, C = p.C;
+    const long long slot = blockIdx.x / blocks;
+    const int block = static_cast<int>(blockIdx.x - slot * blocks);
+    const int column = threadIdx.x % columns, group = threadIdx.x / columns;
+    const int c = (block * columns + column) * V;
+    const Piece r = find_piece(p.seqs, slot, p.span);
+    if (!r.some || c >= C) return;
+    const T* x = view_at<T>(p.x, p.seqs, r) + c;
+    const T* state = p.state == nullptr ? nullptr : static_cast<const T*>(p.state) + static_cast<long long>(r.s) * (K - 1) * C + c;
+    T* y = static_cast<T*>(p.y) + dense_row(p.seqs, r) * C + c;
+    float w[KM][V], bias[V], win[KM][V];
+#pragma unroll
+    for (int k = 0; k < KM; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[k][j] = k < K ? load_param(p.w, p.param_type, k * C + c + j, 0.f) : 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) bias[j] = load_param(p.bias, p.param_type, c + j, 0.f);
+    const long long first = r.first + static_cast<long long>(group) * run;
+    const long long end = first + run < r.end ? first + run : r.end;
+    if (first < end) {
+        // win[i]: the input i positions back
+#pragma unroll
+        for (int i = 1; i < KM; ++i)
+            if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
+#pragma unroll 4
+        for (long long t = first; t < end; ++t) {
+            get<T, V>(win[0], x + t * p.x.row);
+            float f[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] = bias[j];
+#pragma unroll
+            for (int i = KM - 1; i >= 0; --i) {
+                if (i >= K) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[j] = fmaf(KM == 16 ? load_param(p.w, p.param_type, (K - 1 - i) * C + c + j, 0.f) : w[KM - 1 - i][j], win[i][j], f[j]);
+            }
+            if (p.silu) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[j] = silu(f[j]);
+            }
+            put<T, V>(y + t * C, f);
+#pragma unroll
+            for (int i = KM - 1; i > 0; --i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) win[i][j] = win[i - 1][j];
+        }
+    }
+    if (r.last && p.final_state != nullptr) {
+        T* out = static_cast<T*>(p.final_state) + static_cast<long long>(r.s) * (K - 1) * C + c;
+        for (int i = group; i < K - 1; i += kThreads / columns) {
+            float f[V];
+            input<T, V>(f, x, p.x.row, state, C, K, r.length - (K - 1) + i);
+            put<T, V>(out + static_cast<long long>(i) * C, f);
+        }
+    }
+}
+
+// The gradient that reaches position t of the sequence (or of its state, t < 0) as the last inputs kept.
+template <typename T, int V>
+__device__ __forceinline__ void add_dfinal(float (&f)[V], const T* dfinal, const Piece& r, int C, int K, long long t) {
+    const long long i = t - (r.length - (K - 1));
+    if (dfinal == nullptr || i < 0) return;
+    float g[V];
+    get<T, V>(g, dfinal + i * C);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] += g[j];
+}
+
+// A thread walks K - 1 positions past its run: position t gives dpre[t], and with it dx[t - K + 1] is
+// complete.  Parameter gradients count the run's own positions; the CTA's groups are added in order.
+template <typename T, int KM, int V>
+__global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p, int columns, int run, int blocks) {
+    __shared__ float sums[kThreads * V];
+    pdl_trigger();
+    pdl_wait();
+    const int K = KM == 16 ? p.K : KM, C = p.C;
+    const long long slot = blockIdx.x / blocks;
+    const int block = static_cast<int>(blockIdx.x - slot * blocks);
+    const int column = threadIdx.x % columns, group = threadIdx.x / columns, groups = kThreads / columns;
+    const int c = (block * columns + column) * V;
+    const Piece r = find_piece(p.seqs, slot, p.span);
+    const bool here = r.some && c < C;
+    float w[KM][V], bias[V], win[KM][V], dpre[KM][V], dw[KM][V], db[V];
+#pragma unroll
+    for (int k = 0; k < KM; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[k][j] = here && k < K ? load_param(p.w, p.param_type, k * C + c + j, 0.f) : 0.f;
+            dw[k][j] = 0.f;
+            dpre[k][j] = 0.f;
+            win[k][j] = 0.f;
+        }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        bias[j] = here ? load_param(p.bias, p.param_type, c + j, 0.f) : 0.f;
+        db[j] = 0.f;
+    }
+    if (here) {
+        const T* x = view_at<T>(p.x, p.seqs, r) + c;
+        const T* dy = view_at<T>(p.dy, p.seqs, r) + c;
+        const long long kept = static_cast<long long>(r.s) * (K - 1) * C + c;
+        const T* state = p.state == nullptr ? nullptr : static_cast<const T*>(p.state) + kept;
+        const T* dfinal = p.dfinal == nullptr ? nullptr : static_cast<const T*>(p.dfinal) + kept;
+        T* dx = static_cast<T*>(p.dx) + dense_row(p.seqs, r) * C + c;
+        T* dstate = p.dstate == nullptr ? nullptr : static_cast<T*>(p.dstate) + kept;
+        const long long first = r.first + static_cast<long long>(group) * run;
+        const long long end = first + run < r.end ? first + run : r.end;
+        // the first run's walk begins with the state's positions
+        const long long low = first == 0 ? -(K - 1) : first;
+        if (first < end || first == 0) {
+#pragma unroll
+            for (int i = 1; i < KM; ++i)
+                if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
+            for (long long t = first; t < end + K - 1; ++t) {
+                if (t < r.length) {
+                    float f[V], g[V];
+                    get<T, V>(win[0], x + t * p.x.row);
+                    get<T, V>(g, dy + t * p.dy.row);
+                    if (p.silu) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) f[j] = bias[j];
+#pragma unroll
+                        for (int i = KM - 1; i >= 0; --i) {
+                            if (i >= K) continue;
+#pragma unroll
+                            for (int j = 0; j < V; ++j) f[j] = fmaf(KM == 16 ? load_param(p.w, p.param_type, (K - 1 - i) * C + c + j, 0.f) : w[KM - 1 - i][j], win[i][j], f[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < V; ++j) g[j] *= silu_slope(f[j], sigmoid(f[j]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < V; ++j) dpre[0][j] = g[j];
+                    if (t < end) {
+#pragma unroll
+                        for (int i = 0; i < KM; ++i)
+#pragma unroll
+                            for (int j = 0; j < V; ++j)
+                                if (i < K) dw[i][j] = fmaf(g[j], win[i][j], dw[i][j]);   // of tap K - 1 - i
+#pragma unroll
+                        for (int j = 0; j < V; ++j) db[j] += g[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) dpre[0][j] = 0.f;
+                }
+                const long long to = t - (K - 1);
+                if (to >= low) {
+                    float f[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[j] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < KM; ++i) {
+                        if (i >= K) continue;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) f[j] = fmaf(w[i][j], dpre[i][j], f[j]);
+                    }
+                    add_dfinal<T, V>(f, dfinal, r, C, K, to);
+                    if (to >= 0) put<T, V>(dx + to * C, f);
+                    else if (dstate != nullptr) put<T, V>(dstate + (to + K - 1) * C, f);
+                }
+#pragma unroll
+                for (int i = KM - 1; i > 0; --i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        win[i][j] = win[i - 1][j];
+                        dpre[i][j] = dpre[i - 1][j];
+                    }
+            }
+        }
+    }
+    if (p.partial == nullptr) return;
+    float* part = p.partial + slot * (K + 1) * C;
+#pragma unroll
+    for (int k = 0; k <= KM; ++k) {
+        if (k > K) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sums[j * kThreads + threadIdx.x] = k < K ? dw[KM == 16 ? 0 : KM - 1 - k < 0 ? 0 : KM - 1 - k][j] : db[j];
+        if (KM == 16 && k < K) {
+#pragma unroll
+            for (int i = 0; i < KM; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (i == K - 1 - k) sums[j * kThreads + threadIdx.x] = dw[i][j];
+        }
+        __syncthreads();
+        if (group == 0 && c < C) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float s = 0.f;
+                for (int g = 0; g < groups; ++g) s += sums[j * kThreads + g * columns + column];
+                part[static_cast<long long>(k) * C + c + j] = s;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// One position a sequence: a thread per channel; the state's rows move up by one in place.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(CausalConv p, T* states, long long state_stride) {
+    pdl_trigger();
+    pdl_wait();
+    const int K = p.K, C = p.C;
+    const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= static_cast<long long>(p.seqs.count) * C) return;
+    const int s = static_cast<int>(i / C), c = static_cast<int>(i - static_cast<long long>(s) * C);
+    T* state = states + s * state_stride + c;
+    float f = load_param(p.bias, p.param_type, c, 0.f);
+    for (int k = 0; k < K - 1; ++k) {
+        const T v = state[static_cast<long long>(k) * C];
+        f = fmaf(load_param(p.w, p.param_type, k * C + c, 0.f), to_f32(v), f);
+        if (k > 0) state[static_cast<long long>(k - 1) * C] = v;
+    }
+    const T v = static_cast<const T*>(p.x.p)[s * p.x.seq + c];
+    f = fmaf(load_param(p.w, p.param_type, (K - 1) * C + c, 0.f), to_f32(v), f);
+    if (K > 1) state[static_cast<long long>(K - 2) * C] = v;
+    store_out(static_cast<T*>(p.y) + i, p.silu ? silu(f) : f);
+}
+
+// Column sums of `count` rows, `stride` apart: a CTA takes 32 columns, each warp every 32nd row.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) row_sum_kernel(const float* rows, long long count, long long stride,
+                                                              long long width, float* out) {
+    __shared__ float sums[32][33];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long j = static_cast<long long>(blockIdx.x) * 32 + lane;
+    float s = 0.f;
+    if (j < width)
+        for (long long k = warp; k < count; k += 8 * 32) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = k + 32 * i < count ? rows[(k + 32 * i) * stride + j] : 0.f;
+            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+        }
+    sums[warp][lane] = s;
+    __syncthreads();
+    s = warp_sum(sums[lane][warp]);
+    const long long o = static_cast<long long>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && o < width) out[o] = s;
+}
+
+// (nearly always there is nothing to do: the CTAs read two offsets and leave)
+__global__ void __launch_bounds__(256) zero_beside_kernel(ZeroBeside p) {
+    pdl_trigger();
+    pdl_wait();
+    const long long first = seq_offset(p.seqs, 0), last = seq_offset(p.seqs, p.seqs.count);
+    const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<long long>(gridDim.x) * 256;
+    for (int i = 0; i < p.count; ++i) {
+        uint16_t* to = static_cast<uint16_t*>(p.p[i]);
+        for (long long j = at; j < first * p.halves[i]; j += step) to[j] = 0;
+        for (long long j = max(first, last) * p.halves[i] + at; j < p.seqs.length * p.halves[i]; j += step) to[j] = 0;
+    }
+}
+
+// How a call is laid out: lanes across `columns` vectors, and runs of positions.
+struct Layout {
+    int columns, run, blocks;
+    long long slots;
+};
+
+int columns_for(int vectors) {
+    int n = 1;
+    while (n < vectors && n < 32) n *= 2;
+    return n;
+}
+
+template <typename T, int KM, int V>
+cudaError_t fwd_t(CausalConv p) {
+    Layout l;
+    const int vectors = (p.C + V - 1) / V;
+    l.columns = columns_for(vectors);
+    l.blocks = (vectors + l.columns - 1) / l.columns;
+    l.run = 16;
+    p.span = static_cast<long long>(kThreads / l.columns) * l.run;
+    l.slots = seq_slots(p.seqs, p.span);
+    const long long grid = l.slots * l.blocks;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(causal_conv_fwd_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p,
+                      l.columns, l.run, l.blocks);
+}
+
+template <typename T, int KM, int V>
+cudaError_t bwd_t(const CausalConv& p) {
+    const int vectors = (p.C + V - 1) / V, columns = columns_for(vectors), blocks = (vectors + columns - 1) / columns;
+    const int groups = kThreads / columns;
+    const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaError_t err = launch_pdl(causal_conv_bwd_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                                 p.stream, p, columns, static_cast<int>((p.span + groups - 1) / groups), blocks);
+    if (err != cudaSuccess || p.partial == nullptr) return err;
+    const long long taps = static_cast<long long>(p.K) * p.C, width = taps + p.C;
+    if (p.dw != nullptr) err = launch_row_sum(p.partial, slots, width, taps, p.dw, p.stream);
+    if (err == cudaSuccess && p.dbias != nullptr) err = launch_row_sum(p.partial + taps, slots, width, p.C, p.dbias, p.stream);
+    return err;
+}
+
+// 8 channels a thread where every tensor allows it, else one.
+bool vectors_of(const CausalConv& p, bool backward) {
+    const size_t a = 8 * static_cast<size_t>(elem_bytes(p.type));
+    const auto off = [&](const void* t) { return reinterpret_cast<uintptr_t>(t) % a != 0; };
+    return p.C % 8 == 0 && p.x.vec && !off(p.state) &&
+           (backward ? p.dy.vec && !off(p.dx) && !off(p.dstate) && !off(p.dfinal) : !off(p.y) && !off(p.final_state));
+}
+
+template <typename T>
+cudaError_t fwd_k(const CausalConv& p) {
+    const bool vec = vectors_of(p, false);
+    switch (p.K) {
+        case 2: return vec ? fwd_t<T, 2, 8>(p) : fwd_t<T, 2, 1>(p);
+        case 3: return vec ? fwd_t<T, 3, 8>(p) : fwd_t<T, 3, 1>(p);
+        case 4: return vec ? fwd_t<T, 4, 8>(p) : fwd_t<T, 4, 1>(p);
+        default: return fwd_t<T, 16, 1>(p);
+    }
+}
+
+template <typename T>
+cudaError_t bwd_k(const CausalConv& p) {
+    const bool vec = vectors_of(p, true);
+    switch (p.K) {
+        case 2: return vec ? bwd_t<T, 2, 8>(p) : bwd_t<T, 2, 1>(p);
+        case 3: return vec ? bwd_t<T, 3, 8>(p) : bwd_t<T, 3, 1>(p);
+        case 4: return vec ? bwd_t<T, 4, 8>(p) : bwd_t<T, 4, 1>(p);
+        default: return bwd_t<T, 16, 1>(p);
+    }
+}
+
+template <typename T>
+cudaError_t step_t(const CausalConv& p, void* state, long long state_stride) {
+    const long long grid = (static_cast<long long>(p.seqs.count) * p.C + kThreads - 1) / kThreads;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(causal_conv_step_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p,
+                      static_cast<T*>(state), state_stride);
+}
+
+}  // namespace
+
+long long causal_conv_bwd_span(const Seqs&, int) { return 128; }
+
+cudaError_t launch_causal_conv_fwd(const CausalConv& p) {
+    switch (p.type) {
+        case kF32: return fwd_k<float>(p);
+        case kBF16: return fwd_k<__nv_bfloat16>(p);
+        default: return fwd_k<__half>(p);
+    }
+}
+
+cudaError_t launch_causal_conv_bwd(const CausalConv& p) {
+    switch (p.type) {
+        case kF32: return bwd_k<float>(p);
+        case kBF16: return bwd_k<__nv_bfloat16>(p);
+        default: return bwd_k<__half>(p);
+    }
+}
+
+cudaError_t launch_causal_conv_step(const CausalConv& p, void* state, long long state_stride) {
+    switch (p.type) {
+        case kF32: return step_t<float>(p, state, state_stride);
+        case kBF16: return step_t<__nv_bfloat16>(p, state, state_stride);
+        default: return step_t<__half>(p, state, state_stride);
+    }
+}
+
+cudaError_t launch_zero_beside(const ZeroBeside& p) {
+    return launch_pdl(zero_beside_kernel, dim3(static_cast<unsigned>(device_info().sm_count)), dim3(256), 0, p.stream, p);
+}
+
+cudaError_t launch_row_sum(const float* rows, long long count, long long stride, long long width, float* out,
+                           cudaStream_t stream) {
+    const long long grid = (width + 31) / 32;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(row_sum_kernel, dim3(static_cast<unsigned>(grid)), dim3(kSumThreads), 0, stream, rows, count, stride,
+                      width, out);
+}
+
+}  // namespace dwc

@@ -212,6 +212,18 @@ dwc_status_t dropout(const void* x, long long ldx, void* y, long long rows, int 
     return map_cuda(launch_dropout_general(c));
 }
 
+// What both passes of the block norm check.
+dwc_status_t check_block(const BlockNorm& p, dwc_dtype_t stream_type, dwc_dtype_t branch_type, dwc_dtype_t param_dtype) {
+    if (!valid_pair(stream_type, branch_type) || !known(param_dtype)) return DWC_ERR_INVALID_ARG;
+    if (p.act < DWC_GATE_NONE || p.act > DWC_GATE_SILU || !std::isfinite(p.alpha)) return DWC_ERR_INVALID_ARG;
+    const dwc_status_t st = check_rows(p.rows, p.C);
+    if (st != DWC_OK) return st;
+    const int wb = elem_bytes(branch_type), wp = elem_bytes(param_dtype);
+    if (misaligned(p.gamma_post, wp) || misaligned(p.gamma_pre, wp) || misaligned(p.scale, wp)) return DWC_ERR_ALIGNMENT;
+    return first_error({check_tensor(p.x, p.ld_x, p.rows, p.C, wb, false),
+                        check_tensor(p.gate, p.ld_gate, p.rows, p.C, wb, true)});
+}
+
 }  // namespace
 
 extern "C" {
@@ -330,6 +342,131 @@ dwc_status_t dwc_add_layer_norm_bwd(const void* dy, long long lddy, const void* 
     b.C = C;
     b.stream = stream;
     return norm_bwd(b, res_dtype, dtype, param_dtype, workspace, workspace_bytes);
+}
+
+dwc_status_t dwc_block_norm_fwd(const void* x, long long ldx, const void* res, long long ldres, const void* gate,
+                                long long ldgate, dwc_gate_t act, const void* gamma_post, const void* gamma_pre,
+                                const void* scale, dwc_dtype_t param_dtype, float alpha, float eps, void* z, void* y,
+                                float* rstd_post, float* rstd_pre, long long rows, int C, dwc_dtype_t dtype,
+                                dwc_dtype_t res_dtype, dwc_stream_t stream) {
+    BlockNorm p{};
+    p.x = x;
+    p.ld_x = ldx;
+    p.gate = gate;
+    p.ld_gate = ldgate;
+    p.act = gate != nullptr ? act : DWC_GATE_NONE;
+    p.gamma_post = gamma_post;
+    p.gamma_pre = gamma_pre;
+    p.scale = scale;
+    p.alpha = alpha;
+    p.eps = eps;
+    p.rows = rows;
+    p.C = C;
+    p.stream = stream;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return DWC_ERR_INVALID_ARG;
+    dwc_status_t st = check_block(p, res_dtype, dtype, param_dtype);
+    if (st != DWC_OK) return st;
+    const int ws = elem_bytes(res_dtype), wb = elem_bytes(dtype);
+    st = first_error({check_tensor(res, ldres, rows, C, ws, false), check_tensor(z, C, rows, C, ws, false),
+                      check_tensor(y, C, rows, C, wb, false)});
+    if (st != DWC_OK) return st;
+    if (misaligned(rstd_post, 4) || misaligned(rstd_pre, 4)) return DWC_ERR_ALIGNMENT;
+    const auto over = [&](const void* out, int type) {
+        return first_error({check_in_place(out, type, x, ldx, dtype, rows, C, p.in_place),
+                            check_in_place(out, type, res, ldres, res_dtype, rows, C, p.in_place),
+                            check_in_place(out, type, gate, ldgate, dtype, rows, C, p.in_place)});
+    };
+    st = first_error({over(y, dtype), over(z, res_dtype)});
+    if (st != DWC_OK || rows == 0) return st;
+    p.stream_type = res_dtype;
+    p.branch_type = dtype;
+    p.param_type = param_dtype;
+    p.res = res;
+    p.ld_res = ldres;
+    p.z = z;
+    p.y = y;
+    p.rstd_post_out = rstd_post;
+    p.rstd_pre_out = rstd_pre;
+    return map_cuda(launch_block_norm_fwd(p));
+}
+
+size_t dwc_block_norm_bwd_workspace_size(long long rows, int C) {
+    if (check_rows(rows, C) != DWC_OK || rows == 0) return 0;
+    return static_cast<size_t>(block_norm_partials(rows, C)) * 3 * C * sizeof(float);
+}
+
+dwc_status_t dwc_block_norm_bwd(const void* dy, long long lddy, const void* dz, long long lddz, const void* x,
+                                long long ldx, const void* z, long long ldz, const void* gate, long long ldgate,
+                                dwc_gate_t act, const float* rstd_post, const float* rstd_pre, const void* gamma_post,
+                                const void* gamma_pre, const void* scale, dwc_dtype_t param_dtype, float alpha,
+                                void* dx, void* dres, void* dgate, float* dgamma_post, float* dgamma_pre,
+                                float* dscale, long long rows, int C, dwc_dtype_t dtype, dwc_dtype_t res_dtype,
+                                void* workspace, size_t workspace_bytes, dwc_stream_t stream) {
+    BlockNorm p{};
+    p.x = x;
+    p.ld_x = ldx;
+    p.gate = gate;
+    p.ld_gate = ldgate;
+    p.act = gate != nullptr ? act : DWC_GATE_NONE;
+    p.gamma_post = gamma_post;
+    p.gamma_pre = gamma_pre;
+    p.scale = scale;
+    p.alpha = alpha;
+    p.rows = rows;
+    p.C = C;
+    p.stream = stream;
+    dwc_status_t st = check_block(p, res_dtype, dtype, param_dtype);
+    if (st != DWC_OK) return st;
+    const int ws = elem_bytes(res_dtype), wb = elem_bytes(dtype);
+    if (rows > 0 && (rstd_post == nullptr || rstd_pre == nullptr)) return DWC_ERR_INVALID_ARG;
+    if (dgate != nullptr && gate == nullptr) return DWC_ERR_INVALID_ARG;
+    st = first_error({check_tensor(dy, lddy, rows, C, wb, false), check_tensor(dz, lddz, rows, C, ws, true),
+                      check_tensor(z, ldz, rows, C, ws, false), check_tensor(dx, C, rows, C, wb, false),
+                      check_tensor(dres, C, rows, C, ws, false), check_tensor(dgate, C, rows, C, wb, true)});
+    if (st != DWC_OK) return st;
+    float* const grads[3] = {dgamma_post, dgamma_pre, dscale};
+    if (misaligned(rstd_post, 4) || misaligned(rstd_pre, 4)) return DWC_ERR_ALIGNMENT;
+    for (float* g : grads)
+        if (misaligned(g, 4)) return DWC_ERR_ALIGNMENT;
+    const auto over = [&](const void* out, int type) {
+        return first_error({check_in_place(out, type, dy, lddy, dtype, rows, C, p.in_place),
+                            check_in_place(out, type, dz, lddz, res_dtype, rows, C, p.in_place),
+                            check_in_place(out, type, x, ldx, dtype, rows, C, p.in_place),
+                            check_in_place(out, type, z, ldz, res_dtype, rows, C, p.in_place),
+                            check_in_place(out, type, gate, ldgate, dtype, rows, C, p.in_place)});
+    };
+    st = first_error({over(dx, dtype), over(dres, res_dtype), over(dgate, dtype)});
+    if (st != DWC_OK) return st;
+    bool params = false;
+    for (int i = 0; i < 3; ++i) {
+        params = params || grads[i] != nullptr;
+        p.grads[i] = grads[i];
+        if (rows == 0 && grads[i] != nullptr) {
+            const cudaError_t err = cudaMemsetAsync(grads[i], 0, static_cast<size_t>(C) * sizeof(float), stream);
+            if (err != cudaSuccess) return map_cuda(err);
+        }
+    }
+    if (rows == 0) return DWC_OK;
+    if (params) {
+        if (workspace == nullptr || workspace_bytes < dwc_block_norm_bwd_workspace_size(rows, C)) return DWC_ERR_WORKSPACE;
+        if (misaligned(workspace, 16)) return DWC_ERR_ALIGNMENT;
+        p.partial = static_cast<float*>(workspace);
+    }
+    p.stream_type = res_dtype;
+    p.branch_type = dtype;
+    p.param_type = param_dtype;
+    p.dy = dy;
+    p.ld_dy = lddy;
+    p.dz = dz;
+    p.ld_dz = lddz;
+    p.z_in = z;
+    p.ld_z = ldz;
+    p.rstd_post = rstd_post;
+    p.rstd_pre = rstd_pre;
+    p.dx = dx;
+    p.dgate = dgate;
+    p.dres = dres;
+    return map_cuda(launch_block_norm_bwd(p));
 }
 
 }  // extern "C"

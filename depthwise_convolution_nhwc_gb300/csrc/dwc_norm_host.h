@@ -118,6 +118,46 @@ private:
     int count_ = 0;
 };
 
+// z = alpha res + scale act(gate) rms_norm(x) gamma_post, y = rms_norm(z) gamma_pre.
+struct BlockNorm {
+    const void* x;                  // branch type, row stride ld_x
+    const void* gate;               // branch type, or null
+    int act;                        // of the gate: 0 none, 1 sigmoid, 2 silu
+    const void* gamma_post;         // may be null (1), as the next two
+    const void* gamma_pre;
+    const void* scale;
+    int param_type;
+    float alpha, eps;
+    long long rows, ld_x, ld_gate;
+    int C;
+    int stream_type, branch_type;
+    cudaStream_t stream;
+    // forward
+    const void* res;                // stream type, row stride ld_res
+    long long ld_res;
+    void* z;                        // stream type
+    void* y;                        // branch type
+    float* rstd_post_out;           // may be null
+    float* rstd_pre_out;            // may be null
+    // backward
+    const void* dy;                 // branch type
+    const void* dz;                 // stream type, or null
+    const void* z_in;               // stream type
+    long long ld_dy, ld_dz, ld_z;
+    const float* rstd_post;
+    const float* rstd_pre;
+    void* dx;                       // branch type
+    void* dgate;                    // branch type, or null
+    void* dres;                     // stream type
+    float* grads[3];                // gamma_post, gamma_pre, scale; each may be null
+    float* partial;                 // rows of 3 C floats (with a parameter gradient only)
+    bool in_place = false;          // an output is one of the inputs
+};
+// Rows of partial parameter gradients that a backward pass may write.
+int block_norm_partials(long long rows, int C);
+cudaError_t launch_block_norm_fwd(const BlockNorm& p);
+cudaError_t launch_block_norm_bwd(const BlockNorm& p);
+
 // General kernels: any row stride, alignment and channel count.
 cudaError_t launch_norm_fwd_general(const NormFwd& p);
 cudaError_t launch_norm_bwd_general(const NormBwd& p);

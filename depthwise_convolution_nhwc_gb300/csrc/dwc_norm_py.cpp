@@ -1,47 +1,14 @@
-// dwc_norm_py.cpp -- host path of the norm and dropout operators for Python (CPython C API).
+// dwc_norm_py.cpp -- host path of the norm, dropout and sequence operators for Python (CPython C API).
 //
 // Small calls are bound by the host: through ctypes and tensor attributes read one by one a
 // backward pass cost 23 us of Python beside 13 us of GPU work.  Here the checks, the outputs'
 // allocation (PyTorch's allocator, so memory belongs to the current stream or graph) and the
 // call of the C ABI (include/dwc_norm.h) are one C++ function per operator.  Nothing is computed
 // here and nothing is kept between calls.  norm.py documents the functions and handles `stream`.
-#include <torch/csrc/Dtype.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-
-#include <cstdint>
-
-#include "../../include/dwc_norm.h"
+#include "dwc_py.h"
+#include "dwc_seq_py.h"
 
 namespace {
-
-using at::ScalarType;
-using at::Tensor;
-
-PyObject* g_error = nullptr;   // DwcError(function, code), given by norm.py
-
-struct Failed {                // a status code of the library
-    const char* fn;
-    int code;
-};
-
-dwc_dtype_t code_of(ScalarType t) {
-    switch (t) {
-        case ScalarType::Float: return DWC_F32;
-        case ScalarType::BFloat16: return DWC_BF16;
-        case ScalarType::Half: return DWC_F16;
-        default: TORCH_CHECK_TYPE(false, "unsupported dtype ", t, " (fp32, bf16 or fp16)");
-    }
-}
-
-const Tensor& tensor(PyObject* o, const char* what) {
-    TORCH_CHECK_TYPE(THPVariable_Check(o), what, " must be a tensor");
-    return THPVariable_Unpack(o);
-}
 
 // Elements between the rows of [..., C]: one stride over all leading axes, adjacent channels.
 int64_t row_stride(const Tensor& t, const char* what) {
@@ -62,12 +29,6 @@ int64_t row_stride(const Tensor& t, const char* what) {
         }
     }
     return ld < 0 ? C : ld;
-}
-
-// A new dense tensor from PyTorch's allocator (the CUDA backend's own factory: the dispatcher's way
-// to it costs as much again).
-Tensor new_tensor(at::IntArrayRef shape, ScalarType type, const at::Device& device) {
-    return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 // The tensor whose shape, device and channels a call goes by.
@@ -130,6 +91,28 @@ void check_apart(const Tensor& out, const char* what, PyObject* vector, const ch
     if (t.numel() > 0) check_apart(out, what, t, 1, t.numel(), t.numel(), name, false);
 }
 
+// Vectors of C values of one type each, or None.
+struct Vectors {
+    const void* p[3] = {nullptr, nullptr, nullptr};
+    dwc_dtype_t type = DWC_F32;
+    Vectors(const Rows& x, std::initializer_list<std::pair<PyObject*, const char*>> list) {
+        bool any = false;
+        int i = -1;
+        for (const auto& [o, what] : list) {
+            ++i;
+            if (o == Py_None) continue;
+            const Tensor& t = tensor(o, what);
+            TORCH_CHECK_VALUE(t.dim() == 1 && t.numel() == x.C && t.device() == x.t.device() && t.is_contiguous(), what,
+                              " must hold ", x.C, " values on ", x.t.device(), " (got ", t.sizes(), " on ", t.device(), ")");
+            const dwc_dtype_t c = code_of(t.scalar_type());
+            TORCH_CHECK_VALUE(!any || c == type, "gamma_post, gamma_pre and scale must have one dtype");
+            type = c;
+            any = true;
+            p[i] = t.data_ptr();
+        }
+    }
+};
+
 // gamma and beta: C values of one type each, or None.
 struct Params {
     const void* p[2] = {nullptr, nullptr};
@@ -158,12 +141,6 @@ unsigned long long word64(PyObject* o) {
     return v;
 }
 
-double number(PyObject* o) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) throw python_error();
-    return v;
-}
-
 // p, seed and offset of a dropout; an offset may be one int64 value on the device.
 struct Random {
     double p;
@@ -181,21 +158,6 @@ struct Random {
         step = static_cast<const unsigned long long*>(t.data_ptr());
     }
 };
-
-// The current stream of the tensors' device, with that device current.
-struct OnDevice {
-    c10::cuda::OptionalCUDAGuard guard;
-    dwc_stream_t stream;
-    explicit OnDevice(const Rows& x) {
-        const auto index = x.t.get_device();
-        if (index != c10::cuda::current_device()) guard.set_index(index);
-        stream = c10::cuda::getCurrentCUDAStream(index).stream();
-    }
-};
-
-void check(const char* fn, dwc_status_t code) {
-    if (code != DWC_OK) throw Failed{fn, static_cast<int>(code)};
-}
 
 // dgamma, dbeta and the workspace of a backward pass.
 struct ParamGrads {
@@ -215,47 +177,6 @@ struct ParamGrads {
     }
 };
 
-PyObject* wrap(const Tensor& t) {
-    if (t.defined()) return THPVariable_Wrap(t);
-    Py_RETURN_NONE;
-}
-
-PyObject* pack(std::initializer_list<const Tensor*> list) {
-    PyObject* tuple = PyTuple_New(static_cast<Py_ssize_t>(list.size()));
-    if (tuple == nullptr) return nullptr;
-    Py_ssize_t i = 0;
-    for (const Tensor* t : list) {
-        PyObject* o = wrap(*t);
-        if (o == nullptr) {
-            Py_DECREF(tuple);
-            return nullptr;
-        }
-        PyTuple_SET_ITEM(tuple, i++, o);
-    }
-    return tuple;
-}
-
-float* fp(const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
-
-using Fast = PyObject* (*)(PyObject* const*);
-
-// The common frame: the number of arguments, and every C++ exception as a Python one.
-template <Fast f, int kArgs>
-PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    TORCH_CHECK_TYPE(n == kArgs, "expected ", kArgs, " arguments, got ", n);
-    try {
-        return f(a);
-    } catch (const Failed& e) {
-        if (PyObject* x = PyObject_CallFunction(g_error, "si", e.fn, e.code)) {
-            PyErr_SetObject(reinterpret_cast<PyObject*>(Py_TYPE(x)), x);
-            Py_DECREF(x);
-        }
-        return nullptr;
-    }
-    END_HANDLE_TH_ERRORS
-}
-
 // (x, gamma, beta, eps, out, out_dtype, stats)
 PyObject* layer_norm_fwd(PyObject* const* a) {
     const Rows x(tensor(a[0], "x"), "x");
@@ -269,7 +190,7 @@ PyObject* layer_norm_fwd(PyObject* const* a) {
     }
     const dwc_dtype_t in = code_of(x.t.scalar_type()), od = code_of(type);
     const float eps = static_cast<float>(number(a[3]));
-    const OnDevice on(x);
+    const OnDevice on(x.t);
     const Tensor y = x.out(a[4], type, "out");
     if (a[4] != Py_None) {
         check_apart(y, "out", x.t, x.rows, x.C, x.ld, "x");
@@ -296,7 +217,7 @@ PyObject* layer_norm_bwd(PyObject* const* a) {
     const float *mean = x.given_stat(a[2], "mean"), *rstd = x.given_stat(a[3], "rstd");
     const Params w(x, a[4], Py_None);
     const dwc_dtype_t type = code_of(x.t.scalar_type()), dtype = code_of(dy.scalar_type());
-    const OnDevice on(x);
+    const OnDevice on(x.t);
     const Tensor dx = x.out(a[5], x.t.scalar_type(), "out");
     if (a[5] != Py_None) {
         check_apart(dx, "out", dy, x.rows, x.C, lddy, "dy");
@@ -319,7 +240,7 @@ PyObject* dropout(PyObject* const* a) {
     const Rows x(tensor(a[0], what), what);
     const Random rnd(x, a[1], a[2], a[3]);
     const dwc_dtype_t type = code_of(x.t.scalar_type());
-    const OnDevice on(x);
+    const OnDevice on(x.t);
     const Tensor y = x.out(a[4], x.t.scalar_type(), "out");
     if (a[4] != Py_None) {
         check_apart(y, "out", x.t, x.rows, x.C, x.ld, what);
@@ -341,7 +262,7 @@ PyObject* add_layer_norm_fwd(PyObject* const* a) {
     const float eps = static_cast<float>(number(a[4]));
     const Random rnd(x, a[5], a[6], a[7]);
     const dwc_dtype_t type = code_of(x.t.scalar_type()), wide = code_of(res.scalar_type());
-    const OnDevice on(x);
+    const OnDevice on(x.t);
     const Tensor y = x.out(a[8], x.t.scalar_type(), "out"), z = x.out(a[9], res.scalar_type(), "z");
     for (int i = 8; i <= 9; ++i) {
         if (a[i] == Py_None) continue;
@@ -384,7 +305,7 @@ PyObject* add_layer_norm_bwd(PyObject* const* a) {
     const Params w(z, a[4], Py_None);
     const Random rnd(z, a[6], a[7], a[8]);
     const dwc_dtype_t type = code_of(dy.scalar_type()), wide = code_of(z.t.scalar_type());
-    const OnDevice on(z);
+    const OnDevice on(z.t);
     const Tensor dres = z.out(Py_None, z.t.scalar_type(), "dres");
     // without dropout and conversion dx is dres
     const bool own = rnd.p != 0.0 || type != wide;
@@ -395,6 +316,103 @@ PyObject* add_layer_norm_bwd(PyObject* const* a) {
                                  rnd.seed, rnd.offset, rnd.step, own ? dx.data_ptr() : nullptr, dres.data_ptr(), g.dg, g.db,
                                  z.rows, static_cast<int>(z.C), type, wide, g.w, g.bytes, on.stream));
     return pack({&dx, &dres, &g.dgamma, &g.dbeta});
+}
+
+// A gate (rows x C of x's type) or None.
+struct Gate {
+    const void* p = nullptr;
+    int64_t ld = 0;
+    dwc_gate_t act;
+    Gate(const Rows& x, PyObject* o, PyObject* kind) : act(gate_code(kind)) {
+        if (o == Py_None) return;
+        const Tensor& t = tensor(o, "gate");
+        TORCH_CHECK_VALUE(t.scalar_type() == x.t.scalar_type(), "gate must have x's dtype");
+        ld = x.like(t, "gate");
+        p = t.data_ptr();
+    }
+};
+
+// (x, res, gamma_post, gamma_pre, gate, scale, alpha, act, eps, out, z, stats)
+PyObject* block_norm_fwd(PyObject* const* a) {
+    const Rows x(tensor(a[0], "x"), "x");
+    const Tensor& res = tensor(a[1], "res");
+    const int64_t ldres = x.like(res, "res");
+    const Vectors w(x, {{a[2], "gamma_post"}, {a[3], "gamma_pre"}, {a[5], "scale"}});
+    const Gate gate(x, a[4], a[7]);
+    const float alpha = static_cast<float>(number(a[6])), eps = static_cast<float>(number(a[8]));
+    const dwc_dtype_t type = code_of(x.t.scalar_type()), wide = code_of(res.scalar_type());
+    const OnDevice on(x.t);
+    const Tensor y = x.out(a[9], x.t.scalar_type(), "out"), z = x.out(a[10], res.scalar_type(), "z");
+    for (int i = 9; i <= 10; ++i) {
+        if (a[i] == Py_None) continue;
+        const Tensor& o = i == 9 ? y : z;
+        const char* what = i == 9 ? "out" : "z";
+        check_apart(o, what, x.t, x.rows, x.C, x.ld, "x");
+        check_apart(o, what, res, x.rows, x.C, ldres, "res");
+        if (gate.p != nullptr) check_apart(o, what, tensor(a[4], "gate"), x.rows, x.C, gate.ld, "gate");
+        check_apart(o, what, a[2], "gamma_post");
+        check_apart(o, what, a[3], "gamma_pre");
+        check_apart(o, what, a[5], "scale");
+    }
+    if (a[9] != Py_None && a[10] != Py_None) check_apart(y, "out", z, x.rows, x.C, x.C, "z", false);
+    Tensor post, pre;
+    const bool stats = a[11] == Py_True;
+    if (stats) {
+        post = x.stat();
+        pre = x.stat();
+    }
+    check("dwc_block_norm_fwd",
+          dwc_block_norm_fwd(x.t.data_ptr(), x.ld, res.data_ptr(), ldres, gate.p, gate.ld, gate.act, w.p[0], w.p[1], w.p[2],
+                             w.type, alpha, eps, z.data_ptr(), y.data_ptr(), fp(post), fp(pre), x.rows,
+                             static_cast<int>(x.C), type, wide, on.stream));
+    return stats ? pack({&y, &z, &post, &pre}) : pack({&y, &z});
+}
+
+// (dy, x, z, rstd_post, rstd_pre, gamma_post, gamma_pre, gate, scale, alpha, act, dz, param_grads)
+PyObject* block_norm_bwd(PyObject* const* a) {
+    const Rows x(tensor(a[1], "x"), "x");
+    const Tensor &dy = tensor(a[0], "dy"), &z = tensor(a[2], "z");
+    TORCH_CHECK_VALUE(dy.scalar_type() == x.t.scalar_type(), "dy must have x's dtype");
+    const int64_t lddy = x.like(dy, "dy"), ldz = x.like(z, "z");
+    int64_t lddz = x.C;
+    const void* dz = nullptr;
+    if (a[11] != Py_None) {
+        const Tensor& t = tensor(a[11], "dz");
+        TORCH_CHECK_VALUE(t.scalar_type() == z.scalar_type(), "dz must have z's dtype");
+        lddz = x.like(t, "dz");
+        dz = t.data_ptr();
+    }
+    const float *post = x.given_stat(a[3], "rstd_post"), *pre = x.given_stat(a[4], "rstd_pre");
+    const Vectors w(x, {{a[5], "gamma_post"}, {a[6], "gamma_pre"}, {a[8], "scale"}});
+    const Gate gate(x, a[7], a[10]);
+    const float alpha = static_cast<float>(number(a[9]));
+    const dwc_dtype_t type = code_of(x.t.scalar_type()), wide = code_of(z.scalar_type());
+    const OnDevice on(x.t);
+    const Tensor dx = x.out(Py_None, x.t.scalar_type(), "dx"), dres = x.out(Py_None, z.scalar_type(), "dres");
+    Tensor dgate, ws, grads[3];
+    if (gate.p != nullptr) dgate = x.out(Py_None, x.t.scalar_type(), "dgate");
+    size_t bytes = 0;
+    if (a[12] == Py_True) {
+        // (gradients of the parameters that the call has)
+        const int at[3] = {5, 6, 8};
+        bool any = false;
+        for (int i = 0; i < 3; ++i) {
+            if (a[at[i]] == Py_None) continue;
+            grads[i] = new_tensor({x.C}, at::kFloat, x.t.device());
+            any = true;
+        }
+        if (any) {
+            bytes = dwc_block_norm_bwd_workspace_size(x.rows, static_cast<int>(x.C));
+            ws = new_tensor({static_cast<int64_t>(bytes)}, at::kByte, x.t.device());
+        }
+    }
+    check("dwc_block_norm_bwd",
+          dwc_block_norm_bwd(dy.data_ptr(), lddy, dz, lddz, x.t.data_ptr(), x.ld, z.data_ptr(), ldz, gate.p, gate.ld,
+                             gate.act, post, pre, w.p[0], w.p[1], w.p[2], w.type, alpha, dx.data_ptr(), dres.data_ptr(),
+                             dgate.defined() ? dgate.data_ptr() : nullptr, fp(grads[0]), fp(grads[1]), fp(grads[2]),
+                             x.rows, static_cast<int>(x.C), type, wide, ws.defined() ? ws.data_ptr() : nullptr, bytes,
+                             on.stream));
+    return pack({&dx, &dres, &dgate, &grads[0], &grads[1], &grads[2]});
 }
 
 // (tensor, name): the row stride a call would use
@@ -412,17 +430,20 @@ PyObject* set_error(PyObject* const* a) {
     Py_RETURN_NONE;
 }
 
-template <Fast f, int kArgs>
-PyMethodDef method(const char* name) {
-    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, kArgs>)), METH_FASTCALL, nullptr};
-}
-
 PyMethodDef g_methods[] = {method<layer_norm_fwd, 7>("layer_norm_fwd"),
                            method<layer_norm_bwd, 7>("layer_norm_bwd"),
                            method<dropout<false>, 5>("dropout_fwd"),
                            method<dropout<true>, 5>("dropout_bwd"),
                            method<add_layer_norm_fwd, 11>("add_layer_norm_fwd"),
                            method<add_layer_norm_bwd, 10>("add_layer_norm_bwd"),
+                           method<block_norm_fwd, 12>("block_norm_fwd"),
+                           method<block_norm_bwd, 13>("block_norm_bwd"),
+                           method<seq::causal_conv_fwd, 8>("causal_conv_fwd"),
+                           method<seq::causal_conv_bwd, 9>("causal_conv_bwd"),
+                           method<seq::causal_conv_step, 6>("causal_conv_step"),
+                           method<seq::scan_fwd, 14>("selective_scan_fwd"),
+                           method<seq::scan_bwd, 14>("selective_scan_bwd"),
+                           method<seq::scan_step, 11>("selective_scan_step"),
                            method<stride_of, 2>("row_stride"),
                            method<set_error, 1>("set_error"),
                            {nullptr, nullptr, 0, nullptr}};

@@ -1,4 +1,4 @@
-"""Layer norm, dropout and their residual form over channels-last rows.
+"""Layer norm, dropout, their residual form and the block norm over channels-last rows.
 
 Binding over the C ABI in ``include/dwc_norm.h``.  Tensors are ``[..., C]`` on a CUDA device, fp32,
 bf16 or fp16, with adjacent channels and one stride between rows (a slice of a larger tensor's
@@ -16,6 +16,11 @@ stream and the inputs are recorded on it.  Nothing falls back to the CPU.
     # z = res + dropout(x), y = layer_norm(z): the end of one residual branch, the norm of the next
     y, z, mean, rstd = add_layer_norm_fwd(x, res, gamma, beta, p=0.1, seed=seed, offset=k, stats=True)
     dx, dres, dgamma, dbeta = add_layer_norm_bwd(dy, z, mean, rstd, gamma, dz, 0.1, seed, k)
+
+    # z = alpha res + scale act(gate) rms_norm(x), y = rms_norm(z): the norms after a block and before the next
+    y, z, rstd_post, rstd_pre = block_norm_fwd(x, res, gamma_post, gamma_pre, gate, scale, stats=True)
+    dx, dres, dgate, dgamma_post, dgamma_pre, dscale = block_norm_bwd(dy, x, z, rstd_post, rstd_pre, gamma_post,
+                                                                      gamma_pre, gate, scale, dz=dz)
 
 The dropout mask is a function of (seed, offset, element index) and is drawn again in the
 backward pass.  Use another offset for every dropout of a step and another seed or offset range
@@ -117,5 +122,31 @@ def add_layer_norm_bwd(dy, z, mean, rstd, gamma=None, dz=None, p: float = 0.0, s
     return (_module or _host()).add_layer_norm_bwd(dy, z, mean, rstd, gamma, dz, p, seed, offset, bool(param_grads))
 
 
+def block_norm_fwd(x, res, gamma_post=None, gamma_pre=None, gate=None, scale=None, alpha: float = 1.0, act: str = "silu",
+                   eps: float = 1e-5, out=None, z=None, stats: bool = False, stream=None):
+    """z = alpha * res + scale * act(gate) * rms_norm(x) * gamma_post, y = rms_norm(z) * gamma_pre in one pass:
+    the norm behind a block with its gate and scale, the residual sum and the norm in front of the next block.
+    (y, z), or (y, z, rstd_post, rstd_pre) with ``stats``.  y and gate have x's dtype, z has res's: the same, or
+    fp32 with a 16-bit x.  gamma_post, gamma_pre, scale: C values of one dtype each, or None; act "none",
+    "sigmoid" or "silu".  With z=res the residual stream is updated in place."""
+    if stream is not None:
+        return _on(stream, block_norm_fwd, x, res, gamma_post, gamma_pre, gate, scale, alpha, act, eps, out, z, stats)
+    return (_module or _host()).block_norm_fwd(x, res, gamma_post, gamma_pre, gate, scale, alpha, act, eps, out, z,
+                                               bool(stats))
+
+
+def block_norm_bwd(dy, x, z, rstd_post, rstd_pre, gamma_post=None, gamma_pre=None, gate=None, scale=None,
+                   alpha: float = 1.0, act: str = "silu", dz=None, param_grads: bool = True, stream=None):
+    """(dx, dres, dgate, dgamma_post, dgamma_pre, dscale) of ``block_norm_fwd`` from dy, ``dz`` (the gradient that
+    reaches z from the rest of the residual stream; None: zero), its x, z, statistics and parameters: dx and dgate
+    in x's dtype, dres in z's, the others fp32 (None for what the call does not have, or without
+    ``param_grads``)."""
+    if stream is not None:
+        return _on(stream, block_norm_bwd, dy, x, z, rstd_post, rstd_pre, gamma_post, gamma_pre, gate, scale, alpha, act,
+                   dz, param_grads)
+    return (_module or _host()).block_norm_bwd(dy, x, z, rstd_post, rstd_pre, gamma_post, gamma_pre, gate, scale, alpha,
+                                               act, dz, bool(param_grads))
+
+
 __all__ = ["layer_norm_fwd", "layer_norm_bwd", "dropout_fwd", "dropout_bwd", "add_layer_norm_fwd",
-           "add_layer_norm_bwd"]
+           "add_layer_norm_bwd", "block_norm_fwd", "block_norm_bwd"]

@@ -77,6 +77,13 @@ typedef enum {
     DWC_F16 = 2   /* IEEE fp16 inputs, fp32 accumulation and output */
 } dwc_dtype_t;
 
+/* Elementwise functions of gates and of the operators along sequences. */
+typedef enum {
+    DWC_GATE_NONE = 0,    /* v */
+    DWC_GATE_SIGMOID = 1, /* 1 / (1 + exp(-v)) */
+    DWC_GATE_SILU = 2     /* v / (1 + exp(-v)) */
+} dwc_gate_t;
+
 typedef enum {
     DWC_OK = 0,
     DWC_ERR_INVALID_ARG = 1, /* null pointer, negative size, stride < 1, pad < 0, empty filter,

@@ -1,5 +1,5 @@
 /*
- * dwc_norm.h -- layer norm, dropout and their residual form over channels-last rows
+ * dwc_norm.h -- layer norm, dropout, their residual form and the block norm over channels-last rows
  * (libdwc_gb300.so; the conventions of dwc.h hold: device pointers owned by the caller,
  * asynchronous calls on `stream`, host-side validation, status codes, no call aborts or throws,
  * programmatic dependent launches).
@@ -127,6 +127,51 @@ dwc_status_t dwc_add_layer_norm_bwd(const void* dy, long long lddy, const void* 
                                     float* dgamma, float* dbeta, long long rows, int C,
                                     dwc_dtype_t dtype, dwc_dtype_t res_dtype, void* workspace,
                                     size_t workspace_bytes, dwc_stream_t stream);
+
+/* The norms on either side of a residual connection, with a gate and residual scales, in one pass:
+ *     rstd_post = 1 / sqrt(sum_c x^2 / C + eps),   n = x * rstd_post * gamma_post
+ *     z = alpha * res + scale * act(gate) * n
+ *     rstd_pre = 1 / sqrt(sum_c z^2 / C + eps),    y = z * rstd_pre * gamma_pre
+ * (the norm after a block, its gate and scale, the residual sum, the norm in front of the next
+ * block; statistics and y from the fp32 sum, z rounded once where it is stored).
+ *   x : rows x C, dtype, row stride ldx (the block's output)
+ *   res : rows x C, res_dtype, row stride ldres (the residual stream)
+ *   gate : rows x C, dtype, row stride ldgate, or NULL (act is then not used)
+ *   gamma_post, gamma_pre, scale : C values of param_dtype each, or NULL (1)
+ *   z : rows x C, res_dtype (out)   y : rows x C, dtype (out); in place as above
+ *   rstd_post, rstd_pre : rows fp32 values each (out), or NULL
+ *   res_dtype : dtype, or DWC_F32
+ * The rest and the errors as dwc_layer_norm_fwd; DWC_ERR_INVALID_ARG also for an unknown act and a
+ * non-finite alpha.  A row of zeros gives zeros (with eps = 0: NaN, 0 * infinity). */
+dwc_status_t dwc_block_norm_fwd(const void* x, long long ldx, const void* res, long long ldres, const void* gate,
+                                long long ldgate, dwc_gate_t act, const void* gamma_post, const void* gamma_pre,
+                                const void* scale, dwc_dtype_t param_dtype, float alpha, float eps, void* z, void* y,
+                                float* rstd_post, float* rstd_pre, long long rows, int C, dwc_dtype_t dtype,
+                                dwc_dtype_t res_dtype, dwc_stream_t stream);
+
+/* Bytes of workspace dwc_block_norm_bwd needs for rows x C on the CURRENT device (0 for invalid
+ * sizes). */
+size_t dwc_block_norm_bwd_workspace_size(long long rows, int C);
+
+/* Backward of dwc_block_norm_fwd; with zhat = z * rstd_pre, xhat = x * rstd_post, a = dy * gamma_pre:
+ *     g = dz + rstd_pre * (a - zhat * mean_c(a * zhat)),   dres = alpha * g
+ *     dn = scale * act(gate) * g,   b = dn * gamma_post
+ *     dx = rstd_post * (b - xhat * mean_c(b * xhat)),   dgate = scale * g * n * act'(gate)
+ *     dgamma_pre = sum of dy * zhat, dgamma_post = sum of dn * xhat, dscale = sum of g * act(gate) * n
+ *   dy : rows x C, dtype     dz : rows x C, res_dtype: the gradient that reaches z from the rest of the
+ *   residual stream, or NULL (zero)     x, gate, z, rstd_post, rstd_pre : as in the forward pass
+ *   dx : rows x C, dtype (out)     dres : rows x C, res_dtype (out)
+ *   dgate : rows x C, dtype (out), or NULL
+ *   dgamma_post, dgamma_pre, dscale : C fp32 values each (out), or NULL; rows = 0 writes zeros
+ *   workspace : 16-byte aligned, contents ignored and clobbered (not needed without parameter gradients)
+ * Errors as dwc_layer_norm_bwd and dwc_block_norm_fwd; DWC_ERR_INVALID_ARG also for a dgate without a gate. */
+dwc_status_t dwc_block_norm_bwd(const void* dy, long long lddy, const void* dz, long long lddz, const void* x,
+                                long long ldx, const void* z, long long ldz, const void* gate, long long ldgate,
+                                dwc_gate_t act, const float* rstd_post, const float* rstd_pre, const void* gamma_post,
+                                const void* gamma_pre, const void* scale, dwc_dtype_t param_dtype, float alpha,
+                                void* dx, void* dres, void* dgate, float* dgamma_post, float* dgamma_pre,
+                                float* dscale, long long rows, int C, dwc_dtype_t dtype, dwc_dtype_t res_dtype,
+                                void* workspace, size_t workspace_bytes, dwc_stream_t stream);
 
 #ifdef __cplusplus
 }
