@@ -7,8 +7,7 @@
 // thread at a time.
 #include <algorithm>
 
-#include "dwc_norm_device.cuh"
-#include "dwc_seq_host.h"
+#include "dwc_block_norm_device.cuh"
 
 namespace dwc {
 namespace {
@@ -25,17 +24,6 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s += red[w];
     return s;
-}
-
-// act(v) and, where asked for, its derivative.
-__device__ __forceinline__ float gate_of(float v, int act, float* slope = nullptr) {
-    if (act == 0) {
-        if (slope != nullptr) *slope = 1.f;
-        return v;
-    }
-    const float s = __fdividef(1.f, 1.f + expf(-v));
-    if (slope != nullptr) *slope = act == 1 ? s * (1.f - s) : fmaf(v * s, 1.f - s, s);
-    return act == 1 ? s : __fdividef(v, 1.f + expf(-v));
 }
 
 template <typename TS, typename TB>
@@ -87,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_general_kernel(BlockN
     pdl_wait();
     const int C = p.C;
     const float inv = 1.f / static_cast<float>(C);
-    float* part = p.partial == nullptr ? nullptr : p.partial + static_cast<size_t>(blockIdx.x) * 3 * C;
+    float* part = p.partial == nullptr ? nullptr : p.partial + static_cast<size_t>(blockIdx.x) * 2 * C;
     bool first_row = true;
     for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const TB* dy = static_cast<const TB*>(p.dy) + r * p.ld_dy;
@@ -109,12 +97,12 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_general_kernel(BlockN
         for (int c = threadIdx.x; c < C; c += kThreads) {
             const float g = stream(c), xhat = to_f32(x[c]) * post, gamma = load_param(p.gamma_post, p.param_type, c, 1.f);
             const float act = gate != nullptr ? gate_of(to_f32(gate[c]), p.act) : 1.f;
-            const float dn = load_param(p.scale, p.param_type, c, 1.f) * act * g;
-            s = fmaf(dn * gamma, xhat, s);
+            const float t = g * act;
+            s = fmaf(load_param(p.scale, p.param_type, c, 1.f) * gamma * t, xhat, s);
             if (part != nullptr) {
-                const float v[3] = {dn * xhat, to_f32(dy[c]) * (to_f32(z[c]) * pre), g * act * (xhat * gamma)};
+                const float v[2] = {t * xhat, to_f32(dy[c]) * (to_f32(z[c]) * pre)};
 #pragma unroll
-                for (int i = 0; i < 3; ++i) part[i * static_cast<size_t>(C) + c] = first_row ? v[i] : part[i * static_cast<size_t>(C) + c] + v[i];
+                for (int i = 0; i < 2; ++i) part[i * static_cast<size_t>(C) + c] = first_row ? v[i] : part[i * static_cast<size_t>(C) + c] + v[i];
             }
         }
         const float m_post = cta_sum(s, red) * inv;
@@ -131,6 +119,47 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_general_kernel(BlockN
     }
 }
 
+// Column sums of the partial rows: a CTA takes kWidth columns of both sums, each thread every
+// (1024 / kWidth)-th row, 8 loads in flight.  A fixed order, whatever the timing.
+constexpr int kSumThreads = 1024;
+template <int kWidth>
+__global__ void __launch_bounds__(kSumThreads) block_norm_param_kernel(BlockNorm p, int count) {
+    constexpr int kSlots = kSumThreads / kWidth;
+    __shared__ float sums[kSlots][kWidth + 1];
+    pdl_trigger();
+    const int col = threadIdx.x % kWidth, slot = threadIdx.x / kWidth, C = p.C;
+    const long long j = static_cast<long long>(blockIdx.x) * kWidth + col;
+    const size_t step = static_cast<size_t>(2) * C;
+    float s = 0.f;
+    pdl_wait();
+    if (j < 2LL * C) {
+        const float* from = p.partial + j;
+        for (int k = slot; k < count; k += 8 * kSlots) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = k + kSlots * i < count ? from[(k + kSlots * i) * step] : 0.f;
+            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+        }
+    }
+    sums[slot][col] = s;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp >= kWidth) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = lane; i < kSlots; i += 32) s += sums[i][warp];
+    s = warp_sum(s);
+    const long long o = static_cast<long long>(blockIdx.x) * kWidth + warp;
+    if (lane != 0 || o >= 2LL * C) return;
+    const int c = static_cast<int>(o < C ? o : o - C);
+    if (o >= C) {
+        if (p.grads[1] != nullptr) p.grads[1][c] = s;
+        return;
+    }
+    if (p.grads[0] != nullptr) p.grads[0][c] = load_param(p.scale, p.param_type, c, 1.f) * s;
+    if (p.grads[2] != nullptr) p.grads[2][c] = load_param(p.gamma_post, p.param_type, c, 1.f) * s;
+}
+
 template <typename TS, typename TB>
 cudaError_t fwd_t(const BlockNorm& p) {
     const long long cap = static_cast<long long>(device_info().sm_count) * 64;
@@ -141,15 +170,14 @@ cudaError_t fwd_t(const BlockNorm& p) {
 template <typename TS, typename TB>
 cudaError_t bwd_t(const BlockNorm& p) {
     const int parts = block_norm_partials(p.rows, p.C);
-    cudaError_t err = launch_pdl(block_norm_bwd_general_kernel<TS, TB>, dim3(static_cast<unsigned>(parts)), dim3(kThreads), 0, p.stream, p);
-    if (p.partial == nullptr) return err;
-    for (int i = 0; i < 3 && err == cudaSuccess; ++i)
-        if (p.grads[i] != nullptr) err = launch_row_sum(p.partial + static_cast<size_t>(i) * p.C, parts, 3LL * p.C, p.C, p.grads[i], p.stream);
-    return err;
+    const cudaError_t err = launch_pdl(block_norm_bwd_general_kernel<TS, TB>, dim3(static_cast<unsigned>(parts)), dim3(kThreads), 0,
+                                       p.stream, p);
+    return err != cudaSuccess || p.partial == nullptr ? err : launch_block_norm_params(p, parts);
 }
 
 }  // namespace
 
+// Partial rows: two CTAs per SM, and at most 2^25 columns in all (256 MB) for very wide rows.
 int block_norm_partials(long long rows, int C) {
     const long long by_size = std::max<long long>(1, (1LL << 25) / C);
     return static_cast<int>(std::min({rows, 4LL * device_info().sm_count, by_size}));
@@ -162,7 +190,15 @@ int block_norm_partials(long long rows, int C) {
     if ((p).stream_type == kBF16) return fn<__nv_bfloat16, __nv_bfloat16>(p);                     \
     return fn<__half, __half>(p);
 
-cudaError_t launch_block_norm_fwd(const BlockNorm& p) { DWC_BY_PAIR(fwd_t, p) }
-cudaError_t launch_block_norm_bwd(const BlockNorm& p) { DWC_BY_PAIR(bwd_t, p) }
+cudaError_t launch_block_norm_fwd_general(const BlockNorm& p) { DWC_BY_PAIR(fwd_t, p) }
+cudaError_t launch_block_norm_bwd_general(const BlockNorm& p) { DWC_BY_PAIR(bwd_t, p) }
+
+cudaError_t launch_block_norm_params(const BlockNorm& p, int count) {
+    const auto launch = [&](auto kern, int width) {
+        return launch_pdl(kern, dim3(static_cast<unsigned>((2LL * p.C + width - 1) / width)), dim3(kSumThreads), 0, p.stream, p, count);
+    };
+    if (2LL * p.C <= 8LL * 2 * device_info().sm_count) return launch(block_norm_param_kernel<8>, 8);
+    return launch(block_norm_param_kernel<32>, 32);
+}
 
 }  // namespace dwc

@@ -8,6 +8,7 @@
 // channels and walks along a run of positions with the last K inputs in registers; the run's K - 1
 // rows in front (and, backward, behind) are read again from L1 or L2.
 #include <algorithm>
+#include <type_traits>
 
 #include "dwc_seq_device.cuh"
 
@@ -16,56 +17,78 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// V values of a row.
+// V adjacent values of a row as they lie in memory.
 template <typename T, int V>
-__device__ __forceinline__ void get(float (&f)[V], const T* p) {
-    if constexpr (V == 8) {
-        Vec8<T> v;
-        float2 g[4];
-        v.load(p);
-        v.widen(g);
+struct Raw {
+    static constexpr int kBytes = V * sizeof(T);
+    using Word = typename std::conditional<kBytes == 16, uint4, typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
+    Word w;
+    __device__ __forceinline__ void zero() { w = Word{}; }
+    __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
+    __device__ __forceinline__ void widen(float (&f)[V]) const {
+        const T* v = reinterpret_cast<const T*>(&w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = g[j].x;
-            f[2 * j + 1] = g[j].y;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = to_f32(p[j]);
+        for (int j = 0; j < V; ++j) f[j] = to_f32(v[j]);
     }
-}
-template <typename T, int V>
-__device__ __forceinline__ void put(T* p, const float (&f)[V]) {
-    if constexpr (V == 8) {
-        float2 g[4];
+    __device__ static __forceinline__ void store(T* p, const float (&f)[V]) {
+        Raw r;
+        T* v = reinterpret_cast<T*>(&r.w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = make_float2(f[2 * j], f[2 * j + 1]);
-        Vec8<T>::store(p, g);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) store_out(p + j, f[j]);
+        for (int j = 0; j < V; ++j) store_out(v + j, f[j]);
+        *reinterpret_cast<Word*>(p) = r.w;
     }
-}
+};
 
 // Input at position t of a sequence (negative: from its state).
 template <typename T, int V>
 __device__ __forceinline__ void input(float (&f)[V], const T* x, long long row, const T* state, int C, int K, long long t) {
-    if (t >= 0) {
-        get<T, V>(f, x + t * row);
-    } else if (state != nullptr) {
-        get<T, V>(f, state + (t + K - 1) * C);
-    } else {
+    Raw<T, V> r;
+    r.zero();
+    if (t >= 0) r.load(x + t * row);
+    else if (state != nullptr) r.load(state + (t + K - 1) * C);
+    r.widen(f);
+}
+
+// Parameters of V channels: w[i] is the tap on the input i positions back.
+template <int KM, int V>
+__device__ __forceinline__ void load_taps(float (&w)[KM][V], float (&bias)[V], const CausalConv& p, int K, int c, bool here) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = 0.f;
+    for (int i = 0; i < KM; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[i][j] = here && i < K ? load_param(p.w, p.param_type, (K - 1 - i) * p.C + c + j, 0.f) : 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) bias[j] = here ? load_param(p.bias, p.param_type, c + j, 0.f) : 0.f;
+}
+
+template <int KM, int V>
+__device__ __forceinline__ void convolve(float (&f)[V], const float (&w)[KM][V], const float (&bias)[V], const float (&win)[KM][V], int K) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = bias[j];
+#pragma unroll
+    for (int i = KM - 1; i >= 0; --i) {
+        if (i >= K) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = fmaf(w[i][j], win[i][j], f[j]);
     }
 }
 
-// KM: taps held in registers; K == KM unless KM is 16, which serves every K up to it.
+template <int KM, int V>
+__device__ __forceinline__ void shift(float (&win)[KM][V]) {
+#pragma unroll
+    for (int i = KM - 1; i > 0; --i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) win[i][j] = win[i - 1][j];
+}
+
+// Rows that a thread brings in together, one such batch ahead of the one it works on.
+constexpr int kBatch = 4;
+
+// KM: taps held in registers; up to 4 it is the number of taps, 8 and 16 serve every number up to it.
 template <typename T, int KM, int V>
 __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p, int columns, int run, int blocks) {
     pdl_trigger();
     pdl_wait();
-    const int K = KM == 16 ? p.K : KM, C = p.C;
+    const int K = KM >= 8 ? p.K : KM, C = p.C;
     const long long slot = blockIdx.x / blocks;
     const int block = static_cast<int>(blockIdx.x - slot * blocks);
     const int column = threadIdx.x % columns, group = threadIdx.x / columns;
@@ -75,41 +98,39 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p,
     const T* x = view_at<T>(p.x, p.seqs, r) + c;
     const T* state = p.state == nullptr ? nullptr : static_cast<const T*>(p.state) + static_cast<long long>(r.s) * (K - 1) * C + c;
     T* y = static_cast<T*>(p.y) + dense_row(p.seqs, r) * C + c;
-    float w[KM][V], bias[V], win[KM][V];
-#pragma unroll
-    for (int k = 0; k < KM; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[k][j] = k < K ? load_param(p.w, p.param_type, k * C + c + j, 0.f) : 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) bias[j] = load_param(p.bias, p.param_type, c + j, 0.f);
     const long long first = r.first + static_cast<long long>(group) * run;
     const long long end = first + run < r.end ? first + run : r.end;
     if (first < end) {
-        // win[i]: the input i positions back
+        Raw<T, V> next[kBatch];
+        const auto fetch = [&](long long t) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                if (t + q < end) next[q].load(x + (t + q) * p.x.row);
+        };
+        fetch(first);
+        float w[KM][V], bias[V], win[KM][V];       // win[i]: the input i positions back
+        load_taps(w, bias, p, K, c, true);
 #pragma unroll
         for (int i = 1; i < KM; ++i)
             if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
-#pragma unroll 4
-        for (long long t = first; t < end; ++t) {
-            get<T, V>(win[0], x + t * p.x.row);
-            float f[V];
+        for (long long t0 = first; t0 < end; t0 += kBatch) {
+            Raw<T, V> raw[kBatch];
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = bias[j];
+            for (int q = 0; q < kBatch; ++q) raw[q] = next[q];
+            fetch(t0 + kBatch);
 #pragma unroll
-            for (int i = KM - 1; i >= 0; --i) {
-                if (i >= K) continue;
+            for (int q = 0; q < kBatch; ++q) {
+                if (t0 + q >= end) break;
+                raw[q].widen(win[0]);
+                float f[V];
+                convolve(f, w, bias, win, K);
+                if (p.silu) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = fmaf(KM == 16 ? load_param(p.w, p.param_type, (K - 1 - i) * C + c + j, 0.f) : w[KM - 1 - i][j], win[i][j], f[j]);
+                    for (int j = 0; j < V; ++j) f[j] = silu(f[j]);
+                }
+                Raw<T, V>::store(y + (t0 + q) * C, f);
+                shift(win);
             }
-            if (p.silu) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = silu(f[j]);
-            }
-            put<T, V>(y + t * C, f);
-#pragma unroll
-            for (int i = KM - 1; i > 0; --i)
-#pragma unroll
-                for (int j = 0; j < V; ++j) win[i][j] = win[i - 1][j];
         }
     }
     if (r.last && p.final_state != nullptr) {
@@ -117,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p,
         for (int i = group; i < K - 1; i += kThreads / columns) {
             float f[V];
             input<T, V>(f, x, p.x.row, state, C, K, r.length - (K - 1) + i);
-            put<T, V>(out + static_cast<long long>(i) * C, f);
+            Raw<T, V>::store(out + static_cast<long long>(i) * C, f);
         }
     }
 }
@@ -128,7 +149,9 @@ __device__ __forceinline__ void add_dfinal(float (&f)[V], const T* dfinal, const
     const long long i = t - (r.length - (K - 1));
     if (dfinal == nullptr || i < 0) return;
     float g[V];
-    get<T, V>(g, dfinal + i * C);
+    Raw<T, V> raw;
+    raw.load(dfinal + i * C);
+    raw.widen(g);
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] += g[j];
 }
@@ -140,29 +163,23 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
     __shared__ float sums[kThreads * V];
     pdl_trigger();
     pdl_wait();
-    const int K = KM == 16 ? p.K : KM, C = p.C;
+    const int K = KM >= 8 ? p.K : KM, C = p.C;
     const long long slot = blockIdx.x / blocks;
     const int block = static_cast<int>(blockIdx.x - slot * blocks);
     const int column = threadIdx.x % columns, group = threadIdx.x / columns, groups = kThreads / columns;
     const int c = (block * columns + column) * V;
     const Piece r = find_piece(p.seqs, slot, p.span);
     const bool here = r.some && c < C;
-    float w[KM][V], bias[V], win[KM][V], dpre[KM][V], dw[KM][V], db[V];
-#pragma unroll
-    for (int k = 0; k < KM; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w[k][j] = here && k < K ? load_param(p.w, p.param_type, k * C + c + j, 0.f) : 0.f;
-            dw[k][j] = 0.f;
-            dpre[k][j] = 0.f;
-            win[k][j] = 0.f;
-        }
+    float dw[KM][V], db[V];             // dw[i]: of the tap on the input i positions back
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        bias[j] = here ? load_param(p.bias, p.param_type, c + j, 0.f) : 0.f;
         db[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KM; ++i) dw[i][j] = 0.f;
     }
-    if (here) {
+    const long long first = r.first + static_cast<long long>(group) * run;
+    const long long end = first + run < r.end ? first + run : r.end;
+    if (here && (first < end || first == 0)) {
         const T* x = view_at<T>(p.x, p.seqs, r) + c;
         const T* dy = view_at<T>(p.dy, p.seqs, r) + c;
         const long long kept = static_cast<long long>(r.s) * (K - 1) * C + c;
@@ -170,28 +187,42 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
         const T* dfinal = p.dfinal == nullptr ? nullptr : static_cast<const T*>(p.dfinal) + kept;
         T* dx = static_cast<T*>(p.dx) + dense_row(p.seqs, r) * C + c;
         T* dstate = p.dstate == nullptr ? nullptr : static_cast<T*>(p.dstate) + kept;
-        const long long first = r.first + static_cast<long long>(group) * run;
-        const long long end = first + run < r.end ? first + run : r.end;
-        // the first run's walk begins with the state's positions
-        const long long low = first == 0 ? -(K - 1) : first;
-        if (first < end || first == 0) {
+        // the first run's walk gives the state's positions as well
+        const long long low = first == 0 ? -(K - 1) : first, stop = end + K - 1, known = stop < r.length ? stop : r.length;
+        Raw<T, V> next_x[kBatch], next_dy[kBatch];
+        const auto fetch = [&](long long t) {
 #pragma unroll
-            for (int i = 1; i < KM; ++i)
-                if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
-            for (long long t = first; t < end + K - 1; ++t) {
-                if (t < r.length) {
+            for (int q = 0; q < kBatch; ++q) {
+                if (t + q >= known) continue;
+                next_x[q].load(x + (t + q) * p.x.row);
+                next_dy[q].load(dy + (t + q) * p.dy.row);
+            }
+        };
+        fetch(first);
+        float w[KM][V], bias[V], win[KM][V], dpre[KM][V];
+        load_taps(w, bias, p, K, c, true);
+#pragma unroll
+        for (int i = 0; i < KM; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) dpre[i][j] = 0.f;
+#pragma unroll
+        for (int i = 1; i < KM; ++i)
+            if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
+        for (long long t0 = first; t0 < stop; t0 += kBatch) {
+            Raw<T, V> raw_x[kBatch], raw_dy[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) raw_x[q] = next_x[q], raw_dy[q] = next_dy[q];
+            fetch(t0 + kBatch);
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const long long t = t0 + q;
+                if (t >= stop) break;
+                if (t < known) {
                     float f[V], g[V];
-                    get<T, V>(win[0], x + t * p.x.row);
-                    get<T, V>(g, dy + t * p.dy.row);
+                    raw_x[q].widen(win[0]);
+                    raw_dy[q].widen(g);
                     if (p.silu) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) f[j] = bias[j];
-#pragma unroll
-                        for (int i = KM - 1; i >= 0; --i) {
-                            if (i >= K) continue;
-#pragma unroll
-                            for (int j = 0; j < V; ++j) f[j] = fmaf(KM == 16 ? load_param(p.w, p.param_type, (K - 1 - i) * C + c + j, 0.f) : w[KM - 1 - i][j], win[i][j], f[j]);
-                        }
+                        convolve(f, w, bias, win, K);
 #pragma unroll
                         for (int j = 0; j < V; ++j) g[j] *= silu_slope(f[j], sigmoid(f[j]));
                     }
@@ -199,10 +230,11 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
                     for (int j = 0; j < V; ++j) dpre[0][j] = g[j];
                     if (t < end) {
 #pragma unroll
-                        for (int i = 0; i < KM; ++i)
+                        for (int i = 0; i < KM; ++i) {
+                            if (i >= K) continue;
 #pragma unroll
-                            for (int j = 0; j < V; ++j)
-                                if (i < K) dw[i][j] = fmaf(g[j], win[i][j], dw[i][j]);   // of tap K - 1 - i
+                            for (int j = 0; j < V; ++j) dw[i][j] = fmaf(g[j], win[i][j], dw[i][j]);
+                        }
 #pragma unroll
                         for (int j = 0; j < V; ++j) db[j] += g[j];
                     }
@@ -212,50 +244,45 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
                 }
                 const long long to = t - (K - 1);
                 if (to >= low) {
+                    // dx[to] = sum_k w_k dpre[to + K - 1 - k]: the tap i back goes with dpre of i positions on
                     float f[V];
 #pragma unroll
                     for (int j = 0; j < V; ++j) f[j] = 0.f;
 #pragma unroll
                     for (int i = 0; i < KM; ++i) {
                         if (i >= K) continue;
+                        const int back = KM >= 8 ? 0 : KM - 1 - i;
+                        if (KM < 8) {
 #pragma unroll
-                        for (int j = 0; j < V; ++j) f[j] = fmaf(w[i][j], dpre[i][j], f[j]);
+                            for (int j = 0; j < V; ++j) f[j] = fmaf(w[back][j], dpre[i][j], f[j]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < V; ++j) f[j] = fmaf(load_param(p.w, p.param_type, i * C + c + j, 0.f), dpre[i][j], f[j]);
+                        }
                     }
                     add_dfinal<T, V>(f, dfinal, r, C, K, to);
-                    if (to >= 0) put<T, V>(dx + to * C, f);
-                    else if (dstate != nullptr) put<T, V>(dstate + (to + K - 1) * C, f);
+                    if (to >= 0) Raw<T, V>::store(dx + to * C, f);
+                    else if (dstate != nullptr) Raw<T, V>::store(dstate + (to + K - 1) * C, f);
                 }
-#pragma unroll
-                for (int i = KM - 1; i > 0; --i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        win[i][j] = win[i - 1][j];
-                        dpre[i][j] = dpre[i - 1][j];
-                    }
+                shift(win);
+                shift(dpre);
             }
         }
     }
     if (p.partial == nullptr) return;
     float* part = p.partial + slot * (K + 1) * C;
 #pragma unroll
-    for (int k = 0; k <= KM; ++k) {
-        if (k > K) continue;
+    for (int i = 0; i <= KM; ++i) {
+        if (i > K) break;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sums[j * kThreads + threadIdx.x] = k < K ? dw[KM == 16 ? 0 : KM - 1 - k < 0 ? 0 : KM - 1 - k][j] : db[j];
-        if (KM == 16 && k < K) {
-#pragma unroll
-            for (int i = 0; i < KM; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (i == K - 1 - k) sums[j * kThreads + threadIdx.x] = dw[i][j];
-        }
+        for (int j = 0; j < V; ++j) sums[j * kThreads + threadIdx.x] = i < KM && i < K ? dw[i < KM ? i : 0][j] : db[j];
         __syncthreads();
         if (group == 0 && c < C) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float s = 0.f;
                 for (int g = 0; g < groups; ++g) s += sums[j * kThreads + g * columns + column];
-                part[static_cast<long long>(k) * C + c + j] = s;
+                part[static_cast<long long>(i < K ? K - 1 - i : K) * C + c + j] = s;
             }
         }
         __syncthreads();
@@ -284,28 +311,32 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(CausalConv p
     store_out(static_cast<T*>(p.y) + i, p.silu ? silu(f) : f);
 }
 
-// Column sums of `count` rows, `stride` apart: a CTA takes 32 columns, each warp every 32nd row.
+// Column sums of the rows: a CTA takes 32 columns, each warp every 32nd row.
 constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads) row_sum_kernel(const float* rows, long long count, long long stride,
-                                                              long long width, float* out) {
+__global__ void __launch_bounds__(kSumThreads) row_sum_kernel(RowSum p) {
     __shared__ float sums[32][33];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long j = static_cast<long long>(blockIdx.x) * 32 + lane;
+    const long long j = static_cast<long long>(blockIdx.x) * 32 + lane, width = p.widths[0] + p.widths[1] + p.widths[2];
     float s = 0.f;
     if (j < width)
-        for (long long k = warp; k < count; k += 8 * 32) {
+        for (long long k = warp; k < p.count; k += 8 * 32) {
             float t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = k + 32 * i < count ? rows[(k + 32 * i) * stride + j] : 0.f;
+            for (int i = 0; i < 8; ++i) t[i] = k + 32 * i < p.count ? p.rows[(k + 32 * i) * p.stride + j] : 0.f;
             s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
         }
     sums[warp][lane] = s;
     __syncthreads();
     s = warp_sum(sums[lane][warp]);
-    const long long o = static_cast<long long>(blockIdx.x) * 32 + warp;
-    if (lane == 0 && o < width) out[o] = s;
+    long long o = static_cast<long long>(blockIdx.x) * 32 + warp;
+    if (lane != 0) return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        if (o >= 0 && o < p.widths[i] && p.out[i] != nullptr) p.out[i][o] = s;
+        o -= p.widths[i];
+    }
 }
 
 // (nearly always there is nothing to do: the CTAs read two offsets and leave)
@@ -321,31 +352,26 @@ __global__ void __launch_bounds__(256) zero_beside_kernel(ZeroBeside p) {
     }
 }
 
-// How a call is laid out: lanes across `columns` vectors, and runs of positions.
-struct Layout {
-    int columns, run, blocks;
-    long long slots;
-};
-
+// Vectors of a row that lie side by side in a CTA; the rest of its threads have other runs of positions.
 int columns_for(int vectors) {
     int n = 1;
     while (n < vectors && n < 32) n *= 2;
     return n;
 }
 
+// Positions to a thread: 32, fewer where that leaves SMs without their eight CTAs.
+constexpr int kRun = 32;
+
 template <typename T, int KM, int V>
 cudaError_t fwd_t(CausalConv p) {
-    Layout l;
-    const int vectors = (p.C + V - 1) / V;
-    l.columns = columns_for(vectors);
-    l.blocks = (vectors + l.columns - 1) / l.columns;
-    l.run = 16;
-    p.span = static_cast<long long>(kThreads / l.columns) * l.run;
-    l.slots = seq_slots(p.seqs, p.span);
-    const long long grid = l.slots * l.blocks;
+    const int vectors = (p.C + V - 1) / V, columns = columns_for(vectors), blocks = (vectors + columns - 1) / columns;
+    int run = kRun;
+    while (run > kBatch && seq_rows(p.seqs) / (kThreads / columns * run) * blocks < 8LL * device_info().sm_count) run /= 2;
+    p.span = static_cast<long long>(kThreads / columns) * run;
+    const long long grid = seq_slots(p.seqs, p.span) * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(causal_conv_fwd_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p,
-                      l.columns, l.run, l.blocks);
+    return launch_pdl(causal_conv_fwd_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p, columns,
+                      run, blocks);
 }
 
 template <typename T, int KM, int V>
@@ -354,16 +380,14 @@ cudaError_t bwd_t(const CausalConv& p) {
     const int groups = kThreads / columns;
     const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t err = launch_pdl(causal_conv_bwd_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
-                                 p.stream, p, columns, static_cast<int>((p.span + groups - 1) / groups), blocks);
+    const cudaError_t err = launch_pdl(causal_conv_bwd_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                                       p.stream, p, columns, static_cast<int>((p.span + groups - 1) / groups), blocks);
     if (err != cudaSuccess || p.partial == nullptr) return err;
-    const long long taps = static_cast<long long>(p.K) * p.C, width = taps + p.C;
-    if (p.dw != nullptr) err = launch_row_sum(p.partial, slots, width, taps, p.dw, p.stream);
-    if (err == cudaSuccess && p.dbias != nullptr) err = launch_row_sum(p.partial + taps, slots, width, p.C, p.dbias, p.stream);
-    return err;
+    const long long taps = static_cast<long long>(p.K) * p.C;
+    return launch_row_sum(p.partial, slots, taps + p.C, {p.dw, p.dbias}, {taps, p.C}, p.stream);
 }
 
-// 8 channels a thread where every tensor allows it, else one.
+// Several channels a thread where every tensor allows it, else one.
 bool vectors_of(const CausalConv& p, bool backward) {
     const size_t a = 8 * static_cast<size_t>(elem_bytes(p.type));
     const auto off = [&](const void* t) { return reinterpret_cast<uintptr_t>(t) % a != 0; };
@@ -374,23 +398,26 @@ bool vectors_of(const CausalConv& p, bool backward) {
 template <typename T>
 cudaError_t fwd_k(const CausalConv& p) {
     const bool vec = vectors_of(p, false);
+    constexpr int V = sizeof(T) == 2 ? 8 : 4;
     switch (p.K) {
-        case 2: return vec ? fwd_t<T, 2, 8>(p) : fwd_t<T, 2, 1>(p);
-        case 3: return vec ? fwd_t<T, 3, 8>(p) : fwd_t<T, 3, 1>(p);
-        case 4: return vec ? fwd_t<T, 4, 8>(p) : fwd_t<T, 4, 1>(p);
-        default: return fwd_t<T, 16, 1>(p);
+        case 2: return vec ? fwd_t<T, 2, V>(p) : fwd_t<T, 2, 1>(p);
+        case 3: return vec ? fwd_t<T, 3, V>(p) : fwd_t<T, 3, 1>(p);
+        case 4: return vec ? fwd_t<T, 4, V>(p) : fwd_t<T, 4, 1>(p);
     }
+    if (p.K > 8) return fwd_t<T, 16, 1>(p);
+    return vec ? fwd_t<T, 8, 4>(p) : fwd_t<T, 8, 1>(p);
 }
 
 template <typename T>
 cudaError_t bwd_k(const CausalConv& p) {
     const bool vec = vectors_of(p, true);
     switch (p.K) {
-        case 2: return vec ? bwd_t<T, 2, 8>(p) : bwd_t<T, 2, 1>(p);
-        case 3: return vec ? bwd_t<T, 3, 8>(p) : bwd_t<T, 3, 1>(p);
-        case 4: return vec ? bwd_t<T, 4, 8>(p) : bwd_t<T, 4, 1>(p);
-        default: return bwd_t<T, 16, 1>(p);
+        case 2: return vec ? bwd_t<T, 2, 4>(p) : bwd_t<T, 2, 1>(p);
+        case 3: return vec ? bwd_t<T, 3, 4>(p) : bwd_t<T, 3, 1>(p);
+        case 4: return vec ? bwd_t<T, 4, 4>(p) : bwd_t<T, 4, 1>(p);
     }
+    if (p.K > 8) return bwd_t<T, 16, 1>(p);
+    return vec ? bwd_t<T, 8, 2>(p) : bwd_t<T, 8, 1>(p);
 }
 
 template <typename T>
@@ -403,7 +430,14 @@ cudaError_t step_t(const CausalConv& p, void* state, long long state_stride) {
 
 }  // namespace
 
-long long causal_conv_bwd_span(const Seqs&, int) { return 128; }
+// (the same whatever the alignment, since the workspace's size follows from it)
+long long causal_conv_bwd_span(const Seqs& s, int C) {
+    const int vectors = (C + 3) / 4, columns = columns_for(vectors), groups = kThreads / columns;
+    const long long blocks = (vectors + columns - 1) / columns;
+    long long span = static_cast<long long>(groups) * 64;
+    while (span > groups * 8 && seq_rows(s) / span * blocks < 8LL * device_info().sm_count) span /= 2;
+    return span;
+}
 
 cudaError_t launch_causal_conv_fwd(const CausalConv& p) {
     switch (p.type) {
@@ -433,12 +467,14 @@ cudaError_t launch_zero_beside(const ZeroBeside& p) {
     return launch_pdl(zero_beside_kernel, dim3(static_cast<unsigned>(device_info().sm_count)), dim3(256), 0, p.stream, p);
 }
 
-cudaError_t launch_row_sum(const float* rows, long long count, long long stride, long long width, float* out,
-                           cudaStream_t stream) {
-    const long long grid = (width + 31) / 32;
+cudaError_t launch_row_sum(const float* rows, long long count, long long stride, std::initializer_list<float*> out,
+                           std::initializer_list<long long> widths, cudaStream_t stream) {
+    RowSum p{rows, count, stride, {}, {}};
+    std::copy(out.begin(), out.end(), p.out);
+    std::copy(widths.begin(), widths.end(), p.widths);
+    const long long grid = (p.widths[0] + p.widths[1] + p.widths[2] + 31) / 32;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(row_sum_kernel, dim3(static_cast<unsigned>(grid)), dim3(kSumThreads), 0, stream, rows, count, stride,
-                      width, out);
+    return launch_pdl(row_sum_kernel, dim3(static_cast<unsigned>(grid)), dim3(kSumThreads), 0, stream, p);
 }
 
 }  // namespace dwc

@@ -212,6 +212,31 @@ dwc_status_t dropout(const void* x, long long ldx, void* y, long long rows, int 
     return map_cuda(launch_dropout_general(c));
 }
 
+cudaError_t block_fwd_rows(const BlockNorm& p) { DWC_BY_PAIR(launch_block_norm_fwd, p) }
+cudaError_t block_bwd_rows(const BlockNorm& p) { DWC_BY_PAIR(launch_block_norm_bwd, p) }
+
+cudaError_t launch_block_fwd(const BlockNorm& p) {
+    const int ws = elem_bytes(p.stream_type), wb = elem_bytes(p.branch_type);
+    if (lines_up(p.x, wb, p.ld_x, p.rows, p.C) && lines_up(p.gate, wb, p.ld_gate, p.rows, p.C) &&
+        lines_up(p.res, ws, p.ld_res, p.rows, p.C) && lines_up(p.z, ws, p.C, p.rows, p.C) && lines_up(p.y, wb, p.C, p.rows, p.C)) {
+        const cudaError_t err = block_fwd_rows(p);
+        if (err != cudaErrorNotSupported) return err;
+    }
+    return launch_block_norm_fwd_general(p);
+}
+
+cudaError_t launch_block_bwd(const BlockNorm& p) {
+    const int ws = elem_bytes(p.stream_type), wb = elem_bytes(p.branch_type);
+    if (lines_up(p.dy, wb, p.ld_dy, p.rows, p.C) && lines_up(p.dz, ws, p.ld_dz, p.rows, p.C) &&
+        lines_up(p.x, wb, p.ld_x, p.rows, p.C) && lines_up(p.z_in, ws, p.ld_z, p.rows, p.C) &&
+        lines_up(p.gate, wb, p.ld_gate, p.rows, p.C) && lines_up(p.dx, wb, p.C, p.rows, p.C) &&
+        lines_up(p.dres, ws, p.C, p.rows, p.C) && lines_up(p.dgate, wb, p.C, p.rows, p.C)) {
+        const cudaError_t err = block_bwd_rows(p);
+        if (err != cudaErrorNotSupported) return err;
+    }
+    return launch_block_norm_bwd_general(p);
+}
+
 // What both passes of the block norm check.
 dwc_status_t check_block(const BlockNorm& p, dwc_dtype_t stream_type, dwc_dtype_t branch_type, dwc_dtype_t param_dtype) {
     if (!valid_pair(stream_type, branch_type) || !known(param_dtype)) return DWC_ERR_INVALID_ARG;
@@ -387,12 +412,12 @@ dwc_status_t dwc_block_norm_fwd(const void* x, long long ldx, const void* res, l
     p.y = y;
     p.rstd_post_out = rstd_post;
     p.rstd_pre_out = rstd_pre;
-    return map_cuda(launch_block_norm_fwd(p));
+    return map_cuda(launch_block_fwd(p));
 }
 
 size_t dwc_block_norm_bwd_workspace_size(long long rows, int C) {
     if (check_rows(rows, C) != DWC_OK || rows == 0) return 0;
-    return static_cast<size_t>(block_norm_partials(rows, C)) * 3 * C * sizeof(float);
+    return static_cast<size_t>(block_norm_partials(rows, C)) * 2 * C * sizeof(float);
 }
 
 dwc_status_t dwc_block_norm_bwd(const void* dy, long long lddy, const void* dz, long long lddz, const void* x,
@@ -466,7 +491,7 @@ dwc_status_t dwc_block_norm_bwd(const void* dy, long long lddy, const void* dz, 
     p.dx = dx;
     p.dgate = dgate;
     p.dres = dres;
-    return map_cuda(launch_block_norm_bwd(p));
+    return map_cuda(launch_block_bwd(p));
 }
 
 }  // extern "C"

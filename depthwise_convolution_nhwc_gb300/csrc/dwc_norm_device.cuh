@@ -68,6 +68,20 @@ __device__ __forceinline__ float load_param(const void* p, int type, int c, floa
     return __half2float(static_cast<const __half*>(p)[c]);
 }
 
+// 2^v, and through it 1 / (1 + exp(-v)) and v / (1 + exp(-v)).  The argument's scaling by log2(e) costs a relative error of
+// 2^-23 |v| of the exponential, which counts only where the exponential does; the full-range expf in its place made
+// gates as dear as everything else of a memory-bound kernel.
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + exp2_fast(v * -kLog2e)); }
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + exp2_fast(v * -kLog2e)); }
+// d silu / d v, from sigmoid(v)
+__device__ __forceinline__ float silu_slope(float v, float s) { return fmaf(v * s, 1.f - s, s); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);

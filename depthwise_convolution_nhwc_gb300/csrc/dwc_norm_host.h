@@ -150,13 +150,24 @@ struct BlockNorm {
     void* dgate;                    // branch type, or null
     void* dres;                     // stream type
     float* grads[3];                // gamma_post, gamma_pre, scale; each may be null
-    float* partial;                 // rows of 3 C floats (with a parameter gradient only)
+    float* partial;                 // rows of 2 C floats (with a parameter gradient only)
     bool in_place = false;          // an output is one of the inputs
 };
 // Rows of partial parameter gradients that a backward pass may write.
 int block_norm_partials(long long rows, int C);
-cudaError_t launch_block_norm_fwd(const BlockNorm& p);
-cudaError_t launch_block_norm_bwd(const BlockNorm& p);
+// Any row stride, alignment and channel count.
+cudaError_t launch_block_norm_fwd_general(const BlockNorm& p);
+cudaError_t launch_block_norm_bwd_general(const BlockNorm& p);
+// Rows that line up, up to 8192 channels, one file per pair of types; cudaErrorNotSupported beyond that.
+#define DWC_BLOCK_NORM_PAIR(name)                            \
+    cudaError_t launch_block_norm_fwd_##name(const BlockNorm& p); \
+    cudaError_t launch_block_norm_bwd_##name(const BlockNorm& p);
+DWC_BLOCK_NORM_PAIR(f32)
+DWC_BLOCK_NORM_PAIR(bf16)
+DWC_BLOCK_NORM_PAIR(f16)
+DWC_BLOCK_NORM_PAIR(f32_bf16)
+DWC_BLOCK_NORM_PAIR(f32_f16)
+#undef DWC_BLOCK_NORM_PAIR
 
 // General kernels: any row stride, alignment and channel count.
 cudaError_t launch_norm_fwd_general(const NormFwd& p);

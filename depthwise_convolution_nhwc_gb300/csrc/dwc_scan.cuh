@@ -17,14 +17,7 @@ namespace dwc {
 namespace scan {
 
 constexpr int kThreads = 128;
-constexpr int kTile = kScanTile;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_fast(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
+constexpr int kTile = 32;
 
 // log(1 + e) for e in [0, 1] as 2 atanh(s), s = e / (2 + e) <= 1/3: the odd series up to s^15, whose
 // rest is below 2 s^17 / 17 < 1e-9 of it; relative errors stay near 2^-23 however small e is.
@@ -41,7 +34,7 @@ __device__ __forceinline__ float log1p_unit(float e) {
     return fmaf(t * q, p, t);
 }
 // (a NaN stays one: fmaxf would drop it)
-__device__ __forceinline__ float softplus(float v) { return (v < 0.f ? 0.f : v) + log1p_unit(expf(-fabsf(v))); }
+__device__ __forceinline__ float softplus(float v) { return (v < 0.f ? 0.f : v) + log1p_unit(exp2_fast(fabsf(v) * -kLog2e)); }
 
 // The sum over the L lanes of a channel of v[sub], for lane `sub`: halves are exchanged, then quarters.
 template <int L>
@@ -60,8 +53,8 @@ __device__ __forceinline__ float parted(float (&v)[L], int sub) {
 
 // Index among `saved` of the state in front of tile `tile` of a sequence.
 __device__ __forceinline__ long long saved_slot(const Seqs& q, const Piece& r, long long tile) {
-    if (q.offsets != nullptr) return r.base / kTile + r.s + tile;
-    const long long n = q.length == 0 ? 1 : (q.length + kTile - 1) / kTile;
+    if (q.offsets != nullptr) return r.base / kScanTile + r.s + tile;
+    const long long n = q.length == 0 ? 1 : (q.length + kScanTile - 1) / kScanTile;
     return r.s * n + tile;
 }
 
@@ -91,24 +84,16 @@ __device__ __forceinline__ void get_states(float (&h)[N], const float* from, int
     for (int i = 0; i < N; ++i) h[i] = from != nullptr && n0 + i < states ? from[n0 + i] : 0.f;
 }
 
-// Raw vectors of 8 channels of a tile: thread i holds position i / (channels / 8), columns 8 * (i % ...).
-template <typename T, int L>
-struct Tile {
-    static constexpr int kChannels = kThreads / L, kColumns = kChannels / 8;
-    static constexpr int kActive = kTile * kColumns;       // threads that hold a vector (at most all)
-    static_assert(kActive <= kThreads, "one vector a thread");
-};
-
-// B and C of a tile: vectors of 8 states, padded with zeros.
-template <typename T, int NP>
+// B or C of a tile: vectors of 8 states, padded with zeros.
+template <typename T, int NP, int kRows = kTile>
 struct StateRows {
-    static constexpr int kVecs = NP / 8, kEach = (kTile * kVecs + kThreads - 1) / kThreads;
+    static constexpr int kVecs = (NP + 7) / 8, kEach = (kRows * kVecs + kThreads - 1) / kThreads;
     Vec8<T> raw[kEach];
     __device__ __forceinline__ void fetch(const T* base, const RowsView& v, long long t0, long long end, int N) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int i = threadIdx.x + k * kThreads, t = i / kVecs, col = i % kVecs * 8;
-            if (i < kTile * kVecs && t0 + t < end) load8(raw[k], base + (t0 + t) * v.row, col, N, v.vec && N % 8 == 0);
+            if (i < kRows * kVecs && t0 + t < end) load8(raw[k], base + (t0 + t) * v.row, col, N, v.vec && N % 8 == 0);
             else raw[k].zero();
         }
     }
@@ -116,12 +101,33 @@ struct StateRows {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int i = threadIdx.x + k * kThreads;
-            if (i >= kTile * kVecs) continue;
+            if (i >= kRows * kVecs) continue;
             float2 f[4];
             raw[k].widen(f);
             float4* o = reinterpret_cast<float4*>(&to[i / kVecs][i % kVecs * 8]);
             o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
             o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        }
+    }
+    // each four states in 1, 2 or 4 orders: n, n ^ 2 (two orders); n, n ^ 1, n ^ 2, n ^ 3 (four)
+    template <int kOrders>
+    __device__ __forceinline__ void spread(float (*to)[kRows][NP]) const {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x + k * kThreads;
+            if (i >= kRows * kVecs) continue;
+            float2 f[4];
+            raw[k].widen(f);
+#pragma unroll
+            for (int o = 0; o < kOrders; ++o) {
+                const int m = kOrders == 2 ? 2 * o : o;
+                float4* at = reinterpret_cast<float4*>(&to[o][i / kVecs][i % kVecs * 8]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float v[4] = {f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y};
+                    at[q] = make_float4(v[m], v[1 ^ m], v[2 ^ m], v[3 ^ m]);
+                }
+            }
         }
     }
 };
@@ -144,153 +150,366 @@ __device__ __forceinline__ void row_values(float (&v)[N], const float* from) {
     }
 }
 
+template <int N>
+__device__ __forceinline__ void row_pairs(float2 (&v)[N], const float* from) {
+    float f[2 * N];
+    row_values(f, from);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
 // -------------------------------------------------------------------------------- forward
 
-template <typename T, int NS, int L>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(Scan p, int blocks) {
-    constexpr int kChannels = Tile<T, L>::kChannels, kColumns = Tile<T, L>::kColumns, NP = NS * L;
+// Sequences that are too few to fill the GPU are cut into chunks of p.span positions.  kStates: the first of
+// three kernels, which walks every chunk but a sequence's last from a state of zero and keeps the
+// state at its end (`ends`, [slot][C][N]) and the sum of delta (`sums`, [slot][C]); the chunks are then joined,
+// h = exp(A sum delta) h + end, and the second walk begins each chunk with the state in front of it.
+template <typename T, int NS, int L, bool kStates>
+__global__ void __launch_bounds__(kThreads, L == 16 ? 3 : 6) scan_fwd_kernel(Scan p, int blocks, float* ends, float* sums) {
+    constexpr int kChannels = kThreads / L, kColumns = kChannels / 8, NP = NS * L;
+    constexpr int kEach = (kTile * kColumns + kThreads - 1) / kThreads;      // vectors of a tile to a thread
     __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, delta * u
-    __shared__ __align__(16) float bs[kTile][NP], cs[kTile][NP], ys[kTile][kChannels];
+    __shared__ __align__(16) float bs[kTile][NP], cs[kStates ? 1 : kTile][NP], ys[kStates ? 1 : kTile][kChannels];
+    __shared__ __align__(16) float bias[kChannels], skip[kChannels];
     pdl_trigger();
     pdl_wait();
     const long long slot = blockIdx.x / blocks;
     const Block k = block_of(p, static_cast<int>(blockIdx.x - slot * blocks), kChannels);
-    const Piece r = find_piece(p.seqs, slot, p.seqs.length + 1);
-    if (!r.some) return;
+    const Piece r = find_piece(p.seqs, slot, p.span);
+    if (!r.some || (kStates && r.last)) return;
     const int C = p.C, N = p.N;
     const T *u = view_at<T>(p.u, p.seqs, r) + k.c, *dt = view_at<T>(p.dt, p.seqs, r) + k.c;
-    const T* z = p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
+    const T* z = kStates || p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
     const T *b = view_at<T>(p.b, p.seqs, r) + k.g * N, *c = view_at<T>(p.c, p.seqs, r) + k.g * N;
     T* y = static_cast<T*>(p.y) + dense_row(p.seqs, r) * C + k.c;
     const bool even = (C / p.G) % 8 == 0, vec_y = even && reinterpret_cast<uintptr_t>(p.y) % (8 * sizeof(T)) == 0;
-
-    // as a holder of vectors
-    const int row = threadIdx.x / kColumns, col = threadIdx.x % kColumns * 8;
-    const bool holder = row < kTile && col < k.width;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const bool in = holder && col + j < k.width;
-        bias[j] = in && p.dt_bias != nullptr ? p.dt_bias[k.c + col + j] : 0.f;
-        skip[j] = in && p.D != nullptr ? p.D[k.c + col + j] : 0.f;
+    for (int i = threadIdx.x; i < kChannels; i += kThreads) {
+        bias[i] = i < k.width && p.dt_bias != nullptr ? p.dt_bias[k.c + i] : 0.f;
+        skip[i] = i < k.width && p.D != nullptr ? p.D[k.c + i] : 0.f;
     }
     // as a server of a channel's states
     const int ch = threadIdx.x / L, sub = threadIdx.x % L, n0 = sub * NS;
     const bool serves = ch < k.width;
-    const long long mine = (static_cast<long long>(r.s) * C + k.c + ch) * N;
-    float a2[NS], h[NS];
+    const long long mine = (static_cast<long long>(r.s) * C + k.c + ch) * N, here = (slot * C + k.c + ch) * N;
+    float a2[NS], h[NS], total = 0.f;
     get_states(a2, serves ? p.A + static_cast<long long>(k.c + ch) * N : nullptr, n0, N);
 #pragma unroll
     for (int i = 0; i < NS; ++i) a2[i] *= kLog2e;
-    get_states(h, serves && p.state != nullptr ? p.state + mine : nullptr, n0, N);
+    if (kStates) get_states(h, nullptr, n0, N);
+    else if (ends != nullptr) get_states(h, serves ? ends + here : nullptr, n0, N);
+    else get_states(h, serves && p.state != nullptr ? p.state + mine : nullptr, n0, N);
 
-    Vec8<T> ru, rdt, rz, nu, ndt, nz;
-    StateRows<T, NP> nb, nc;
+    Vec8<T> ru[kEach], rz[kEach], rdt[kEach];
+    StateRows<T, NP> rb, rc;
+    const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
+    const auto col_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) % kColumns * 8; };
     auto fetch = [&](long long t0) {
-        nu.zero(), ndt.zero(), nz.zero();
-        if (holder && t0 + row < r.end) {
-            load8(nu, u + (t0 + row) * p.u.row, col, k.width, p.u.vec && even);
-            load8(ndt, dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
-            if (z != nullptr) load8(nz, z + (t0 + row) * p.z.row, col, k.width, p.z.vec && even);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i), col = col_of(i);
+            ru[i].zero(), rdt[i].zero();
+            if (row >= kTile || t0 + row >= r.end) continue;
+            load8(ru[i], u + (t0 + row) * p.u.row, col, k.width, p.u.vec && even);
+            load8(rdt[i], dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
         }
-        nb.fetch(b, p.b, t0, r.end, N);
-        nc.fetch(c, p.c, t0, r.end, N);
+        rb.fetch(b, p.b, t0, r.end, N);
+        if (!kStates) rc.fetch(c, p.c, t0, r.end, N);
     };
     fetch(r.first);
+    __syncthreads();
     for (long long t0 = r.first; t0 < r.end; t0 += kTile) {
-        ru = nu, rdt = ndt, rz = nz;
-        if (row < kTile) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i), col = col_of(i);
+            if (row >= kTile) continue;
             float2 fu[4], fd[4];
-            ru.widen(fu);
-            rdt.widen(fd);
+            ru[i].widen(fu);
+            rdt[i].widen(fd);
             const bool in = t0 + row < r.end;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float d0 = fd[j].x + bias[2 * j], d1 = fd[j].y + bias[2 * j + 1];
+                const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
+                float d0 = fd[j].x + o.x, d1 = fd[j].y + o.y;
                 if (p.softplus) d0 = softplus(d0), d1 = softplus(d1);
                 if (!in) d0 = d1 = 0.f;        // positions past the end leave the states alone
-                step[row][col + 2 * j] = make_float2(d0, d0 * fu[j].x);
-                step[row][col + 2 * j + 1] = make_float2(d1, d1 * fu[j].y);
+                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d0, d0 * fu[j].x, d1, d1 * fu[j].y);
             }
         }
-        nb.spread(bs);
-        nc.spread(cs);
+        rb.spread(bs);
+        if (!kStates) rc.spread(cs);
         __syncthreads();
+        Vec8<T> keep[kEach];
+        if (!kStates) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                keep[i] = ru[i];
+                rz[i].zero();
+                if (z != nullptr && row_of(i) < kTile && t0 + row_of(i) < r.end)
+                    load8(rz[i], z + (t0 + row_of(i)) * p.z.row, col_of(i), k.width, p.z.vec && even);
+            }
+        }
         if (t0 + kTile < r.end) fetch(t0 + kTile);
-        if (p.saved != nullptr && serves)
-            put_states(p.saved + (saved_slot(p.seqs, r, t0 / kTile) * C + k.c + ch) * N, h, n0, N);
 #pragma unroll 1
         for (int t = 0; t < kTile; t += L) {
-            float sums[L];
+            if (!kStates && p.saved != nullptr && t % kScanTile == 0 && serves && (t == 0 || t0 + t < r.end))
+                put_states(p.saved + (saved_slot(p.seqs, r, (t0 + t) / kScanTile) * C + k.c + ch) * N, h, n0, N);
+            float part[L];
 #pragma unroll
             for (int q = 0; q < L; ++q) {
                 const float2 s = step[t + q][ch];
-                float fb[NS], fc[NS];
-                row_values(fb, &bs[t + q][n0]);
-                row_values(fc, &cs[t + q][n0]);
-                float sum = 0.f;
+                float2 fb[NS / 2], fc[NS / 2], sum = both(0.f);
+                row_pairs(fb, &bs[t + q][n0]);
+                if (!kStates) row_pairs(fc, &cs[t + q][n0]);
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    h[i] = fmaf(exp2_fast(s.x * a2[i]), h[i], s.y * fb[i]);
-                    sum = fmaf(fc[i], h[i], sum);
+                for (int i = 0; i < NS / 2; ++i) {
+                    float2 a = __fmul2_rn(both(s.x), make_float2(a2[2 * i], a2[2 * i + 1])), hh = make_float2(h[2 * i], h[2 * i + 1]);
+                    a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
+                    hh = __ffma2_rn(both(s.y), fb[i], __fmul2_rn(a, hh));
+                    h[2 * i] = hh.x, h[2 * i + 1] = hh.y;
+                    if (!kStates) sum = __ffma2_rn(fc[i], hh, sum);
                 }
-                sums[q] = sum;
+                if (kStates) total += s.x;
+                part[q] = sum.x + sum.y;
             }
-            const float sum = parted<L>(sums, sub);
-            ys[t + sub][ch] = sum;
+            if (!kStates) ys[t + sub][ch] = parted<L>(part, sub);
         }
         __syncthreads();
-        if (holder && t0 + row < r.end) {
-            float2 fu[4], fz[4], f[4];
-            ru.widen(fu);
-            rz.widen(fz);
+        if constexpr (!kStates) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[j].x = fmaf(skip[2 * j], fu[j].x, ys[row][col + 2 * j]);
-                f[j].y = fmaf(skip[2 * j + 1], fu[j].y, ys[row][col + 2 * j + 1]);
-                if (z != nullptr) {
-                    f[j].x *= silu(fz[j].x);
-                    f[j].y *= silu(fz[j].y);
+            for (int i = 0; i < kEach; ++i) {
+                const int row = row_of(i), col = col_of(i);
+                if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
+                float2 fu[4], fz[4], f[4];
+                keep[i].widen(fu);
+                rz[i].widen(fz);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 o = *reinterpret_cast<const float2*>(&skip[col + 2 * j]);
+                    f[j] = __ffma2_rn(o, fu[j], *reinterpret_cast<const float2*>(&ys[row][col + 2 * j]));
+                    if (z != nullptr) f[j] = __fmul2_rn(f[j], make_float2(silu(fz[j].x), silu(fz[j].y)));
                 }
+                store8(y + (t0 + row) * C, f, col, k.width, vec_y);
             }
-            store8(y + (t0 + row) * C, f, col, k.width, vec_y);
         }
     }
-    if (r.last && p.final_state != nullptr && serves) put_states(p.final_state + mine, h, n0, N);
+    if (!serves) return;
+    if (kStates) {
+        put_states(ends + here, h, n0, N);
+        if (sub == 0) sums[slot * C + k.c + ch] = total;
+    } else if (r.last && p.final_state != nullptr) {
+        put_states(p.final_state + mine, h, n0, N);
+    }
+}
+
+// The states in front of every chunk, in place of those at their ends: a thread per sequence, channel and state.
+// Eight chunks' values are on their way together.
+template <bool kBackward>
+__global__ void __launch_bounds__(256) scan_join_kernel(Scan p, float* ends, const float* sums, const float* from) {
+    pdl_trigger();
+    pdl_wait();
+    const int C = p.C, N = p.N;
+    const long long width = static_cast<long long>(C) * N, i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const int s = static_cast<int>(i / width);
+    if (s >= p.seqs.count) return;
+    const long long j = i - s * width, c = j / N;
+    long long first, n;          // the sequence's slots
+    if (p.seqs.offsets != nullptr) {
+        const long long at = seq_offset(p.seqs, s), end = seq_offset(p.seqs, s + 1);
+        first = at / p.span + s;
+        n = end > at ? (end - at + p.span - 1) / p.span : 1;
+    } else {
+        n = p.seqs.length == 0 ? 1 : (p.seqs.length + p.span - 1) / p.span;
+        first = s * n;
+    }
+    const float a2 = p.A[j] * kLog2e;
+    float h = from != nullptr ? from[i] : 0.f;
+    constexpr int U = 8;
+    for (long long k = 0; k < n; k += U) {
+        float e[U], d[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            // (the last chunk's end is not needed, nor formed)
+            const bool in = k + q < n - 1;
+            const long long slot = first + (kBackward ? n - 1 - k - q : k + q);
+            e[q] = in ? ends[slot * width + j] : 0.f;
+            d[q] = in ? sums[slot * C + c] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            if (k + q >= n) break;
+            const long long slot = first + (kBackward ? n - 1 - k - q : k + q);
+            ends[slot * width + j] = h;
+            h = fmaf(exp2_fast(d[q] * a2), h, e[q]);
+        }
+    }
 }
 
 // ------------------------------------------------------------------------------- backward
 
-// Tiles from the last to the first.  From the state in front of a tile (kept by the forward pass)
-// the states at every SB-th position are formed again; then, SB positions at a time from the last,
-// a h[t-1] and a of each of them, in registers, and the gradients going back:
+// The first of the backward pass's kernels where sequences are cut into chunks: what reaches the
+// position in front of a chunk from within it, dh = g C + carry, carry = exp(delta A) dh (`ends`), and the sum
+// of delta.  Every chunk but a sequence's first is walked, from its end.
+template <typename T, int NS, int L>
+__global__ void __launch_bounds__(kThreads, 6) scan_adjoint_kernel(Scan p, int blocks, float* ends, float* sums) {
+    constexpr int kChannels = kThreads / L, kColumns = kChannels / 8, NP = NS * L;
+    constexpr int kEach = (kTile * kColumns + kThreads - 1) / kThreads;
+    __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, g
+    __shared__ __align__(16) float cs[kTile][NP];
+    __shared__ __align__(16) float bias[kChannels];
+    pdl_trigger();
+    pdl_wait();
+    const long long slot = blockIdx.x / blocks;
+    const Block k = block_of(p, static_cast<int>(blockIdx.x - slot * blocks), kChannels);
+    const Piece r = find_piece(p.seqs, slot, p.span);
+    if (!r.some || r.index == 0) return;
+    const int C = p.C, N = p.N;
+    const T *dt = view_at<T>(p.dt, p.seqs, r) + k.c, *dy = view_at<T>(p.dy, p.seqs, r) + k.c;
+    const T* z = p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
+    const T* c = view_at<T>(p.c, p.seqs, r) + k.g * N;
+    const bool even = (C / p.G) % 8 == 0;
+    for (int i = threadIdx.x; i < kChannels; i += kThreads)
+        bias[i] = i < k.width && p.dt_bias != nullptr ? p.dt_bias[k.c + i] : 0.f;
+    const int ch = threadIdx.x / L, sub = threadIdx.x % L, n0 = sub * NS;
+    const bool serves = ch < k.width;
+    float a2[NS], carry[NS], total = 0.f;
+    get_states(a2, serves ? p.A + static_cast<long long>(k.c + ch) * N : nullptr, n0, N);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        a2[i] *= kLog2e;
+        carry[i] = 0.f;
+    }
+    const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
+    const auto col_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) % kColumns * 8; };
+    Vec8<T> rdt[kEach], rdy[kEach], rz[kEach];
+    StateRows<T, NP> rc;
+    auto fetch = [&](long long t0) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i), col = col_of(i);
+            rdt[i].zero(), rdy[i].zero(), rz[i].zero();
+            if (row >= kTile || t0 + row >= r.end) continue;
+            load8(rdt[i], dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
+            load8(rdy[i], dy + (t0 + row) * p.dy.row, col, k.width, p.dy.vec && even);
+            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row, col, k.width, p.z.vec && even);
+        }
+        rc.fetch(c, p.c, t0, r.end, N);
+    };
+    const long long tiles = (r.end - r.first + kTile - 1) / kTile;
+    fetch(r.first + (tiles - 1) * kTile);
+    for (long long tile = tiles - 1; tile >= 0; --tile) {
+        const long long t0 = r.first + tile * kTile;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i), col = col_of(i);
+            if (row >= kTile) continue;
+            float2 fd[4], fy[4], fz[4];
+            rdt[i].widen(fd);
+            rdy[i].widen(fy);
+            rz[i].widen(fz);
+            const bool in = t0 + row < r.end;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
+                float d0 = fd[j].x + o.x, d1 = fd[j].y + o.y;
+                if (p.softplus) d0 = softplus(d0), d1 = softplus(d1);
+                if (!in) d0 = d1 = 0.f;
+                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], make_float2(silu(fz[j].x), silu(fz[j].y)));
+                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d0, fy[j].x, d1, fy[j].y);
+            }
+        }
+        rc.spread(cs);
+        __syncthreads();
+        if (tile > 0) fetch(t0 - kTile);
+#pragma unroll 4
+        for (int t = kTile - 1; t >= 0; --t) {
+            const float2 s = step[t][ch];
+            float2 fc[NS / 2];
+            row_pairs(fc, &cs[t][n0]);
+#pragma unroll
+            for (int i = 0; i < NS / 2; ++i) {
+                float2 a = __fmul2_rn(both(s.x), make_float2(a2[2 * i], a2[2 * i + 1]));
+                a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
+                const float2 dh = __ffma2_rn(both(s.y), fc[i], make_float2(carry[2 * i], carry[2 * i + 1]));
+                a = __fmul2_rn(a, dh);
+                carry[2 * i] = a.x, carry[2 * i + 1] = a.y;
+            }
+            total += s.x;
+        }
+    }
+    if (!serves) return;
+    put_states(ends + (slot * C + k.c + ch) * N, carry, n0, N);
+    if (sub == 0) sums[slot * C + k.c + ch] = total;
+}
+
+// Tiles of 16 positions from the last to the first.  From the state in front of a tile (kept by the
+// forward pass) the states in front of every 4th position are formed again (`front`); then, 4 positions
+// at a time from the last, a h[t-1] and a of each, in registers, and the gradients going back:
 //     dh = g C + carry,  carry = a dh  (g: the gradient of the sum over the states and D u)
 //     dC = sum_c g h,  dB = sum_c dh delta u,  dA += dh a h[t-1] delta
 //     into = sum_n dh B,  decay = sum_n dh a h[t-1] A,  du = into delta + D g,  ddelta = into u + decay
-// The sums of dB and dC over a CTA's channels go to partial rows, one per block of channels.
-template <typename T, int NS, int L, int SB>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(Scan p, int blocks, float* part_bc, float* part_a, float* part_d,
-                                                            float* part_bias) {
-    constexpr int kChannels = Tile<T, L>::kChannels, kColumns = Tile<T, L>::kColumns, NP = NS * L;
-    constexpr int kWarps = kThreads / 32, kLanes = 32 / L;      // channels of a warp
-    static_assert(SB % L == 0 || L % SB == 0, "parts");
-    constexpr int kPart = SB < L ? SB : L;
+// Bound by the exchanges between lanes as much as by the arithmetic (10 packed operations on a pair of states
+// going back, 1.75 times 3 and two exponentials to form the states again), so a lane has two channels and four
+// states of each: dB and dC are added over its channels before they leave it, and lanes part the sums
+// among themselves without selecting what to send.  For that a lane holds its four states in the
+// order n ^ perm, so that the upper pair is always what the partner keeps (B and C lie in shared
+// memory in each of the orders), and odd lanes hold their two channels the other way round.
+constexpr int kBwdTile = kScanTile, kBwdStep = 4;
+
+// Values of four states in a lane's order.
+struct Four {
+    float2 v[2];
+    __device__ __forceinline__ void get(const float* from, int n0, int perm, int states) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + (i ^ perm);
+            f[i] = from != nullptr && n < states ? from[n] : 0.f;
+        }
+        v[0] = make_float2(f[0], f[1]), v[1] = make_float2(f[2], f[3]);
+    }
+    __device__ __forceinline__ void put(float* to, int n0, int perm, int states) const {
+        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + (i ^ perm);
+            if (n < states) to[n] = f[i];
+        }
+    }
+};
+
+template <int L>
+struct BwdShape {
+    static constexpr int kLanes = 32 / L;                  // lanes of a warp that share states
+    static constexpr int kOrders = kLanes >= 4 ? 4 : kLanes;
+    static constexpr int kChannels = 2 * kThreads / L, NP = 4 * L, kWarps = kThreads / 32;
+    static constexpr size_t kFloats = kBwdTile * kChannels * 3 + 2 * kOrders * kBwdTile * NP +
+                                      kBwdTile / kBwdStep * 8 * kThreads + kWarps * kBwdTile * 2 * NP + 2 * kChannels;
+};
+
+__device__ __forceinline__ float from_lane(float v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
+
+template <typename T, int L>
+__global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int blocks, const float* carries, float* part_bc, float* part_p) {
+    using S = BwdShape<L>;
+    constexpr int kChannels = S::kChannels, kColumns = kChannels / 8, NP = S::NP, W = S::kLanes, kOrders = S::kOrders;
+    constexpr int kEach = (kBwdTile * kColumns + kThreads - 1) / kThreads;
     extern __shared__ __align__(16) float smem[];
-    float2 (*step)[kChannels] = reinterpret_cast<float2 (*)[kChannels]>(smem);
-    float (*bs)[NP] = reinterpret_cast<float (*)[NP]>(smem + kTile * kChannels * 2);
-    float (*cs)[NP] = bs + kTile;
-    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(cs + kTile);
-    float (*into_s)[kChannels] = gs + kTile;
-    float (*decay_s)[kChannels] = into_s + kTile;
-    float (*ys)[kChannels] = decay_s + kTile;
-    float* sums = reinterpret_cast<float*>(ys + kTile);        // warps x positions x (dB, dC)
-    float* front = sums + kWarps * kTile * 2 * NP + threadIdx.x;    // states in front of every SB-th position
+    float2 (*step)[kChannels] = reinterpret_cast<float2 (*)[kChannels]>(smem);      // delta, u; then du, ddelta
+    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(step + kBwdTile);       // g; then the sum over the states
+    float (*bs)[kBwdTile][NP] = reinterpret_cast<float (*)[kBwdTile][NP]>(gs + kBwdTile);
+    float (*cs)[kBwdTile][NP] = bs + kOrders;
+    float* front = reinterpret_cast<float*>(cs + kOrders);
+    float* sums = front + kBwdTile / kBwdStep * 8 * kThreads;       // warps x positions x (dB, dC)
+    float* bias = sums + S::kWarps * kBwdTile * 2 * NP;
+    float* skip = bias + kChannels;
+    front += threadIdx.x;
     pdl_trigger();
     pdl_wait();
     const long long slot = blockIdx.x / blocks;
     const int block = static_cast<int>(blockIdx.x - slot * blocks);
     const Block k = block_of(p, block, kChannels);
-    const Piece r = find_piece(p.seqs, slot, p.seqs.length + 1);
+    const Piece r = find_piece(p.seqs, slot, p.span);
     const int C = p.C, N = p.N;
     const bool even = (C / p.G) % 8 == 0;
     const long long dense = r.some ? dense_row(p.seqs, r) : 0;
@@ -298,194 +517,269 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(Scan p, int blocks, 
     const T *u = view_at<T>(p.u, p.seqs, r) + k.c, *dt = view_at<T>(p.dt, p.seqs, r) + k.c, *dy = view_at<T>(p.dy, p.seqs, r) + k.c;
     const T* z = p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
     const T *b = view_at<T>(p.b, p.seqs, r) + k.g * N, *c = view_at<T>(p.c, p.seqs, r) + k.g * N;
-
-    const int row = threadIdx.x / kColumns, col = threadIdx.x % kColumns * 8;
-    const bool holder = row < kTile && col < k.width;
-    float bias[8], skip[8], sum_d[8], sum_bias[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const bool in = holder && col + j < k.width;
-        bias[j] = in && p.dt_bias != nullptr ? p.dt_bias[k.c + col + j] : 0.f;
-        skip[j] = in && p.D != nullptr ? p.D[k.c + col + j] : 0.f;
-        sum_d[j] = sum_bias[j] = 0.f;
+    for (int i = threadIdx.x; i < kChannels; i += kThreads) {
+        bias[i] = i < k.width && p.dt_bias != nullptr ? p.dt_bias[k.c + i] : 0.f;
+        skip[i] = i < k.width && p.D != nullptr ? p.D[k.c + i] : 0.f;
     }
-    const int ch = threadIdx.x / L, sub = threadIdx.x % L, n0 = sub * NS;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool serves = ch < k.width;
-    const long long mine = (static_cast<long long>(r.s) * C + k.c + ch) * N;
-    float a2[NS], an[NS], carry[NS], da[NS];
-    get_states(an, serves ? p.A + static_cast<long long>(k.c + ch) * N : nullptr, n0, N);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, cl = lane / L, n0 = sub * 4;
+    const int perm = (W >= 2 && (cl & (W / 2)) ? 2 : 0) | (W >= 4 && (cl & (W / 4)) ? 1 : 0);
+    const int order = W >= 4 ? perm : perm >> 1;
+    // this lane's channels within the block
+    const int pair = (warp * W + cl) * 2;
+    const int ch[2] = {pair + (sub & 1), pair + 1 - (sub & 1)};
+    Four a2[2], da[2], carry[2];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        a2[i] = an[i] * kLog2e;
-        da[i] = 0.f;
-    }
-    get_states(carry, serves && r.some && p.dfinal != nullptr ? p.dfinal + mine : nullptr, n0, N);
-
-    const long long tiles = r.some ? (r.end - r.first + kTile - 1) / kTile : 0;
-    for (long long tile = tiles - 1; tile >= 0; --tile) {
-        const long long t0 = r.first + tile * kTile;
-        const bool in = t0 + row < r.end;
-        Vec8<T> ru, rdt, rz, rdy;
-        ru.zero(), rdt.zero(), rz.zero(), rdy.zero();
-        StateRows<T, NP> rb, rc;
-        if (holder && in) {
-            load8(ru, u + (t0 + row) * p.u.row, col, k.width, p.u.vec && even);
-            load8(rdt, dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
-            load8(rdy, dy + (t0 + row) * p.dy.row, col, k.width, p.dy.vec && even);
-            if (z != nullptr) load8(rz, z + (t0 + row) * p.z.row, col, k.width, p.z.vec && even);
+    for (int j = 0; j < 2; ++j) {
+        const bool serves = ch[j] < k.width;
+        const long long at = static_cast<long long>(k.c + ch[j]) * N, wide = static_cast<long long>(C) * N;
+        a2[j].get(serves ? p.A + at : nullptr, n0, perm, N);
+        if (carries != nullptr) carry[j].get(serves && r.some ? carries + slot * wide + at : nullptr, n0, perm, N);
+        else carry[j].get(serves && r.some && p.dfinal != nullptr ? p.dfinal + r.s * wide + at : nullptr, n0, perm, N);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a2[j].v[i] = __fmul2_rn(a2[j].v[i], both(kLog2e));
+            da[j].v[i] = both(0.f);
         }
+    }
+    float sum_d = 0.f, sum_bias[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum_bias[j] = 0.f;
+    const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
+    const int col = threadIdx.x % kColumns * 8;            // (kColumns divides the threads)
+
+    const long long tiles = r.some ? (r.end - r.first + kBwdTile - 1) / kBwdTile : 0;
+    for (long long tile = tiles - 1; tile >= 0; --tile) {
+        const long long t0 = r.first + tile * kBwdTile;
+        Vec8<T> ru[kEach], rdt[kEach], rz[kEach], rdy[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i);
+            ru[i].zero(), rdt[i].zero(), rz[i].zero(), rdy[i].zero();
+            if (row >= kBwdTile || t0 + row >= r.end || col >= k.width) continue;
+            load8(ru[i], u + (t0 + row) * p.u.row, col, k.width, p.u.vec && even);
+            load8(rdt[i], dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
+            load8(rdy[i], dy + (t0 + row) * p.dy.row, col, k.width, p.dy.vec && even);
+            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row, col, k.width, p.z.vec && even);
+        }
+        StateRows<T, NP, kBwdTile> rb, rc;
         rb.fetch(b, p.b, t0, r.end, N);
         rc.fetch(c, p.c, t0, r.end, N);
-        float h[NS];
-        get_states(h, serves ? p.saved + (saved_slot(p.seqs, r, t0 / kTile) * C + k.c + ch) * N : nullptr, n0, N);
+        Four h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            h[j].get(ch[j] < k.width ? p.saved + (saved_slot(p.seqs, r, t0 / kScanTile) * C + k.c + ch[j]) * N : nullptr, n0, perm, N);
         __syncthreads();            // the last tile's sums have been read
-        if (row < kTile) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i);
+            if (row >= kBwdTile) continue;
             float2 fu[4], fd[4], fz[4], fy[4];
-            ru.widen(fu);
-            rdt.widen(fd);
-            rz.widen(fz);
-            rdy.widen(fy);
+            ru[i].widen(fu);
+            rdt[i].widen(fd);
+            rz[i].widen(fz);
+            rdy[i].widen(fy);
+            const bool in = t0 + row < r.end;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float d0 = fd[j].x + bias[2 * j], d1 = fd[j].y + bias[2 * j + 1];
+                const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
+                float d0 = fd[j].x + o.x, d1 = fd[j].y + o.y;
                 if (p.softplus) d0 = softplus(d0), d1 = softplus(d1);
-                if (!in) d0 = d1 = 0.f;
-                step[row][col + 2 * j] = make_float2(d0, d0 * fu[j].x);
-                step[row][col + 2 * j + 1] = make_float2(d1, d1 * fu[j].y);
-                gs[row][col + 2 * j] = z != nullptr ? fy[j].x * silu(fz[j].x) : fy[j].x;
-                gs[row][col + 2 * j + 1] = z != nullptr ? fy[j].y * silu(fz[j].y) : fy[j].y;
+                if (!in) d0 = d1 = 0.f;        // positions past the end change nothing
+                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], make_float2(silu(fz[j].x), silu(fz[j].y)));
+                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d0, fu[j].x, d1, fu[j].y);
+                *reinterpret_cast<float2*>(&gs[row][col + 2 * j]) = fy[j];
             }
         }
-        rb.spread(bs);
-        rc.spread(cs);
+        rb.template spread<kOrders>(bs);
+        rc.template spread<kOrders>(cs);
         __syncthreads();
 #pragma unroll 1
-        for (int w = 0; w < kTile / SB; ++w) {
+        for (int w = 0; w < kBwdTile / kBwdStep; ++w) {
 #pragma unroll
-            for (int i = 0; i < NS; ++i) front[(w * NS + i) * kThreads] = h[i];
-            if (w == kTile / SB - 1) break;
+            for (int j = 0; j < 2; ++j) {
+                front[(w * 8 + j * 4 + 0) * kThreads] = h[j].v[0].x, front[(w * 8 + j * 4 + 1) * kThreads] = h[j].v[0].y;
+                front[(w * 8 + j * 4 + 2) * kThreads] = h[j].v[1].x, front[(w * 8 + j * 4 + 3) * kThreads] = h[j].v[1].y;
+            }
+            if (w == kBwdTile / kBwdStep - 1) break;
 #pragma unroll
-            for (int q = 0; q < SB; ++q) {
-                const float2 s = step[w * SB + q][ch];
-                float fb[NS];
-                row_values(fb, &bs[w * SB + q][n0]);
+            for (int q = 0; q < kBwdStep; ++q) {
+                const int t = w * kBwdStep + q;
+                const float4 fb = *reinterpret_cast<const float4*>(&bs[order][t][n0]);
 #pragma unroll
-                for (int i = 0; i < NS; ++i) h[i] = fmaf(exp2_fast(s.x * a2[i]), h[i], s.y * fb[i]);
+                for (int j = 0; j < 2; ++j) {
+                    const float2 s = step[t][ch[j]];
+                    const float in = s.x * s.y;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 e = __fmul2_rn(both(s.x), a2[j].v[i]);
+                        const float2 a = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                        h[j].v[i] = __ffma2_rn(both(in), i == 0 ? make_float2(fb.x, fb.y) : make_float2(fb.z, fb.w),
+                                               __fmul2_rn(a, h[j].v[i]));
+                    }
+                }
             }
         }
 #pragma unroll 1
-        for (int w = kTile / SB - 1; w >= 0; --w) {
-            float held[SB][NS], decay[SB][NS];       // a h[t-1], a
+        for (int w = kBwdTile / kBwdStep - 1; w >= 0; --w) {
+            float2 held[kBwdStep][2][2], decay[kBwdStep][2][2];       // a h[t-1], a
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[i] = front[(w * NS + i) * kThreads];
-#pragma unroll
-            for (int q = 0; q < SB; ++q) {
-                const float2 s = step[w * SB + q][ch];
-                float fb[NS];
-                row_values(fb, &bs[w * SB + q][n0]);
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    decay[q][i] = exp2_fast(s.x * a2[i]);
-                    held[q][i] = decay[q][i] * h[i];
-                    h[i] = fmaf(s.y, fb[i], held[q][i]);
-                }
+            for (int j = 0; j < 2; ++j) {
+                h[j].v[0] = make_float2(front[(w * 8 + j * 4 + 0) * kThreads], front[(w * 8 + j * 4 + 1) * kThreads]);
+                h[j].v[1] = make_float2(front[(w * 8 + j * 4 + 2) * kThreads], front[(w * 8 + j * 4 + 3) * kThreads]);
             }
-            float s1[SB], s2[SB], s3[SB];
 #pragma unroll
-            for (int q = SB - 1; q >= 0; --q) {
-                const int t = w * SB + q;
-                const float2 s = step[t][ch];
-                const float g = gs[t][ch];
-                float fb[NS], fc[NS], v[2 * NS];
-                row_values(fb, &bs[t][n0]);
-                row_values(fc, &cs[t][n0]);
-                s1[q] = s2[q] = s3[q] = 0.f;
+            for (int q = 0; q < kBwdStep; ++q) {
+                const int t = w * kBwdStep + q;
+                const float4 fb = *reinterpret_cast<const float4*>(&bs[order][t][n0]);
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const float dh = fmaf(g, fc[i], carry[i]);
-                    const float now = fmaf(s.y, fb[i], held[q][i]);
-                    const float x = dh * held[q][i];
-                    v[i] = dh * s.y;
-                    v[NS + i] = g * now;
-                    s1[q] = fmaf(dh, fb[i], s1[q]);
-                    s2[q] = fmaf(x, an[i], s2[q]);
-                    s3[q] = fmaf(fc[i], now, s3[q]);
-                    da[i] = fmaf(x, s.x, da[i]);
-                    carry[i] = dh * decay[q][i];
-                }
-                // over the warp's channels: lanes of the same states part the 2 NS values among themselves
-                int m = kLanes / 2, at_v = 0;
-                constexpr int kV = 2 * NS;
+                for (int j = 0; j < 2; ++j) {
+                    const float2 s = step[t][ch[j]];
+                    const float in = s.x * s.y;
 #pragma unroll
-                for (int half = kV / 2; half > 0 && m > 0; half >>= 1, m >>= 1) {
-                    const bool upper = (lane / L & m) != 0;
-                    if (upper) at_v += half;
-#pragma unroll
-                    for (int i = 0; i < half; ++i) {
-                        const float keep = upper ? v[half + i] : v[i], send = upper ? v[i] : v[half + i];
-                        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m * L);
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 e = __fmul2_rn(both(s.x), a2[j].v[i]);
+                        decay[q][j][i] = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                        held[q][j][i] = __fmul2_rn(decay[q][j][i], h[j].v[i]);
+                        if (q + 1 < kBwdStep)
+                            h[j].v[i] = __ffma2_rn(both(in), i == 0 ? make_float2(fb.x, fb.y) : make_float2(fb.z, fb.w), held[q][j][i]);
                     }
                 }
-                constexpr int kHeld = kV > kLanes ? kV / kLanes : 1;        // values left to a lane
-                if constexpr (kLanes > kV) {
+            }
+            float into[kBwdStep], decays[kBwdStep], ys[kBwdStep];
 #pragma unroll
-                    for (; m > 0; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m * L);
+            for (int q = kBwdStep - 1; q >= 0; --q) {
+                const int t = w * kBwdStep + q;
+                const float4 b4 = *reinterpret_cast<const float4*>(&bs[order][t][n0]);
+                const float4 c4 = *reinterpret_cast<const float4*>(&cs[order][t][n0]);
+                const float2 fb[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+                const float2 fc[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+                float2 vb[2] = {both(0.f), both(0.f)}, vc[2] = {both(0.f), both(0.f)};
+                float s1[2], s2[2], s3[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 s = step[t][ch[j]];
+                    const float g = gs[t][ch[j]], in = s.x * s.y;
+                    float2 x1 = both(0.f), x2 = both(0.f), x3 = both(0.f);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 dh = __ffma2_rn(both(g), fc[i], carry[j].v[i]);
+                        const float2 now = __ffma2_rn(both(in), fb[i], held[q][j][i]);
+                        const float2 x = __fmul2_rn(dh, held[q][j][i]);
+                        vb[i] = __ffma2_rn(dh, both(in), vb[i]);
+                        vc[i] = __ffma2_rn(both(g), now, vc[i]);
+                        x1 = __ffma2_rn(dh, fb[i], x1);
+                        x2 = __ffma2_rn(x, a2[j].v[i], x2);
+                        x3 = __ffma2_rn(fc[i], now, x3);
+                        da[j].v[i] = __ffma2_rn(x, both(s.x), da[j].v[i]);
+                        carry[j].v[i] = __fmul2_rn(dh, decay[q][j][i]);
+                    }
+                    s1[j] = x1.x + x1.y, s2[j] = x2.x + x2.y, s3[j] = x3.x + x3.y;
                 }
-#pragma unroll
-                for (int i = 0; i < kHeld; ++i) {
-                    const int j = at_v + i, which = j / NS, n = n0 + j % NS;
-                    if (kLanes <= kV || (lane / L) % (kLanes / kV > 0 ? kLanes / kV : 1) == 0)
-                        sums[((warp * kTile + t) * 2 + which) * NP + n] = v[i];
+                // over the states, first step: the partner's other channel is this lane's first
+                into[q] = s1[0] + from_lane(s1[1], 1);
+                decays[q] = s2[0] + from_lane(s2[1], 1);
+                ys[q] = s3[0] + from_lane(s3[1], 1);
+                // over the warp's channels
+                float* to = sums + (warp * kBwdTile + t) * 2 * NP;
+                if constexpr (W >= 2) {
+                    vb[0] = make_float2(vb[0].x + from_lane(vb[1].x, W / 2 * L), vb[0].y + from_lane(vb[1].y, W / 2 * L));
+                    vc[0] = make_float2(vc[0].x + from_lane(vc[1].x, W / 2 * L), vc[0].y + from_lane(vc[1].y, W / 2 * L));
+                }
+                if constexpr (W >= 4) {
+                    vb[0].x += from_lane(vb[0].y, W / 4 * L);
+                    vc[0].x += from_lane(vc[0].y, W / 4 * L);
+                }
+                if constexpr (W >= 8) {
+                    const bool which = (cl & (W / 8)) != 0;
+                    float v = (which ? vc[0].x : vb[0].x) + from_lane(which ? vb[0].x : vc[0].x, W / 8 * L);
+                    if constexpr (W >= 16) v += from_lane(v, W / 16 * L);
+                    if (W < 16 || (cl & (W / 16)) == 0) to[(which ? NP : 0) + n0 + perm] = v;
+                } else if constexpr (W == 4) {
+                    to[n0 + perm] = vb[0].x;
+                    to[NP + n0 + perm] = vc[0].x;
+                } else if constexpr (W == 2) {
+                    to[n0 + perm] = vb[0].x, to[n0 + (1 ^ perm)] = vb[0].y;
+                    to[NP + n0 + perm] = vc[0].x, to[NP + n0 + (1 ^ perm)] = vc[0].y;
+                } else {
+                    *reinterpret_cast<float4*>(to + n0) = make_float4(vb[0].x, vb[0].y, vb[1].x, vb[1].y);
+                    *reinterpret_cast<float4*>(to + NP + n0) = make_float4(vc[0].x, vc[0].y, vc[1].x, vc[1].y);
                 }
             }
+            // over the states: the lanes part the positions among themselves
+            constexpr int kParts = L >= 8 ? 4 : L / 2, kMine = kBwdStep / kParts;
+            int first = 0;
+            if constexpr (L >= 4) {
+                const bool upper = (sub & 2) != 0;
+                first = upper ? 2 : 0;
 #pragma unroll
-            for (int q = 0; q < SB; q += kPart) {
-                float v1[L], v2[L], v3[L];
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    v1[i] = i < kPart ? s1[q + (i < kPart ? i : 0)] : 0.f;
-                    v2[i] = i < kPart ? s2[q + (i < kPart ? i : 0)] : 0.f;
-                    v3[i] = i < kPart ? s3[q + (i < kPart ? i : 0)] : 0.f;
+                for (int q = 0; q < 2; ++q) {
+                    into[q] = (upper ? into[q + 2] : into[q]) + from_lane(upper ? into[q] : into[q + 2], 2);
+                    decays[q] = (upper ? decays[q + 2] : decays[q]) + from_lane(upper ? decays[q] : decays[q + 2], 2);
+                    ys[q] = (upper ? ys[q + 2] : ys[q]) + from_lane(upper ? ys[q] : ys[q + 2], 2);
                 }
-                const float x1 = parted<L>(v1, sub), x2 = parted<L>(v2, sub), x3 = parted<L>(v3, sub);
-                if (sub < kPart) {
-                    into_s[w * SB + q + sub][ch] = x1;
-                    decay_s[w * SB + q + sub][ch] = x2;
-                    ys[w * SB + q + sub][ch] = x3;
+            }
+            if constexpr (L >= 8) {
+                const bool upper = (sub & 4) != 0;
+                first += upper ? 1 : 0;
+                into[0] = (upper ? into[1] : into[0]) + from_lane(upper ? into[0] : into[1], 4);
+                decays[0] = (upper ? decays[1] : decays[0]) + from_lane(upper ? decays[0] : decays[1], 4);
+                ys[0] = (upper ? ys[1] : ys[0]) + from_lane(upper ? ys[0] : ys[1], 4);
+            }
+#pragma unroll
+            for (int m = 8; m < L; m *= 2) {
+                into[0] += from_lane(into[0], m);
+                decays[0] += from_lane(decays[0], m);
+                ys[0] += from_lane(ys[0], m);
+            }
+            __syncwarp();       // all lanes have read these positions
+            if (L < 16 || sub < 8) {
+#pragma unroll
+                for (int q = 0; q < kMine; ++q) {
+                    const int t = w * kBwdStep + first + q;
+                    const float2 s = step[t][ch[0]];
+                    const float g = gs[t][ch[0]];
+                    sum_d = fmaf(g, s.y, sum_d);
+                    step[t][ch[0]] = make_float2(fmaf(into[q], s.x, skip[ch[0]] * g), fmaf(into[q], s.y, decays[q] * 0.6931471805599453f));
+                    gs[t][ch[0]] = ys[q];
                 }
             }
         }
         __syncthreads();
         // dB and dC of the CTA's channels
-        for (int i = threadIdx.x; i < kTile * 2 * N; i += kThreads) {
-            const int t = i / (2 * N), j = i - t * 2 * N, which = j / N, n = j - which * N;
-            if (t0 + t >= r.end) break;
+        for (int i = threadIdx.x; i < kBwdTile * 2 * NP; i += kThreads) {
+            const int t = i / (2 * NP), j = i % (2 * NP), which = j / NP, n = j % NP;
+            if (n >= N || t0 + t >= r.end) continue;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += sums[((w * kTile + t) * 2 + which) * NP + n];
-            part_bc[(block * seq_rows_device(p.seqs) + dense + t0 + t) * 2 * N + j] = s;
+            for (int w = 0; w < S::kWarps; ++w) s += sums[(w * kBwdTile + t) * 2 * NP + j];
+            part_bc[((block * seq_rows_device(p.seqs) + dense + t0 + t) * 2 + which) * N + n] = s;
         }
-        if (holder && in) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int row = row_of(i);
+            if (row >= kBwdTile || t0 + row >= r.end || col >= k.width) continue;
             float2 fu[4], fd[4], fz[4], fy[4], du[4], ddt[4], dz[4];
-            ru.widen(fu);
-            rdt.widen(fd);
-            rz.widen(fz);
-            rdy.widen(fy);
-            const auto finish = [&](int j, float uu, float raw, float zz, float dyy, float& o_u, float& o_dt, float& o_z) {
-                const float g = gs[row][col + j], into = into_s[row][col + j], delta = step[row][col + j].x;
-                o_u = fmaf(into, delta, skip[j] * g);
-                float d = fmaf(into, uu, decay_s[row][col + j]);
-                if (p.softplus) d *= sigmoid(raw + bias[j]);
-                o_dt = d;
-                sum_d[j] = fmaf(g, uu, sum_d[j]);
-                sum_bias[j] += d;
-                if (z != nullptr) o_z = dyy * fmaf(skip[j], uu, ys[row][col + j]) * silu_slope(zz, sigmoid(zz));
-            };
+            ru[i].widen(fu);
+            rdt[i].widen(fd);
+            rz[i].widen(fz);
+            rdy[i].widen(fy);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                finish(2 * j, fu[j].x, fd[j].x, fz[j].x, fy[j].x, du[j].x, ddt[j].x, dz[j].x);
-                finish(2 * j + 1, fu[j].y, fd[j].y, fz[j].y, fy[j].y, du[j].y, ddt[j].y, dz[j].y);
+                const float4 s = *reinterpret_cast<const float4*>(&step[row][col + 2 * j]);
+                du[j] = make_float2(s.x, s.z);
+                ddt[j] = make_float2(s.y, s.w);
+                if (p.softplus) {
+                    const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
+                    ddt[j] = __fmul2_rn(ddt[j], make_float2(sigmoid(fd[j].x + o.x), sigmoid(fd[j].y + o.y)));
+                }
+                sum_bias[2 * j] += ddt[j].x;
+                sum_bias[2 * j + 1] += ddt[j].y;
+                if (z != nullptr) {
+                    const float2 sum = __ffma2_rn(*reinterpret_cast<const float2*>(&skip[col + 2 * j]), fu[j],
+                                                  *reinterpret_cast<const float2*>(&gs[row][col + 2 * j]));
+                    dz[j] = __fmul2_rn(__fmul2_rn(fy[j], sum), make_float2(silu_slope(fz[j].x, sigmoid(fz[j].x)),
+                                                                           silu_slope(fz[j].y, sigmoid(fz[j].y))));
+                }
             }
             const long long o = (dense + t0 + row) * C + k.c;
             store8(static_cast<T*>(p.du) + o, du, col, k.width, aligned(p.du));
@@ -493,25 +787,37 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(Scan p, int blocks, 
             if (z != nullptr) store8(static_cast<T*>(p.dz) + o, dz, col, k.width, aligned(p.dz));
         }
     }
-    if (serves) {
-        if (r.some && p.dstate != nullptr) put_states(p.dstate + mine, carry, n0, N);
-        put_states(part_a + (slot * C + k.c + ch) * N, da, n0, N);
-    }
-    // over the threads of a column
-    __syncthreads();
-    float* red = smem;
-    if (row < kTile) {
+    // this chunk's rows of parameter gradients: C x N of dA, C of dD, C of the bias's
+    float* part = part_p + slot * C * (N + 2);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            red[(row * kChannels + col + j) * 2] = sum_d[j];
-            red[(row * kChannels + col + j) * 2 + 1] = sum_bias[j];
-        }
+    for (int j = 0; j < 2; ++j) {
+        if (ch[j] >= k.width) continue;
+        const long long at = static_cast<long long>(k.c + ch[j]) * N;
+        if (r.some && r.index == 0 && p.dstate != nullptr) carry[j].put(p.dstate + static_cast<long long>(r.s) * C * N + at, n0, perm, N);
+        da[j].put(part + at, n0, perm, N);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < k.width * 2; i += kThreads) {
+    // over the threads of a column, and over the lanes that had a channel first
+    float* red = smem;
+    constexpr int kRows = kThreads / kColumns;
+    constexpr int kStride = kChannels + 4;      // (rows of 8 columns apart: fewer conflicts)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[static_cast<int>(threadIdx.x) / kColumns * kStride + col + j] = sum_bias[j];
+    __syncthreads();
+    float* mine = part + static_cast<long long>(C) * N + k.c;
+    for (int i = threadIdx.x; i < k.width; i += kThreads) {
         float s = 0.f;
-        for (int q = 0; q < kTile; ++q) s += red[q * kChannels * 2 + i];
-        (i % 2 == 0 ? part_d : part_bias)[slot * C + k.c + i / 2] = s;
+        for (int q = 0; q < kRows; ++q) s += red[q * kStride + i];
+        mine[C + i] = s;
+    }
+    __syncthreads();
+    red[threadIdx.x] = sum_d;
+    __syncthreads();
+    for (int i = threadIdx.x; i < k.width; i += kThreads) {
+        const int lanes = i / 2 * L + (i & 1);      // the first lane whose first channel is i
+        float s = 0.f;
+        for (int q = 0; q < L; q += 2) s += red[lanes + q];
+        mine[i] = s;
     }
 }
 
@@ -535,71 +841,120 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(Scan p, const float* part,
 
 inline int channel_blocks(const Scan& p, int channels) { return p.G * ((p.C / p.G + channels - 1) / channels); }
 
-// Lanes to a channel by the number of states.
-inline int lanes_of(int N) { return N <= 32 ? 4 : N <= 64 ? 8 : 16; }
+// Forward: states to a lane and lanes to a channel, by the number of states.
+#define DWC_SCAN_FWD_SHAPE(N, call)                 \
+    if ((N) <= 8) return call(2, 4);                \
+    if ((N) <= 16) return call(4, 4);               \
+    if ((N) <= 32) return call(8, 4);               \
+    if ((N) <= 64) return call(8, 8);               \
+    return call(8, 16);
+inline int fwd_channels(int N) {
+#define DWC_CHANNELS(NS, L) (kThreads / (L))
+    DWC_SCAN_FWD_SHAPE(N, DWC_CHANNELS)
+#undef DWC_CHANNELS
+}
+inline int bwd_lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+
+// The workspaces, in floats.
+struct FwdSpace {
+    long long ends = 0, sums = 0;      // with chunks only
+    explicit FwdSpace(const Scan& p) {
+        if (p.span >= p.seqs.length) return;
+        sums = seq_slots(p.seqs, p.span) * p.C;
+        ends = sums * p.N;
+    }
+};
+struct BwdSpace {
+    long long bc, params, ends = 0, sums = 0;
+    explicit BwdSpace(const Scan& p) {
+        const long long slots = seq_slots(p.seqs, p.span), C = p.C;
+        bc = static_cast<long long>(channel_blocks(p, 2 * kThreads / bwd_lanes(p.N))) * seq_rows(p.seqs) * 2 * p.N;
+        params = slots * C * (p.N + 2);
+        if (p.span >= p.seqs.length) return;
+        sums = slots * C;
+        ends = sums * p.N;
+    }
+};
+
+template <bool kBackward>
+cudaError_t launch_join(const Scan& p, float* ends, const float* sums, const float* from) {
+    const long long grid = (static_cast<long long>(p.seqs.count) * p.C * p.N + 255) / 256;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(scan_join_kernel<kBackward>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, p.stream, p, ends, sums, from);
+}
 
 template <typename T, int NS, int L>
 cudaError_t fwd_t(const Scan& p) {
     const int blocks = channel_blocks(p, kThreads / L);
-    const long long grid = seq_slots(p.seqs, p.seqs.length + 1) * blocks;
+    const long long grid = seq_slots(p.seqs, p.span) * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(scan_fwd_kernel<T, NS, L>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p, blocks);
+    const FwdSpace space(p);
+    float *ends = space.ends > 0 ? p.workspace : nullptr, *sums = p.workspace + space.ends;
+    if (ends != nullptr) {
+        cudaError_t err = launch_pdl(scan_fwd_kernel<T, NS, L, true>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream,
+                                     p, blocks, ends, sums);
+        if (err == cudaSuccess) err = launch_join<false>(p, ends, sums, p.state);
+        if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(scan_fwd_kernel<T, NS, L, false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p, blocks,
+                      ends, sums);
 }
 
-// The backward pass's workspace, in floats: partial dB and dC, dA, dD and the bias's gradient.
-struct Partials {
-    long long bc, a, d, total;
-    explicit Partials(const Scan& p) {
-        const long long slots = seq_slots(p.seqs, p.seqs.length + 1), C = p.C;
-        bc = static_cast<long long>(channel_blocks(p, kThreads / lanes_of(p.N))) * seq_rows(p.seqs) * 2 * p.N;
-        a = slots * C * p.N;
-        d = slots * C;
-        total = bc + a + 2 * d;
-    }
-};
-
-template <typename T, int NS, int L, int SB>
-cudaError_t bwd_t(const Scan& p) {
-    constexpr int kChannels = kThreads / L, NP = NS * L;
-    constexpr size_t smem = sizeof(float) * (kTile * kChannels * 6 + kTile * NP * 2 + kThreads / 32 * kTile * 2 * NP + kTile / SB * NS * kThreads);
-    const int blocks = channel_blocks(p, kChannels);
-    const long long slots = seq_slots(p.seqs, p.seqs.length + 1), grid = slots * blocks, rows = seq_rows(p.seqs);
-    const Partials part(p);
-    float *bc = p.workspace, *a = bc + part.bc, *d = a + part.a, *bias = d + part.d;
-    static DeviceOnce once;
-    cudaError_t err = opt_in_smem(scan_bwd_kernel<T, NS, L, SB>, once, static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
+template <typename T, int NS, int L>
+cudaError_t adjoint_t(const Scan& p, float* ends, float* sums) {
+    const int blocks = channel_blocks(p, kThreads / L);
+    const long long grid = seq_slots(p.seqs, p.span) * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    err = launch_pdl(scan_bwd_kernel<T, NS, L, SB>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, p.stream, p, blocks,
-                     bc, a, d, bias);
+    const cudaError_t err = launch_pdl(scan_adjoint_kernel<T, NS, L>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream,
+                                       p, blocks, ends, sums);
+    return err != cudaSuccess ? err : launch_join<true>(p, ends, sums, p.dfinal);
+}
+template <typename T>
+cudaError_t adjoint(const Scan& p, float* ends, float* sums) {
+#define DWC_ADJOINT(NS, L) (adjoint_t<T, NS, L>(p, ends, sums))
+    DWC_SCAN_FWD_SHAPE(p.N, DWC_ADJOINT)
+#undef DWC_ADJOINT
+}
+
+template <typename T, int L>
+cudaError_t bwd_t(const Scan& p) {
+    using S = BwdShape<L>;
+    constexpr size_t smem = S::kFloats * sizeof(float);
+    const int blocks = channel_blocks(p, S::kChannels);
+    const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks, rows = seq_rows(p.seqs), C = p.C;
     const long long sums = (rows * p.G * 2 * p.N + 255) / 256;
-    if (sums > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (grid > 0x7fffffffLL || sums > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const BwdSpace space(p);
+    float *bc = p.workspace, *params = bc + space.bc, *ends = params + space.params;
+    static DeviceOnce once;
+    cudaError_t err = opt_in_smem(scan_bwd_kernel<T, L>, once, static_cast<int>(smem));
+    if (err == cudaSuccess && space.ends > 0) err = adjoint<T>(p, ends, ends + space.ends);
+    if (err == cudaSuccess)
+        err = launch_pdl(scan_bwd_kernel<T, L>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, p.stream, p, blocks,
+                         static_cast<const float*>(space.ends > 0 ? ends : nullptr), bc, params);
     if (err == cudaSuccess && sums > 0)
         err = launch_pdl(scan_bc_kernel<T>, dim3(static_cast<unsigned>(sums)), dim3(256), 0, p.stream, p,
                          static_cast<const float*>(bc), blocks / p.G, rows);
-    const long long C = p.C;
-    if (err == cudaSuccess) err = launch_row_sum(a, slots, C * p.N, C * p.N, p.dA, p.stream);
-    if (err == cudaSuccess) err = launch_row_sum(d, slots, C, C, p.dD, p.stream);
-    if (err == cudaSuccess) err = launch_row_sum(bias, slots, C, C, p.ddt_bias, p.stream);
+    if (err == cudaSuccess) err = launch_row_sum(params, slots, C * (p.N + 2), {p.dA, p.dD, p.ddt_bias}, {C * p.N, C, C}, p.stream);
     return err;
 }
 
 template <typename T>
 cudaError_t fwd(const Scan& p) {
-    if (p.N <= 8) return fwd_t<T, 2, 4>(p);
-    if (p.N <= 16) return fwd_t<T, 4, 4>(p);
-    if (p.N <= 32) return fwd_t<T, 8, 4>(p);
-    if (p.N <= 64) return fwd_t<T, 8, 8>(p);
-    return fwd_t<T, 8, 16>(p);
+#define DWC_FWD(NS, L) (fwd_t<T, NS, L>(p))
+    DWC_SCAN_FWD_SHAPE(p.N, DWC_FWD)
+#undef DWC_FWD
 }
 
 template <typename T>
 cudaError_t bwd(const Scan& p) {
-    if (p.N <= 8) return bwd_t<T, 2, 4, 8>(p);
-    if (p.N <= 16) return bwd_t<T, 4, 4, 8>(p);
-    if (p.N <= 32) return bwd_t<T, 8, 4, 4>(p);
-    if (p.N <= 64) return bwd_t<T, 8, 8, 4>(p);
-    return bwd_t<T, 8, 16, 4>(p);
+    switch (bwd_lanes(p.N)) {
+        case 2: return bwd_t<T, 2>(p);
+        case 4: return bwd_t<T, 4>(p);
+        case 8: return bwd_t<T, 8>(p);
+        case 16: return bwd_t<T, 16>(p);
+        default: return bwd_t<T, 32>(p);
+    }
 }
 
 }  // namespace scan

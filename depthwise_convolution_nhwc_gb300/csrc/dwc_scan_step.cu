@@ -95,7 +95,31 @@ cudaError_t launch_scan_step(const Scan& p, float* state, long long state_stride
     }
 }
 
-size_t scan_fwd_workspace_floats(const Scan&) { return 0; }
-size_t scan_bwd_workspace_floats(const Scan& p) { return static_cast<size_t>(scan::Partials(p).total); }
+namespace {
+
+// Positions to a chunk: the whole sequence where there are enough CTAs, else what gives every SM about
+// four of them, 128 at least.  Packed sequences differ in length: those up to twice the mean stay whole.
+long long span_of(const Seqs& s, long long blocks) {
+    const long long sms = device_info().sm_count;
+    if (s.count == 0 || s.length == 0) return 1 << 20;
+    const long long rows = seq_rows(s), whole = s.offsets != nullptr ? std::max(2 * (rows / s.count), rows * blocks / (4 * sms))
+                                                                      : s.count * blocks >= 2 * sms ? s.length : rows * blocks / (4 * sms);
+    return std::max<long long>(128, (whole + 31) / 32 * 32);
+}
+
+}  // namespace
+
+long long scan_fwd_span(const Scan& p) { return span_of(p.seqs, scan::channel_blocks(p, scan::fwd_channels(p.N))); }
+long long scan_bwd_span(const Scan& p) {
+    return span_of(p.seqs, scan::channel_blocks(p, 2 * scan::kThreads / scan::bwd_lanes(p.N)));
+}
+size_t scan_fwd_workspace_floats(const Scan& p) {
+    const scan::FwdSpace s(p);
+    return static_cast<size_t>(s.ends + s.sums);
+}
+size_t scan_bwd_workspace_floats(const Scan& p) {
+    const scan::BwdSpace s(p);
+    return static_cast<size_t>(s.bc + s.params + s.ends + s.sums);
+}
 
 }  // namespace dwc

@@ -260,12 +260,16 @@ size_t dwc_selective_scan_saved_floats(const dwc_scan_t* scan) {
 
 size_t dwc_selective_scan_fwd_workspace_size(const dwc_scan_t* scan) {
     if (check_scan(scan, false) != DWC_OK || scan->seqs.count == 0) return 0;
-    return scan_fwd_workspace_floats(scan_of(*scan, nullptr)) * sizeof(float);
+    Scan p = scan_of(*scan, nullptr);
+    p.span = scan_fwd_span(p);
+    return scan_fwd_workspace_floats(p) * sizeof(float);
 }
 
 size_t dwc_selective_scan_bwd_workspace_size(const dwc_scan_t* scan) {
     if (check_scan(scan, false) != DWC_OK || scan->seqs.count == 0) return 0;
-    return scan_bwd_workspace_floats(scan_of(*scan, nullptr)) * sizeof(float);
+    Scan p = scan_of(*scan, nullptr);
+    p.span = scan_bwd_span(p);
+    return scan_bwd_workspace_floats(p) * sizeof(float);
 }
 
 dwc_status_t dwc_selective_scan_fwd(const dwc_scan_t* scan, const float* state, void* y, float* final_state,
@@ -278,6 +282,7 @@ dwc_status_t dwc_selective_scan_fwd(const dwc_scan_t* scan, const float* state, 
     if (scan->seqs.count == 0 || (positions(scan->seqs) == 0 && final_state == nullptr)) return DWC_OK;
     if (scan->A == nullptr) return DWC_ERR_INVALID_ARG;
     Scan p = scan_of(*scan, stream);
+    p.span = scan_fwd_span(p);
     st = check_workspace(workspace, workspace_bytes, scan_fwd_workspace_floats(p) * sizeof(float));
     if (st != DWC_OK) return st;
     p.state = state;
@@ -308,6 +313,7 @@ dwc_status_t dwc_selective_scan_bwd(const dwc_scan_t* scan, const dwc_rows_t* dy
                             zero(ddt_bias, scan->C, stream)});
     if (scan->A == nullptr) return DWC_ERR_INVALID_ARG;
     Scan p = scan_of(*scan, stream);
+    p.span = scan_bwd_span(p);
     st = check_workspace(workspace, workspace_bytes, scan_bwd_workspace_floats(p) * sizeof(float));
     if (st != DWC_OK) return st;
     p.dy = view_of(*dy, scan->seqs, bytes);

@@ -64,11 +64,6 @@ __device__ __forceinline__ long long dense_row(const Seqs& q, const Piece& r) {
     return q.offsets != nullptr ? r.base : r.s * q.length;
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + expf(-v)); }
-// d silu / d v, from sigmoid(v)
-__device__ __forceinline__ float silu_slope(float v, float s) { return fmaf(v * s, 1.f - s, s); }
-
 // 8 values of a row from column `col`, those at `limit` and beyond as zeros.
 template <typename T>
 __device__ __forceinline__ void load8(Vec8<T>& v, const T* row, int col, int limit, bool vec) {

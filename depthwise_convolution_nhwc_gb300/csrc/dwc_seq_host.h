@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "dwc_host.h"
 
 namespace dwc {
@@ -66,8 +68,8 @@ cudaError_t launch_causal_conv_fwd(const CausalConv& p);
 cudaError_t launch_causal_conv_bwd(const CausalConv& p);
 cudaError_t launch_causal_conv_step(const CausalConv& p, void* state, long long state_stride);
 
-// Positions between the states that the forward pass keeps for the backward pass, and of a tile.
-constexpr int kScanTile = 32;
+// Positions between the states that the forward pass keeps for the backward pass.
+constexpr int kScanTile = 16;
 constexpr int kScanMaxStates = 128;
 
 struct Scan {
@@ -97,9 +99,13 @@ struct Scan {
     float* ddt_bias;
     float* dstate;          // may be null
     float* workspace;
+    long long span;         // positions to a chunk
     cudaStream_t stream;
 };
 
+// Positions to a chunk (a multiple of 32; a sequence's length or more: no chunks) and, with them, the workspaces.
+long long scan_fwd_span(const Scan& p);
+long long scan_bwd_span(const Scan& p);
 size_t scan_fwd_workspace_floats(const Scan& p);
 size_t scan_bwd_workspace_floats(const Scan& p);
 #define DWC_SCAN_TYPE(name)                            \
@@ -120,8 +126,15 @@ struct ZeroBeside {
 };
 cudaError_t launch_zero_beside(const ZeroBeside& p);
 
-// out[j] = sum of `count` rows of `width` floats that lie `stride` apart, in a fixed order.
-cudaError_t launch_row_sum(const float* rows, long long count, long long stride, long long width, float* out,
-                           cudaStream_t stream);
+// Sums of `count` rows that lie `stride` floats apart, in a fixed order: of the first widths[0] columns to out[0]
+// (may be null), of the next widths[1] to out[1] and so on.
+struct RowSum {
+    const float* rows;
+    long long count, stride;
+    float* out[3];
+    long long widths[3];
+};
+cudaError_t launch_row_sum(const float* rows, long long count, long long stride, std::initializer_list<float*> out,
+                           std::initializer_list<long long> widths, cudaStream_t stream);
 
 }  // namespace dwc

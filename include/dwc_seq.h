@@ -115,7 +115,7 @@ typedef struct {
     const float* dt_bias;    /* C values, or NULL (0) */
 } dwc_scan_t;
 
-/* Floats of `saved`: the states in front of every 32nd position of each sequence, what the
+/* Floats of `saved`: the states in front of every 16th position of each sequence, what the
  * backward pass starts from (0 for invalid sizes). */
 size_t dwc_selective_scan_saved_floats(const dwc_scan_t* scan);
 /* Bytes of workspace of the two passes on the CURRENT device (0: none, or invalid sizes). */

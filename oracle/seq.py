@@ -15,7 +15,9 @@ import numpy as np
 from .norm import TINY, U
 
 u = U["f32"]
-SMALL = 2.0 ** -120        # beside results that fp32 cannot hold relative errors of (flushed subnormals)
+# beside results that fp32 cannot hold relative errors of: exp2 flushes results below 2^-126 to zero, a quotient by
+# more than 2^126 (1 + exp(-v) from v = -87.3 on) gives zero, which silu multiplies by v
+SMALL = 2.0 ** -118
 
 
 class Val:
@@ -81,8 +83,9 @@ def exp(x):
 def sigmoid(x):
     with np.errstate(over="ignore"):
         s = 1 / (1 + np.exp(-x.v))
-    # 1 / (1 + exp(-x)): the exponential's relative error counts by its share 1 - s, then a sum and a quotient
-    return Val(s, s * (1 - s) * (np.expm1(np.minimum(x.e, 50.0)) + 4 * u) + 4 * u * s + SMALL)
+    # 1 / (1 + 2^(-x log2(e))): the exponential's relative error (its argument's, the constant's and the product's
+    # roundings, 2 u |x|, and its own, 4 u) counts by its share 1 - s, then a sum and a quotient
+    return Val(s, s * (1 - s) * (np.expm1(np.minimum(x.e + 2 * u * np.abs(x.v), 50.0)) + 4 * u) + 4 * u * s + SMALL)
 
 
 def silu(x):
@@ -99,9 +102,9 @@ def softplus(x):
     v = np.maximum(x.v, 0) + np.log1p(np.exp(-np.abs(x.v)))
     s = 1 / (1 + np.exp(-x.v))
     small = np.log1p(np.exp(-np.abs(x.v)))
-    # log1p(e) of a relative error of e (4 u) is off by at most as much; its series 8 u (a sum, a quotient of 3 u, the
+    # log1p(e) of a relative error of e = 2^(-|x| log2(e)) (4 u + 2 u |x|, as above) is off by at most as much; its series 8 u (a sum, a quotient of 3 u, the
     # odd series: each step's rounding is scaled by s^2 <= 1/9); then the sum with max(x, 0)
-    return Val(v, s * x.e + 12 * u * small + u * v + SMALL)
+    return Val(v, s * x.e + (12 + 2 * np.abs(x.v)) * u * small + u * v + SMALL)
 
 
 GATES = {"none": (lambda x: x, lambda x: Val(np.ones_like(x.v))), "sigmoid": (sigmoid, lambda x: sigmoid(x) * (1.0 - sigmoid(x))),

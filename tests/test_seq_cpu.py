@@ -228,7 +228,7 @@ def test_scan_outputs_and_workspace(lib):
         assert fwd(**{k: FAKE + 2}) == ALIGNMENT
     need = lib.dwc_selective_scan_bwd_workspace_size(s)
     assert need > 0 and lib.dwc_selective_scan_bwd_workspace_size(scan(N=129)) == 0
-    assert lib.dwc_selective_scan_saved_floats(s) == 2 * 8 * 4 and lib.dwc_selective_scan_saved_floats(scan(length=33)) == 4 * 8 * 4
+    assert lib.dwc_selective_scan_saved_floats(s) == 2 * 8 * 4 and lib.dwc_selective_scan_saved_floats(scan(length=33)) == 6 * 8 * 4
 
     def bwd(**kw):
         a = dict(dy=dy, saved=FAKE, dfinal=None, du=FAKE, ddt=FAKE, dz=FAKE, db=FAKE, dc=FAKE, dA=FAKE, dD=FAKE, bias=FAKE,
