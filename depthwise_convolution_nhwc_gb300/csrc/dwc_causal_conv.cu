@@ -17,7 +17,46 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// V adjacent values of a row as they lie in memory.
+// fp32 values of V adjacent channels, in pairs for the packed arithmetic.
+template <int V>
+struct Lanes {
+    float2 v[V / 2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[j] = both(0.f);
+    }
+    __device__ __forceinline__ void fma(const Lanes& a, const Lanes& b) {        // += a b
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[j] = __ffma2_rn(a.v[j], b.v[j], v[j]);
+    }
+    __device__ __forceinline__ void add(const Lanes& a) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[j] = __fadd2_rn(v[j], a.v[j]);
+    }
+    __device__ __forceinline__ void to_silu() {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[j] = silu2(v[j]);
+    }
+    __device__ __forceinline__ void by_slope(const Lanes& a) {                   // *= silu'(a)
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[j] = __fmul2_rn(v[j], silu_slope2(a.v[j]));
+    }
+    __device__ __forceinline__ float get(int j) const { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+    __device__ __forceinline__ void set(int j, float f) { (j & 1 ? v[j / 2].y : v[j / 2].x) = f; }
+};
+template <>
+struct Lanes<1> {
+    float v;
+    __device__ __forceinline__ void clear() { v = 0.f; }
+    __device__ __forceinline__ void fma(const Lanes& a, const Lanes& b) { v = fmaf(a.v, b.v, v); }
+    __device__ __forceinline__ void add(const Lanes& a) { v += a.v; }
+    __device__ __forceinline__ void to_silu() { v = silu(v); }
+    __device__ __forceinline__ void by_slope(const Lanes& a) { v *= silu_slope(a.v, sigmoid(a.v)); }
+    __device__ __forceinline__ float get(int) const { return v; }
+    __device__ __forceinline__ void set(int, float f) { v = f; }
+};
+
+// The same as they lie in memory.
 template <typename T, int V>
 struct Raw {
     static constexpr int kBytes = V * sizeof(T);
@@ -25,59 +64,60 @@ struct Raw {
     Word w;
     __device__ __forceinline__ void zero() { w = Word{}; }
     __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
-    __device__ __forceinline__ void widen(float (&f)[V]) const {
-        const T* v = reinterpret_cast<const T*>(&w);
+    __device__ __forceinline__ Lanes<V> widen() const {
+        Lanes<V> f;
+        if constexpr (V == 1) {
+            f.v = to_f32(*reinterpret_cast<const T*>(&w));
+        } else {
+            using Pair = typename Elem<T>::pair_t;
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = to_f32(v[j]);
+            for (int j = 0; j < V / 2; ++j) f.v[j] = Elem<T>::load_pair(reinterpret_cast<const T*>(reinterpret_cast<const Pair*>(&w) + j));
+        }
+        return f;
     }
-    __device__ static __forceinline__ void store(T* p, const float (&f)[V]) {
+    __device__ static __forceinline__ void store(T* p, const Lanes<V>& f) {
         Raw r;
         T* v = reinterpret_cast<T*>(&r.w);
 #pragma unroll
-        for (int j = 0; j < V; ++j) store_out(v + j, f[j]);
+        for (int j = 0; j < V; ++j) store_out(v + j, f.get(j));
         *reinterpret_cast<Word*>(p) = r.w;
     }
 };
 
 // Input at position t of a sequence (negative: from its state).
 template <typename T, int V>
-__device__ __forceinline__ void input(float (&f)[V], const T* x, long long row, const T* state, int C, int K, long long t) {
+__device__ __forceinline__ Lanes<V> input(const T* x, long long row, const T* state, int C, int K, long long t) {
     Raw<T, V> r;
     r.zero();
     if (t >= 0) r.load(x + t * row);
     else if (state != nullptr) r.load(state + (t + K - 1) * C);
-    r.widen(f);
+    return r.widen();
 }
 
 // Parameters of V channels: w[i] is the tap on the input i positions back.
 template <int KM, int V>
-__device__ __forceinline__ void load_taps(float (&w)[KM][V], float (&bias)[V], const CausalConv& p, int K, int c, bool here) {
+__device__ __forceinline__ void load_taps(Lanes<V> (&w)[KM], Lanes<V>& bias, const CausalConv& p, int K, int c) {
 #pragma unroll
     for (int i = 0; i < KM; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) w[i][j] = here && i < K ? load_param(p.w, p.param_type, (K - 1 - i) * p.C + c + j, 0.f) : 0.f;
+        for (int j = 0; j < V; ++j) w[i].set(j, i < K ? load_param(p.w, p.param_type, (K - 1 - i) * p.C + c + j, 0.f) : 0.f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) bias[j] = here ? load_param(p.bias, p.param_type, c + j, 0.f) : 0.f;
+    for (int j = 0; j < V; ++j) bias.set(j, load_param(p.bias, p.param_type, c + j, 0.f));
 }
 
 template <int KM, int V>
-__device__ __forceinline__ void convolve(float (&f)[V], const float (&w)[KM][V], const float (&bias)[V], const float (&win)[KM][V], int K) {
+__device__ __forceinline__ Lanes<V> convolve(const Lanes<V> (&w)[KM], const Lanes<V>& bias, const Lanes<V> (&win)[KM], int K) {
+    Lanes<V> f = bias;
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = bias[j];
-#pragma unroll
-    for (int i = KM - 1; i >= 0; --i) {
-        if (i >= K) continue;
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = fmaf(w[i][j], win[i][j], f[j]);
-    }
+    for (int i = KM - 1; i >= 0; --i)
+        if (i < K) f.fma(w[i], win[i]);
+    return f;
 }
 
 template <int KM, int V>
-__device__ __forceinline__ void shift(float (&win)[KM][V]) {
+__device__ __forceinline__ void shift(Lanes<V> (&win)[KM]) {
 #pragma unroll
-    for (int i = KM - 1; i > 0; --i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) win[i][j] = win[i - 1][j];
+    for (int i = KM - 1; i > 0; --i) win[i] = win[i - 1];
 }
 
 // Rows that a thread brings in together, one such batch ahead of the one it works on.
@@ -97,63 +137,46 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p,
     if (!r.some || c >= C) return;
     const T* x = view_at<T>(p.x, p.seqs, r) + c;
     const T* state = p.state == nullptr ? nullptr : static_cast<const T*>(p.state) + static_cast<long long>(r.s) * (K - 1) * C + c;
-    T* y = static_cast<T*>(p.y) + dense_row(p.seqs, r) * C + c;
     const long long first = r.first + static_cast<long long>(group) * run;
-    const long long end = first + run < r.end ? first + run : r.end;
-    if (first < end) {
+    const int n = static_cast<int>((first + run < r.end ? first + run : r.end) - first);      // positions of this thread
+    if (n > 0) {
+        const T* from = x + first * p.x.row;
+        T* to = static_cast<T*>(p.y) + (dense_row(p.seqs, r) + first) * C + c;
         Raw<T, V> next[kBatch];
-        const auto fetch = [&](long long t) {
+        const auto fetch = [&](int t) {       // (positions t .. t + kBatch - 1, in turn)
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-                if (t + q < end) next[q].load(x + (t + q) * p.x.row);
+            for (int q = 0; q < kBatch; ++q) {
+                if (t + q < n) next[q].load(from);
+                from += p.x.row;
+            }
         };
-        fetch(first);
-        float w[KM][V], bias[V], win[KM][V];       // win[i]: the input i positions back
-        load_taps(w, bias, p, K, c, true);
+        fetch(0);
+        Lanes<V> w[KM], bias, win[KM];        // win[i]: the input i positions back
+        load_taps(w, bias, p, K, c);
 #pragma unroll
         for (int i = 1; i < KM; ++i)
-            if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
-        for (long long t0 = first; t0 < end; t0 += kBatch) {
+            if (i < K) win[i] = input<T, V>(x, p.x.row, state, C, K, first - i);
+        for (int t0 = 0; t0 < n; t0 += kBatch) {
             Raw<T, V> raw[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) raw[q] = next[q];
             fetch(t0 + kBatch);
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                if (t0 + q >= end) break;
-                raw[q].widen(win[0]);
-                float f[V];
-                convolve(f, w, bias, win, K);
-                if (p.silu) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) f[j] = silu(f[j]);
-                }
-                Raw<T, V>::store(y + (t0 + q) * C, f);
+                win[0] = raw[q].widen();
+                Lanes<V> f = convolve(w, bias, win, K);
+                if (p.silu) f.to_silu();
+                if (t0 + q < n) Raw<T, V>::store(to, f);
+                to += C;
                 shift(win);
             }
         }
     }
     if (r.last && p.final_state != nullptr) {
         T* out = static_cast<T*>(p.final_state) + static_cast<long long>(r.s) * (K - 1) * C + c;
-        for (int i = group; i < K - 1; i += kThreads / columns) {
-            float f[V];
-            input<T, V>(f, x, p.x.row, state, C, K, r.length - (K - 1) + i);
-            Raw<T, V>::store(out + static_cast<long long>(i) * C, f);
-        }
+        for (int i = group; i < K - 1; i += kThreads / columns)
+            Raw<T, V>::store(out + static_cast<long long>(i) * C, input<T, V>(x, p.x.row, state, C, K, r.length - (K - 1) + i));
     }
-}
-
-// The gradient that reaches position t of the sequence (or of its state, t < 0) as the last inputs kept.
-template <typename T, int V>
-__device__ __forceinline__ void add_dfinal(float (&f)[V], const T* dfinal, const Piece& r, int C, int K, long long t) {
-    const long long i = t - (r.length - (K - 1));
-    if (dfinal == nullptr || i < 0) return;
-    float g[V];
-    Raw<T, V> raw;
-    raw.load(dfinal + i * C);
-    raw.widen(g);
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] += g[j];
 }
 
 // A thread walks K - 1 positions past its run: position t gives dpre[t], and with it dx[t - K + 1] is
@@ -170,100 +193,90 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
     const int c = (block * columns + column) * V;
     const Piece r = find_piece(p.seqs, slot, p.span);
     const bool here = r.some && c < C;
-    float dw[KM][V], db[V];             // dw[i]: of the tap on the input i positions back
+    Lanes<V> dw[KM], db;             // dw[i]: of the tap on the input i positions back
+    db.clear();
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        db[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < KM; ++i) dw[i][j] = 0.f;
-    }
+    for (int i = 0; i < KM; ++i) dw[i].clear();
     const long long first = r.first + static_cast<long long>(group) * run;
-    const long long end = first + run < r.end ? first + run : r.end;
-    if (here && (first < end || first == 0)) {
+    const int n = first < r.end ? static_cast<int>((first + run < r.end ? first + run : r.end) - first) : 0;
+    if (here && (n > 0 || first == 0)) {
         const T* x = view_at<T>(p.x, p.seqs, r) + c;
-        const T* dy = view_at<T>(p.dy, p.seqs, r) + c;
-        const long long kept = static_cast<long long>(r.s) * (K - 1) * C + c;
+        const long long kept = static_cast<long long>(r.s) * (K - 1) * C + c, rest = r.length - first;
         const T* state = p.state == nullptr ? nullptr : static_cast<const T*>(p.state) + kept;
         const T* dfinal = p.dfinal == nullptr ? nullptr : static_cast<const T*>(p.dfinal) + kept;
-        T* dx = static_cast<T*>(p.dx) + dense_row(p.seqs, r) * C + c;
         T* dstate = p.dstate == nullptr ? nullptr : static_cast<T*>(p.dstate) + kept;
         // the first run's walk gives the state's positions as well
-        const long long low = first == 0 ? -(K - 1) : first, stop = end + K - 1, known = stop < r.length ? stop : r.length;
+        const int low = first == 0 ? -(K - 1) : 0, stop = n + K - 1, known = stop < rest ? stop : static_cast<int>(rest);
+        // (positions that the last inputs kept have a gradient through them: from this one on)
+        const int kept_from = dfinal != nullptr && rest - (K - 1) < stop ? static_cast<int>(rest) - (K - 1) : stop;
+        const T* from_x = x + first * p.x.row;
+        const T* from_dy = view_at<T>(p.dy, p.seqs, r) + c + first * p.dy.row;
+        T* to = static_cast<T*>(p.dx) + (dense_row(p.seqs, r) + first - (K - 1)) * C + c;
         Raw<T, V> next_x[kBatch], next_dy[kBatch];
-        const auto fetch = [&](long long t) {
+        const auto fetch = [&](int t) {       // (positions t .. t + kBatch - 1, in turn)
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                if (t + q >= known) continue;
-                next_x[q].load(x + (t + q) * p.x.row);
-                next_dy[q].load(dy + (t + q) * p.dy.row);
+                if (t + q < known) {
+                    next_x[q].load(from_x);
+                    next_dy[q].load(from_dy);
+                }
+                from_x += p.x.row;
+                from_dy += p.dy.row;
             }
         };
-        fetch(first);
-        float w[KM][V], bias[V], win[KM][V], dpre[KM][V];
-        load_taps(w, bias, p, K, c, true);
+        fetch(0);
+        Lanes<V> w[KM], bias, win[KM], dpre[KM];
+        load_taps(w, bias, p, K, c);
 #pragma unroll
-        for (int i = 0; i < KM; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) dpre[i][j] = 0.f;
+        for (int i = 0; i < KM; ++i) dpre[i].clear();
 #pragma unroll
         for (int i = 1; i < KM; ++i)
-            if (i < K) input<T, V>(win[i], x, p.x.row, state, C, K, first - i);
-        for (long long t0 = first; t0 < stop; t0 += kBatch) {
+            if (i < K) win[i] = input<T, V>(x, p.x.row, state, C, K, first - i);
+        for (int t0 = 0; t0 < stop; t0 += kBatch) {
             Raw<T, V> raw_x[kBatch], raw_dy[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) raw_x[q] = next_x[q], raw_dy[q] = next_dy[q];
             fetch(t0 + kBatch);
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                const long long t = t0 + q;
-                if (t >= stop) break;
+                const int t = t0 + q, at = t - (K - 1);
+                dpre[0].clear();
                 if (t < known) {
-                    float f[V], g[V];
-                    raw_x[q].widen(win[0]);
-                    raw_dy[q].widen(g);
-                    if (p.silu) {
-                        convolve(f, w, bias, win, K);
-#pragma unroll
-                        for (int j = 0; j < V; ++j) g[j] *= silu_slope(f[j], sigmoid(f[j]));
-                    }
-#pragma unroll
-                    for (int j = 0; j < V; ++j) dpre[0][j] = g[j];
-                    if (t < end) {
-#pragma unroll
-                        for (int i = 0; i < KM; ++i) {
-                            if (i >= K) continue;
-#pragma unroll
-                            for (int j = 0; j < V; ++j) dw[i][j] = fmaf(g[j], win[i][j], dw[i][j]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < V; ++j) db[j] += g[j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) dpre[0][j] = 0.f;
+                    win[0] = raw_x[q].widen();
+                    dpre[0] = raw_dy[q].widen();
+                    if (p.silu) dpre[0].by_slope(convolve(w, bias, win, K));
                 }
-                const long long to = t - (K - 1);
-                if (to >= low) {
-                    // dx[to] = sum_k w_k dpre[to + K - 1 - k]: the tap i back goes with dpre of i positions on
-                    float f[V];
+                if (t < n) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) f[j] = 0.f;
+                    for (int i = 0; i < KM; ++i)
+                        if (i < K) dw[i].fma(dpre[0], win[i]);
+                    db.add(dpre[0]);
+                }
+                if (at >= low && t < stop) {
+                    // dx[at] = sum_k w_k dpre[at + K - 1 - k]: the tap i back goes with dpre of i positions on
+                    Lanes<V> f;
+                    f.clear();
 #pragma unroll
                     for (int i = 0; i < KM; ++i) {
                         if (i >= K) continue;
-                        const int back = KM >= 8 ? 0 : KM - 1 - i;
-                        if (KM < 8) {
-#pragma unroll
-                            for (int j = 0; j < V; ++j) f[j] = fmaf(w[back][j], dpre[i][j], f[j]);
+                        if constexpr (KM < 8) {
+                            f.fma(w[KM - 1 - i], dpre[i]);
                         } else {
+                            Lanes<V> tap;
 #pragma unroll
-                            for (int j = 0; j < V; ++j) f[j] = fmaf(load_param(p.w, p.param_type, i * C + c + j, 0.f), dpre[i][j], f[j]);
+                            for (int j = 0; j < V; ++j) tap.set(j, load_param(p.w, p.param_type, i * C + c + j, 0.f));
+                            f.fma(tap, dpre[i]);
                         }
                     }
-                    add_dfinal<T, V>(f, dfinal, r, C, K, to);
-                    if (to >= 0) Raw<T, V>::store(dx + to * C, f);
-                    else if (dstate != nullptr) Raw<T, V>::store(dstate + (to + K - 1) * C, f);
+                    if (at >= kept_from) {
+                        Raw<T, V> g;
+                        g.load(dfinal + (first + at - (r.length - (K - 1))) * C);
+                        f.add(g.widen());
+                    }
+                    if (at >= 0) Raw<T, V>::store(to, f);
+                    else if (dstate != nullptr) Raw<T, V>::store(dstate + (at + K - 1) * C, f);
                 }
+                to += C;
                 shift(win);
                 shift(dpre);
             }
@@ -274,8 +287,9 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
 #pragma unroll
     for (int i = 0; i <= KM; ++i) {
         if (i > K) break;
+        const Lanes<V>& mine = i < KM && i < K ? dw[i < KM ? i : 0] : db;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sums[j * kThreads + threadIdx.x] = i < KM && i < K ? dw[i < KM ? i : 0][j] : db[j];
+        for (int j = 0; j < V; ++j) sums[j * kThreads + threadIdx.x] = mine.get(j);
         __syncthreads();
         if (group == 0 && c < C) {
 #pragma unroll

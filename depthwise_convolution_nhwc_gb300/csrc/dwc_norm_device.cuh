@@ -68,19 +68,36 @@ __device__ __forceinline__ float load_param(const void* p, int type, int c, floa
     return __half2float(static_cast<const __half*>(p)[c]);
 }
 
-// 2^v, and through it 1 / (1 + exp(-v)) and v / (1 + exp(-v)).  The argument's scaling by log2(e) costs a relative error of
-// 2^-23 |v| of the exponential, which counts only where the exponential does; the full-range expf in its place made
-// gates as dear as everything else of a memory-bound kernel.
+// 2^v and 1 / v by the approximations of one instruction (2 ulp, 1 ulp), and through them 1 / (1 + exp(-v)) and v / (1 +
+// exp(-v)).  The argument's scaling by log2(e) costs a relative error of 2^-23 |v| of the exponential, which counts
+// only where the exponential does; the full-range expf and division in their place made gates as dear as
+// everything else of a memory-bound kernel.
 __device__ __forceinline__ float exp2_fast(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + exp2_fast(v * -kLog2e)); }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + exp2_fast(v * -kLog2e)); }
+__device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.f + exp2_fast(v * -kLog2e)); }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // d silu / d v, from sigmoid(v)
 __device__ __forceinline__ float silu_slope(float v, float s) { return fmaf(v * s, 1.f - s, s); }
+// two of each
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 t = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
+    const float2 w = __fadd2_rn(make_float2(exp2_fast(t.x), exp2_fast(t.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp_fast(w.x), rcp_fast(w.y));
+}
+__device__ __forceinline__ float2 silu2(float2 v) { return __fmul2_rn(v, sigmoid2(v)); }
+__device__ __forceinline__ float2 silu_slope2(float2 v) {
+    const float2 s = sigmoid2(v), vs = __fmul2_rn(v, s);
+    return __fadd2_rn(s, __ffma2_rn(vs, make_float2(-s.x, -s.y), vs));
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

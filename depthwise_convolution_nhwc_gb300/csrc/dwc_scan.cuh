@@ -3,10 +3,14 @@
 //     h[t, n] = exp(delta[t] A[n]) h[t-1, n] + delta[t] u[t] B[t, n]
 //     y[t]    = (sum_n C[t, n] h[t, n] + D u[t]) silu(z[t])
 //
-// L lanes serve a channel, NS states each, and walk along the positions with the states in registers.
-// Tiles of 32 positions are brought in by the whole CTA: per channel and position delta and
-// delta * u, once, as fp32 in shared memory, and B and C widened.  The sums over the states are
-// parted among the lanes: L positions together, each lane ends with one of them.
+// L lanes serve a pair of channels, four states of each to a lane, and walk along the positions with
+// the states in registers.  Tiles of 16 positions are brought in by the whole CTA: per channel and position delta
+// and u, once, as fp32 in shared memory, and B and C widened.
+//
+// What bounds it: per state and position 4 packed operations (2 cycles a warp for a pair of states), an exponential (4
+// cycles a warp) and what shared memory hands to the lanes, 128 bytes a cycle for the whole SM, broadcast or not: a lane
+// that had one channel took 8 bytes of B and C a state, twice the time of the arithmetic (16-byte loads count four
+// times).  Hence two channels to a lane.
 #pragma once
 
 #include <algorithm>
@@ -16,40 +20,48 @@
 namespace dwc {
 namespace scan {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 32;
+constexpr int kTile = kScanTile, kStep = 4;       // positions of a tile, and that go through together
 
-// log(1 + e) for e in [0, 1] as 2 atanh(s), s = e / (2 + e) <= 1/3: the odd series up to s^15, whose
-// rest is below 2 s^17 / 17 < 1e-9 of it; relative errors stay near 2^-23 however small e is.
-__device__ __forceinline__ float log1p_unit(float e) {
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    const float t = s + s;
-    return fmaf(t * q, p, t);
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|): the logarithm as 2 atanh(s), s = e / (2 + e) <= 1/3, whose odd
+// series is s + s^3 P(s^2) with P of degree 3 by Chebyshev interpolation on [0, 1/9] (relative error 1.6e-8): relative
+// errors stay near 2^-22 however small e is.  (A NaN stays one: fmaxf would drop it.)
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    const float2 e = make_float2(exp2_fast(fabsf(v.x) * -kLog2e), exp2_fast(fabsf(v.y) * -kLog2e));
+    const float2 w = __fadd2_rn(e, both(2.f));
+    const float2 s = __fmul2_rn(e, make_float2(rcp_fast(w.x), rcp_fast(w.y))), q = __fmul2_rn(s, s);
+    float2 p = __ffma2_rn(both(0.13433775305747986f), q, both(0.14116978645324707f));
+    p = __ffma2_rn(p, q, both(0.2000383585691452f));
+    p = __ffma2_rn(p, q, both(0.33333319425582886f));
+    const float2 t = __fadd2_rn(s, s);
+    return __fadd2_rn(make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y), __ffma2_rn(__fmul2_rn(t, q), p, t));
 }
-// (a NaN stays one: fmaxf would drop it)
-__device__ __forceinline__ float softplus(float v) { return (v < 0.f ? 0.f : v) + log1p_unit(exp2_fast(fabsf(v) * -kLog2e)); }
+__device__ __forceinline__ float softplus(float v) { return softplus2(both(v)).x; }
 
-// The sum over the L lanes of a channel of v[sub], for lane `sub`: halves are exchanged, then quarters.
+__device__ __forceinline__ float from_lane(float v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
+
+// Sums over the lanes 2, 4, ... L / 2 apart of a channel pair's L, of kStep values each: the lanes part the values among
+// themselves, lane `sub` ends with the first kMine of them (values first_of(sub) ...).
 template <int L>
-__device__ __forceinline__ float parted(float (&v)[L], int sub) {
-#pragma unroll
-    for (int m = L / 2; m > 0; m >>= 1) {
-        const bool upper = (sub & m) != 0;
-#pragma unroll
-        for (int i = 0; i < m; ++i) {
-            const float keep = upper ? v[m + i] : v[i], send = upper ? v[i] : v[m + i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-        }
+struct Parts {
+    static constexpr int kMine = L >= 8 ? 1 : L == 4 ? 2 : 4;
+    static __device__ __forceinline__ int first_of(int sub) {
+        return (L >= 4 && (sub & 2) ? 2 : 0) + (L >= 8 && (sub & 4) ? 1 : 0);
     }
-    return v[0];
-}
+    static __device__ __forceinline__ bool owner(int sub) { return L <= 8 || sub < 8; }      // (others hold copies)
+    static __device__ __forceinline__ void sum(float (&v)[kStep], int sub) {
+        if constexpr (L >= 4) {
+            const bool upper = (sub & 2) != 0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) v[q] = (upper ? v[q + 2] : v[q]) + from_lane(upper ? v[q] : v[q + 2], 2);
+        }
+        if constexpr (L >= 8) {
+            const bool upper = (sub & 4) != 0;
+            v[0] = (upper ? v[1] : v[0]) + from_lane(upper ? v[0] : v[1], 4);
+        }
+#pragma unroll
+        for (int m = 8; m < L; m *= 2) v[0] += from_lane(v[0], m);
+    }
+};
 
 // Index among `saved` of the state in front of tile `tile` of a sequence.
 __device__ __forceinline__ long long saved_slot(const Seqs& q, const Piece& r, long long tile) {
@@ -85,28 +97,16 @@ __device__ __forceinline__ void get_states(float (&h)[N], const float* from, int
 }
 
 // B or C of a tile: vectors of 8 states, padded with zeros.
-template <typename T, int NP, int kRows = kTile>
+template <typename T, int NP, int kThreads>
 struct StateRows {
-    static constexpr int kVecs = (NP + 7) / 8, kEach = (kRows * kVecs + kThreads - 1) / kThreads;
+    static constexpr int kRows = kTile, kVecs = NP / 8, kEach = (kRows * kVecs + kThreads - 1) / kThreads;
     Vec8<T> raw[kEach];
     __device__ __forceinline__ void fetch(const T* base, const RowsView& v, long long t0, long long end, int N) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int i = threadIdx.x + k * kThreads, t = i / kVecs, col = i % kVecs * 8;
-            if (i < kRows * kVecs && t0 + t < end) load8(raw[k], base + (t0 + t) * v.row, col, N, v.vec && N % 8 == 0);
+            if (i < kRows * kVecs && t0 + t < end) load8(raw[k], base + (t0 + t) * v.row + col, N - col, v.vec && N % 8 == 0 && col < N);
             else raw[k].zero();
-        }
-    }
-    __device__ __forceinline__ void spread(float (*to)[NP]) const {
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int i = threadIdx.x + k * kThreads;
-            if (i >= kRows * kVecs) continue;
-            float2 f[4];
-            raw[k].widen(f);
-            float4* o = reinterpret_cast<float4*>(&to[i / kVecs][i % kVecs * 8]);
-            o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-            o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
         }
     }
     // each four states in 1, 2 or 4 orders: n, n ^ 2 (two orders); n, n ^ 1, n ^ 2, n ^ 3 (four)
@@ -132,44 +132,84 @@ struct StateRows {
     }
 };
 
-template <int N>
-__device__ __forceinline__ void row_values(float (&v)[N], const float* from) {
-    static_assert(N % 2 == 0, "pairs");
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(from + i);
-            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+// Values of four states in a lane's order (n ^ perm).
+struct Four {
+    float2 v[2];
+    // (`four`: the number of states is a multiple of 4 and the array aligned to 16 bytes)
+    __device__ __forceinline__ void get4(const float* from, int n0, int perm, int states, bool four) {
+        if (!four) {
+            get(from, n0, perm, states);
+            return;
         }
-    } else {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from != nullptr && n0 < states) f = *reinterpret_cast<const float4*>(from + n0);
+        if (perm & 2) f = make_float4(f.z, f.w, f.x, f.y);
+        if (perm & 1) f = make_float4(f.y, f.x, f.w, f.z);
+        v[0] = make_float2(f.x, f.y), v[1] = make_float2(f.z, f.w);
+    }
+    // (in the states' own order)
+    __device__ __forceinline__ void put4(float* to, int n0, int states, bool four) const {
+        if (!four) put(to, n0, 0, states);
+        else if (n0 < states) *reinterpret_cast<float4*>(to + n0) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+    __device__ __forceinline__ void get(const float* from, int n0, int perm, int states) {
+        float f[4];
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(from + i);
-            v[i] = f.x, v[i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + (i ^ perm);
+            f[i] = from != nullptr && n < states ? from[n] : 0.f;
+        }
+        v[0] = make_float2(f[0], f[1]), v[1] = make_float2(f[2], f[3]);
+    }
+    __device__ __forceinline__ void put(float* to, int n0, int perm, int states) const {
+        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + (i ^ perm);
+            if (n < states) to[n] = f[i];
         }
     }
+    __device__ __forceinline__ void load(const float* from) {
+        const float4 f = *reinterpret_cast<const float4*>(from);
+        v[0] = make_float2(f.x, f.y), v[1] = make_float2(f.z, f.w);
+    }
+    __device__ __forceinline__ void scale(float s) { v[0] = __fmul2_rn(v[0], both(s)), v[1] = __fmul2_rn(v[1], both(s)); }
+    __device__ __forceinline__ void clear() { v[0] = v[1] = both(0.f); }
+};
+
+// exp(delta A) of two states, from A log2(e)
+__device__ __forceinline__ float2 decay_of(float delta, float2 a2) {
+    const float2 e = __fmul2_rn(both(delta), a2);
+    return make_float2(exp2_fast(e.x), exp2_fast(e.y));
 }
 
-template <int N>
-__device__ __forceinline__ void row_pairs(float2 (&v)[N], const float* from) {
-    float f[2 * N];
-    row_values(f, from);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+// delta of two channels
+__device__ __forceinline__ float2 delta_of(float2 raw, float2 bias, bool plus, bool in) {
+    const float2 v = __fadd2_rn(raw, bias);
+    const float2 d = plus ? softplus2(v) : v;
+    return in ? d : both(0.f);      // positions past the end leave the states alone
 }
 
 // -------------------------------------------------------------------------------- forward
+
+template <int L>
+struct FwdShape {
+    // (small CTAs spread evenly: 8 sequences of 4096 channels are 1024 CTAs of 64 threads, about 7 to an SM)
+    static constexpr int kThreads = L == 32 ? 128 : 64, kResident = 640 / kThreads;       // CTAs to an SM: 96 registers a thread
+    static constexpr int kChannels = 2 * kThreads / L, NP = 4 * L;
+};
 
 // Sequences that are too few to fill the GPU are cut into chunks of p.span positions.  kStates: the first of
 // three kernels, which walks every chunk but a sequence's last from a state of zero and keeps the
 // state at its end (`ends`, [slot][C][N]) and the sum of delta (`sums`, [slot][C]); the chunks are then joined,
 // h = exp(A sum delta) h + end, and the second walk begins each chunk with the state in front of it.
-template <typename T, int NS, int L, bool kStates>
-__global__ void __launch_bounds__(kThreads, L == 16 ? 3 : 6) scan_fwd_kernel(Scan p, int blocks, float* ends, float* sums) {
-    constexpr int kChannels = kThreads / L, kColumns = kChannels / 8, NP = NS * L;
+template <typename T, int L, bool kStates>
+__global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident) scan_fwd_kernel(Scan p, int blocks, float* ends, float* sums) {
+    using S = FwdShape<L>;
+    constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = kChannels / 8, NP = S::NP, W = 32 / L;
     constexpr int kEach = (kTile * kColumns + kThreads - 1) / kThreads;      // vectors of a tile to a thread
-    __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, delta * u
-    __shared__ __align__(16) float bs[kTile][NP], cs[kStates ? 1 : kTile][NP], ys[kStates ? 1 : kTile][kChannels];
+    __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, u
+    __shared__ __align__(16) float bs[1][kTile][NP], cs[1][kStates ? 1 : kTile][NP], ys[kStates ? 1 : kTile][kChannels];
     __shared__ __align__(16) float bias[kChannels], skip[kChannels];
     pdl_trigger();
     pdl_wait();
@@ -182,35 +222,43 @@ __global__ void __launch_bounds__(kThreads, L == 16 ? 3 : 6) scan_fwd_kernel(Sca
     const T* z = kStates || p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
     const T *b = view_at<T>(p.b, p.seqs, r) + k.g * N, *c = view_at<T>(p.c, p.seqs, r) + k.g * N;
     T* y = static_cast<T*>(p.y) + dense_row(p.seqs, r) * C + k.c;
-    const bool even = (C / p.G) % 8 == 0, vec_y = even && reinterpret_cast<uintptr_t>(p.y) % (8 * sizeof(T)) == 0;
+    const bool even = (C / p.G) % 8 == 0, four = N % 4 == 0 && reinterpret_cast<uintptr_t>(p.saved) % 16 == 0;
     for (int i = threadIdx.x; i < kChannels; i += kThreads) {
         bias[i] = i < k.width && p.dt_bias != nullptr ? p.dt_bias[k.c + i] : 0.f;
         skip[i] = i < k.width && p.D != nullptr ? p.D[k.c + i] : 0.f;
     }
-    // as a server of a channel's states
-    const int ch = threadIdx.x / L, sub = threadIdx.x % L, n0 = sub * NS;
-    const bool serves = ch < k.width;
-    const long long mine = (static_cast<long long>(r.s) * C + k.c + ch) * N, here = (slot * C + k.c + ch) * N;
-    float a2[NS], h[NS], total = 0.f;
-    get_states(a2, serves ? p.A + static_cast<long long>(k.c + ch) * N : nullptr, n0, N);
+    // this lane's channels within the block (odd lanes hold them the other way round) and states
+    const int lane = threadIdx.x & 31, sub = lane % L, n0 = sub * 4;
+    const int pair = (static_cast<int>(threadIdx.x >> 5) * W + lane / L) * 2;
+    const int ch[2] = {pair + (sub & 1), pair + 1 - (sub & 1)};
+    const long long wide = static_cast<long long>(C) * N;
+    Four a2[2], h[2];
+    float total[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NS; ++i) a2[i] *= kLog2e;
-    if (kStates) get_states(h, nullptr, n0, N);
-    else if (ends != nullptr) get_states(h, serves ? ends + here : nullptr, n0, N);
-    else get_states(h, serves && p.state != nullptr ? p.state + mine : nullptr, n0, N);
+    for (int j = 0; j < 2; ++j) {
+        const bool serves = ch[j] < k.width;
+        const long long at = static_cast<long long>(k.c + ch[j]) * N;
+        a2[j].get(serves ? p.A + at : nullptr, n0, 0, N);
+        a2[j].scale(kLog2e);
+        if (kStates) h[j].clear();
+        else if (ends != nullptr) h[j].get(serves ? ends + slot * wide + at : nullptr, n0, 0, N);
+        else h[j].get(serves && p.state != nullptr ? p.state + r.s * wide + at : nullptr, n0, 0, N);
+    }
 
     Vec8<T> ru[kEach], rz[kEach], rdt[kEach];
-    StateRows<T, NP> rb, rc;
+    StateRows<T, NP, kThreads> rb, rc;
     const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
-    const auto col_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) % kColumns * 8; };
+    const int col = threadIdx.x % kColumns * 8, left = k.width - col;            // (kColumns divides the threads)
+    const bool vec_u = p.u.vec && even && left >= 8, vec_dt = p.dt.vec && even && left >= 8, vec_z = p.z.vec && even && left >= 8;
+    const bool vec_y = even && left >= 8 && reinterpret_cast<uintptr_t>(p.y) % (8 * sizeof(T)) == 0;
     auto fetch = [&](long long t0) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int row = row_of(i), col = col_of(i);
+            const int row = row_of(i);
             ru[i].zero(), rdt[i].zero();
             if (row >= kTile || t0 + row >= r.end) continue;
-            load8(ru[i], u + (t0 + row) * p.u.row, col, k.width, p.u.vec && even);
-            load8(rdt[i], dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
+            load8(ru[i], u + (t0 + row) * p.u.row + col, left, vec_u);
+            load8(rdt[i], dt + (t0 + row) * p.dt.row + col, left, vec_dt);
         }
         rb.fetch(b, p.b, t0, r.end, N);
         if (!kStates) rc.fetch(c, p.c, t0, r.end, N);
@@ -218,66 +266,86 @@ __global__ void __launch_bounds__(kThreads, L == 16 ? 3 : 6) scan_fwd_kernel(Sca
     fetch(r.first);
     __syncthreads();
     for (long long t0 = r.first; t0 < r.end; t0 += kTile) {
+        Vec8<T> keep[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int row = row_of(i), col = col_of(i);
+            const int row = row_of(i);
+            keep[i] = ru[i];
             if (row >= kTile) continue;
             float2 fu[4], fd[4];
             ru[i].widen(fu);
             rdt[i].widen(fd);
-            const bool in = t0 + row < r.end;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
-                float d0 = fd[j].x + o.x, d1 = fd[j].y + o.y;
-                if (p.softplus) d0 = softplus(d0), d1 = softplus(d1);
-                if (!in) d0 = d1 = 0.f;        // positions past the end leave the states alone
-                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d0, d0 * fu[j].x, d1, d1 * fu[j].y);
+                const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < r.end);
+                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
             }
         }
-        rb.spread(bs);
-        if (!kStates) rc.spread(cs);
+        rb.template spread<1>(bs);
+        if constexpr (!kStates) rc.template spread<1>(cs);
         __syncthreads();
-        Vec8<T> keep[kEach];
-        if (!kStates) {
+        if constexpr (!kStates) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                keep[i] = ru[i];
                 rz[i].zero();
                 if (z != nullptr && row_of(i) < kTile && t0 + row_of(i) < r.end)
-                    load8(rz[i], z + (t0 + row_of(i)) * p.z.row, col_of(i), k.width, p.z.vec && even);
+                    load8(rz[i], z + (t0 + row_of(i)) * p.z.row + col, left, vec_z);
+            }
+            if (p.saved != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (ch[j] < k.width)
+                        h[j].put4(p.saved + saved_slot(p.seqs, r, t0 / kScanTile) * wide + static_cast<long long>(k.c + ch[j]) * N, n0, N, four);
             }
         }
         if (t0 + kTile < r.end) fetch(t0 + kTile);
 #pragma unroll 1
-        for (int t = 0; t < kTile; t += L) {
-            if (!kStates && p.saved != nullptr && t % kScanTile == 0 && serves && (t == 0 || t0 + t < r.end))
-                put_states(p.saved + (saved_slot(p.seqs, r, (t0 + t) / kScanTile) * C + k.c + ch) * N, h, n0, N);
-            float part[L];
+        for (int t = 0; t < kTile; t += kStep) {
+            // (decays and inputs of all four positions first: they wait for nothing, the states only for them)
+            float part[kStep], in[kStep][2];
+            float2 a[kStep][2][2];
 #pragma unroll
-            for (int q = 0; q < L; ++q) {
-                const float2 s = step[t + q][ch];
-                float2 fb[NS / 2], fc[NS / 2], sum = both(0.f);
-                row_pairs(fb, &bs[t + q][n0]);
-                if (!kStates) row_pairs(fc, &cs[t + q][n0]);
+            for (int q = 0; q < kStep; ++q)
 #pragma unroll
-                for (int i = 0; i < NS / 2; ++i) {
-                    float2 a = __fmul2_rn(both(s.x), make_float2(a2[2 * i], a2[2 * i + 1])), hh = make_float2(h[2 * i], h[2 * i + 1]);
-                    a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
-                    hh = __ffma2_rn(both(s.y), fb[i], __fmul2_rn(a, hh));
-                    h[2 * i] = hh.x, h[2 * i + 1] = hh.y;
-                    if (!kStates) sum = __ffma2_rn(fc[i], hh, sum);
+                for (int j = 0; j < 2; ++j) {
+                    const float2 s = step[t + q][ch[j]];
+                    in[q][j] = s.x * s.y;
+                    if (kStates) total[j] += s.x;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) a[q][j][i] = decay_of(s.x, a2[j].v[i]);
                 }
-                if (kStates) total += s.x;
-                part[q] = sum.x + sum.y;
+#pragma unroll
+            for (int q = 0; q < kStep; ++q) {
+                Four fb, fc;
+                fb.load(&bs[0][t + q][n0]);
+                if constexpr (!kStates) fc.load(&cs[0][t + q][n0]);
+                float sum[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float2 x = both(0.f);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        h[j].v[i] = __ffma2_rn(both(in[q][j]), fb.v[i], __fmul2_rn(a[q][j][i], h[j].v[i]));
+                        if constexpr (!kStates) x = __ffma2_rn(fc.v[i], h[j].v[i], x);
+                    }
+                    sum[j] = x.x + x.y;
+                }
+                // (the partner's other channel is this lane's first)
+                if constexpr (!kStates) part[q] = sum[0] + from_lane(sum[1], 1);
             }
-            if (!kStates) ys[t + sub][ch] = parted<L>(part, sub);
+            if constexpr (!kStates) {
+                Parts<L>::sum(part, sub);
+                if (Parts<L>::owner(sub)) {
+#pragma unroll
+                    for (int q = 0; q < Parts<L>::kMine; ++q) ys[t + Parts<L>::first_of(sub) + q][ch[0]] = part[q];
+                }
+            }
         }
         __syncthreads();
         if constexpr (!kStates) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const int row = row_of(i), col = col_of(i);
+                const int row = row_of(i);
                 if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
                 float2 fu[4], fz[4], f[4];
                 keep[i].widen(fu);
@@ -286,18 +354,22 @@ __global__ void __launch_bounds__(kThreads, L == 16 ? 3 : 6) scan_fwd_kernel(Sca
                 for (int j = 0; j < 4; ++j) {
                     const float2 o = *reinterpret_cast<const float2*>(&skip[col + 2 * j]);
                     f[j] = __ffma2_rn(o, fu[j], *reinterpret_cast<const float2*>(&ys[row][col + 2 * j]));
-                    if (z != nullptr) f[j] = __fmul2_rn(f[j], make_float2(silu(fz[j].x), silu(fz[j].y)));
+                    if (z != nullptr) f[j] = __fmul2_rn(f[j], silu2(fz[j]));
                 }
-                store8(y + (t0 + row) * C, f, col, k.width, vec_y);
+                store8(y + (t0 + row) * C + col, f, left, vec_y);
             }
         }
     }
-    if (!serves) return;
-    if (kStates) {
-        put_states(ends + here, h, n0, N);
-        if (sub == 0) sums[slot * C + k.c + ch] = total;
-    } else if (r.last && p.final_state != nullptr) {
-        put_states(p.final_state + mine, h, n0, N);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (ch[j] >= k.width) continue;
+        const long long at = static_cast<long long>(k.c + ch[j]) * N;
+        if (kStates) {
+            h[j].put(ends + slot * wide + at, n0, 0, N);
+            if (sub == 0) sums[slot * C + k.c + ch[j]] = total[j];
+        } else if (r.last && p.final_state != nullptr) {
+            h[j].put(p.final_state + r.s * wide + at, n0, 0, N);
+        }
     }
 }
 
@@ -349,12 +421,13 @@ __global__ void __launch_bounds__(256) scan_join_kernel(Scan p, float* ends, con
 // The first of the backward pass's kernels where sequences are cut into chunks: what reaches the
 // position in front of a chunk from within it, dh = g C + carry, carry = exp(delta A) dh (`ends`), and the sum
 // of delta.  Every chunk but a sequence's first is walked, from its end.
-template <typename T, int NS, int L>
-__global__ void __launch_bounds__(kThreads, 6) scan_adjoint_kernel(Scan p, int blocks, float* ends, float* sums) {
-    constexpr int kChannels = kThreads / L, kColumns = kChannels / 8, NP = NS * L;
+template <typename T, int L>
+__global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident) scan_adjoint_kernel(Scan p, int blocks, float* ends, float* sums) {
+    using S = FwdShape<L>;
+    constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = kChannels / 8, NP = S::NP, W = 32 / L;
     constexpr int kEach = (kTile * kColumns + kThreads - 1) / kThreads;
     __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, g
-    __shared__ __align__(16) float cs[kTile][NP];
+    __shared__ __align__(16) float cs[1][kTile][NP];
     __shared__ __align__(16) float bias[kChannels];
     pdl_trigger();
     pdl_wait();
@@ -369,28 +442,30 @@ __global__ void __launch_bounds__(kThreads, 6) scan_adjoint_kernel(Scan p, int b
     const bool even = (C / p.G) % 8 == 0;
     for (int i = threadIdx.x; i < kChannels; i += kThreads)
         bias[i] = i < k.width && p.dt_bias != nullptr ? p.dt_bias[k.c + i] : 0.f;
-    const int ch = threadIdx.x / L, sub = threadIdx.x % L, n0 = sub * NS;
-    const bool serves = ch < k.width;
-    float a2[NS], carry[NS], total = 0.f;
-    get_states(a2, serves ? p.A + static_cast<long long>(k.c + ch) * N : nullptr, n0, N);
+    const int lane = threadIdx.x & 31, sub = lane % L, n0 = sub * 4;
+    const int ch = (static_cast<int>(threadIdx.x >> 5) * W + lane / L) * 2;
+    Four a2[2], carry[2];
+    float total[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        a2[i] *= kLog2e;
-        carry[i] = 0.f;
+    for (int j = 0; j < 2; ++j) {
+        a2[j].get(ch + j < k.width ? p.A + static_cast<long long>(k.c + ch + j) * N : nullptr, n0, 0, N);
+        a2[j].scale(kLog2e);
+        carry[j].clear();
     }
     const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
-    const auto col_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) % kColumns * 8; };
+    const int col = threadIdx.x % kColumns * 8, left = k.width - col;
+    const bool vec_dt = p.dt.vec && even && left >= 8, vec_dy = p.dy.vec && even && left >= 8, vec_z = p.z.vec && even && left >= 8;
     Vec8<T> rdt[kEach], rdy[kEach], rz[kEach];
-    StateRows<T, NP> rc;
+    StateRows<T, NP, kThreads> rc;
     auto fetch = [&](long long t0) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int row = row_of(i), col = col_of(i);
+            const int row = row_of(i);
             rdt[i].zero(), rdy[i].zero(), rz[i].zero();
             if (row >= kTile || t0 + row >= r.end) continue;
-            load8(rdt[i], dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
-            load8(rdy[i], dy + (t0 + row) * p.dy.row, col, k.width, p.dy.vec && even);
-            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row, col, k.width, p.z.vec && even);
+            load8(rdt[i], dt + (t0 + row) * p.dt.row + col, left, vec_dt);
+            load8(rdy[i], dy + (t0 + row) * p.dy.row + col, left, vec_dy);
+            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row + col, left, vec_z);
         }
         rc.fetch(c, p.c, t0, r.end, N);
     };
@@ -401,45 +476,43 @@ __global__ void __launch_bounds__(kThreads, 6) scan_adjoint_kernel(Scan p, int b
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int row = row_of(i), col = col_of(i);
+            const int row = row_of(i);
             if (row >= kTile) continue;
             float2 fd[4], fy[4], fz[4];
             rdt[i].widen(fd);
             rdy[i].widen(fy);
             rz[i].widen(fz);
-            const bool in = t0 + row < r.end;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
-                float d0 = fd[j].x + o.x, d1 = fd[j].y + o.y;
-                if (p.softplus) d0 = softplus(d0), d1 = softplus(d1);
-                if (!in) d0 = d1 = 0.f;
-                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], make_float2(silu(fz[j].x), silu(fz[j].y)));
-                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d0, fy[j].x, d1, fy[j].y);
+                const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < r.end);
+                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], silu2(fz[j]));
+                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fy[j].x, d.y, fy[j].y);
             }
         }
-        rc.spread(cs);
+        rc.template spread<1>(cs);
         __syncthreads();
         if (tile > 0) fetch(t0 - kTile);
 #pragma unroll 4
         for (int t = kTile - 1; t >= 0; --t) {
-            const float2 s = step[t][ch];
-            float2 fc[NS / 2];
-            row_pairs(fc, &cs[t][n0]);
+            Four fc;
+            fc.load(&cs[0][t][n0]);
+            const float4 s = *reinterpret_cast<const float4*>(&step[t][ch]);
+            const float delta[2] = {s.x, s.z}, g[2] = {s.y, s.w};
 #pragma unroll
-            for (int i = 0; i < NS / 2; ++i) {
-                float2 a = __fmul2_rn(both(s.x), make_float2(a2[2 * i], a2[2 * i + 1]));
-                a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
-                const float2 dh = __ffma2_rn(both(s.y), fc[i], make_float2(carry[2 * i], carry[2 * i + 1]));
-                a = __fmul2_rn(a, dh);
-                carry[2 * i] = a.x, carry[2 * i + 1] = a.y;
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    carry[j].v[i] = __fmul2_rn(decay_of(delta[j], a2[j].v[i]), __ffma2_rn(both(g[j]), fc.v[i], carry[j].v[i]));
+                total[j] += delta[j];
             }
-            total += s.x;
         }
     }
-    if (!serves) return;
-    put_states(ends + (slot * C + k.c + ch) * N, carry, n0, N);
-    if (sub == 0) sums[slot * C + k.c + ch] = total;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (ch + j >= k.width) continue;
+        carry[j].put(ends + (slot * C + k.c + ch + j) * N, n0, 0, N);
+        if (sub == 0) sums[slot * C + k.c + ch + j] = total[j];
+    }
 }
 
 // Tiles of 16 positions from the last to the first.  From the state in front of a tile (kept by the
@@ -454,55 +527,34 @@ __global__ void __launch_bounds__(kThreads, 6) scan_adjoint_kernel(Scan p, int b
 // among themselves without selecting what to send.  For that a lane holds its four states in the
 // order n ^ perm, so that the upper pair is always what the partner keeps (B and C lie in shared
 // memory in each of the orders), and odd lanes hold their two channels the other way round.
-constexpr int kBwdTile = kScanTile, kBwdStep = 4;
-
-// Values of four states in a lane's order.
-struct Four {
-    float2 v[2];
-    __device__ __forceinline__ void get(const float* from, int n0, int perm, int states) {
-        float f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + (i ^ perm);
-            f[i] = from != nullptr && n < states ? from[n] : 0.f;
-        }
-        v[0] = make_float2(f[0], f[1]), v[1] = make_float2(f[2], f[3]);
-    }
-    __device__ __forceinline__ void put(float* to, int n0, int perm, int states) const {
-        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + (i ^ perm);
-            if (n < states) to[n] = f[i];
-        }
-    }
-};
-
 template <int L>
 struct BwdShape {
     static constexpr int kLanes = 32 / L;                  // lanes of a warp that share states
     static constexpr int kOrders = kLanes >= 4 ? 4 : kLanes;
-    static constexpr int kChannels = 2 * kThreads / L, NP = 4 * L, kWarps = kThreads / 32;
-    static constexpr size_t kFloats = kBwdTile * kChannels * 3 + 2 * kOrders * kBwdTile * NP +
-                                      kBwdTile / kBwdStep * 8 * kThreads + kWarps * kBwdTile * 2 * NP + 2 * kChannels;
+    static constexpr int kThreads = 128, kChannels = 2 * kThreads / L, NP = 4 * L, kWarps = kThreads / 32;
+    static constexpr int kColumns = kChannels / 8, kEach = (kTile * kColumns + kThreads - 1) / kThreads;
+    static constexpr size_t kFloats = kTile * kChannels * 3 + 2 * kOrders * kTile * NP +
+                                      kTile / kStep * 8 * kThreads + kWarps * kTile * 2 * NP + 2 * kChannels + 8 * kThreads;
+    // and a thread's vectors of u, dt, z and dy while it walks
+    static constexpr size_t bytes(size_t elem) { return kFloats * sizeof(float) + kEach * 4 * kThreads * 8 * elem; }
 };
 
-__device__ __forceinline__ float from_lane(float v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
-
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int blocks, const float* carries, float* part_bc, float* part_p) {
+__global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan p, int blocks, const float* carries, float* part_bc, float* part_p) {
     using S = BwdShape<L>;
-    constexpr int kChannels = S::kChannels, kColumns = kChannels / 8, NP = S::NP, W = S::kLanes, kOrders = S::kOrders;
-    constexpr int kEach = (kBwdTile * kColumns + kThreads - 1) / kThreads;
+    constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = S::kColumns, NP = S::NP, W = S::kLanes;
+    constexpr int kOrders = S::kOrders, kEach = S::kEach;
     extern __shared__ __align__(16) float smem[];
     float2 (*step)[kChannels] = reinterpret_cast<float2 (*)[kChannels]>(smem);      // delta, u; then du, ddelta
-    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(step + kBwdTile);       // g; then the sum over the states
-    float (*bs)[kBwdTile][NP] = reinterpret_cast<float (*)[kBwdTile][NP]>(gs + kBwdTile);
-    float (*cs)[kBwdTile][NP] = bs + kOrders;
+    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(step + kTile);       // g; then the sum over the states
+    float (*bs)[kTile][NP] = reinterpret_cast<float (*)[kTile][NP]>(gs + kTile);
+    float (*cs)[kTile][NP] = bs + kOrders;
     float* front = reinterpret_cast<float*>(cs + kOrders);
-    float* sums = front + kBwdTile / kBwdStep * 8 * kThreads;       // warps x positions x (dB, dC)
-    float* bias = sums + S::kWarps * kBwdTile * 2 * NP;
+    float* sums = front + kTile / kStep * 8 * kThreads;       // warps x positions x (dB, dC)
+    float* bias = sums + S::kWarps * kTile * 2 * NP;
     float* skip = bias + kChannels;
+    float4* sum_bias = reinterpret_cast<float4*>(skip + kChannels) + threadIdx.x;         // (two of them, kThreads apart)
+    Vec8<T>* stash = reinterpret_cast<Vec8<T>*>(skip + kChannels + 8 * kThreads) + threadIdx.x;      // u, dt, z, dy
     front += threadIdx.x;
     pdl_trigger();
     pdl_wait();
@@ -513,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
     const int C = p.C, N = p.N;
     const bool even = (C / p.G) % 8 == 0;
     const long long dense = r.some ? dense_row(p.seqs, r) : 0;
-    const auto aligned = [&](const void* t) { return even && reinterpret_cast<uintptr_t>(t) % (8 * sizeof(T)) == 0; };
     const T *u = view_at<T>(p.u, p.seqs, r) + k.c, *dt = view_at<T>(p.dt, p.seqs, r) + k.c, *dy = view_at<T>(p.dy, p.seqs, r) + k.c;
     const T* z = p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
     const T *b = view_at<T>(p.b, p.seqs, r) + k.g * N, *c = view_at<T>(p.c, p.seqs, r) + k.g * N;
@@ -533,126 +584,132 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
         const bool serves = ch[j] < k.width;
         const long long at = static_cast<long long>(k.c + ch[j]) * N, wide = static_cast<long long>(C) * N;
         a2[j].get(serves ? p.A + at : nullptr, n0, perm, N);
+        a2[j].scale(kLog2e);
+        da[j].clear();
         if (carries != nullptr) carry[j].get(serves && r.some ? carries + slot * wide + at : nullptr, n0, perm, N);
         else carry[j].get(serves && r.some && p.dfinal != nullptr ? p.dfinal + r.s * wide + at : nullptr, n0, perm, N);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            a2[j].v[i] = __fmul2_rn(a2[j].v[i], both(kLog2e));
-            da[j].v[i] = both(0.f);
-        }
     }
-    float sum_d = 0.f, sum_bias[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum_bias[j] = 0.f;
+    float sum_d = 0.f;
+    sum_bias[0] = sum_bias[kThreads] = make_float4(0.f, 0.f, 0.f, 0.f);
     const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
-    const int col = threadIdx.x % kColumns * 8;            // (kColumns divides the threads)
+    const int col = threadIdx.x % kColumns * 8, left = k.width - col;            // (kColumns divides the threads)
+    const bool eight = even && left >= 8, four = N % 4 == 0 && reinterpret_cast<uintptr_t>(p.saved) % 16 == 0;
+    const bool vec_u = p.u.vec && eight, vec_dt = p.dt.vec && eight, vec_z = p.z.vec && eight, vec_dy = p.dy.vec && eight;
+    const auto aligned = [&](const void* t) { return eight && reinterpret_cast<uintptr_t>(t) % (8 * sizeof(T)) == 0; };
+    const bool vec_du = aligned(p.du), vec_ddt = aligned(p.ddt), vec_dz = aligned(p.dz);
 
-    const long long tiles = r.some ? (r.end - r.first + kBwdTile - 1) / kBwdTile : 0;
+    const long long tiles = r.some ? (r.end - r.first + kTile - 1) / kTile : 0;
     for (long long tile = tiles - 1; tile >= 0; --tile) {
-        const long long t0 = r.first + tile * kBwdTile;
+        const long long t0 = r.first + tile * kTile;
         Vec8<T> ru[kEach], rdt[kEach], rz[kEach], rdy[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int row = row_of(i);
             ru[i].zero(), rdt[i].zero(), rz[i].zero(), rdy[i].zero();
-            if (row >= kBwdTile || t0 + row >= r.end || col >= k.width) continue;
-            load8(ru[i], u + (t0 + row) * p.u.row, col, k.width, p.u.vec && even);
-            load8(rdt[i], dt + (t0 + row) * p.dt.row, col, k.width, p.dt.vec && even);
-            load8(rdy[i], dy + (t0 + row) * p.dy.row, col, k.width, p.dy.vec && even);
-            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row, col, k.width, p.z.vec && even);
+            if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
+            load8(ru[i], u + (t0 + row) * p.u.row + col, left, vec_u);
+            load8(rdt[i], dt + (t0 + row) * p.dt.row + col, left, vec_dt);
+            load8(rdy[i], dy + (t0 + row) * p.dy.row + col, left, vec_dy);
+            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row + col, left, vec_z);
         }
-        StateRows<T, NP, kBwdTile> rb, rc;
+        StateRows<T, NP, kThreads> rb, rc;
         rb.fetch(b, p.b, t0, r.end, N);
         rc.fetch(c, p.c, t0, r.end, N);
+        if (tile > 0) {
+            // (the tile in front of this one: a whole one)
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int row = row_of(i);
+                if (row >= kTile || left <= 0) continue;
+                const long long at = t0 - kTile + row;
+                prefetch_l2(u + at * p.u.row + col);
+                prefetch_l2(dt + at * p.dt.row + col);
+                prefetch_l2(dy + at * p.dy.row + col);
+                if (z != nullptr) prefetch_l2(z + at * p.z.row + col);
+            }
+        }
         Four h[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            h[j].get(ch[j] < k.width ? p.saved + (saved_slot(p.seqs, r, t0 / kScanTile) * C + k.c + ch[j]) * N : nullptr, n0, perm, N);
+            h[j].get4(ch[j] < k.width ? p.saved + (saved_slot(p.seqs, r, t0 / kScanTile) * C + k.c + ch[j]) * N : nullptr, n0, perm, N, four);
         __syncthreads();            // the last tile's sums have been read
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int row = row_of(i);
-            if (row >= kBwdTile) continue;
+            if (row >= kTile) continue;
             float2 fu[4], fd[4], fz[4], fy[4];
             ru[i].widen(fu);
             rdt[i].widen(fd);
             rz[i].widen(fz);
             rdy[i].widen(fy);
-            const bool in = t0 + row < r.end;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
-                float d0 = fd[j].x + o.x, d1 = fd[j].y + o.y;
-                if (p.softplus) d0 = softplus(d0), d1 = softplus(d1);
-                if (!in) d0 = d1 = 0.f;        // positions past the end change nothing
-                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], make_float2(silu(fz[j].x), silu(fz[j].y)));
-                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d0, fu[j].x, d1, fu[j].y);
+                const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < r.end);
+                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], silu2(fz[j]));
+                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
                 *reinterpret_cast<float2*>(&gs[row][col + 2 * j]) = fy[j];
             }
+            stash[(i * 4 + 0) * kThreads] = ru[i], stash[(i * 4 + 1) * kThreads] = rdt[i];
+            stash[(i * 4 + 2) * kThreads] = rz[i], stash[(i * 4 + 3) * kThreads] = rdy[i];
         }
         rb.template spread<kOrders>(bs);
         rc.template spread<kOrders>(cs);
         __syncthreads();
 #pragma unroll 1
-        for (int w = 0; w < kBwdTile / kBwdStep; ++w) {
+        for (int w = 0; w < kTile / kStep; ++w) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 front[(w * 8 + j * 4 + 0) * kThreads] = h[j].v[0].x, front[(w * 8 + j * 4 + 1) * kThreads] = h[j].v[0].y;
                 front[(w * 8 + j * 4 + 2) * kThreads] = h[j].v[1].x, front[(w * 8 + j * 4 + 3) * kThreads] = h[j].v[1].y;
             }
-            if (w == kBwdTile / kBwdStep - 1) break;
+            if (w == kTile / kStep - 1) break;
 #pragma unroll
-            for (int q = 0; q < kBwdStep; ++q) {
-                const int t = w * kBwdStep + q;
-                const float4 fb = *reinterpret_cast<const float4*>(&bs[order][t][n0]);
+            for (int q = 0; q < kStep; ++q) {
+                const int t = w * kStep + q;
+                Four fb;
+                fb.load(&bs[order][t][n0]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float2 s = step[t][ch[j]];
                     const float in = s.x * s.y;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 e = __fmul2_rn(both(s.x), a2[j].v[i]);
-                        const float2 a = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-                        h[j].v[i] = __ffma2_rn(both(in), i == 0 ? make_float2(fb.x, fb.y) : make_float2(fb.z, fb.w),
-                                               __fmul2_rn(a, h[j].v[i]));
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        h[j].v[i] = __ffma2_rn(both(in), fb.v[i], __fmul2_rn(decay_of(s.x, a2[j].v[i]), h[j].v[i]));
                 }
             }
         }
 #pragma unroll 1
-        for (int w = kBwdTile / kBwdStep - 1; w >= 0; --w) {
-            float2 held[kBwdStep][2][2], decay[kBwdStep][2][2];       // a h[t-1], a
+        for (int w = kTile / kStep - 1; w >= 0; --w) {
+            float2 held[kStep][2][2], decay[kStep][2][2];       // a h[t-1], a
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 h[j].v[0] = make_float2(front[(w * 8 + j * 4 + 0) * kThreads], front[(w * 8 + j * 4 + 1) * kThreads]);
                 h[j].v[1] = make_float2(front[(w * 8 + j * 4 + 2) * kThreads], front[(w * 8 + j * 4 + 3) * kThreads]);
             }
 #pragma unroll
-            for (int q = 0; q < kBwdStep; ++q) {
-                const int t = w * kBwdStep + q;
-                const float4 fb = *reinterpret_cast<const float4*>(&bs[order][t][n0]);
+            for (int q = 0; q < kStep; ++q) {
+                const int t = w * kStep + q;
+                Four fb;
+                fb.load(&bs[order][t][n0]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float2 s = step[t][ch[j]];
                     const float in = s.x * s.y;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 e = __fmul2_rn(both(s.x), a2[j].v[i]);
-                        decay[q][j][i] = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                        decay[q][j][i] = decay_of(s.x, a2[j].v[i]);
                         held[q][j][i] = __fmul2_rn(decay[q][j][i], h[j].v[i]);
-                        if (q + 1 < kBwdStep)
-                            h[j].v[i] = __ffma2_rn(both(in), i == 0 ? make_float2(fb.x, fb.y) : make_float2(fb.z, fb.w), held[q][j][i]);
+                        if (q + 1 < kStep) h[j].v[i] = __ffma2_rn(both(in), fb.v[i], held[q][j][i]);
                     }
                 }
             }
-            float into[kBwdStep], decays[kBwdStep], ys[kBwdStep];
+            float into[kStep], decays[kStep], ys[kStep];
 #pragma unroll
-            for (int q = kBwdStep - 1; q >= 0; --q) {
-                const int t = w * kBwdStep + q;
-                const float4 b4 = *reinterpret_cast<const float4*>(&bs[order][t][n0]);
-                const float4 c4 = *reinterpret_cast<const float4*>(&cs[order][t][n0]);
-                const float2 fb[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-                const float2 fc[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+            for (int q = kStep - 1; q >= 0; --q) {
+                const int t = w * kStep + q;
+                Four fb, fc;
+                fb.load(&bs[order][t][n0]);
+                fc.load(&cs[order][t][n0]);
                 float2 vb[2] = {both(0.f), both(0.f)}, vc[2] = {both(0.f), both(0.f)};
                 float s1[2], s2[2], s3[2];
 #pragma unroll
@@ -662,14 +719,14 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
                     float2 x1 = both(0.f), x2 = both(0.f), x3 = both(0.f);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 dh = __ffma2_rn(both(g), fc[i], carry[j].v[i]);
-                        const float2 now = __ffma2_rn(both(in), fb[i], held[q][j][i]);
+                        const float2 dh = __ffma2_rn(both(g), fc.v[i], carry[j].v[i]);
+                        const float2 now = __ffma2_rn(both(in), fb.v[i], held[q][j][i]);
                         const float2 x = __fmul2_rn(dh, held[q][j][i]);
                         vb[i] = __ffma2_rn(dh, both(in), vb[i]);
                         vc[i] = __ffma2_rn(both(g), now, vc[i]);
-                        x1 = __ffma2_rn(dh, fb[i], x1);
+                        x1 = __ffma2_rn(dh, fb.v[i], x1);
                         x2 = __ffma2_rn(x, a2[j].v[i], x2);
-                        x3 = __ffma2_rn(fc[i], now, x3);
+                        x3 = __ffma2_rn(fc.v[i], now, x3);
                         da[j].v[i] = __ffma2_rn(x, both(s.x), da[j].v[i]);
                         carry[j].v[i] = __fmul2_rn(dh, decay[q][j][i]);
                     }
@@ -680,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
                 decays[q] = s2[0] + from_lane(s2[1], 1);
                 ys[q] = s3[0] + from_lane(s3[1], 1);
                 // over the warp's channels
-                float* to = sums + (warp * kBwdTile + t) * 2 * NP;
+                float* to = sums + (warp * kTile + t) * 2 * NP;
                 if constexpr (W >= 2) {
                     vb[0] = make_float2(vb[0].x + from_lane(vb[1].x, W / 2 * L), vb[0].y + from_lane(vb[1].y, W / 2 * L));
                     vc[0] = make_float2(vc[0].x + from_lane(vc[1].x, W / 2 * L), vc[0].y + from_lane(vc[1].y, W / 2 * L));
@@ -705,37 +762,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
                     *reinterpret_cast<float4*>(to + NP + n0) = make_float4(vc[0].x, vc[0].y, vc[1].x, vc[1].y);
                 }
             }
-            // over the states: the lanes part the positions among themselves
-            constexpr int kParts = L >= 8 ? 4 : L / 2, kMine = kBwdStep / kParts;
-            int first = 0;
-            if constexpr (L >= 4) {
-                const bool upper = (sub & 2) != 0;
-                first = upper ? 2 : 0;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    into[q] = (upper ? into[q + 2] : into[q]) + from_lane(upper ? into[q] : into[q + 2], 2);
-                    decays[q] = (upper ? decays[q + 2] : decays[q]) + from_lane(upper ? decays[q] : decays[q + 2], 2);
-                    ys[q] = (upper ? ys[q + 2] : ys[q]) + from_lane(upper ? ys[q] : ys[q + 2], 2);
-                }
-            }
-            if constexpr (L >= 8) {
-                const bool upper = (sub & 4) != 0;
-                first += upper ? 1 : 0;
-                into[0] = (upper ? into[1] : into[0]) + from_lane(upper ? into[0] : into[1], 4);
-                decays[0] = (upper ? decays[1] : decays[0]) + from_lane(upper ? decays[0] : decays[1], 4);
-                ys[0] = (upper ? ys[1] : ys[0]) + from_lane(upper ? ys[0] : ys[1], 4);
-            }
-#pragma unroll
-            for (int m = 8; m < L; m *= 2) {
-                into[0] += from_lane(into[0], m);
-                decays[0] += from_lane(decays[0], m);
-                ys[0] += from_lane(ys[0], m);
-            }
+            // over the states
+            Parts<L>::sum(into, sub);
+            Parts<L>::sum(decays, sub);
+            Parts<L>::sum(ys, sub);
             __syncwarp();       // all lanes have read these positions
-            if (L < 16 || sub < 8) {
+            if (Parts<L>::owner(sub)) {
 #pragma unroll
-                for (int q = 0; q < kMine; ++q) {
-                    const int t = w * kBwdStep + first + q;
+                for (int q = 0; q < Parts<L>::kMine; ++q) {
+                    const int t = w * kStep + Parts<L>::first_of(sub) + q;
                     const float2 s = step[t][ch[0]];
                     const float g = gs[t][ch[0]];
                     sum_d = fmaf(g, s.y, sum_d);
@@ -746,45 +781,49 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
         }
         __syncthreads();
         // dB and dC of the CTA's channels
-        for (int i = threadIdx.x; i < kBwdTile * 2 * NP; i += kThreads) {
-            const int t = i / (2 * NP), j = i % (2 * NP), which = j / NP, n = j % NP;
-            if (n >= N || t0 + t >= r.end) continue;
+        float* rows = part_bc + (block * seq_rows_device(p.seqs) + dense + t0) * 2 * N;
+        const int here = static_cast<int>(r.end - t0 < kTile ? r.end - t0 : kTile);
+#pragma unroll
+        for (int i = 0; i < kTile * 2 * NP / kThreads; ++i) {
+            const int j = (threadIdx.x + i * kThreads) % (2 * NP), t = (threadIdx.x + i * kThreads) / (2 * NP), n = j % NP;
+            if (n >= N || t >= here) continue;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) s += sums[(w * kBwdTile + t) * 2 * NP + j];
-            part_bc[((block * seq_rows_device(p.seqs) + dense + t0 + t) * 2 + which) * N + n] = s;
+            for (int w = 0; w < S::kWarps; ++w) s += sums[(w * kTile + t) * 2 * NP + j];
+            rows[(2 * t + j / NP) * N + n] = s;
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int row = row_of(i);
-            if (row >= kBwdTile || t0 + row >= r.end || col >= k.width) continue;
+            if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
             float2 fu[4], fd[4], fz[4], fy[4], du[4], ddt[4], dz[4];
-            ru[i].widen(fu);
-            rdt[i].widen(fd);
-            rz[i].widen(fz);
-            rdy[i].widen(fy);
+            stash[(i * 4 + 0) * kThreads].widen(fu);
+            stash[(i * 4 + 1) * kThreads].widen(fd);
+            stash[(i * 4 + 2) * kThreads].widen(fz);
+            stash[(i * 4 + 3) * kThreads].widen(fy);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float4 s = *reinterpret_cast<const float4*>(&step[row][col + 2 * j]);
                 du[j] = make_float2(s.x, s.z);
                 ddt[j] = make_float2(s.y, s.w);
-                if (p.softplus) {
-                    const float2 o = *reinterpret_cast<const float2*>(&bias[col + 2 * j]);
-                    ddt[j] = __fmul2_rn(ddt[j], make_float2(sigmoid(fd[j].x + o.x), sigmoid(fd[j].y + o.y)));
-                }
-                sum_bias[2 * j] += ddt[j].x;
-                sum_bias[2 * j + 1] += ddt[j].y;
+                if (p.softplus)
+                    ddt[j] = __fmul2_rn(ddt[j], sigmoid2(__fadd2_rn(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]))));
                 if (z != nullptr) {
                     const float2 sum = __ffma2_rn(*reinterpret_cast<const float2*>(&skip[col + 2 * j]), fu[j],
                                                   *reinterpret_cast<const float2*>(&gs[row][col + 2 * j]));
-                    dz[j] = __fmul2_rn(__fmul2_rn(fy[j], sum), make_float2(silu_slope(fz[j].x, sigmoid(fz[j].x)),
-                                                                           silu_slope(fz[j].y, sigmoid(fz[j].y))));
+                    dz[j] = __fmul2_rn(__fmul2_rn(fy[j], sum), silu_slope2(fz[j]));
                 }
             }
-            const long long o = (dense + t0 + row) * C + k.c;
-            store8(static_cast<T*>(p.du) + o, du, col, k.width, aligned(p.du));
-            store8(static_cast<T*>(p.ddt) + o, ddt, col, k.width, aligned(p.ddt));
-            if (z != nullptr) store8(static_cast<T*>(p.dz) + o, dz, col, k.width, aligned(p.dz));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float4 s = sum_bias[j * kThreads];
+                s.x += ddt[2 * j].x, s.y += ddt[2 * j].y, s.z += ddt[2 * j + 1].x, s.w += ddt[2 * j + 1].y;
+                sum_bias[j * kThreads] = s;
+            }
+            const long long o = (dense + t0 + row) * C + k.c + col;
+            store8(static_cast<T*>(p.du) + o, du, left, vec_du);
+            store8(static_cast<T*>(p.ddt) + o, ddt, left, vec_ddt);
+            if (z != nullptr) store8(static_cast<T*>(p.dz) + o, dz, left, vec_dz);
         }
     }
     // this chunk's rows of parameter gradients: C x N of dA, C of dD, C of the bias's
@@ -802,7 +841,8 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(Scan p, int block
     constexpr int kRows = kThreads / kColumns;
     constexpr int kStride = kChannels + 4;      // (rows of 8 columns apart: fewer conflicts)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) red[static_cast<int>(threadIdx.x) / kColumns * kStride + col + j] = sum_bias[j];
+    for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<float4*>(&red[static_cast<int>(threadIdx.x) / kColumns * kStride + col + 4 * j]) = sum_bias[j * kThreads];
     __syncthreads();
     float* mine = part + static_cast<long long>(C) * N + k.c;
     for (int i = threadIdx.x; i < k.width; i += kThreads) {
@@ -841,19 +881,27 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(Scan p, const float* part,
 
 inline int channel_blocks(const Scan& p, int channels) { return p.G * ((p.C / p.G + channels - 1) / channels); }
 
-// Forward: states to a lane and lanes to a channel, by the number of states.
-#define DWC_SCAN_FWD_SHAPE(N, call)                 \
-    if ((N) <= 8) return call(2, 4);                \
-    if ((N) <= 16) return call(4, 4);               \
-    if ((N) <= 32) return call(8, 4);               \
-    if ((N) <= 64) return call(8, 8);               \
-    return call(8, 16);
+// Lanes to a pair of channels, four states of each to a lane.
+inline int lanes_of(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+#define DWC_SCAN_BY_LANES(N, call)   \
+    switch (lanes_of(N)) {           \
+        case 2: return call(2);      \
+        case 4: return call(4);      \
+        case 8: return call(8);      \
+        case 16: return call(16);    \
+        default: return call(32);    \
+    }
 inline int fwd_channels(int N) {
-#define DWC_CHANNELS(NS, L) (kThreads / (L))
-    DWC_SCAN_FWD_SHAPE(N, DWC_CHANNELS)
+#define DWC_CHANNELS(L) (FwdShape<L>::kChannels)
+    DWC_SCAN_BY_LANES(N, DWC_CHANNELS)
 #undef DWC_CHANNELS
 }
-inline int bwd_lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+inline int fwd_threads(int N) { return N <= 64 ? FwdShape<4>::kThreads : FwdShape<32>::kThreads; }
+inline int bwd_channels(int N) {
+#define DWC_CHANNELS(L) (BwdShape<L>::kChannels)
+    DWC_SCAN_BY_LANES(N, DWC_CHANNELS)
+#undef DWC_CHANNELS
+}
 
 // The workspaces, in floats.
 struct FwdSpace {
@@ -868,7 +916,7 @@ struct BwdSpace {
     long long bc, params, ends = 0, sums = 0;
     explicit BwdSpace(const Scan& p) {
         const long long slots = seq_slots(p.seqs, p.span), C = p.C;
-        bc = static_cast<long long>(channel_blocks(p, 2 * kThreads / bwd_lanes(p.N))) * seq_rows(p.seqs) * 2 * p.N;
+        bc = static_cast<long long>(channel_blocks(p, bwd_channels(p.N))) * seq_rows(p.seqs) * 2 * p.N;
         params = slots * C * (p.N + 2);
         if (p.span >= p.seqs.length) return;
         sums = slots * C;
@@ -883,43 +931,38 @@ cudaError_t launch_join(const Scan& p, float* ends, const float* sums, const flo
     return launch_pdl(scan_join_kernel<kBackward>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, p.stream, p, ends, sums, from);
 }
 
-template <typename T, int NS, int L>
+template <typename T, int L>
 cudaError_t fwd_t(const Scan& p) {
-    const int blocks = channel_blocks(p, kThreads / L);
+    using S = FwdShape<L>;
+    const int blocks = channel_blocks(p, S::kChannels);
     const long long grid = seq_slots(p.seqs, p.span) * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const FwdSpace space(p);
     float *ends = space.ends > 0 ? p.workspace : nullptr, *sums = p.workspace + space.ends;
+    const dim3 ctas(static_cast<unsigned>(grid)), threads(S::kThreads);
     if (ends != nullptr) {
-        cudaError_t err = launch_pdl(scan_fwd_kernel<T, NS, L, true>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream,
-                                     p, blocks, ends, sums);
+        cudaError_t err = launch_pdl(scan_fwd_kernel<T, L, true>, ctas, threads, 0, p.stream, p, blocks, ends, sums);
         if (err == cudaSuccess) err = launch_join<false>(p, ends, sums, p.state);
         if (err != cudaSuccess) return err;
     }
-    return launch_pdl(scan_fwd_kernel<T, NS, L, false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p, blocks,
-                      ends, sums);
+    return launch_pdl(scan_fwd_kernel<T, L, false>, ctas, threads, 0, p.stream, p, blocks, ends, sums);
 }
 
-template <typename T, int NS, int L>
+template <typename T, int L>
 cudaError_t adjoint_t(const Scan& p, float* ends, float* sums) {
-    const int blocks = channel_blocks(p, kThreads / L);
+    using S = FwdShape<L>;
+    const int blocks = channel_blocks(p, S::kChannels);
     const long long grid = seq_slots(p.seqs, p.span) * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const cudaError_t err = launch_pdl(scan_adjoint_kernel<T, NS, L>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream,
+    const cudaError_t err = launch_pdl(scan_adjoint_kernel<T, L>, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), 0, p.stream,
                                        p, blocks, ends, sums);
     return err != cudaSuccess ? err : launch_join<true>(p, ends, sums, p.dfinal);
-}
-template <typename T>
-cudaError_t adjoint(const Scan& p, float* ends, float* sums) {
-#define DWC_ADJOINT(NS, L) (adjoint_t<T, NS, L>(p, ends, sums))
-    DWC_SCAN_FWD_SHAPE(p.N, DWC_ADJOINT)
-#undef DWC_ADJOINT
 }
 
 template <typename T, int L>
 cudaError_t bwd_t(const Scan& p) {
     using S = BwdShape<L>;
-    constexpr size_t smem = S::kFloats * sizeof(float);
+    constexpr size_t smem = S::bytes(sizeof(T));
     const int blocks = channel_blocks(p, S::kChannels);
     const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks, rows = seq_rows(p.seqs), C = p.C;
     const long long sums = (rows * p.G * 2 * p.N + 255) / 256;
@@ -928,9 +971,9 @@ cudaError_t bwd_t(const Scan& p) {
     float *bc = p.workspace, *params = bc + space.bc, *ends = params + space.params;
     static DeviceOnce once;
     cudaError_t err = opt_in_smem(scan_bwd_kernel<T, L>, once, static_cast<int>(smem));
-    if (err == cudaSuccess && space.ends > 0) err = adjoint<T>(p, ends, ends + space.ends);
+    if (err == cudaSuccess && space.ends > 0) err = adjoint_t<T, L>(p, ends, ends + space.ends);
     if (err == cudaSuccess)
-        err = launch_pdl(scan_bwd_kernel<T, L>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, p.stream, p, blocks,
+        err = launch_pdl(scan_bwd_kernel<T, L>, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), smem, p.stream, p, blocks,
                          static_cast<const float*>(space.ends > 0 ? ends : nullptr), bc, params);
     if (err == cudaSuccess && sums > 0)
         err = launch_pdl(scan_bc_kernel<T>, dim3(static_cast<unsigned>(sums)), dim3(256), 0, p.stream, p,
@@ -941,20 +984,16 @@ cudaError_t bwd_t(const Scan& p) {
 
 template <typename T>
 cudaError_t fwd(const Scan& p) {
-#define DWC_FWD(NS, L) (fwd_t<T, NS, L>(p))
-    DWC_SCAN_FWD_SHAPE(p.N, DWC_FWD)
+#define DWC_FWD(L) (fwd_t<T, L>(p))
+    DWC_SCAN_BY_LANES(p.N, DWC_FWD)
 #undef DWC_FWD
 }
 
 template <typename T>
 cudaError_t bwd(const Scan& p) {
-    switch (bwd_lanes(p.N)) {
-        case 2: return bwd_t<T, 2>(p);
-        case 4: return bwd_t<T, 4>(p);
-        case 8: return bwd_t<T, 8>(p);
-        case 16: return bwd_t<T, 16>(p);
-        default: return bwd_t<T, 32>(p);
-    }
+#define DWC_BWD(L) (bwd_t<T, L>(p))
+    DWC_SCAN_BY_LANES(p.N, DWC_BWD)
+#undef DWC_BWD
 }
 
 }  // namespace scan

@@ -64,29 +64,31 @@ __device__ __forceinline__ long long dense_row(const Seqs& q, const Piece& r) {
     return q.offsets != nullptr ? r.base : r.s * q.length;
 }
 
-// 8 values of a row from column `col`, those at `limit` and beyond as zeros.
+// 8 values, of which `left` exist (the others: zeros, not stored).  vec: one access for all 8.
 template <typename T>
-__device__ __forceinline__ void load8(Vec8<T>& v, const T* row, int col, int limit, bool vec) {
-    if (vec && col + 8 <= limit) {
-        v.load(row + col);
+__device__ __forceinline__ void load8(Vec8<T>& v, const T* p, int left, bool vec) {
+    if (vec) {
+        v.load(p);
     } else {
         v.zero();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (col + j < limit) v.set(j, row[col + j]);
+            if (j < left) v.set(j, p[j]);
     }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* row, const float2 (&f)[4], int col, int limit, bool vec) {
-    if (vec && col + 8 <= limit) {
-        Vec8<T>::store(row + col, f);
+__device__ __forceinline__ void store8(T* p, const float2 (&f)[4], int left, bool vec) {
+    if (vec) {
+        Vec8<T>::store(p, f);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (col + 2 * j < limit) store_out(row + col + 2 * j, f[j].x);
-            if (col + 2 * j + 1 < limit) store_out(row + col + 2 * j + 1, f[j].y);
+            if (2 * j < left) store_out(p + 2 * j, f[j].x);
+            if (2 * j + 1 < left) store_out(p + 2 * j + 1, f[j].y);
         }
     }
 }
+// Brings a line that a later load reads from DRAM to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 }  // namespace dwc

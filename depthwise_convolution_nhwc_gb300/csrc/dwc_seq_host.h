@@ -103,7 +103,7 @@ struct Scan {
     cudaStream_t stream;
 };
 
-// Positions to a chunk (a multiple of 32; a sequence's length or more: no chunks) and, with them, the workspaces.
+// Positions to a chunk (a multiple of 16; a sequence's length or more: no chunks) and, with them, the workspaces.
 long long scan_fwd_span(const Scan& p);
 long long scan_bwd_span(const Scan& p);
 size_t scan_fwd_workspace_floats(const Scan& p);

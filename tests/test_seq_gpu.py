@@ -246,7 +246,7 @@ def check_scan(rng, lead, C, N, G, dtype, offsets=None, state=True, dfinal=True,
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("N", [1, 2, 4, 7, 8, 11, 16, 17, 32, 33, 64, 65, 100, 128])
+@pytest.mark.parametrize("N", [1, 2, 4, 7, 8, 11, 12, 16, 17, 24, 32, 33, 40, 64, 65, 72, 100, 128])
 def test_scan_states(N, dtype):
     rng = np.random.default_rng(N)
     check_scan(rng, (2, 37), 19 if N % 2 else 40, N, 1, dtype, gate=N % 3 != 0, state=N % 4 != 0, dfinal=N % 4 != 1)
