@@ -120,12 +120,14 @@ __device__ __forceinline__ void shift(Lanes<V> (&win)[KM]) {
     for (int i = KM - 1; i > 0; --i) win[i] = win[i - 1];
 }
 
-// Rows that a thread brings in together, one such batch ahead of the one it works on.
-constexpr int kBatch = 4;
+// Rows that a thread brings in together, one such batch ahead of the one it works on: what is in flight is what counts
+// (bf16 8 x 2048 x 4096, 4 taps, forward: 8 rows of 4 channels, five CTAs to an SM 47 us, 4 rows 54, 4 rows of 8 channels
+// 58; backward, which holds two tensors' rows and the sums: 4 rows).
+constexpr int kFwdBatch = 8, kBwdBatch = 4;
 
 // KM: taps held in registers; up to 4 it is the number of taps, 8 and 16 serve every number up to it.
 template <typename T, int KM, int V>
-__global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p, int columns, int run, int blocks) {
+__global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kernel(CausalConv p, int columns, int run, int blocks) {
     pdl_trigger();
     pdl_wait();
     const int K = KM >= 8 ? p.K : KM, C = p.C;
@@ -142,10 +144,10 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p,
     if (n > 0) {
         const T* from = x + first * p.x.row;
         T* to = static_cast<T*>(p.y) + (dense_row(p.seqs, r) + first) * C + c;
-        Raw<T, V> next[kBatch];
-        const auto fetch = [&](int t) {       // (positions t .. t + kBatch - 1, in turn)
+        Raw<T, V> next[kFwdBatch];
+        const auto fetch = [&](int t) {       // (positions t .. t + kFwdBatch - 1, in turn)
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
+            for (int q = 0; q < kFwdBatch; ++q) {
                 if (t + q < n) next[q].load(from);
                 from += p.x.row;
             }
@@ -156,13 +158,13 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p,
 #pragma unroll
         for (int i = 1; i < KM; ++i)
             if (i < K) win[i] = input<T, V>(x, p.x.row, state, C, K, first - i);
-        for (int t0 = 0; t0 < n; t0 += kBatch) {
-            Raw<T, V> raw[kBatch];
+        for (int t0 = 0; t0 < n; t0 += kFwdBatch) {
+            Raw<T, V> raw[kFwdBatch];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) raw[q] = next[q];
-            fetch(t0 + kBatch);
+            for (int q = 0; q < kFwdBatch; ++q) raw[q] = next[q];
+            fetch(t0 + kFwdBatch);
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
+            for (int q = 0; q < kFwdBatch; ++q) {
                 win[0] = raw[q].widen();
                 Lanes<V> f = convolve(w, bias, win, K);
                 if (p.silu) f.to_silu();
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) causal_conv_fwd_kernel(CausalConv p,
 // A thread walks K - 1 positions past its run: position t gives dpre[t], and with it dx[t - K + 1] is
 // complete.  Parameter gradients count the run's own positions; the CTA's groups are added in order.
 template <typename T, int KM, int V>
-__global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p, int columns, int run, int blocks) {
+__global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kernel(CausalConv p, int columns, int run, int blocks) {
     __shared__ float sums[kThreads * V];
     pdl_trigger();
     pdl_wait();
@@ -212,10 +214,10 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
         const T* from_x = x + first * p.x.row;
         const T* from_dy = view_at<T>(p.dy, p.seqs, r) + c + first * p.dy.row;
         T* to = static_cast<T*>(p.dx) + (dense_row(p.seqs, r) + first - (K - 1)) * C + c;
-        Raw<T, V> next_x[kBatch], next_dy[kBatch];
-        const auto fetch = [&](int t) {       // (positions t .. t + kBatch - 1, in turn)
+        Raw<T, V> next_x[kBwdBatch], next_dy[kBwdBatch];
+        const auto fetch = [&](int t) {       // (positions t .. t + kBwdBatch - 1, in turn)
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
+            for (int q = 0; q < kBwdBatch; ++q) {
                 if (t + q < known) {
                     next_x[q].load(from_x);
                     next_dy[q].load(from_dy);
@@ -232,54 +234,61 @@ __global__ void __launch_bounds__(kThreads) causal_conv_bwd_kernel(CausalConv p,
 #pragma unroll
         for (int i = 1; i < KM; ++i)
             if (i < K) win[i] = input<T, V>(x, p.x.row, state, C, K, first - i);
-        for (int t0 = 0; t0 < stop; t0 += kBatch) {
-            Raw<T, V> raw_x[kBatch], raw_dy[kBatch];
+        for (int t0 = 0; t0 < stop; t0 += kBwdBatch) {
+            Raw<T, V> raw_x[kBwdBatch], raw_dy[kBwdBatch];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) raw_x[q] = next_x[q], raw_dy[q] = next_dy[q];
-            fetch(t0 + kBatch);
+            for (int q = 0; q < kBwdBatch; ++q) raw_x[q] = next_x[q], raw_dy[q] = next_dy[q];
+            fetch(t0 + kBwdBatch);
+            // (nearly every batch lies within the run and needs no test of its rows)
+            const auto work = [&](auto whole) {
+                constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int t = t0 + q, at = t - (K - 1);
-                dpre[0].clear();
-                if (t < known) {
-                    win[0] = raw_x[q].widen();
-                    dpre[0] = raw_dy[q].widen();
-                    if (p.silu) dpre[0].by_slope(convolve(w, bias, win, K));
-                }
-                if (t < n) {
+                for (int q = 0; q < kBwdBatch; ++q) {
+                    const int t = t0 + q, at = t - (K - 1);
+                    if (kWhole || t < known) {
+                        win[0] = raw_x[q].widen();
+                        dpre[0] = raw_dy[q].widen();
+                        if (p.silu) dpre[0].by_slope(convolve(w, bias, win, K));
+                    } else {
+                        dpre[0].clear();
+                    }
+                    if (kWhole || t < n) {
 #pragma unroll
-                    for (int i = 0; i < KM; ++i)
-                        if (i < K) dw[i].fma(dpre[0], win[i]);
-                    db.add(dpre[0]);
-                }
-                if (at >= low && t < stop) {
-                    // dx[at] = sum_k w_k dpre[at + K - 1 - k]: the tap i back goes with dpre of i positions on
-                    Lanes<V> f;
-                    f.clear();
+                        for (int i = 0; i < KM; ++i)
+                            if (i < K) dw[i].fma(dpre[0], win[i]);
+                        db.add(dpre[0]);
+                    }
+                    if (kWhole || (at >= low && t < stop)) {
+                        // dx[at] = sum_k w_k dpre[at + K - 1 - k]: the tap i back goes with dpre of i positions on
+                        Lanes<V> f;
+                        f.clear();
 #pragma unroll
-                    for (int i = 0; i < KM; ++i) {
-                        if (i >= K) continue;
-                        if constexpr (KM < 8) {
-                            f.fma(w[KM - 1 - i], dpre[i]);
-                        } else {
-                            Lanes<V> tap;
+                        for (int i = 0; i < KM; ++i) {
+                            if (i >= K) continue;
+                            if constexpr (KM < 8) {
+                                f.fma(w[KM - 1 - i], dpre[i]);
+                            } else {
+                                Lanes<V> tap;
 #pragma unroll
-                            for (int j = 0; j < V; ++j) tap.set(j, load_param(p.w, p.param_type, i * C + c + j, 0.f));
-                            f.fma(tap, dpre[i]);
+                                for (int j = 0; j < V; ++j) tap.set(j, load_param(p.w, p.param_type, i * C + c + j, 0.f));
+                                f.fma(tap, dpre[i]);
+                            }
                         }
+                        if (!kWhole && at >= kept_from) {
+                            Raw<T, V> g;
+                            g.load(dfinal + (first + at - (r.length - (K - 1))) * C);
+                            f.add(g.widen());
+                        }
+                        if (kWhole || at >= 0) Raw<T, V>::store(to, f);
+                        else if (dstate != nullptr) Raw<T, V>::store(dstate + (at + K - 1) * C, f);
                     }
-                    if (at >= kept_from) {
-                        Raw<T, V> g;
-                        g.load(dfinal + (first + at - (r.length - (K - 1))) * C);
-                        f.add(g.widen());
-                    }
-                    if (at >= 0) Raw<T, V>::store(to, f);
-                    else if (dstate != nullptr) Raw<T, V>::store(dstate + (at + K - 1) * C, f);
+                    to += C;
+                    shift(win);
+                    shift(dpre);
                 }
-                to += C;
-                shift(win);
-                shift(dpre);
-            }
+            };
+            if (t0 >= K - 1 && t0 + kBwdBatch <= n && t0 + kBwdBatch - (K - 1) <= kept_from) work(std::true_type{});
+            else work(std::false_type{});
         }
     }
     if (p.partial == nullptr) return;
@@ -373,14 +382,14 @@ int columns_for(int vectors) {
     return n;
 }
 
-// Positions to a thread: 32, fewer where that leaves SMs without their eight CTAs.
-constexpr int kRun = 32;
+// Positions to a thread: 64, fewer where that leaves SMs without their eight CTAs.
+constexpr int kRun = 64;
 
 template <typename T, int KM, int V>
 cudaError_t fwd_t(CausalConv p) {
     const int vectors = (p.C + V - 1) / V, columns = columns_for(vectors), blocks = (vectors + columns - 1) / columns;
     int run = kRun;
-    while (run > kBatch && seq_rows(p.seqs) / (kThreads / columns * run) * blocks < 8LL * device_info().sm_count) run /= 2;
+    while (run > kFwdBatch && seq_rows(p.seqs) / (kThreads / columns * run) * blocks < 8LL * device_info().sm_count) run /= 2;
     p.span = static_cast<long long>(kThreads / columns) * run;
     const long long grid = seq_slots(p.seqs, p.span) * blocks;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -388,8 +397,19 @@ cudaError_t fwd_t(CausalConv p) {
                       run, blocks);
 }
 
+// Positions to a slot of the backward pass, for V channels a thread: runs of 64, fewer where that leaves SMs without
+// their eight CTAs.  
+long long bwd_span(const Seqs& s, int C, int V) {
+    const int vectors = (C + V - 1) / V, columns = columns_for(vectors), groups = kThreads / columns;
+    const long long blocks = (vectors + columns - 1) / columns;
+    long long span = static_cast<long long>(groups) * 64;
+    while (span > groups * 8 && seq_rows(s) / span * blocks < 8LL * device_info().sm_count) span /= 2;
+    return span;
+}
+
 template <typename T, int KM, int V>
-cudaError_t bwd_t(const CausalConv& p) {
+cudaError_t bwd_t(CausalConv p) {
+    p.span = bwd_span(p.seqs, p.C, V);
     const int vectors = (p.C + V - 1) / V, columns = columns_for(vectors), blocks = (vectors + columns - 1) / columns;
     const int groups = kThreads / columns;
     const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks;
@@ -412,11 +432,10 @@ bool vectors_of(const CausalConv& p, bool backward) {
 template <typename T>
 cudaError_t fwd_k(const CausalConv& p) {
     const bool vec = vectors_of(p, false);
-    constexpr int V = sizeof(T) == 2 ? 8 : 4;
     switch (p.K) {
-        case 2: return vec ? fwd_t<T, 2, V>(p) : fwd_t<T, 2, 1>(p);
-        case 3: return vec ? fwd_t<T, 3, V>(p) : fwd_t<T, 3, 1>(p);
-        case 4: return vec ? fwd_t<T, 4, V>(p) : fwd_t<T, 4, 1>(p);
+        case 2: return vec ? fwd_t<T, 2, 4>(p) : fwd_t<T, 2, 1>(p);
+        case 3: return vec ? fwd_t<T, 3, 4>(p) : fwd_t<T, 3, 1>(p);
+        case 4: return vec ? fwd_t<T, 4, 4>(p) : fwd_t<T, 4, 1>(p);
     }
     if (p.K > 8) return fwd_t<T, 16, 1>(p);
     return vec ? fwd_t<T, 8, 4>(p) : fwd_t<T, 8, 1>(p);
@@ -444,13 +463,11 @@ cudaError_t step_t(const CausalConv& p, void* state, long long state_stride) {
 
 }  // namespace
 
-// (the same whatever the alignment, since the workspace's size follows from it)
-long long causal_conv_bwd_span(const Seqs& s, int C) {
-    const int vectors = (C + 3) / 4, columns = columns_for(vectors), groups = kThreads / columns;
-    const long long blocks = (vectors + columns - 1) / columns;
-    long long span = static_cast<long long>(groups) * 64;
-    while (span > groups * 8 && seq_rows(s) / span * blocks < 8LL * device_info().sm_count) span /= 2;
-    return span;
+// (Whatever the alignment: of the kernels' vectors the one with the most slots.)
+long long causal_conv_bwd_slots(const Seqs& s, int C) {
+    long long most = 0;
+    for (int V : {1, 2, 4}) most = std::max(most, seq_slots(s, bwd_span(s, C, V)));
+    return most;
 }
 
 cudaError_t launch_causal_conv_fwd(const CausalConv& p) {

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
             }
         }
         if (t0 + kTile < r.end) fetch(t0 + kTile);
-#pragma unroll 1
+#pragma unroll
         for (int t = 0; t < kTile; t += kStep) {
             // (decays and inputs of all four positions first: they wait for nothing, the states only for them)
             float part[kStep], in[kStep][2];
@@ -531,30 +531,42 @@ template <int L>
 struct BwdShape {
     static constexpr int kLanes = 32 / L;                  // lanes of a warp that share states
     static constexpr int kOrders = kLanes >= 4 ? 4 : kLanes;
-    static constexpr int kThreads = 128, kChannels = 2 * kThreads / L, NP = 4 * L, kWarps = kThreads / 32;
+    // (small CTAs, seven to an SM at 144 registers a thread: 8 sequences of 4096 channels are 1024 of them, one round)
+    static constexpr int kThreads = L == 32 ? 128 : 64, kResident = L == 32 ? 3 : 7;
+    static constexpr int kChannels = 2 * kThreads / L, NP = 4 * L, kWarps = kThreads / 32;
     static constexpr int kColumns = kChannels / 8, kEach = (kTile * kColumns + kThreads - 1) / kThreads;
-    static constexpr size_t kFloats = kTile * kChannels * 3 + 2 * kOrders * kTile * NP +
-                                      kTile / kStep * 8 * kThreads + kWarps * kTile * 2 * NP + 2 * kChannels + 8 * kThreads;
-    // and a thread's vectors of u, dt, z and dy while it walks
-    static constexpr size_t bytes(size_t elem) { return kFloats * sizeof(float) + kEach * 4 * kThreads * 8 * elem; }
+    // dB and dC of kStep positions take the place of the states in front of them where they fit
+    static constexpr bool kShared = kStep * 2 * NP <= 8 * 32;
+    static constexpr size_t kFloats = kTile * kChannels * 3 + 2 * kOrders * kTile * NP + kTile / kStep * 8 * kThreads +
+                                      (kShared ? 0 : kWarps * kTile * 2 * NP) + 2 * kChannels + 8 * kThreads;
+    // and a thread's vectors of dt, z and dy while it walks
+    static constexpr size_t bytes(size_t elem) { return kFloats * sizeof(float) + kEach * 3 * kThreads * 8 * elem; }
+    // place of dB (0) or dC (1) of position t and state n among `front` or the sums
+    static __device__ __forceinline__ int place(int warp, int t, int which, int n) {
+        if constexpr (kShared) {
+            const int at = (t % kStep * 2 + which) * NP + n;
+            return (t / kStep * 8 + at / 32) * kThreads + warp * 32 + at % 32;
+        }
+        return ((warp * kTile + t) * 2 + which) * NP + n;
+    }
 };
 
 template <typename T, int L>
-__global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan p, int blocks, const float* carries, float* part_bc, float* part_p) {
+__global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident) scan_bwd_kernel(Scan p, int blocks, const float* carries, float* part_bc, float* part_p) {
     using S = BwdShape<L>;
     constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = S::kColumns, NP = S::NP, W = S::kLanes;
     constexpr int kOrders = S::kOrders, kEach = S::kEach;
     extern __shared__ __align__(16) float smem[];
     float2 (*step)[kChannels] = reinterpret_cast<float2 (*)[kChannels]>(smem);      // delta, u; then du, ddelta
-    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(step + kTile);       // g; then the sum over the states
+    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(step + kTile);       // g; then the sum over the states and D u
     float (*bs)[kTile][NP] = reinterpret_cast<float (*)[kTile][NP]>(gs + kTile);
     float (*cs)[kTile][NP] = bs + kOrders;
     float* front = reinterpret_cast<float*>(cs + kOrders);
-    float* sums = front + kTile / kStep * 8 * kThreads;       // warps x positions x (dB, dC)
-    float* bias = sums + S::kWarps * kTile * 2 * NP;
+    float* sums = S::kShared ? front : front + kTile / kStep * 8 * kThreads;       // dB and dC of every warp
+    float* bias = front + kTile / kStep * 8 * kThreads + (S::kShared ? 0 : S::kWarps * kTile * 2 * NP);
     float* skip = bias + kChannels;
     float4* sum_bias = reinterpret_cast<float4*>(skip + kChannels) + threadIdx.x;         // (two of them, kThreads apart)
-    Vec8<T>* stash = reinterpret_cast<Vec8<T>*>(skip + kChannels + 8 * kThreads) + threadIdx.x;      // u, dt, z, dy
+    Vec8<T>* stash = reinterpret_cast<Vec8<T>*>(skip + kChannels + 8 * kThreads) + threadIdx.x;      // dt, z, dy
     front += threadIdx.x;
     pdl_trigger();
     pdl_wait();
@@ -649,8 +661,7 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
                 *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
                 *reinterpret_cast<float2*>(&gs[row][col + 2 * j]) = fy[j];
             }
-            stash[(i * 4 + 0) * kThreads] = ru[i], stash[(i * 4 + 1) * kThreads] = rdt[i];
-            stash[(i * 4 + 2) * kThreads] = rz[i], stash[(i * 4 + 3) * kThreads] = rdy[i];
+            stash[(i * 3 + 0) * kThreads] = rdt[i], stash[(i * 3 + 1) * kThreads] = rz[i], stash[(i * 3 + 2) * kThreads] = rdy[i];
         }
         rb.template spread<kOrders>(bs);
         rc.template spread<kOrders>(cs);
@@ -686,6 +697,7 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
                 h[j].v[0] = make_float2(front[(w * 8 + j * 4 + 0) * kThreads], front[(w * 8 + j * 4 + 1) * kThreads]);
                 h[j].v[1] = make_float2(front[(w * 8 + j * 4 + 2) * kThreads], front[(w * 8 + j * 4 + 3) * kThreads]);
             }
+            __syncwarp();       // (their place is taken by dB and dC)
 #pragma unroll
             for (int q = 0; q < kStep; ++q) {
                 const int t = w * kStep + q;
@@ -737,7 +749,6 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
                 decays[q] = s2[0] + from_lane(s2[1], 1);
                 ys[q] = s3[0] + from_lane(s3[1], 1);
                 // over the warp's channels
-                float* to = sums + (warp * kTile + t) * 2 * NP;
                 if constexpr (W >= 2) {
                     vb[0] = make_float2(vb[0].x + from_lane(vb[1].x, W / 2 * L), vb[0].y + from_lane(vb[1].y, W / 2 * L));
                     vc[0] = make_float2(vc[0].x + from_lane(vc[1].x, W / 2 * L), vc[0].y + from_lane(vc[1].y, W / 2 * L));
@@ -746,20 +757,19 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
                     vb[0].x += from_lane(vb[0].y, W / 4 * L);
                     vc[0].x += from_lane(vc[0].y, W / 4 * L);
                 }
+                const auto keep = [&](int which, int n, float v) { sums[S::place(warp, t, which, n0 + n)] = v; };
                 if constexpr (W >= 8) {
                     const bool which = (cl & (W / 8)) != 0;
                     float v = (which ? vc[0].x : vb[0].x) + from_lane(which ? vb[0].x : vc[0].x, W / 8 * L);
                     if constexpr (W >= 16) v += from_lane(v, W / 16 * L);
-                    if (W < 16 || (cl & (W / 16)) == 0) to[(which ? NP : 0) + n0 + perm] = v;
-                } else if constexpr (W == 4) {
-                    to[n0 + perm] = vb[0].x;
-                    to[NP + n0 + perm] = vc[0].x;
-                } else if constexpr (W == 2) {
-                    to[n0 + perm] = vb[0].x, to[n0 + (1 ^ perm)] = vb[0].y;
-                    to[NP + n0 + perm] = vc[0].x, to[NP + n0 + (1 ^ perm)] = vc[0].y;
+                    if (W < 16 || (cl & (W / 16)) == 0) keep(which, perm, v);
                 } else {
-                    *reinterpret_cast<float4*>(to + n0) = make_float4(vb[0].x, vb[0].y, vb[1].x, vb[1].y);
-                    *reinterpret_cast<float4*>(to + NP + n0) = make_float4(vc[0].x, vc[0].y, vc[1].x, vc[1].y);
+                    keep(0, perm, vb[0].x), keep(1, perm, vc[0].x);
+                    if constexpr (W <= 2) keep(0, 1 ^ perm, vb[0].y), keep(1, 1 ^ perm, vc[0].y);
+                    if constexpr (W == 1) {
+                        keep(0, 2, vb[1].x), keep(0, 3, vb[1].y);
+                        keep(1, 2, vc[1].x), keep(1, 3, vc[1].y);
+                    }
                 }
             }
             // over the states
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
                     const float g = gs[t][ch[0]];
                     sum_d = fmaf(g, s.y, sum_d);
                     step[t][ch[0]] = make_float2(fmaf(into[q], s.x, skip[ch[0]] * g), fmaf(into[q], s.y, decays[q] * 0.6931471805599453f));
-                    gs[t][ch[0]] = ys[q];
+                    gs[t][ch[0]] = fmaf(skip[ch[0]], s.y, ys[q]);
                 }
             }
         }
@@ -789,18 +799,17 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
             if (n >= N || t >= here) continue;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) s += sums[(w * kTile + t) * 2 * NP + j];
+            for (int w = 0; w < S::kWarps; ++w) s += sums[S::place(w, t, j / NP, n)];
             rows[(2 * t + j / NP) * N + n] = s;
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int row = row_of(i);
             if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
-            float2 fu[4], fd[4], fz[4], fy[4], du[4], ddt[4], dz[4];
-            stash[(i * 4 + 0) * kThreads].widen(fu);
-            stash[(i * 4 + 1) * kThreads].widen(fd);
-            stash[(i * 4 + 2) * kThreads].widen(fz);
-            stash[(i * 4 + 3) * kThreads].widen(fy);
+            float2 fd[4], fz[4], fy[4], du[4], ddt[4], dz[4];
+            stash[(i * 3 + 0) * kThreads].widen(fd);
+            stash[(i * 3 + 1) * kThreads].widen(fz);
+            stash[(i * 3 + 2) * kThreads].widen(fy);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float4 s = *reinterpret_cast<const float4*>(&step[row][col + 2 * j]);
@@ -808,11 +817,8 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, 4) scan_bwd_kernel(Scan
                 ddt[j] = make_float2(s.y, s.w);
                 if (p.softplus)
                     ddt[j] = __fmul2_rn(ddt[j], sigmoid2(__fadd2_rn(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]))));
-                if (z != nullptr) {
-                    const float2 sum = __ffma2_rn(*reinterpret_cast<const float2*>(&skip[col + 2 * j]), fu[j],
-                                                  *reinterpret_cast<const float2*>(&gs[row][col + 2 * j]));
-                    dz[j] = __fmul2_rn(__fmul2_rn(fy[j], sum), silu_slope2(fz[j]));
-                }
+                if (z != nullptr)
+                    dz[j] = __fmul2_rn(__fmul2_rn(fy[j], *reinterpret_cast<const float2*>(&gs[row][col + 2 * j])), silu_slope2(fz[j]));
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {

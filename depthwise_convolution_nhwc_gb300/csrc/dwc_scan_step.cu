@@ -98,21 +98,21 @@ cudaError_t launch_scan_step(const Scan& p, float* state, long long state_stride
 namespace {
 
 // Positions to a chunk.  A batch whose sequences fill `enough` CTAs of the `resident` that the GPU holds together
-// stays whole; else there are as many chunks as make one round of CTAs, 128 positions at least.  Packed sequences
-// differ in length: those up to twice the mean stay whole.
+// stays whole (packed sequences differ in length: those up to twice the mean do); else there are as many chunks
+// as make one round of CTAs, 64 positions at least.
 long long span_of(const Seqs& s, long long blocks, long long resident, long long enough) {
     if (s.count == 0 || s.length == 0) return 1 << 20;
     const long long rows = seq_rows(s);
     long long span;
-    if (s.offsets != nullptr) {
-        span = std::max(2 * (rows / s.count), rows * blocks / resident);
-    } else if (s.count * blocks >= enough) {
-        span = s.length;
+    if (s.count * blocks >= enough) {
+        span = s.offsets != nullptr ? 2 * (rows / s.count) : s.length;
+    } else if (s.offsets != nullptr) {
+        span = rows * blocks / resident;
     } else {
         const long long each = std::max<long long>(1, resident / (s.count * blocks));
         span = (s.length + each - 1) / each;
     }
-    return std::max<long long>(128, (span + 15) / 16 * 16);
+    return std::max<long long>(64, (span + 15) / 16 * 16);
 }
 
 }  // namespace
@@ -122,7 +122,7 @@ long long scan_fwd_span(const Scan& p) {
     return span_of(p.seqs, scan::channel_blocks(p, scan::fwd_channels(p.N)), resident, resident / 3);
 }
 long long scan_bwd_span(const Scan& p) {
-    const long long resident = 4LL * device_info().sm_count;
+    const long long resident = (p.N <= 64 ? scan::BwdShape<4>::kResident : scan::BwdShape<32>::kResident) * static_cast<long long>(device_info().sm_count);
     return span_of(p.seqs, scan::channel_blocks(p, scan::bwd_channels(p.N)), resident, resident / 2);
 }
 size_t scan_fwd_workspace_floats(const Scan& p) {

@@ -100,7 +100,7 @@ CausalConv conv_of(const dwc_causal_conv_t& c, dwc_stream_t stream) {
 
 size_t conv_workspace(const dwc_causal_conv_t& c) {
     const Seqs s = seqs_of(c.seqs);
-    return static_cast<size_t>(seq_slots(s, causal_conv_bwd_span(s, c.C))) * (c.K + 1) * c.C * sizeof(float);
+    return static_cast<size_t>(causal_conv_bwd_slots(s, c.C)) * (c.K + 1) * c.C * sizeof(float);
 }
 
 // ---- scan
@@ -222,7 +222,6 @@ dwc_status_t dwc_causal_conv_bwd(const dwc_causal_conv_t* conv, const dwc_rows_t
         return first_error({zero(dw, static_cast<long long>(conv->K) * conv->C, stream), zero(dbias, conv->C, stream)});
     if (conv->w == nullptr) return DWC_ERR_INVALID_ARG;
     CausalConv p = conv_of(*conv, stream);
-    p.span = causal_conv_bwd_span(p.seqs, p.C);
     if (dw != nullptr || dbias != nullptr) {
         st = check_workspace(workspace, workspace_bytes, conv_workspace(*conv));
         if (st != DWC_OK) return st;

@@ -62,8 +62,8 @@ struct CausalConv {
     cudaStream_t stream;
 };
 
-// Positions to a slot of the backward pass.
-long long causal_conv_bwd_span(const Seqs& s, int C);
+// Slots that the backward pass may take.
+long long causal_conv_bwd_slots(const Seqs& s, int C);
 cudaError_t launch_causal_conv_fwd(const CausalConv& p);
 cudaError_t launch_causal_conv_bwd(const CausalConv& p);
 cudaError_t launch_causal_conv_step(const CausalConv& p, void* state, long long state_stride);
