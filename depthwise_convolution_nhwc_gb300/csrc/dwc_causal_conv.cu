@@ -64,6 +64,7 @@ struct Raw {
     Word w;
     __device__ __forceinline__ void zero() { w = Word{}; }
     __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
+    __device__ __forceinline__ void put(T* p) const { *reinterpret_cast<Word*>(p) = w; }
     __device__ __forceinline__ Lanes<V> widen() const {
         Lanes<V> f;
         if constexpr (V == 1) {
@@ -312,26 +313,37 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
     }
 }
 
-// One position a sequence: a thread per channel; the state's rows move up by one in place.
-template <typename T>
+// One position a sequence, V channels to a thread; the state's rows move up by one in place.  KM as above.
+template <typename T, int KM, int V>
 __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(CausalConv p, T* states, long long state_stride) {
     pdl_trigger();
     pdl_wait();
-    const int K = p.K, C = p.C;
+    const int K = KM >= 8 ? p.K : KM, C = p.C, vectors = C / V;
     const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= static_cast<long long>(p.seqs.count) * C) return;
-    const int s = static_cast<int>(i / C), c = static_cast<int>(i - static_cast<long long>(s) * C);
+    if (i >= static_cast<long long>(p.seqs.count) * vectors) return;
+    const int s = static_cast<int>(i / vectors), c = static_cast<int>(i - static_cast<long long>(s) * vectors) * V;
     T* state = states + s * state_stride + c;
-    float f = load_param(p.bias, p.param_type, c, 0.f);
-    for (int k = 0; k < K - 1; ++k) {
-        const T v = state[static_cast<long long>(k) * C];
-        f = fmaf(load_param(p.w, p.param_type, k * C + c, 0.f), to_f32(v), f);
-        if (k > 0) state[static_cast<long long>(k - 1) * C] = v;
+    Raw<T, V> rows[KM];          // rows[j]: the input j positions back
+#pragma unroll
+    for (int j = 1; j < KM; ++j)
+        if (j < K) rows[j].load(state + static_cast<long long>(K - 1 - j) * C);
+    rows[0].load(static_cast<const T*>(p.x.p) + s * p.x.seq + c);
+    Lanes<V> f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) f.set(j, load_param(p.bias, p.param_type, c + j, 0.f));
+#pragma unroll
+    for (int j = KM - 1; j >= 0; --j) {
+        if (j >= K) continue;
+        Lanes<V> w;
+#pragma unroll
+        for (int q = 0; q < V; ++q) w.set(q, load_param(p.w, p.param_type, (K - 1 - j) * C + c + q, 0.f));
+        f.fma(w, rows[j].widen());
     }
-    const T v = static_cast<const T*>(p.x.p)[s * p.x.seq + c];
-    f = fmaf(load_param(p.w, p.param_type, (K - 1) * C + c, 0.f), to_f32(v), f);
-    if (K > 1) state[static_cast<long long>(K - 2) * C] = v;
-    store_out(static_cast<T*>(p.y) + i, p.silu ? silu(f) : f);
+    if (p.silu) f.to_silu();
+    Raw<T, V>::store(static_cast<T*>(p.y) + static_cast<long long>(s) * C + c, f);
+#pragma unroll
+    for (int j = 0; j < KM - 1; ++j)
+        if (j < K - 1) rows[j].put(state + static_cast<long long>(K - 2 - j) * C);
 }
 
 // Column sums of the rows: a CTA takes 32 columns, each warp every 32nd row.
@@ -453,12 +465,21 @@ cudaError_t bwd_k(const CausalConv& p) {
     return vec ? bwd_t<T, 8, 2>(p) : bwd_t<T, 8, 1>(p);
 }
 
-template <typename T>
+template <typename T, int KM, int V>
 cudaError_t step_t(const CausalConv& p, void* state, long long state_stride) {
-    const long long grid = (static_cast<long long>(p.seqs.count) * p.C + kThreads - 1) / kThreads;
+    const long long grid = (static_cast<long long>(p.seqs.count) * (p.C / V) + kThreads - 1) / kThreads;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(causal_conv_step_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p,
+    return launch_pdl(causal_conv_step_kernel<T, KM, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, p.stream, p,
                       static_cast<T*>(state), state_stride);
+}
+
+template <typename T>
+cudaError_t step_k(const CausalConv& p, void* state, long long state_stride) {
+    const auto off = [](const void* t) { return reinterpret_cast<uintptr_t>(t) % (2 * sizeof(T)) != 0; };
+    const bool one = p.seqs.count <= 1;
+    const bool vec = p.C % 2 == 0 && !off(p.x.p) && !off(state) && !off(p.y) && (one || (p.x.seq % 2 == 0 && state_stride % 2 == 0));
+    if (p.K == 4) return vec ? step_t<T, 4, 2>(p, state, state_stride) : step_t<T, 4, 1>(p, state, state_stride);
+    return vec ? step_t<T, 16, 2>(p, state, state_stride) : step_t<T, 16, 1>(p, state, state_stride);
 }
 
 }  // namespace
@@ -488,9 +509,9 @@ cudaError_t launch_causal_conv_bwd(const CausalConv& p) {
 
 cudaError_t launch_causal_conv_step(const CausalConv& p, void* state, long long state_stride) {
     switch (p.type) {
-        case kF32: return step_t<float>(p, state, state_stride);
-        case kBF16: return step_t<__nv_bfloat16>(p, state, state_stride);
-        default: return step_t<__half>(p, state, state_stride);
+        case kF32: return step_k<float>(p, state, state_stride);
+        case kBF16: return step_k<__nv_bfloat16>(p, state, state_stride);
+        default: return step_k<__half>(p, state, state_stride);
     }
 }
 

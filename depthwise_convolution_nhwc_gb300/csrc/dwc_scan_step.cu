@@ -1,8 +1,9 @@
 // dwc_scan_step.cu -- selective scan of one position for each of several sequences, states updated in
-// place.
+// place; how the sequences of the other passes are cut into chunks.
 //
 // Bound by memory: the fp32 states are read and written once (8 N bytes a channel; everything else
-// is a few bytes).  A lane has four adjacent states of a channel; the lanes of a channel add up y.
+// is a few bytes).  A lane has four adjacent states of a channel, of kSeqs sequences whose loads are in flight
+// together; the lanes of a channel add up y.
 #include <algorithm>
 
 #include "dwc_scan.cuh"
@@ -11,67 +12,99 @@ namespace dwc {
 namespace scan {
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128;
 
-// kVec: N is a multiple of 4 and the states and A are aligned to 16 bytes.
-template <typename T, int L, bool kVec>
+// Four adjacent states of B or C (zeros past the last): one load of 4 values where kVec.
+template <typename T, bool kVec>
+__device__ __forceinline__ Four four_of(const T* p, int n0, int N) {
+    Four f;
+    if constexpr (kVec) {
+        f.clear();
+        if (n0 >= N) return f;
+        if constexpr (sizeof(T) == 4) {
+            f.load(p + n0);
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + n0);
+            f.v[0] = Elem<T>::load_pair(reinterpret_cast<const T*>(&w.x)), f.v[1] = Elem<T>::load_pair(reinterpret_cast<const T*>(&w.y));
+        }
+    } else {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = n0 + j < N ? to_f32(p[n0 + j]) : 0.f;
+        f.v[0] = make_float2(v[0], v[1]), f.v[1] = make_float2(v[2], v[3]);
+    }
+    return f;
+}
+
+// kVec: N is a multiple of 4, the states and A are aligned to 16 bytes, B and C to four values.
+template <typename T, int L, bool kVec, int kSeqs>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(Scan p, float* states, long long state_stride) {
     pdl_trigger();
     pdl_wait();
-    const int C = p.C, N = p.N;
+    const int C = p.C, N = p.N, groups = (p.seqs.count + kSeqs - 1) / kSeqs;
     const long long i = static_cast<long long>(blockIdx.x) * kStepThreads + threadIdx.x;
     const int at = static_cast<int>(i / (static_cast<long long>(C) * L));
-    const bool live = at < p.seqs.count;     // (the last CTA's other threads go along for the exchanges)
-    const int s = live ? at : 0;
+    const bool live = at < groups;           // (the last CTA's other threads go along for the exchanges)
+    const int first = live ? at * kSeqs : 0;
     const int rest = static_cast<int>(i - static_cast<long long>(at) * C * L), ch = rest / L, n0 = rest % L * 4;
     const int g = ch / (C / p.G);
-    float* state = states + s * state_stride + static_cast<long long>(ch) * N;
-    const float* a = p.A + static_cast<long long>(ch) * N;
-    const T *b = static_cast<const T*>(p.b.p) + s * p.b.seq + g * N, *c = static_cast<const T*>(p.c.p) + s * p.c.seq + g * N;
-    float h[4], an[4];
-    if (kVec) {
-        if (n0 < N) {
-            const float4 v = *reinterpret_cast<const float4*>(state + n0), w = *reinterpret_cast<const float4*>(a + n0);
-            h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
-            an[0] = w.x, an[1] = w.y, an[2] = w.z, an[3] = w.w;
+    Four h[kSeqs], b[kSeqs], c[kSeqs], a2;
+    float u[kSeqs], dt[kSeqs], z[kSeqs];
+    a2.get4(p.A + static_cast<long long>(ch) * N, n0, 0, N, kVec);
+    a2.scale(kLog2e);
+    const float bias = p.dt_bias != nullptr ? p.dt_bias[ch] : 0.f, skip = p.D != nullptr ? p.D[ch] : 0.f;
+#pragma unroll
+    for (int q = 0; q < kSeqs; ++q) {
+        const int s = min(first + q, p.seqs.count - 1);
+        h[q].get4(states + s * state_stride + static_cast<long long>(ch) * N, n0, 0, N, kVec);
+        b[q] = four_of<T, kVec>(static_cast<const T*>(p.b.p) + s * p.b.seq + g * N, n0, N);
+        c[q] = four_of<T, kVec>(static_cast<const T*>(p.c.p) + s * p.c.seq + g * N, n0, N);
+        u[q] = to_f32(static_cast<const T*>(p.u.p)[s * p.u.seq + ch]);
+        dt[q] = to_f32(static_cast<const T*>(p.dt.p)[s * p.dt.seq + ch]);
+        z[q] = p.z.p != nullptr ? to_f32(static_cast<const T*>(p.z.p)[s * p.z.seq + ch]) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < kSeqs; ++q) {
+        const int s = first + q;
+        float delta = dt[q] + bias;
+        if (p.softplus) delta = softplus(delta);
+        const float in = delta * u[q];
+        float2 sum2 = both(0.f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            h[q].v[j] = __ffma2_rn(both(in), b[q].v[j], __fmul2_rn(decay_of(delta, a2.v[j]), h[q].v[j]));
+            sum2 = __ffma2_rn(c[q].v[j], h[q].v[j], sum2);
         }
-    } else {
-        get_states(h, state, n0, N);
-        get_states(an, a, n0, N);
-    }
-    const float u = to_f32(static_cast<const T*>(p.u.p)[s * p.u.seq + ch]);
-    float delta = to_f32(static_cast<const T*>(p.dt.p)[s * p.dt.seq + ch]) + (p.dt_bias != nullptr ? p.dt_bias[ch] : 0.f);
-    if (p.softplus) delta = softplus(delta);
-    const float in = delta * u;
-    float sum = 0.f;
+        float sum = sum2.x + sum2.y;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (n0 + j >= N) continue;
-        h[j] = fmaf(exp2_fast(delta * (an[j] * kLog2e)), h[j], in * to_f32(b[n0 + j]));
-        sum = fmaf(to_f32(c[n0 + j]), h[j], sum);
+        for (int m = L / 2; m > 0; m >>= 1) sum += from_lane(sum, m);
+        if (!live || s >= p.seqs.count) continue;       // (no exchange below)
+        h[q].put4(states + s * state_stride + static_cast<long long>(ch) * N, n0, N, kVec);
+        if (rest % L != 0) continue;
+        sum = fmaf(skip, u[q], sum);
+        if (p.z.p != nullptr) sum *= silu(z[q]);
+        store_out(static_cast<T*>(p.y) + static_cast<long long>(s) * C + ch, sum);
     }
-    if (!live) {
-    } else if (kVec) {
-        if (n0 < N) *reinterpret_cast<float4*>(state + n0) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
-        put_states(state, h, n0, N);
-    }
-#pragma unroll
-    for (int m = L / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (!live || rest % L != 0) return;
-    if (p.D != nullptr) sum = fmaf(p.D[ch], u, sum);
-    if (p.z.p != nullptr) sum *= silu(to_f32(static_cast<const T*>(p.z.p)[s * p.z.seq + ch]));
-    store_out(static_cast<T*>(p.y) + static_cast<long long>(s) * C + ch, sum);
+}
+
+template <typename T, int L, bool kVec, int kSeqs>
+cudaError_t step_s(const Scan& p, float* state, long long state_stride) {
+    const long long groups = (p.seqs.count + kSeqs - 1) / kSeqs;
+    const long long grid = (groups * p.C * L + kStepThreads - 1) / kStepThreads;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(scan_step_kernel<T, L, kVec, kSeqs>, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads), 0, p.stream, p, state,
+                      state_stride);
 }
 
 template <typename T, int L>
 cudaError_t step_l(const Scan& p, float* state, long long state_stride) {
-    const long long grid = (static_cast<long long>(p.seqs.count) * p.C * L + kStepThreads - 1) / kStepThreads;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const auto off = [](const void* t) { return reinterpret_cast<uintptr_t>(t) % 16 != 0; };
-    const bool vec = p.N % 4 == 0 && state_stride % 4 == 0 && !off(state) && !off(p.A);
-    return launch_pdl(vec ? scan_step_kernel<T, L, true> : scan_step_kernel<T, L, false>, dim3(static_cast<unsigned>(grid)),
-                      dim3(kStepThreads), 0, p.stream, p, state, state_stride);
+    const auto off = [](const void* t, size_t a) { return reinterpret_cast<uintptr_t>(t) % a != 0; };
+    const auto four = [&](const RowsView& v) { return !off(v.p, 4 * sizeof(T)) && (p.seqs.count <= 1 || v.seq % 4 == 0); };
+    const bool vec = p.N % 4 == 0 && (p.seqs.count <= 1 || state_stride % 4 == 0) && !off(state, 16) && !off(p.A, 16) && four(p.b) && four(p.c);
+    if (!vec) return step_s<T, L, false, 1>(p, state, state_stride);
+    // several sequences to a thread once that leaves every SM 1024 threads
+    const bool many = static_cast<long long>(p.seqs.count) * p.C * L >= 4LL * 1024 * device_info().sm_count;
+    return many ? step_s<T, L, true, 4>(p, state, state_stride) : step_s<T, L, true, 1>(p, state, state_stride);
 }
 
 template <typename T>
