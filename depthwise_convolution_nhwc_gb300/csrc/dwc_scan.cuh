@@ -25,7 +25,7 @@ constexpr int kTile = kScanTile, kStep = 4;       // positions of a tile, and th
 // log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|): the logarithm as 2 atanh(s), s = e / (2 + e) <= 1/3, whose odd
 // series is s + s^3 P(s^2) with P of degree 3 by Chebyshev interpolation on [0, 1/9] (relative error 1.6e-8): relative
 // errors stay near 2^-22 however small e is.  (A NaN stays one: fmaxf would drop it.)
-__device__ __forceinline__ float2 softplus2(float2 v) {
+__device__ __forceinline__ float2 softplus2(float2 v, float2* slope = nullptr) {
     const float2 e = make_float2(exp2_fast(fabsf(v.x) * -kLog2e), exp2_fast(fabsf(v.y) * -kLog2e));
     const float2 w = __fadd2_rn(e, both(2.f));
     const float2 s = __fmul2_rn(e, make_float2(rcp_fast(w.x), rcp_fast(w.y))), q = __fmul2_rn(s, s);
@@ -33,34 +33,60 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
     p = __ffma2_rn(p, q, both(0.2000383585691452f));
     p = __ffma2_rn(p, q, both(0.33333319425582886f));
     const float2 t = __fadd2_rn(s, s);
+    if (slope != nullptr) {         // 1 / (1 + exp(-v)) = 1 / (1 + e), or e / (1 + e) where v < 0
+        const float2 o = __fadd2_rn(e, both(1.f)), r = make_float2(rcp_fast(o.x), rcp_fast(o.y));
+        *slope = make_float2(v.x < 0.f ? e.x * r.x : r.x, v.y < 0.f ? e.y * r.y : r.y);
+    }
     return __fadd2_rn(make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y), __ffma2_rn(__fmul2_rn(t, q), p, t));
 }
 __device__ __forceinline__ float softplus(float v) { return softplus2(both(v)).x; }
 
 __device__ __forceinline__ float from_lane(float v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
 
-// Sums over the lanes 2, 4, ... L / 2 apart of a channel pair's L, of kStep values each: the lanes part the values among
-// themselves, lane `sub` ends with the first kMine of them (values first_of(sub) ...).
+// Places in shared memory, such that neither the threads that write vectors of 8 channels or states nor the lanes that
+// read a channel's or four states' values meet in the banks, and that a position adds a constant to an address.
+// Two values per position and channel: units of two channels (16 bytes) change places among four, rows 64 bytes longer.
+template <int kChannels>
+struct StepAt {
+    static constexpr int kRow = kChannels + 8, kSize = kTile * kRow;
+    static __device__ __forceinline__ int at(int t, int ch) { return t * kRow + ((((ch >> 1) ^ (ch >> 3 & 3)) << 1) | (ch & 1)); }
+};
+// One value per position and channel: rows 8 bytes longer.
+template <int kChannels>
+struct ValueAt {
+    static constexpr int kRow = kChannels + 2, kSize = kTile * kRow;
+    static __device__ __forceinline__ int at(int t, int ch) { return t * kRow + ch; }
+};
+// Rows of NP states: 16 bytes more after every 128.  The position is w * kStep + q.
+template <int NP>
+struct RowAt {
+    static constexpr int U = NP / 4, kSize = kTile * U / 8 * 9 * 4;
+    static __device__ __forceinline__ int at(int w, int q, int n) {
+        const int more = U >= 8 ? (w * kStep + q) * (U / 8) : U == 4 ? w * (kStep / 2) + (q >> 1) : w;
+        return ((w * kStep + q) * U + more + (n >> 2) + (U > 8 ? n >> 5 : 0)) * 4 + (n & 3);
+    }
+};
+static_assert(kStep == 4, "RowAt");
+
+// Sums over the lanes 2, 4, ... L / 2 apart of a channel pair's L, of kStep values each.  The lanes part the values among
+// themselves: of two neighbouring positions' values a lane keeps one, then (from 8 lanes on) of the two pairs'.
 template <int L>
 struct Parts {
-    static constexpr int kMine = L >= 8 ? 1 : L == 4 ? 2 : 4;
-    static __device__ __forceinline__ int first_of(int sub) {
-        return (L >= 4 && (sub & 2) ? 2 : 0) + (L >= 8 && (sub & 4) ? 1 : 0);
+    static constexpr int kHeld = L >= 4 ? 2 : 4, kMine = L >= 8 ? 1 : kHeld;
+    static __device__ __forceinline__ float either(float low, float high, int mask, int sub) {
+        const bool upper = (sub & mask) != 0;
+        return (upper ? high : low) + from_lane(upper ? low : high, mask);
     }
-    static __device__ __forceinline__ bool owner(int sub) { return L <= 8 || sub < 8; }      // (others hold copies)
-    static __device__ __forceinline__ void sum(float (&v)[kStep], int sub) {
-        if constexpr (L >= 4) {
-            const bool upper = (sub & 2) != 0;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) v[q] = (upper ? v[q + 2] : v[q]) + from_lane(upper ? v[q] : v[q + 2], 2);
-        }
-        if constexpr (L >= 8) {
-            const bool upper = (sub & 4) != 0;
-            v[0] = (upper ? v[1] : v[0]) + from_lane(upper ? v[0] : v[1], 4);
-        }
+    static __device__ __forceinline__ void finish(float (&v)[kHeld], int sub) {
+        if constexpr (L >= 8) v[0] = either(v[0], v[1], 4, sub);
 #pragma unroll
         for (int m = 8; m < L; m *= 2) v[0] += from_lane(v[0], m);
     }
+    // position of a lane's i-th value
+    static __device__ __forceinline__ int position(int i, int sub) {
+        return L < 4 ? i : (L >= 8 ? (sub >> 1 & 2) : 2 * i) + (sub >> 1 & 1);
+    }
+    static __device__ __forceinline__ bool owner(int sub) { return L <= 8 || sub < 8; }      // (others hold copies)
 };
 
 // Index among `saved` of the state in front of tile `tile` of a sequence.
@@ -111,7 +137,7 @@ struct StateRows {
     }
     // each four states in 1, 2 or 4 orders: n, n ^ 2 (two orders); n, n ^ 1, n ^ 2, n ^ 3 (four)
     template <int kOrders>
-    __device__ __forceinline__ void spread(float (*to)[kRows][NP]) const {
+    __device__ __forceinline__ void spread(float* to) const {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int i = threadIdx.x + k * kThreads;
@@ -119,13 +145,13 @@ struct StateRows {
             float2 f[4];
             raw[k].widen(f);
 #pragma unroll
-            for (int o = 0; o < kOrders; ++o) {
-                const int m = kOrders == 2 ? 2 * o : o;
-                float4* at = reinterpret_cast<float4*>(&to[o][i / kVecs][i % kVecs * 8]);
+            for (int q = 0; q < 2; ++q) {
+                float* at = to + RowAt<NP>::at(i / kVecs / kStep, i / kVecs % kStep, i % kVecs * 8 + 4 * q);
+                const float v[4] = {f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float v[4] = {f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y};
-                    at[q] = make_float4(v[m], v[1 ^ m], v[2 ^ m], v[3 ^ m]);
+                for (int o = 0; o < kOrders; ++o) {
+                    const int m = kOrders == 2 ? 2 * o : o;
+                    *reinterpret_cast<float4*>(at + o * RowAt<NP>::kSize) = make_float4(v[m], v[1 ^ m], v[2 ^ m], v[3 ^ m]);
                 }
             }
         }
@@ -183,10 +209,11 @@ __device__ __forceinline__ float2 decay_of(float delta, float2 a2) {
     return make_float2(exp2_fast(e.x), exp2_fast(e.y));
 }
 
-// delta of two channels
-__device__ __forceinline__ float2 delta_of(float2 raw, float2 bias, bool plus, bool in) {
+// delta of two channels, and its derivative by dt
+__device__ __forceinline__ float2 delta_of(float2 raw, float2 bias, bool plus, bool in, float2* slope = nullptr) {
     const float2 v = __fadd2_rn(raw, bias);
-    const float2 d = plus ? softplus2(v) : v;
+    if (slope != nullptr) *slope = both(1.f);
+    const float2 d = plus ? softplus2(v, slope) : v;
     return in ? d : both(0.f);      // positions past the end leave the states alone
 }
 
@@ -208,8 +235,11 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
     using S = FwdShape<L>;
     constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = kChannels / 8, NP = S::NP, W = 32 / L;
     constexpr int kEach = (kTile * kColumns + kThreads - 1) / kThreads;      // vectors of a tile to a thread
-    __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, u
-    __shared__ __align__(16) float bs[1][kTile][NP], cs[1][kStates ? 1 : kTile][NP], ys[kStates ? 1 : kTile][kChannels];
+    using Step = StepAt<kChannels>;
+    using Value = ValueAt<kChannels>;
+    using Row = RowAt<NP>;
+    __shared__ __align__(16) float2 step[Step::kSize];    // delta, u
+    __shared__ __align__(16) float bs[Row::kSize], cs[kStates ? 4 : Row::kSize], ys[kStates ? 4 : Value::kSize];
     __shared__ __align__(16) float bias[kChannels], skip[kChannels];
     pdl_trigger();
     pdl_wait();
@@ -278,7 +308,7 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < r.end);
-                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
+                *reinterpret_cast<float4*>(&step[Step::at(row, col + 2 * j)]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
             }
         }
         rb.template spread<1>(bs);
@@ -302,13 +332,13 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 #pragma unroll
         for (int t = 0; t < kTile; t += kStep) {
             // (decays and inputs of all four positions first: they wait for nothing, the states only for them)
-            float part[kStep], in[kStep][2];
+            float part[Parts<L>::kHeld], last = 0.f, in[kStep][2];
             float2 a[kStep][2][2];
 #pragma unroll
             for (int q = 0; q < kStep; ++q)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float2 s = step[t + q][ch[j]];
+                    const float2 s = step[Step::at(t + q, ch[j])];
                     in[q][j] = s.x * s.y;
                     if (kStates) total[j] += s.x;
 #pragma unroll
@@ -317,8 +347,8 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 #pragma unroll
             for (int q = 0; q < kStep; ++q) {
                 Four fb, fc;
-                fb.load(&bs[0][t + q][n0]);
-                if constexpr (!kStates) fc.load(&cs[0][t + q][n0]);
+                fb.load(&bs[Row::at(t / kStep, q, n0)]);
+                if constexpr (!kStates) fc.load(&cs[Row::at(t / kStep, q, n0)]);
                 float sum[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -330,14 +360,19 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
                     }
                     sum[j] = x.x + x.y;
                 }
-                // (the partner's other channel is this lane's first)
-                if constexpr (!kStates) part[q] = sum[0] + from_lane(sum[1], 1);
+                if constexpr (!kStates) {
+                    // (the partner's other channel is this lane's first)
+                    const float v = sum[0] + from_lane(sum[1], 1);
+                    if constexpr (L < 4) part[q] = v;
+                    else if (q % 2 == 0) last = v;
+                    else part[q / 2] = Parts<L>::either(last, v, 2, sub);
+                }
             }
             if constexpr (!kStates) {
-                Parts<L>::sum(part, sub);
+                Parts<L>::finish(part, sub);
                 if (Parts<L>::owner(sub)) {
 #pragma unroll
-                    for (int q = 0; q < Parts<L>::kMine; ++q) ys[t + Parts<L>::first_of(sub) + q][ch[0]] = part[q];
+                    for (int i = 0; i < Parts<L>::kMine; ++i) ys[Value::at(t + Parts<L>::position(i, sub), ch[0])] = part[i];
                 }
             }
         }
@@ -353,7 +388,7 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 o = *reinterpret_cast<const float2*>(&skip[col + 2 * j]);
-                    f[j] = __ffma2_rn(o, fu[j], *reinterpret_cast<const float2*>(&ys[row][col + 2 * j]));
+                    f[j] = __ffma2_rn(o, fu[j], *reinterpret_cast<const float2*>(&ys[Value::at(row, col + 2 * j)]));
                     if (z != nullptr) f[j] = __fmul2_rn(f[j], silu2(fz[j]));
                 }
                 store8(y + (t0 + row) * C + col, f, left, vec_y);
@@ -426,8 +461,10 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
     using S = FwdShape<L>;
     constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = kChannels / 8, NP = S::NP, W = 32 / L;
     constexpr int kEach = (kTile * kColumns + kThreads - 1) / kThreads;
-    __shared__ __align__(16) float2 step[kTile][kChannels];    // delta, g
-    __shared__ __align__(16) float cs[1][kTile][NP];
+    using Step = StepAt<kChannels>;
+    using Row = RowAt<NP>;
+    __shared__ __align__(16) float2 step[Step::kSize];    // delta, g
+    __shared__ __align__(16) float cs[Row::kSize];
     __shared__ __align__(16) float bias[kChannels];
     pdl_trigger();
     pdl_wait();
@@ -486,7 +523,7 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
             for (int j = 0; j < 4; ++j) {
                 const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < r.end);
                 if (z != nullptr) fy[j] = __fmul2_rn(fy[j], silu2(fz[j]));
-                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fy[j].x, d.y, fy[j].y);
+                *reinterpret_cast<float4*>(&step[Step::at(row, col + 2 * j)]) = make_float4(d.x, fy[j].x, d.y, fy[j].y);
             }
         }
         rc.template spread<1>(cs);
@@ -495,8 +532,8 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 #pragma unroll 4
         for (int t = kTile - 1; t >= 0; --t) {
             Four fc;
-            fc.load(&cs[0][t][n0]);
-            const float4 s = *reinterpret_cast<const float4*>(&step[t][ch]);
+            fc.load(&cs[Row::at(t / kStep, t % kStep, n0)]);
+            const float4 s = *reinterpret_cast<const float4*>(&step[Step::at(t, ch)]);
             const float delta[2] = {s.x, s.z}, g[2] = {s.y, s.w};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -537,10 +574,8 @@ struct BwdShape {
     static constexpr int kColumns = kChannels / 8, kEach = (kTile * kColumns + kThreads - 1) / kThreads;
     // dB and dC of kStep positions take the place of the states in front of them where they fit
     static constexpr bool kShared = kStep * 2 * NP <= 8 * 32;
-    static constexpr size_t kFloats = kTile * kChannels * 3 + 2 * kOrders * kTile * NP + kTile / kStep * 8 * kThreads +
-                                      (kShared ? 0 : kWarps * kTile * 2 * NP) + 2 * kChannels + 8 * kThreads;
-    // and a thread's vectors of dt, z and dy while it walks
-    static constexpr size_t bytes(size_t elem) { return kFloats * sizeof(float) + kEach * 3 * kThreads * 8 * elem; }
+    static constexpr size_t kFloats = 2 * StepAt<kChannels>::kSize + ValueAt<kChannels>::kSize + 2 * kOrders * RowAt<NP>::kSize + kTile / kStep * 8 * kThreads +
+                                      (kShared ? 0 : kWarps * kTile * 2 * NP) + 2 * kChannels + 8 * kThreads + kEach * 16 * kThreads;
     // place of dB (0) or dC (1) of position t and state n among `front` or the sums
     static __device__ __forceinline__ int place(int warp, int t, int which, int n) {
         if constexpr (kShared) {
@@ -557,16 +592,20 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
     constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = S::kColumns, NP = S::NP, W = S::kLanes;
     constexpr int kOrders = S::kOrders, kEach = S::kEach;
     extern __shared__ __align__(16) float smem[];
-    float2 (*step)[kChannels] = reinterpret_cast<float2 (*)[kChannels]>(smem);      // delta, u; then du, ddelta
-    float (*gs)[kChannels] = reinterpret_cast<float (*)[kChannels]>(step + kTile);       // g; then the sum over the states and D u
-    float (*bs)[kTile][NP] = reinterpret_cast<float (*)[kTile][NP]>(gs + kTile);
-    float (*cs)[kTile][NP] = bs + kOrders;
-    float* front = reinterpret_cast<float*>(cs + kOrders);
+    using Step = StepAt<kChannels>;
+    using Value = ValueAt<kChannels>;
+    using Row = RowAt<NP>;
+    float2* const step = reinterpret_cast<float2*>(smem);      // delta, u; then du, ddelta
+    float* const bs = smem + 2 * Step::kSize;                  // in each order
+    float* const cs = bs + kOrders * Row::kSize;
+    float* front = cs + kOrders * Row::kSize;
     float* sums = S::kShared ? front : front + kTile / kStep * 8 * kThreads;       // dB and dC of every warp
     float* bias = front + kTile / kStep * 8 * kThreads + (S::kShared ? 0 : S::kWarps * kTile * 2 * NP);
     float* skip = bias + kChannels;
     float4* sum_bias = reinterpret_cast<float4*>(skip + kChannels) + threadIdx.x;         // (two of them, kThreads apart)
-    Vec8<T>* stash = reinterpret_cast<Vec8<T>*>(skip + kChannels + 8 * kThreads) + threadIdx.x;      // dt, z, dy
+    // of this thread's vectors the derivatives of delta by dt, and dy silu'(z)
+    float4* stash = reinterpret_cast<float4*>(skip + kChannels + 8 * kThreads) + threadIdx.x;
+    float* const gs = skip + kChannels + 8 * kThreads + kEach * 16 * kThreads;   // g; then the sum over the states and D u
     front += threadIdx.x;
     pdl_trigger();
     pdl_wait();
@@ -577,9 +616,31 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
     const int C = p.C, N = p.N;
     const bool even = (C / p.G) % 8 == 0;
     const long long dense = r.some ? dense_row(p.seqs, r) : 0;
-    const T *u = view_at<T>(p.u, p.seqs, r) + k.c, *dt = view_at<T>(p.dt, p.seqs, r) + k.c, *dy = view_at<T>(p.dy, p.seqs, r) + k.c;
-    const T* z = p.z.p == nullptr ? nullptr : view_at<T>(p.z, p.seqs, r) + k.c;
-    const T *b = view_at<T>(p.b, p.seqs, r) + k.g * N, *c = view_at<T>(p.c, p.seqs, r) + k.g * N;
+    // (where the tensors begin: in shared memory, since registers are what the walk has too few of, and spilled ones come
+    // back from L2, which the shared memory leaves no L1 in front of)
+    __shared__ struct {
+        const T *u, *dt, *z, *dy, *b, *c;
+        T *du, *ddt, *dz;
+        float* rows;
+        const float* saved;
+    } at_;
+    const bool gated = p.z.p != nullptr;
+    if (threadIdx.x == 0) {
+        at_.u = view_at<T>(p.u, p.seqs, r) + k.c;
+        at_.dt = view_at<T>(p.dt, p.seqs, r) + k.c;
+        at_.z = gated ? view_at<T>(p.z, p.seqs, r) + k.c : nullptr;
+        at_.dy = view_at<T>(p.dy, p.seqs, r) + k.c;
+        at_.b = view_at<T>(p.b, p.seqs, r) + k.g * N;
+        at_.c = view_at<T>(p.c, p.seqs, r) + k.g * N;
+        const long long o = dense * C + k.c;
+        at_.du = static_cast<T*>(p.du) + o;
+        at_.ddt = static_cast<T*>(p.ddt) + o;
+        at_.dz = static_cast<T*>(p.dz) + o;
+        at_.rows = part_bc + (block * seq_rows_device(p.seqs) + dense) * 2 * N;
+        at_.saved = p.saved + (saved_slot(p.seqs, r, 0) * C + k.c) * N;
+    }
+    __syncthreads();
+    const volatile auto& at = at_;
     for (int i = threadIdx.x; i < kChannels; i += kThreads) {
         bias[i] = i < k.width && p.dt_bias != nullptr ? p.dt_bias[k.c + i] : 0.f;
         skip[i] = i < k.width && p.D != nullptr ? p.D[k.c + i] : 0.f;
@@ -594,56 +655,57 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const bool serves = ch[j] < k.width;
-        const long long at = static_cast<long long>(k.c + ch[j]) * N, wide = static_cast<long long>(C) * N;
-        a2[j].get(serves ? p.A + at : nullptr, n0, perm, N);
+        const long long mine = static_cast<long long>(k.c + ch[j]) * N, wide = static_cast<long long>(C) * N;
+        a2[j].get(serves ? p.A + mine : nullptr, n0, perm, N);
         a2[j].scale(kLog2e);
         da[j].clear();
-        if (carries != nullptr) carry[j].get(serves && r.some ? carries + slot * wide + at : nullptr, n0, perm, N);
-        else carry[j].get(serves && r.some && p.dfinal != nullptr ? p.dfinal + r.s * wide + at : nullptr, n0, perm, N);
+        if (carries != nullptr) carry[j].get(serves && r.some ? carries + slot * wide + mine : nullptr, n0, perm, N);
+        else carry[j].get(serves && r.some && p.dfinal != nullptr ? p.dfinal + r.s * wide + mine : nullptr, n0, perm, N);
     }
     float sum_d = 0.f;
     sum_bias[0] = sum_bias[kThreads] = make_float4(0.f, 0.f, 0.f, 0.f);
     const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
     const int col = threadIdx.x % kColumns * 8, left = k.width - col;            // (kColumns divides the threads)
     const bool eight = even && left >= 8, four = N % 4 == 0 && reinterpret_cast<uintptr_t>(p.saved) % 16 == 0;
-    const bool vec_u = p.u.vec && eight, vec_dt = p.dt.vec && eight, vec_z = p.z.vec && eight, vec_dy = p.dy.vec && eight;
     const auto aligned = [&](const void* t) { return eight && reinterpret_cast<uintptr_t>(t) % (8 * sizeof(T)) == 0; };
-    const bool vec_du = aligned(p.du), vec_ddt = aligned(p.ddt), vec_dz = aligned(p.dz);
+    // whether this thread's vectors take one access each: u, dt, z, dy, du, ddt, dz
+    const unsigned whole = (p.u.vec && eight ? 1u : 0u) | (p.dt.vec && eight ? 2u : 0u) | (p.z.vec && eight ? 4u : 0u) |
+                           (p.dy.vec && eight ? 8u : 0u) | (aligned(p.du) ? 16u : 0u) | (aligned(p.ddt) ? 32u : 0u) |
+                           (aligned(p.dz) ? 64u : 0u);
 
-    const long long tiles = r.some ? (r.end - r.first + kTile - 1) / kTile : 0;
-    for (long long tile = tiles - 1; tile >= 0; --tile) {
-        const long long t0 = r.first + tile * kTile;
+    // (positions are 32-bit numbers)
+    const int begin = static_cast<int>(r.first), end = r.some ? static_cast<int>(r.end) : begin;
+    for (int t0 = begin + (end - begin - 1) / kTile * kTile; t0 >= begin && t0 < end; t0 -= kTile) {
         Vec8<T> ru[kEach], rdt[kEach], rz[kEach], rdy[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int row = row_of(i);
             ru[i].zero(), rdt[i].zero(), rz[i].zero(), rdy[i].zero();
-            if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
-            load8(ru[i], u + (t0 + row) * p.u.row + col, left, vec_u);
-            load8(rdt[i], dt + (t0 + row) * p.dt.row + col, left, vec_dt);
-            load8(rdy[i], dy + (t0 + row) * p.dy.row + col, left, vec_dy);
-            if (z != nullptr) load8(rz[i], z + (t0 + row) * p.z.row + col, left, vec_z);
-        }
-        StateRows<T, NP, kThreads> rb, rc;
-        rb.fetch(b, p.b, t0, r.end, N);
-        rc.fetch(c, p.c, t0, r.end, N);
-        if (tile > 0) {
-            // (the tile in front of this one: a whole one)
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int row = row_of(i);
-                if (row >= kTile || left <= 0) continue;
-                const long long at = t0 - kTile + row;
-                prefetch_l2(u + at * p.u.row + col);
-                prefetch_l2(dt + at * p.dt.row + col);
-                prefetch_l2(dy + at * p.dy.row + col);
-                if (z != nullptr) prefetch_l2(z + at * p.z.row + col);
+            if (row >= kTile || left <= 0) continue;
+            const long long t = t0 + row;
+            if (t < end) {
+                load8(ru[i], at.u + t * p.u.row + col, left, (whole & 1) != 0);
+                load8(rdt[i], at.dt + t * p.dt.row + col, left, (whole & 2) != 0);
+                load8(rdy[i], at.dy + t * p.dy.row + col, left, (whole & 8) != 0);
+                if (gated) load8(rz[i], at.z + t * p.z.row + col, left, (whole & 4) != 0);
+            }
+            if (t0 > begin) {         // (the tile in front of this one: a whole one)
+                prefetch_l2(at.u + (t - kTile) * p.u.row + col);
+                prefetch_l2(at.dt + (t - kTile) * p.dt.row + col);
+                prefetch_l2(at.dy + (t - kTile) * p.dy.row + col);
+                if (gated) prefetch_l2(at.z + (t - kTile) * p.z.row + col);
             }
         }
+        StateRows<T, NP, kThreads> rb, rc;
+        rb.fetch(at.b, p.b, t0, end, N);
+        rc.fetch(at.c, p.c, t0, end, N);
         Four h[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            h[j].get4(ch[j] < k.width ? p.saved + (saved_slot(p.seqs, r, t0 / kScanTile) * C + k.c + ch[j]) * N : nullptr, n0, perm, N, four);
+        for (int j = 0; j < 2; ++j) {
+            const float* from = at.saved + (static_cast<long long>(t0 / kScanTile) * C + ch[j]) * N;
+            h[j].get4(ch[j] < k.width ? from : nullptr, n0, perm, N, four);
+            if (t0 > begin && ch[j] < k.width && n0 < N) prefetch_l2(from - static_cast<long long>(C) * N + n0);
+        }
         __syncthreads();            // the last tile's sums have been read
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
@@ -656,12 +718,22 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
             rdy[i].widen(fy);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < r.end);
-                if (z != nullptr) fy[j] = __fmul2_rn(fy[j], silu2(fz[j]));
-                *reinterpret_cast<float4*>(&step[row][col + 2 * j]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
-                *reinterpret_cast<float2*>(&gs[row][col + 2 * j]) = fy[j];
+                float2 slope;
+                const float2 d = delta_of(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]), p.softplus, t0 + row < end, &slope);
+                fd[j] = slope;
+                if (gated) {
+                    const float2 s = sigmoid2(fz[j]), zs = __fmul2_rn(fz[j], s);
+                    fz[j] = __fmul2_rn(fy[j], __fadd2_rn(s, __ffma2_rn(zs, make_float2(-s.x, -s.y), zs)));
+                    fy[j] = __fmul2_rn(fy[j], zs);
+                }
+                *reinterpret_cast<float4*>(&step[Step::at(row, col + 2 * j)]) = make_float4(d.x, fu[j].x, d.y, fu[j].y);
+                *reinterpret_cast<float2*>(&gs[Value::at(row, col + 2 * j)]) = fy[j];
             }
-            stash[(i * 3 + 0) * kThreads] = rdt[i], stash[(i * 3 + 1) * kThreads] = rz[i], stash[(i * 3 + 2) * kThreads] = rdy[i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                stash[(4 * i + j) * kThreads] = make_float4(fd[2 * j].x, fd[2 * j].y, fd[2 * j + 1].x, fd[2 * j + 1].y);
+                stash[(4 * i + 2 + j) * kThreads] = make_float4(fz[2 * j].x, fz[2 * j].y, fz[2 * j + 1].x, fz[2 * j + 1].y);
+            }
         }
         rb.template spread<kOrders>(bs);
         rc.template spread<kOrders>(cs);
@@ -678,10 +750,10 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
             for (int q = 0; q < kStep; ++q) {
                 const int t = w * kStep + q;
                 Four fb;
-                fb.load(&bs[order][t][n0]);
+                fb.load(bs + (order * Row::kSize + Row::at(w, q, n0)));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float2 s = step[t][ch[j]];
+                    const float2 s = step[Step::at(t, ch[j])];
                     const float in = s.x * s.y;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -702,10 +774,10 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
             for (int q = 0; q < kStep; ++q) {
                 const int t = w * kStep + q;
                 Four fb;
-                fb.load(&bs[order][t][n0]);
+                fb.load(bs + (order * Row::kSize + Row::at(w, q, n0)));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float2 s = step[t][ch[j]];
+                    const float2 s = step[Step::at(t, ch[j])];
                     const float in = s.x * s.y;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -715,19 +787,19 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
                     }
                 }
             }
-            float into[kStep], decays[kStep], ys[kStep];
+            float into[Parts<L>::kHeld], decays[Parts<L>::kHeld], ys[Parts<L>::kHeld], last[3];
 #pragma unroll
             for (int q = kStep - 1; q >= 0; --q) {
                 const int t = w * kStep + q;
                 Four fb, fc;
-                fb.load(&bs[order][t][n0]);
-                fc.load(&cs[order][t][n0]);
+                fb.load(bs + (order * Row::kSize + Row::at(w, q, n0)));
+                fc.load(cs + (order * Row::kSize + Row::at(w, q, n0)));
                 float2 vb[2] = {both(0.f), both(0.f)}, vc[2] = {both(0.f), both(0.f)};
                 float s1[2], s2[2], s3[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float2 s = step[t][ch[j]];
-                    const float g = gs[t][ch[j]], in = s.x * s.y;
+                    const float2 s = step[Step::at(t, ch[j])];
+                    const float g = gs[Value::at(t, ch[j])], in = s.x * s.y;
                     float2 x1 = both(0.f), x2 = both(0.f), x3 = both(0.f);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -745,9 +817,16 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
                     s1[j] = x1.x + x1.y, s2[j] = x2.x + x2.y, s3[j] = x3.x + x3.y;
                 }
                 // over the states, first step: the partner's other channel is this lane's first
-                into[q] = s1[0] + from_lane(s1[1], 1);
-                decays[q] = s2[0] + from_lane(s2[1], 1);
-                ys[q] = s3[0] + from_lane(s3[1], 1);
+                const float x1 = s1[0] + from_lane(s1[1], 1), x2 = s2[0] + from_lane(s2[1], 1), x3 = s3[0] + from_lane(s3[1], 1);
+                if constexpr (L < 4) {
+                    into[q] = x1, decays[q] = x2, ys[q] = x3;
+                } else if (q % 2 != 0) {
+                    last[0] = x1, last[1] = x2, last[2] = x3;
+                } else {
+                    into[q / 2] = Parts<L>::either(x1, last[0], 2, sub);
+                    decays[q / 2] = Parts<L>::either(x2, last[1], 2, sub);
+                    ys[q / 2] = Parts<L>::either(x3, last[2], 2, sub);
+                }
                 // over the warp's channels
                 if constexpr (W >= 2) {
                     vb[0] = make_float2(vb[0].x + from_lane(vb[1].x, W / 2 * L), vb[0].y + from_lane(vb[1].y, W / 2 * L));
@@ -757,42 +836,42 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
                     vb[0].x += from_lane(vb[0].y, W / 4 * L);
                     vc[0].x += from_lane(vc[0].y, W / 4 * L);
                 }
-                const auto keep = [&](int which, int n, float v) { sums[S::place(warp, t, which, n0 + n)] = v; };
+                const auto give = [&](int which, int n, float v) { sums[S::place(warp, t, which, n0 + n)] = v; };
                 if constexpr (W >= 8) {
                     const bool which = (cl & (W / 8)) != 0;
                     float v = (which ? vc[0].x : vb[0].x) + from_lane(which ? vb[0].x : vc[0].x, W / 8 * L);
                     if constexpr (W >= 16) v += from_lane(v, W / 16 * L);
-                    if (W < 16 || (cl & (W / 16)) == 0) keep(which, perm, v);
+                    if (W < 16 || (cl & (W / 16)) == 0) give(which, perm, v);
                 } else {
-                    keep(0, perm, vb[0].x), keep(1, perm, vc[0].x);
-                    if constexpr (W <= 2) keep(0, 1 ^ perm, vb[0].y), keep(1, 1 ^ perm, vc[0].y);
+                    give(0, perm, vb[0].x), give(1, perm, vc[0].x);
+                    if constexpr (W <= 2) give(0, 1 ^ perm, vb[0].y), give(1, 1 ^ perm, vc[0].y);
                     if constexpr (W == 1) {
-                        keep(0, 2, vb[1].x), keep(0, 3, vb[1].y);
-                        keep(1, 2, vc[1].x), keep(1, 3, vc[1].y);
+                        give(0, 2, vb[1].x), give(0, 3, vb[1].y);
+                        give(1, 2, vc[1].x), give(1, 3, vc[1].y);
                     }
                 }
             }
             // over the states
-            Parts<L>::sum(into, sub);
-            Parts<L>::sum(decays, sub);
-            Parts<L>::sum(ys, sub);
+            Parts<L>::finish(into, sub);
+            Parts<L>::finish(decays, sub);
+            Parts<L>::finish(ys, sub);
             __syncwarp();       // all lanes have read these positions
             if (Parts<L>::owner(sub)) {
 #pragma unroll
                 for (int q = 0; q < Parts<L>::kMine; ++q) {
-                    const int t = w * kStep + Parts<L>::first_of(sub) + q;
-                    const float2 s = step[t][ch[0]];
-                    const float g = gs[t][ch[0]];
+                    const int t = w * kStep + Parts<L>::position(q, sub);
+                    const float2 s = step[Step::at(t, ch[0])];
+                    const float g = gs[Value::at(t, ch[0])];
                     sum_d = fmaf(g, s.y, sum_d);
-                    step[t][ch[0]] = make_float2(fmaf(into[q], s.x, skip[ch[0]] * g), fmaf(into[q], s.y, decays[q] * 0.6931471805599453f));
-                    gs[t][ch[0]] = fmaf(skip[ch[0]], s.y, ys[q]);
+                    step[Step::at(t, ch[0])] = make_float2(fmaf(into[q], s.x, skip[ch[0]] * g), fmaf(into[q], s.y, decays[q] * 0.6931471805599453f));
+                    gs[Value::at(t, ch[0])] = fmaf(skip[ch[0]], s.y, ys[q]);
                 }
             }
         }
         __syncthreads();
         // dB and dC of the CTA's channels
-        float* rows = part_bc + (block * seq_rows_device(p.seqs) + dense + t0) * 2 * N;
-        const int here = static_cast<int>(r.end - t0 < kTile ? r.end - t0 : kTile);
+        float* rows = at.rows + static_cast<long long>(t0) * 2 * N;
+        const int here = min(end - t0, kTile);
 #pragma unroll
         for (int i = 0; i < kTile * 2 * NP / kThreads; ++i) {
             const int j = (threadIdx.x + i * kThreads) % (2 * NP), t = (threadIdx.x + i * kThreads) / (2 * NP), n = j % NP;
@@ -805,20 +884,16 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int row = row_of(i);
-            if (row >= kTile || t0 + row >= r.end || col >= k.width) continue;
-            float2 fd[4], fz[4], fy[4], du[4], ddt[4], dz[4];
-            stash[(i * 3 + 0) * kThreads].widen(fd);
-            stash[(i * 3 + 1) * kThreads].widen(fz);
-            stash[(i * 3 + 2) * kThreads].widen(fy);
+            if (row >= kTile || t0 + row >= end || col >= k.width) continue;
+            float2 du[4], ddt[4], dz[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 s = *reinterpret_cast<const float4*>(&step[row][col + 2 * j]);
+                const float4 s = *reinterpret_cast<const float4*>(&step[Step::at(row, col + 2 * j)]);
+                const float4 slope = stash[(4 * i + j / 2) * kThreads], z = stash[(4 * i + 2 + j / 2) * kThreads];
                 du[j] = make_float2(s.x, s.z);
-                ddt[j] = make_float2(s.y, s.w);
-                if (p.softplus)
-                    ddt[j] = __fmul2_rn(ddt[j], sigmoid2(__fadd2_rn(fd[j], *reinterpret_cast<const float2*>(&bias[col + 2 * j]))));
-                if (z != nullptr)
-                    dz[j] = __fmul2_rn(__fmul2_rn(fy[j], *reinterpret_cast<const float2*>(&gs[row][col + 2 * j])), silu_slope2(fz[j]));
+                ddt[j] = __fmul2_rn(make_float2(s.y, s.w), j % 2 ? make_float2(slope.z, slope.w) : make_float2(slope.x, slope.y));
+                dz[j] = __fmul2_rn(j % 2 ? make_float2(z.z, z.w) : make_float2(z.x, z.y),
+                                   *reinterpret_cast<const float2*>(&gs[Value::at(row, col + 2 * j)]));
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -826,10 +901,10 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
                 s.x += ddt[2 * j].x, s.y += ddt[2 * j].y, s.z += ddt[2 * j + 1].x, s.w += ddt[2 * j + 1].y;
                 sum_bias[j * kThreads] = s;
             }
-            const long long o = (dense + t0 + row) * C + k.c + col;
-            store8(static_cast<T*>(p.du) + o, du, left, vec_du);
-            store8(static_cast<T*>(p.ddt) + o, ddt, left, vec_ddt);
-            if (z != nullptr) store8(static_cast<T*>(p.dz) + o, dz, left, vec_dz);
+            const long long o = static_cast<long long>(t0 + row) * C + col;
+            store8(at.du + o, du, left, (whole & 16) != 0);
+            store8(at.ddt + o, ddt, left, (whole & 32) != 0);
+            if (gated) store8(at.dz + o, dz, left, (whole & 64) != 0);
         }
     }
     // this chunk's rows of parameter gradients: C x N of dA, C of dD, C of the bias's
@@ -968,7 +1043,7 @@ cudaError_t adjoint_t(const Scan& p, float* ends, float* sums) {
 template <typename T, int L>
 cudaError_t bwd_t(const Scan& p) {
     using S = BwdShape<L>;
-    constexpr size_t smem = S::bytes(sizeof(T));
+    constexpr size_t smem = S::kFloats * sizeof(float);
     const int blocks = channel_blocks(p, S::kChannels);
     const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks, rows = seq_rows(p.seqs), C = p.C;
     const long long sums = (rows * p.G * 2 * p.N + 255) / 256;

@@ -10,7 +10,7 @@ using namespace dwc;
 namespace {
 
 constexpr long long kMaxElems = 1LL << 40;
-constexpr long long kMaxPositions = 0x7fffffffLL;
+constexpr long long kMaxPositions = (1LL << 31) - 64;      // (kernels count to the end of a tile behind the last one)
 constexpr int kMaxChannels = 1 << 20;
 constexpr int kMaxTaps = 16;
 

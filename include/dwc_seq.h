@@ -70,7 +70,7 @@ typedef struct {
  * its state in front), the state of a later call; or NULL.
  * DWC_ERR_INVALID_ARG: null x, w or y with positions to work on, negative sizes or strides, C < 1,
  * K < 1, unknown types or activation.  DWC_ERR_UNSUPPORTED: K above 16, C above 2^20, more than
- * 2^31 - 1 positions, more than 2^40 elements.  DWC_ERR_ALIGNMENT: a pointer not aligned to its
+ * 2^31 - 64 positions, more than 2^40 elements.  DWC_ERR_ALIGNMENT: a pointer not aligned to its
  * element.  No sequences or no positions: DWC_OK (the final states are written). */
 dwc_status_t dwc_causal_conv_fwd(const dwc_causal_conv_t* conv, void* y, void* final_state, dwc_stream_t stream);
 
