@@ -42,7 +42,7 @@ struct Input {
         return {v.data_ptr(), stride(0), stride(1)};
     }
     dwc_rows_t own(const char* what) const {
-        TORCH_CHECK_VALUE(C == 1 || t.stride(-1) == 1, what, ": channels must be adjacent (stride ", t.stride(-1), ")");
+        TORCH_CHECK_VALUE(C == 1 || t.stride(-1) == 1 || t.numel() == 0, what, ": channels must be adjacent (stride ", t.stride(-1), ")");
         return rows(t);
     }
     // an input of this tensor's shape and type
@@ -52,7 +52,7 @@ struct Input {
         TORCH_CHECK_VALUE(v.sizes() == t.sizes() && v.device() == t.device(), what, " must be a ", t.sizes(), " tensor on ",
                           t.device(), " (got ", v.sizes(), " on ", v.device(), ")");
         TORCH_CHECK_VALUE(v.scalar_type() == t.scalar_type(), what, " must be ", t.scalar_type(), " (got ", v.scalar_type(), ")");
-        TORCH_CHECK_VALUE(C == 1 || v.stride(-1) == 1, what, ": channels must be adjacent (stride ", v.stride(-1), ")");
+        TORCH_CHECK_VALUE(C == 1 || v.stride(-1) == 1 || v.numel() == 0, what, ": channels must be adjacent (stride ", v.stride(-1), ")");
         return rows(v);
     }
     // B or C of a scan: the leading axes, then [G, N] or [N]
@@ -64,7 +64,7 @@ struct Input {
                           what, " must be ", leading(), " x groups x ", N, " of ", t.scalar_type(), " on ", t.device(), " (got ",
                           v.sizes(), " ", v.scalar_type(), " on ", v.device(), ")");
         G = grouped ? v.size(-2) : 1;
-        TORCH_CHECK_VALUE((N == 1 || v.stride(-1) == 1) && (G <= 1 || v.stride(-2) == N), what,
+        TORCH_CHECK_VALUE(v.numel() == 0 || ((N == 1 || v.stride(-1) == 1) && (G <= 1 || v.stride(-2) == N)), what,
                           ": the groups' states must be adjacent (strides ", v.strides(), ")");
         return rows(v);
     }
