@@ -167,6 +167,9 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_fw
     copy_wait<0>();
 }
 
+template <typename TB>
+constexpr bool params_in_registers(int NV) { return NV == 1 || sizeof(TB) == 4; }
+
 // With zhat = z rstd_pre, xhat = x rstd_post, a = dy gamma_pre, w = scale gamma_post:
 //     g = dz + rstd_pre (a - zhat mean(a zhat)),  t = act g,  b = w t
 //     dx = rstd_post (b - xhat mean(b xhat)),  dres = alpha g,  dgate = w g xhat act'
@@ -217,17 +220,46 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
 #pragma unroll
     for (int i = 0; i < S; ++i) fetch(i, me.group + static_cast<long long>(i) * me.groups);
     const Edges<NV, kAligned> edges(at, C);
-    float2 w[NV][4], pre_w[NV][4], sum_t[NV][4], sum_pre[NV][4];
-    load_params(w, p.gamma_post, p.param_type, C, at, 1.f);
-    load_params(pre_w, p.scale, p.param_type, C, at, 1.f);
+    // scale * gamma_post and gamma_pre of a vector: in registers; where a thread has two vectors of 16-bit branches in its own
+    // places in shared memory (registers would be spilled: bf16 4096 x 8192 151 us, 124 so; beside fp32 branches of 8192
+    // channels there is no room)
+    constexpr bool kKept = params_in_registers<TB>(NV);
+    float2 held_w[NV][4], held_pre[NV][4], sum_t[NV][4], sum_pre[NV][4];
+    float4* const places = reinterpret_cast<float4*>(slots + S * row_granules) + threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        const Columns one{at.of(k), at.end, 1, 0};
+        float2 f[1][4], g[1][4];
+        load_params(f, p.gamma_post, p.param_type, C, one, 1.f);
+        load_params(g, p.scale, p.param_type, C, one, 1.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            w[k][j] = __fmul2_rn(w[k][j], pre_w[k][j]);
+            held_w[k][j] = __fmul2_rn(f[0][j], g[0][j]);
             sum_t[k][j] = sum_pre[k][j] = both(0.f);
         }
-    load_params(pre_w, p.gamma_pre, p.param_type, C, at, 1.f);
+        load_params(f, p.gamma_pre, p.param_type, C, one, 1.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) held_pre[k][j] = f[0][j];
+        if constexpr (!kKept) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                places[(k * 4 + q) * threads] = make_float4(held_w[k][2 * q].x, held_w[k][2 * q].y, held_w[k][2 * q + 1].x, held_w[k][2 * q + 1].y);
+                places[(k * 4 + 2 + q) * threads] = make_float4(held_pre[k][2 * q].x, held_pre[k][2 * q].y, held_pre[k][2 * q + 1].x, held_pre[k][2 * q + 1].y);
+            }
+        }
+    }
+    const auto params_of = [&](float2 (&f)[4], int k, int which) {
+        if constexpr (kKept) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = which == 0 ? held_w[k][j] : held_pre[k][j];
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 v = places[(k * 4 + 2 * which + q) * threads];
+                f[2 * q] = make_float2(v.x, v.y), f[2 * q + 1] = make_float2(v.z, v.w);
+            }
+        }
+    };
     GroupSum<G> sum{exchange, me.local, me.width, 0};
     int stage = 0;
     const int in_warp = G > 0 ? me.local % (32 / GW) : 0;
@@ -249,6 +281,8 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
             const int limit = !live || at.of(k) >= at.end ? 0 : C;
             read_slot<TB>(t[k], row + k * kBranch * threads + mine_b);
             read_slot<TS>(zhat[k], row + z_at + k * kStream * threads + mine_s);
+            float2 pre_w[4];
+            params_of(pre_w, k, 1);
             if (!live || !edges.full[k]) {
                 mask8(t[k], at.of(k), limit);
                 mask8(zhat[k], at.of(k), limit);
@@ -257,7 +291,7 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
             for (int j = 0; j < 4; ++j) {
                 zhat[k][j] = __fmul2_rn(zhat[k][j], both(pre));
                 sum_pre[k][j] = __ffma2_rn(t[k][j], zhat[k][j], sum_pre[k][j]);
-                t[k][j] = __fmul2_rn(t[k][j], pre_w[k][j]);          // a
+                t[k][j] = __fmul2_rn(t[k][j], pre_w[j]);          // a
                 q = __ffma2_rn(t[k][j], zhat[k][j], q);
             }
         }
@@ -266,7 +300,8 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int limit = !live || at.of(k) >= at.end ? 0 : C;
-            float2 x[4], v[4];
+            float2 x[4], v[4], w[4];
+            params_of(w, k, 0);
             read_slot<TB>(x, row + x_at + k * kBranch * threads + mine_b);
             if (!live || !edges.full[k]) mask8(x, at.of(k), limit);
 #pragma unroll
@@ -294,7 +329,7 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
                     float2 act, slope;
                     act.x = gate_of(v[j].x, p.act, &slope.x);
                     act.y = gate_of(v[j].y, p.act, &slope.y);
-                    o[j] = __fmul2_rn(__fmul2_rn(__fmul2_rn(w[k][j], t[k][j]), x[j]), slope);
+                    o[j] = __fmul2_rn(__fmul2_rn(__fmul2_rn(w[j], t[k][j]), x[j]), slope);
                     t[k][j] = __fmul2_rn(t[k][j], act);
                 }
                 if (live && at.of(k) < at.end && p.dgate != nullptr)
@@ -303,7 +338,7 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum_t[k][j] = __ffma2_rn(t[k][j], x[j], sum_t[k][j]);
-                t[k][j] = __fmul2_rn(t[k][j], w[k][j]);             // b
+                t[k][j] = __fmul2_rn(t[k][j], w[j]);             // b
                 q = __ffma2_rn(t[k][j], x[j], q);
                 zhat[k][j] = x[j];
             }
@@ -350,11 +385,12 @@ struct Plan {
     size_t smem;
 };
 
+// `slot`: bytes of a vector's tensors in a stage, `more`: besides the stages.
 // One CTA to an SM (lane groups: as many as fit), groups of the fewest threads that hold a row; as many
 // groups to a CTA as serve its share of the rows in the fewest rounds.  Where rows are shifted the
 // number of groups is a multiple of 8, so that a group's rows all have one shift.
 template <class K>
-cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int NV, int S, size_t slot, int vectors, int parts, Plan& l) {
+cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int NV, int S, size_t slot, size_t more, int vectors, int parts, Plan& l) {
     const int sms = device_info().sm_count;
     if (G > 0) {
         l.width = G;
@@ -367,7 +403,7 @@ cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int
         l.per_cta = static_cast<int>((share + rounds - 1) / rounds);
     }
     l.threads = l.width * l.per_cta;
-    l.smem = static_cast<size_t>(S) * NV * l.threads * slot;
+    l.smem = static_cast<size_t>(l.threads) * NV * (S * slot + more);
     if (parts > 0 && l.per_cta > 1) l.smem = std::max(l.smem, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
     if (l.smem > kDynamicSmem) return cudaErrorNotSupported;
     const cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
@@ -389,7 +425,7 @@ cudaError_t fwd_launch(const BlockNorm& p, int vectors) {
     static KernelFacts facts;
     Plan l;
     const size_t slot = 8 * (sizeof(TS) + sizeof(TB) * (p.gate != nullptr ? 2 : 1));
-    const cudaError_t err = plan_rows(kern, facts, p, G, NV, S, slot, vectors, 0, l);
+    const cudaError_t err = plan_rows(kern, facts, p, G, NV, S, slot, 0, vectors, 0, l);
     if (err != cudaSuccess) return err;
     return launch_pdl(kern, dim3(static_cast<unsigned>(l.grid)), dim3(static_cast<unsigned>(l.threads)), l.smem, p.stream, p, l.width,
                       vectors);
@@ -401,7 +437,8 @@ cudaError_t bwd_launch(const BlockNorm& p, int vectors) {
     static KernelFacts facts;
     Plan l;
     const size_t slot = 8 * (sizeof(TB) * (p.gate != nullptr ? 3 : 2) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
-    cudaError_t err = plan_rows(kern, facts, p, G, NV, S, slot, vectors, p.partial != nullptr ? block_norm_partials(p.rows, p.C) : 0, l);
+    cudaError_t err = plan_rows(kern, facts, p, G, NV, S, slot, params_in_registers<TB>(NV) ? 0 : 64, vectors,
+                                p.partial != nullptr ? block_norm_partials(p.rows, p.C) : 0, l);
     if (err != cudaSuccess) return err;
     err = launch_pdl(kern, dim3(static_cast<unsigned>(l.grid)), dim3(static_cast<unsigned>(l.threads)), l.smem, p.stream, p, l.width,
                      vectors);
