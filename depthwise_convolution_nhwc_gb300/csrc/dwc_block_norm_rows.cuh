@@ -36,12 +36,47 @@ struct GroupSum {
         if (warps == 1) return v;
         if (lane == 0) e[parity][which][warp] = v;
         group_barrier(1 + local, width);
+        if (warps <= 4) {           // (fewer steps than exchanges)
+            v = 0.f;
+            for (int w = 0; w < warps; ++w) v += e[parity][which][local * warps + w];
+            return v;
+        }
         v = lane < warps ? e[parity][which][local * warps + lane] : 0.f;
 #pragma unroll
         for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);    // (at most 16 warps)
         return __shfl_sync(0xffffffffu, v, 0);
     }
 };
+
+// Parameters of a thread's vectors: one access each where the parameters are aligned and the vectors are not shifted.
+template <bool kAligned, int NV>
+__device__ __forceinline__ void params(float2 (&f)[NV][4], const void* p, int type, int C, const Columns& at) {
+    const size_t align = type == kF32 ? 32 : 16;
+    if (!kAligned || p == nullptr || reinterpret_cast<uintptr_t>(p) % align != 0) {
+        load_params(f, p, type, C, at, 1.f);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = at.of(k);
+        if (c >= at.end) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[k][j] = both(0.f);
+        } else if (type == kF32) {
+            Vec8<float> v;
+            v.load(static_cast<const float*>(p) + c);
+            v.widen(f[k]);
+        } else if (type == kBF16) {
+            Vec8<__nv_bfloat16> v;
+            v.load(static_cast<const __nv_bfloat16*>(p) + c);
+            v.widen(f[k]);
+        } else {
+            Vec8<__half> v;
+            v.load(static_cast<const __half*>(p) + c);
+            v.widen(f[k]);
+        }
+    }
+}
 
 // Common to both passes: which columns and rows a thread has.
 template <bool kAligned, int G, int NV>
@@ -105,13 +140,13 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_fw
     for (int i = 0; i < S; ++i) fetch(i, me.group + static_cast<long long>(i) * me.groups);
     const Edges<NV, kAligned> edges(at, C);
     float2 w[NV][4], pre_w[NV][4];       // scale * gamma_post, gamma_pre
-    load_params(w, p.gamma_post, p.param_type, C, at, 1.f);
-    load_params(pre_w, p.scale, p.param_type, C, at, 1.f);
+    params<kAligned>(w, p.gamma_post, p.param_type, C, at);
+    params<kAligned>(pre_w, p.scale, p.param_type, C, at);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[k][j] = __fmul2_rn(w[k][j], pre_w[k][j]);
-    load_params(pre_w, p.gamma_pre, p.param_type, C, at, 1.f);
+    params<kAligned>(pre_w, p.gamma_pre, p.param_type, C, at);
     GroupSum<G> sum{exchange, me.local, me.width, 0};
     int stage = 0;
     const int in_warp = G > 0 ? me.local % (32 / GW) : 0;   // (the lane groups of a warp stay together)
@@ -133,14 +168,18 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_fw
         q = both(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float2 g[4];
-            if (has_gate) read_slot<TB>(g, row + gate_at + k * kBranch * threads + mine_b);
+            float2 m[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float2 m = __fmul2_rn(__fmul2_rn(x[k][j], both(post)), w[k][j]);
-                if (has_gate) m = __fmul2_rn(m, make_float2(gate_of(g[j].x, p.act), gate_of(g[j].y, p.act)));
-                z[k][j] = __ffma2_rn(both(p.alpha), z[k][j], m);
+            for (int j = 0; j < 4; ++j) m[j] = __fmul2_rn(__fmul2_rn(x[k][j], both(post)), w[k][j]);
+            if (has_gate) {
+                float2 g[4];
+                read_slot<TB>(g, row + gate_at + k * kBranch * threads + mine_b);
+                gate8(g, p.act);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[j] = __fmul2_rn(m[j], g[j]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[k][j] = __ffma2_rn(both(p.alpha), z[k][j], m[j]);
             if (!edges.full[k]) mask8(z[k], at.of(k), at.of(k) >= at.end ? 0 : C);
 #pragma unroll
             for (int j = 0; j < 4; ++j) q = __ffma2_rn(z[k][j], z[k][j], q);
@@ -230,14 +269,14 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
     for (int k = 0; k < NV; ++k) {
         const Columns one{at.of(k), at.end, 1, 0};
         float2 f[1][4], g[1][4];
-        load_params(f, p.gamma_post, p.param_type, C, one, 1.f);
-        load_params(g, p.scale, p.param_type, C, one, 1.f);
+        params<kAligned>(f, p.gamma_post, p.param_type, C, one);
+        params<kAligned>(g, p.scale, p.param_type, C, one);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             held_w[k][j] = __fmul2_rn(f[0][j], g[0][j]);
             sum_t[k][j] = sum_pre[k][j] = both(0.f);
         }
-        load_params(f, p.gamma_pre, p.param_type, C, one, 1.f);
+        params<kAligned>(f, p.gamma_pre, p.param_type, C, one);
 #pragma unroll
         for (int j = 0; j < 4; ++j) held_pre[k][j] = f[0][j];
         if constexpr (!kKept) {
@@ -324,13 +363,11 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
                 read_slot<TB>(v, row + gate_at + k * kBranch * threads + mine_b);
                 if (!live || !edges.full[k]) mask8(v, at.of(k), limit);
                 float2 o[4];
+                gate8(v, o, p.act);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 act, slope;
-                    act.x = gate_of(v[j].x, p.act, &slope.x);
-                    act.y = gate_of(v[j].y, p.act, &slope.y);
-                    o[j] = __fmul2_rn(__fmul2_rn(__fmul2_rn(w[j], t[k][j]), x[j]), slope);
-                    t[k][j] = __fmul2_rn(t[k][j], act);
+                    o[j] = __fmul2_rn(__fmul2_rn(__fmul2_rn(w[j], t[k][j]), x[j]), o[j]);
+                    t[k][j] = __fmul2_rn(t[k][j], v[j]);
                 }
                 if (live && at.of(k) < at.end && p.dgate != nullptr)
                     store_row8(static_cast<TB*>(p.dgate) + r * C, o, at.of(k), C, edges.whole[k]);
@@ -451,6 +488,8 @@ cudaError_t fwd_rows(const BlockNorm& p) {
     if (v <= 8) return fwd_launch<TS, TB, kAligned, 8, 1, 2>(p, v);
     if (v <= 16) return fwd_launch<TS, TB, kAligned, 16, 1, 2>(p, v);
     if (v <= 32) return fwd_launch<TS, TB, kAligned, 32, 1, 2>(p, v);
+    // (a row to an SM: the most threads it can take)
+    if (v <= kMost && p.rows <= device_info().sm_count) return fwd_launch<TS, TB, kAligned, 0, 1, 1>(p, v);
     const cudaError_t err = fwd_launch<TS, TB, kAligned, 0, 2, 2>(p, v);
     return err == cudaErrorNotSupported ? fwd_launch<TS, TB, kAligned, 0, 2, 1>(p, v) : err;
 }

@@ -78,10 +78,19 @@ struct Raw {
     }
     __device__ static __forceinline__ void store(T* p, const Lanes<V>& f) {
         Raw r;
-        T* v = reinterpret_cast<T*>(&r.w);
+        if constexpr (V == 1) {
+            store_out(reinterpret_cast<T*>(&r.w), f.v);
+        } else {
+            using Pair = typename Elem<T>::pair_t;
+            Pair* v = reinterpret_cast<Pair*>(&r.w);
 #pragma unroll
-        for (int j = 0; j < V; ++j) store_out(v + j, f.get(j));
-        *reinterpret_cast<Word*>(p) = r.w;
+            for (int j = 0; j < V / 2; ++j) {
+                if constexpr (std::is_same<T, float>::value) v[j] = f.v[j];
+                else if constexpr (std::is_same<T, __half>::value) v[j] = __float22half2_rn(f.v[j]);
+                else v[j] = __float22bfloat162_rn(f.v[j]);
+            }
+        }
+        r.put(p);
     }
 };
 
