@@ -355,27 +355,30 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(CausalConv p
         if (j < K - 1) rows[j].put(state + static_cast<long long>(K - 2 - j) * C);
 }
 
-// Column sums of the rows: a CTA takes 32 columns, each warp every 32nd row.
-constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads) row_sum_kernel(RowSum p) {
-    __shared__ float sums[32][33];
+// Column sums of the rows: a CTA takes 32 columns, each of its kSlots warps every kSlots-th row, 8 loads in flight.  (Few
+// rows leave most of 32 warps idle: 8 rows of 73728 columns 24 us with 32 warps.)
+template <int kSlots>
+__global__ void __launch_bounds__(32 * kSlots) row_sum_kernel(RowSum p) {
+    __shared__ float sums[kSlots][33];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long j = static_cast<long long>(blockIdx.x) * 32 + lane, width = p.widths[0] + p.widths[1] + p.widths[2];
     float s = 0.f;
     if (j < width)
-        for (long long k = warp; k < p.count; k += 8 * 32) {
+        for (long long k = warp; k < p.count; k += 8 * kSlots) {
             float t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = k + 32 * i < p.count ? p.rows[(k + 32 * i) * p.stride + j] : 0.f;
+            for (int i = 0; i < 8; ++i) t[i] = k + kSlots * i < p.count ? p.rows[(k + kSlots * i) * p.stride + j] : 0.f;
             s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
         }
     sums[warp][lane] = s;
     __syncthreads();
-    s = warp_sum(sums[lane][warp]);
-    long long o = static_cast<long long>(blockIdx.x) * 32 + warp;
-    if (lane != 0) return;
+    if (warp != 0) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) s += sums[i][lane];
+    long long o = j;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         if (o >= 0 && o < p.widths[i] && p.out[i] != nullptr) p.out[i][o] = s;
@@ -535,7 +538,10 @@ cudaError_t launch_row_sum(const float* rows, long long count, long long stride,
     std::copy(widths.begin(), widths.end(), p.widths);
     const long long grid = (p.widths[0] + p.widths[1] + p.widths[2] + 31) / 32;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(row_sum_kernel, dim3(static_cast<unsigned>(grid)), dim3(kSumThreads), 0, stream, p);
+    const dim3 ctas(static_cast<unsigned>(grid));
+    if (count <= 16) return launch_pdl(row_sum_kernel<2>, ctas, dim3(64), 0, stream, p);
+    if (count <= 128) return launch_pdl(row_sum_kernel<8>, ctas, dim3(256), 0, stream, p);
+    return launch_pdl(row_sum_kernel<32>, ctas, dim3(1024), 0, stream, p);
 }
 
 }  // namespace dwc

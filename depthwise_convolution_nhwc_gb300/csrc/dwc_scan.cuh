@@ -953,8 +953,17 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(Scan p, const float* part,
     const long long row = i / (G * 2 * N);
     const int j = static_cast<int>(i - row * G * 2 * N), g = j / (2 * N), which = (j - g * 2 * N) / N, n = j % N;
     if (p.seqs.offsets != nullptr && (row < seq_offset(p.seqs, 0) || row >= seq_offset(p.seqs, p.seqs.count))) return;
+    const float* from = part + (static_cast<long long>(g) * per_group * rows + row) * 2 * N + which * N + n;
+    const long long step = rows * 2 * N;
     float s = 0.f;
-    for (int k = 0; k < per_group; ++k) s += part[((static_cast<long long>(g) * per_group + k) * rows + row) * 2 * N + which * N + n];
+    int k = 0;
+    for (; k + 8 <= per_group; k += 8) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = from[(k + i) * step];
+        s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+    }
+    for (; k < per_group; ++k) s += from[k * step];
     store_out(static_cast<T*>(which == 0 ? p.db : p.dc) + (row * G + g) * N + n, s);
 }
 

@@ -114,11 +114,15 @@ def test_past_32_bits():
     rows = x[0]
     g1 = torch.ones(C, device="cuda")
     y, z, post, pre = dwc.block_norm_fwd(rows, rows, g1, g1, None, g1, out=y[0], stats=True)
-    y2, z2, post2, pre2 = dwc.block_norm_fwd(rows[-tail:], rows[-tail:], g1, g1, None, g1, stats=True)
-    assert torch.equal(y[-tail:], y2) and torch.equal(z[-tail:], z2) and torch.equal(post[-tail:], post2)
+    # (a call of fewer rows may add a row up in another order, so the last rows are held to the definition's bounds)
+    last, one = d(rows[-tail:]), np.ones(C)
+    for got, want in zip((y, z, post, pre), ref.block_norm(last, last, one, one, None, one, 1.0, "none", 1e-5)):
+        within(got[-tail:], want, "block norm past 32 bits")
     dx, dres = dwc.block_norm_bwd(rows, rows, z, post, pre, g1, g1, None, g1)[:2]
-    dx2, dres2 = dwc.block_norm_bwd(rows[-tail:], rows[-tail:], z2, post2, pre2, g1, g1, None, g1)[:2]
-    assert torch.equal(dx[-tail:], dx2) and torch.equal(dres[-tail:], dres2)
+    want = ref.block_norm_bwd(last, last, d(z[-tail:]), d(post[-tail:]), d(pre[-tail:]), one, one, None, one, 1.0, "none",
+                              np.zeros_like(last))
+    within(dx[-tail:], want["dx"], "dx")
+    within(dres[-tail:], want["dres"], "dres")
 
 
 @pytest.mark.parametrize("pair", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")], ids="-".join)
