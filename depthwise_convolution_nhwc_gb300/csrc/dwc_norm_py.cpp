@@ -323,8 +323,9 @@ struct Gate {
     const void* p = nullptr;
     int64_t ld = 0;
     dwc_gate_t act;
-    Gate(const Rows& x, PyObject* o, PyObject* kind) : act(gate_code(kind)) {
-        if (o == Py_None) return;
+    bool given;
+    Gate(const Rows& x, PyObject* o, PyObject* kind) : act(gate_code(kind)), given(o != Py_None) {
+        if (!given) return;
         const Tensor& t = tensor(o, "gate");
         TORCH_CHECK_VALUE(t.scalar_type() == x.t.scalar_type(), "gate must have x's dtype");
         ld = x.like(t, "gate");
@@ -349,7 +350,7 @@ PyObject* block_norm_fwd(PyObject* const* a) {
         const char* what = i == 9 ? "out" : "z";
         check_apart(o, what, x.t, x.rows, x.C, x.ld, "x");
         check_apart(o, what, res, x.rows, x.C, ldres, "res");
-        if (gate.p != nullptr) check_apart(o, what, tensor(a[4], "gate"), x.rows, x.C, gate.ld, "gate");
+        if (gate.given) check_apart(o, what, tensor(a[4], "gate"), x.rows, x.C, gate.ld, "gate");
         check_apart(o, what, a[2], "gamma_post");
         check_apart(o, what, a[3], "gamma_pre");
         check_apart(o, what, a[5], "scale");
@@ -390,7 +391,7 @@ PyObject* block_norm_bwd(PyObject* const* a) {
     const OnDevice on(x.t);
     const Tensor dx = x.out(Py_None, x.t.scalar_type(), "dx"), dres = x.out(Py_None, z.scalar_type(), "dres");
     Tensor dgate, ws, grads[3];
-    if (gate.p != nullptr) dgate = x.out(Py_None, x.t.scalar_type(), "dgate");
+    if (gate.given) dgate = x.out(Py_None, x.t.scalar_type(), "dgate");
     size_t bytes = 0;
     if (a[12] == Py_True) {
         // (gradients of the parameters that the call has)
@@ -409,7 +410,7 @@ PyObject* block_norm_bwd(PyObject* const* a) {
     check("dwc_block_norm_bwd",
           dwc_block_norm_bwd(dy.data_ptr(), lddy, dz, lddz, x.t.data_ptr(), x.ld, z.data_ptr(), ldz, gate.p, gate.ld,
                              gate.act, post, pre, w.p[0], w.p[1], w.p[2], w.type, alpha, dx.data_ptr(), dres.data_ptr(),
-                             dgate.defined() ? dgate.data_ptr() : nullptr, fp(grads[0]), fp(grads[1]), fp(grads[2]),
+                             gate.p != nullptr ? dgate.data_ptr() : nullptr, fp(grads[0]), fp(grads[1]), fp(grads[2]),
                              x.rows, static_cast<int>(x.C), type, wide, ws.defined() ? ws.data_ptr() : nullptr, bytes,
                              on.stream));
     return pack({&dx, &dres, &dgate, &grads[0], &grads[1], &grads[2]});

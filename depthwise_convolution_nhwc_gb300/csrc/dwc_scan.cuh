@@ -7,6 +7,10 @@
 // the states in registers.  Tiles of 16 positions are brought in by the whole CTA: per channel and position delta
 // and u, once, as fp32 in shared memory, and B and C widened.
 //
+// Measured (bf16, 16 states, device time): forward of one sequence of 16384 positions and 2048 channels, in chunks, 119 + 6 + 178 us
+// (its bytes would take 40), of 8 sequences of 2048 positions and 4096 channels with what the backward pass needs 432 us,
+// backward 1455 us (both: 158).
+//
 // What bounds it: per state and position 4 packed operations (2 cycles a warp for a pair of states), an exponential (4
 // cycles a warp) and what shared memory hands to the lanes, 128 bytes a cycle for the whole SM, broadcast or not: a lane
 // that had one channel took 8 bytes of B and C a state, twice the time of the arithmetic (16-byte loads count four
@@ -108,18 +112,6 @@ __device__ __forceinline__ Block block_of(const Scan& p, int block, int channels
     b.c = b.g * per + at;
     b.width = min(channels, per - at);
     return b;
-}
-
-template <int N>
-__device__ __forceinline__ void put_states(float* to, const float (&h)[N], int n0, int states) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (n0 + i < states) to[n0 + i] = h[i];
-}
-template <int N>
-__device__ __forceinline__ void get_states(float (&h)[N], const float* from, int n0, int states) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) h[i] = from != nullptr && n0 + i < states ? from[n0 + i] : 0.f;
 }
 
 // B or C of a tile: vectors of 8 states, padded with zeros.
@@ -558,9 +550,10 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 //     dh = g C + carry,  carry = a dh  (g: the gradient of the sum over the states and D u)
 //     dC = sum_c g h,  dB = sum_c dh delta u,  dA += dh a h[t-1] delta
 //     into = sum_n dh B,  decay = sum_n dh a h[t-1] A,  du = into delta + D g,  ddelta = into u + decay
-// Bound by the exchanges between lanes as much as by the arithmetic (10 packed operations on a pair of states
-// going back, 1.75 times 3 and two exponentials to form the states again), so a lane has two channels and four
-// states of each: dB and dC are added over its channels before they leave it, and lanes part the sums
+// Bound by the instructions and their latency (27 a state and position, at 0.55 a cycle with three to four warps a
+// scheduler; shared memory hands out values in 60 % of the cycles): 10 packed operations on a pair of states going back, 1.75
+// times 3 and two exponentials to form the states again, the rest exchanges between lanes, register pairs for
+// scalars and what each position and channel takes once.  So a lane has two channels and four states of each: dB and dC are added over its channels before they leave it, and lanes part the sums
 // among themselves without selecting what to send.  For that a lane holds its four states in the
 // order n ^ perm, so that the upper pair is always what the partner keeps (B and C lie in shared
 // memory in each of the orders), and odd lanes hold their two channels the other way round.
@@ -568,7 +561,8 @@ template <int L>
 struct BwdShape {
     static constexpr int kLanes = 32 / L;                  // lanes of a warp that share states
     static constexpr int kOrders = kLanes >= 4 ? 4 : kLanes;
-    // (small CTAs, seven to an SM at 144 registers a thread: 8 sequences of 4096 channels are 1024 of them, one round)
+    // (small CTAs, seven to an SM at 128 registers a thread: 8 sequences of 4096 channels are 1024 of them, one round of 1064;
+    // of 128 threads they were 512, three or four to an SM, and took a quarter longer)
     static constexpr int kThreads = L == 32 ? 128 : 64, kResident = L == 32 ? 3 : 7;
     static constexpr int kChannels = 2 * kThreads / L, NP = 4 * L, kWarps = kThreads / 32;
     static constexpr int kColumns = kChannels / 8, kEach = (kTile * kColumns + kThreads - 1) / kThreads;
