@@ -315,7 +315,7 @@ cudaError_t bwd_t(const BlockNorm& p) {
 
 }  // namespace
 
-// Partial rows: two CTAs per SM, and at most 2^25 columns in all (256 MB) for very wide rows.
+// Partial rows: four CTAs per SM, and at most 2^25 columns in all (256 MB) for very wide rows.
 int block_norm_partials(long long rows, int C) {
     const long long by_size = std::max<long long>(1, (1LL << 25) / C);
     return static_cast<int>(std::min({rows, 4LL * device_info().sm_count, by_size}));

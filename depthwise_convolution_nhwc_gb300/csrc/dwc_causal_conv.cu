@@ -7,6 +7,11 @@
 // Bound by memory: x (and dy) are read once and y (dx) written once.  A thread owns V adjacent
 // channels and walks along a run of positions with the last K inputs in registers; the run's K - 1
 // rows in front (and, backward, behind) are read again from L1 or L2.
+//
+// Measured (bf16, 8 sequences of 2048 positions, 4096 channels, 4 taps, SiLU): forward 45 us on the device (85 % of the
+// copy bandwidth), with one load at a time 107; backward 95 us and 4 us for the sums of partial rows (its bytes take 59).
+// The backward pass waits on its instructions: 26 a value, half of them issue slots that two rows of x, dy and dpre in
+// 128 registers (14 warps to an SM) leave empty.  fp32 packed rows of 1001 channels, one channel a thread: 20 us (9).
 #include <algorithm>
 #include <type_traits>
 
