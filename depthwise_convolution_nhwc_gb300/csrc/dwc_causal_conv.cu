@@ -135,9 +135,9 @@ __device__ __forceinline__ void shift(Lanes<V> (&win)[KM]) {
     for (int i = KM - 1; i > 0; --i) win[i] = win[i - 1];
 }
 
-// Rows that a thread brings in together, one such batch ahead of the one it works on: what is in flight is what counts
+// Rows that a thread brings in together, batches ahead of the one it works on: what is in flight is what counts
 // (bf16 8 x 2048 x 4096, 4 taps, forward: 8 rows of 4 channels, five CTAs to an SM 47 us, 4 rows 54, 4 rows of 8 channels
-// 58; backward, which holds two tensors' rows and the sums: 4 rows).
+// 58; backward: 4 rows 90, 8 rows 103, 2 rows 96).
 constexpr int kFwdBatch = 8, kBwdBatch = 4;
 
 // KM: taps held in registers; up to 4 it is the number of taps, 8 and 16 serve every number up to it.
@@ -196,11 +196,31 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kern
     }
 }
 
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Where the backward pass's batches wait: in shared memory, brought there by each thread for itself (no barrier), or,
+// where a thread's values are less than the 4 bytes that a copy takes, in registers (8 x 2048 x 4096 as above: two batches
+// under way in shared memory 90 us, one 94, one in registers 99).
+template <typename T, int V>
+struct BwdStage {
+    using Word = typename Raw<T, V>::Word;
+    static constexpr bool kOn = sizeof(Word) >= 4;
+    static constexpr int kBatches = !kOn || sizeof(Word) == 16 ? 2 : 3;      // one of them in work
+};
+
 // A thread walks K - 1 positions past its run: position t gives dpre[t], and with it dx[t - K + 1] is
 // complete.  Parameter gradients count the run's own positions; the CTA's groups are added in order.
 template <typename T, int KM, int V>
 __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kernel(CausalConv p, int columns, int run, int blocks) {
+    using S = BwdStage<T, V>;
     __shared__ float sums[kThreads * V];
+    __shared__ __align__(16) typename S::Word ring[S::kOn ? S::kBatches * 2 * kBwdBatch : 1][kThreads];
     pdl_trigger();
     pdl_wait();
     const int K = KM >= 8 ? p.K : KM, C = p.C;
@@ -229,19 +249,31 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
         const T* from_x = x + first * p.x.row;
         const T* from_dy = view_at<T>(p.dy, p.seqs, r) + c + first * p.dy.row;
         T* to = static_cast<T*>(p.dx) + (dense_row(p.seqs, r) + first - (K - 1)) * C + c;
-        Raw<T, V> next_x[kBwdBatch], next_dy[kBwdBatch];
+        Raw<T, V> next_x[kBwdBatch], next_dy[kBwdBatch];        // (without copies)
+        int place = 0;                                           // of the next batch in the ring
         const auto fetch = [&](int t) {       // (positions t .. t + kBwdBatch - 1, in turn)
+            typename S::Word* to = &ring[place * 2 * kBwdBatch][threadIdx.x];
 #pragma unroll
             for (int q = 0; q < kBwdBatch; ++q) {
                 if (t + q < known) {
-                    next_x[q].load(from_x);
-                    next_dy[q].load(from_dy);
+                    if constexpr (S::kOn) {
+                        copy_async<sizeof(typename S::Word)>(to + 2 * q * kThreads, from_x);
+                        copy_async<sizeof(typename S::Word)>(to + (2 * q + 1) * kThreads, from_dy);
+                    } else {
+                        next_x[q].load(from_x);
+                        next_dy[q].load(from_dy);
+                    }
                 }
                 from_x += p.x.row;
                 from_dy += p.dy.row;
             }
+            if constexpr (S::kOn) {
+                copy_commit();
+                place = place == S::kBatches - 1 ? 0 : place + 1;
+            }
         };
-        fetch(0);
+#pragma unroll
+        for (int i = 0; i < S::kBatches - 1; ++i) fetch(i * kBwdBatch);
         Lanes<V> w[KM], bias, win[KM], dpre[KM];
         load_taps(w, bias, p, K, c);
 #pragma unroll
@@ -251,9 +283,16 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
             if (i < K) win[i] = input<T, V>(x, p.x.row, state, C, K, first - i);
         for (int t0 = 0; t0 < stop; t0 += kBwdBatch) {
             Raw<T, V> raw_x[kBwdBatch], raw_dy[kBwdBatch];
+            // the oldest batch of the ring, whose copies came before the others'
+            const typename S::Word* batch = &ring[(place == S::kBatches - 1 ? 0 : place + 1) * 2 * kBwdBatch][threadIdx.x];
+            if constexpr (S::kOn) {
+                copy_wait<S::kBatches - 2>();
+            } else {
 #pragma unroll
-            for (int q = 0; q < kBwdBatch; ++q) raw_x[q] = next_x[q], raw_dy[q] = next_dy[q];
-            fetch(t0 + kBwdBatch);
+                for (int q = 0; q < kBwdBatch; ++q) raw_x[q] = next_x[q], raw_dy[q] = next_dy[q];
+            }
+            // (into the place of the batch before, whose values are used up)
+            fetch(t0 + (S::kBatches - 1) * kBwdBatch);
             // (nearly every batch lies within the run and needs no test of its rows)
             const auto work = [&](auto whole) {
                 constexpr bool kWhole = decltype(whole)::value;
@@ -261,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
                 for (int q = 0; q < kBwdBatch; ++q) {
                     const int t = t0 + q, at = t - (K - 1);
                     if (kWhole || t < known) {
+                        if constexpr (S::kOn) raw_x[q].w = batch[2 * q * kThreads], raw_dy[q].w = batch[(2 * q + 1) * kThreads];
                         win[0] = raw_x[q].widen();
                         dpre[0] = raw_dy[q].widen();
                         if (p.silu) dpre[0].by_slope(convolve(w, bias, win, K));
@@ -426,13 +466,14 @@ cudaError_t fwd_t(CausalConv p) {
                       run, blocks);
 }
 
-// Positions to a slot of the backward pass, for V channels a thread: runs of 64, fewer where that leaves SMs without
-// their eight CTAs.  
+// Positions to a slot of the backward pass, for V channels a thread: runs of 128, fewer where that leaves SMs without
+// the CTAs that they hold together, 4 of several channels a thread, 8 of one (8 x 2048 x 4096 as above: runs of 128 85 us,
+// 64 90, 256 94; fp32 packed 5005 x 1001: runs of 32 23 us, 64 25).
 long long bwd_span(const Seqs& s, int C, int V) {
     const int vectors = (C + V - 1) / V, columns = columns_for(vectors), groups = kThreads / columns;
-    const long long blocks = (vectors + columns - 1) / columns;
-    long long span = static_cast<long long>(groups) * 64;
-    while (span > groups * 8 && seq_rows(s) / span * blocks < 8LL * device_info().sm_count) span /= 2;
+    const long long blocks = (vectors + columns - 1) / columns, enough = (V > 1 ? 4LL : 8LL) * device_info().sm_count;
+    long long span = static_cast<long long>(groups) * 128;
+    while (span > groups * 8 && seq_rows(s) / span * blocks < enough) span /= 2;
     return span;
 }
 
