@@ -276,6 +276,14 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
         for (int i = 0; i < S::kBatches - 1; ++i) fetch(i * kBwdBatch);
         Lanes<V> w[KM], bias, win[KM], dpre[KM];
         load_taps(w, bias, p, K, c);
+        // (the number of taps is not known: the same in the other order, since registers have no variable index)
+        Lanes<V> ahead[KM < 8 ? 1 : KM];
+        if constexpr (KM >= 8) {
+#pragma unroll
+            for (int i = 0; i < KM; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) ahead[i].set(j, i < K ? load_param(p.w, p.param_type, i * C + c + j, 0.f) : 0.f);
+        }
 #pragma unroll
         for (int i = 0; i < KM; ++i) dpre[i].clear();
 #pragma unroll
@@ -320,14 +328,8 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
 #pragma unroll
                         for (int i = 0; i < KM; ++i) {
                             if (i >= K) continue;
-                            if constexpr (KM < 8) {
-                                f.fma(w[KM - 1 - i], dpre[i]);
-                            } else {
-                                Lanes<V> tap;
-#pragma unroll
-                                for (int j = 0; j < V; ++j) tap.set(j, load_param(p.w, p.param_type, i * C + c + j, 0.f));
-                                f.fma(tap, dpre[i]);
-                            }
+                            if constexpr (KM < 8) f.fma(w[KM - 1 - i], dpre[i]);
+                            else f.fma(ahead[i], dpre[i]);
                         }
                         if (!kWhole && at >= kept_from) {
                             Raw<T, V> g;
