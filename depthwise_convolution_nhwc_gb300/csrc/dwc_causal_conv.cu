@@ -140,7 +140,7 @@ __device__ __forceinline__ void shift(Lanes<V> (&win)[KM]) {
 // 58; backward: 4 rows 90, 8 rows 103, 2 rows 96).
 constexpr int kFwdBatch = 8, kBwdBatch = 4;
 
-// KM: taps held in registers; up to 4 it is the number of taps, 8 and 16 serve every number up to it.
+// KM: taps held in registers; up to 4 it is the number of taps, 8 and 16 serve the numbers up to it.
 template <typename T, int KM, int V>
 __global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kernel(CausalConv p, int columns, int run, int blocks) {
     pdl_trigger();
@@ -494,6 +494,8 @@ cudaError_t bwd_t(CausalConv p) {
 }
 
 // Several channels a thread where every tensor allows it, else one.
+// (bf16 8 x 2048 x 2048, two channels a thread and one: 12 taps forward 75 and 89 us, backward 173 and 243, 8 taps backward
+// 96 and 138; four: 86, 8 taps backward 116.)
 bool vectors_of(const CausalConv& p, bool backward) {
     const size_t a = 8 * static_cast<size_t>(elem_bytes(p.type));
     const auto off = [&](const void* t) { return reinterpret_cast<uintptr_t>(t) % a != 0; };
@@ -505,11 +507,12 @@ template <typename T>
 cudaError_t fwd_k(const CausalConv& p) {
     const bool vec = vectors_of(p, false);
     switch (p.K) {
+        case 1: return vec ? fwd_t<T, 1, 4>(p) : fwd_t<T, 1, 1>(p);
         case 2: return vec ? fwd_t<T, 2, 4>(p) : fwd_t<T, 2, 1>(p);
         case 3: return vec ? fwd_t<T, 3, 4>(p) : fwd_t<T, 3, 1>(p);
         case 4: return vec ? fwd_t<T, 4, 4>(p) : fwd_t<T, 4, 1>(p);
     }
-    if (p.K > 8) return fwd_t<T, 16, 1>(p);
+    if (p.K > 8) return vec ? fwd_t<T, 16, 2>(p) : fwd_t<T, 16, 1>(p);
     return vec ? fwd_t<T, 8, 4>(p) : fwd_t<T, 8, 1>(p);
 }
 
@@ -517,11 +520,12 @@ template <typename T>
 cudaError_t bwd_k(const CausalConv& p) {
     const bool vec = vectors_of(p, true);
     switch (p.K) {
+        case 1: return vec ? bwd_t<T, 1, 4>(p) : bwd_t<T, 1, 1>(p);
         case 2: return vec ? bwd_t<T, 2, 4>(p) : bwd_t<T, 2, 1>(p);
         case 3: return vec ? bwd_t<T, 3, 4>(p) : bwd_t<T, 3, 1>(p);
         case 4: return vec ? bwd_t<T, 4, 4>(p) : bwd_t<T, 4, 1>(p);
     }
-    if (p.K > 8) return bwd_t<T, 16, 1>(p);
+    if (p.K > 8) return vec ? bwd_t<T, 16, 2>(p) : bwd_t<T, 16, 1>(p);
     return vec ? bwd_t<T, 8, 2>(p) : bwd_t<T, 8, 1>(p);
 }
 
