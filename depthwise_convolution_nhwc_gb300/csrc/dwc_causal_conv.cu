@@ -8,10 +8,11 @@
 // channels and walks along a run of positions with the last K inputs in registers; the run's K - 1
 // rows in front (and, backward, behind) are read again from L1 or L2.
 //
-// Measured (bf16, 8 sequences of 2048 positions, 4096 channels, 4 taps, SiLU): forward 45 us on the device (85 % of the
-// copy bandwidth), with one load at a time 107; backward 95 us and 4 us for the sums of partial rows (its bytes take 59).
-// The backward pass waits on its instructions: 26 a value, half of them issue slots that two rows of x, dy and dpre in
-// 128 registers (14 warps to an SM) leave empty.  fp32 packed rows of 1001 channels, one channel a thread: 20 us (9).
+// Measured (bf16, 8 sequences of 2048 positions, 4096 channels, 4 taps, SiLU): forward 44 us (89 % of the copy bandwidth),
+// with one load at a time 107; backward 85 us with 4 us for the sums of partial rows (its bytes take 59).  In fp32, whose
+// bytes bind both, 82 (96 %) and 128 (92 %).  The bf16 backward pass waits on its instructions, 26 a value, of which 16 warps
+// to an SM (128 registers a thread) issue one every other cycle.  fp32 packed rows of 1001 channels, one channel a thread:
+// 22 us (9).
 #include <algorithm>
 #include <type_traits>
 
@@ -136,13 +137,34 @@ __device__ __forceinline__ void shift(Lanes<V> (&win)[KM]) {
 }
 
 // Rows that a thread brings in together, batches ahead of the one it works on: what is in flight is what counts
-// (bf16 8 x 2048 x 4096, 4 taps, forward: 8 rows of 4 channels, five CTAs to an SM 47 us, 4 rows 54, 4 rows of 8 channels
-// 58; backward: 4 rows 90, 8 rows 103, 2 rows 96).
+// (bf16 8 x 2048 x 4096, 4 taps, forward: 8 rows of 4 channels, two batches under way, five CTAs to an SM 44 us, one batch in registers
+// 46, of 4 rows 54, of 4 rows of 8 channels 58; backward: 4 rows 90, 8 rows 103, 2 rows 96).
 constexpr int kFwdBatch = 8, kBwdBatch = 4;
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Where batches wait: in shared memory, brought there by each thread for itself (no barrier), or in registers.
+// Backward in registers only where a thread's values are less than the 4 bytes that a copy takes (8 x 2048 x 4096 as above: two
+// batches under way in shared memory 90 us, one 94, one in registers 99; fp32 129 and 256).  Forward with several channels and
+// taps (bf16 44 us, in registers 46, fp32 82 and 97; one channel 26 and 25, one tap of 2048 channels 26 and 20).
+template <typename T, int V, bool kWanted>
+struct Stage {
+    using Word = typename Raw<T, V>::Word;
+    static constexpr bool kOn = kWanted && sizeof(Word) >= 4;
+    static constexpr int kBatches = !kOn || sizeof(Word) == 16 ? 2 : 3;      // one of them in work
+};
 
 // KM: taps held in registers; up to 4 it is the number of taps, 8 and 16 serve the numbers up to it.
 template <typename T, int KM, int V>
 __global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kernel(CausalConv p, int columns, int run, int blocks) {
+    using S = Stage<T, V, (V > 1 && KM > 1)>;
+    __shared__ __align__(16) typename S::Word ring[S::kOn ? S::kBatches * kFwdBatch : 1][kThreads];
     pdl_trigger();
     pdl_wait();
     const int K = KM >= 8 ? p.K : KM, C = p.C;
@@ -159,15 +181,25 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kern
     if (n > 0) {
         const T* from = x + first * p.x.row;
         T* to = static_cast<T*>(p.y) + (dense_row(p.seqs, r) + first) * C + c;
-        Raw<T, V> next[kFwdBatch];
+        Raw<T, V> next[kFwdBatch];               // (without copies)
+        int place = 0;                           // of the next batch in the ring
         const auto fetch = [&](int t) {       // (positions t .. t + kFwdBatch - 1, in turn)
+            typename S::Word* to = &ring[S::kOn ? place * kFwdBatch : 0][threadIdx.x];
 #pragma unroll
             for (int q = 0; q < kFwdBatch; ++q) {
-                if (t + q < n) next[q].load(from);
+                if (t + q < n) {
+                    if constexpr (S::kOn) copy_async<sizeof(typename S::Word)>(to + q * kThreads, from);
+                    else next[q].load(from);
+                }
                 from += p.x.row;
             }
+            if constexpr (S::kOn) {
+                copy_commit();
+                place = place == S::kBatches - 1 ? 0 : place + 1;
+            }
         };
-        fetch(0);
+#pragma unroll
+        for (int i = 0; i < S::kBatches - 1; ++i) fetch(i * kFwdBatch);
         Lanes<V> w[KM], bias, win[KM];        // win[i]: the input i positions back
         load_taps(w, bias, p, K, c);
 #pragma unroll
@@ -175,11 +207,19 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kern
             if (i < K) win[i] = input<T, V>(x, p.x.row, state, C, K, first - i);
         for (int t0 = 0; t0 < n; t0 += kFwdBatch) {
             Raw<T, V> raw[kFwdBatch];
+            // the oldest batch of the ring, whose copies came before the others'
+            const typename S::Word* batch = &ring[S::kOn ? (place == S::kBatches - 1 ? 0 : place + 1) * kFwdBatch : 0][threadIdx.x];
+            if constexpr (S::kOn) {
+                copy_wait<S::kBatches - 2>();
+            } else {
 #pragma unroll
-            for (int q = 0; q < kFwdBatch; ++q) raw[q] = next[q];
-            fetch(t0 + kFwdBatch);
+                for (int q = 0; q < kFwdBatch; ++q) raw[q] = next[q];
+            }
+            // (into the place of the batch before, whose values are used up)
+            fetch(t0 + (S::kBatches - 1) * kFwdBatch);
 #pragma unroll
             for (int q = 0; q < kFwdBatch; ++q) {
+                if constexpr (S::kOn) raw[q].w = batch[q * kThreads];
                 win[0] = raw[q].widen();
                 Lanes<V> f = convolve(w, bias, win, K);
                 if (p.silu) f.to_silu();
@@ -196,29 +236,11 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 5 : 1) causal_conv_fwd_kern
     }
 }
 
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(kBytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Where the backward pass's batches wait: in shared memory, brought there by each thread for itself (no barrier), or,
-// where a thread's values are less than the 4 bytes that a copy takes, in registers (8 x 2048 x 4096 as above: two batches
-// under way in shared memory 90 us, one 94, one in registers 99).
-template <typename T, int V>
-struct BwdStage {
-    using Word = typename Raw<T, V>::Word;
-    static constexpr bool kOn = sizeof(Word) >= 4;
-    static constexpr int kBatches = !kOn || sizeof(Word) == 16 ? 2 : 3;      // one of them in work
-};
-
 // A thread walks K - 1 positions past its run: position t gives dpre[t], and with it dx[t - K + 1] is
 // complete.  Parameter gradients count the run's own positions; the CTA's groups are added in order.
 template <typename T, int KM, int V>
 __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kernel(CausalConv p, int columns, int run, int blocks) {
-    using S = BwdStage<T, V>;
+    using S = Stage<T, V, true>;
     __shared__ float sums[kThreads * V];
     __shared__ __align__(16) typename S::Word ring[S::kOn ? S::kBatches * 2 * kBwdBatch : 1][kThreads];
     pdl_trigger();
@@ -252,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
         Raw<T, V> next_x[kBwdBatch], next_dy[kBwdBatch];        // (without copies)
         int place = 0;                                           // of the next batch in the ring
         const auto fetch = [&](int t) {       // (positions t .. t + kBwdBatch - 1, in turn)
-            typename S::Word* to = &ring[place * 2 * kBwdBatch][threadIdx.x];
+            typename S::Word* to = &ring[S::kOn ? place * 2 * kBwdBatch : 0][threadIdx.x];
 #pragma unroll
             for (int q = 0; q < kBwdBatch; ++q) {
                 if (t + q < known) {
@@ -292,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, KM < 8 ? 4 : 1) causal_conv_bwd_kern
         for (int t0 = 0; t0 < stop; t0 += kBwdBatch) {
             Raw<T, V> raw_x[kBwdBatch], raw_dy[kBwdBatch];
             // the oldest batch of the ring, whose copies came before the others'
-            const typename S::Word* batch = &ring[(place == S::kBatches - 1 ? 0 : place + 1) * 2 * kBwdBatch][threadIdx.x];
+            const typename S::Word* batch = &ring[S::kOn ? (place == S::kBatches - 1 ? 0 : place + 1) * 2 * kBwdBatch : 0][threadIdx.x];
             if constexpr (S::kOn) {
                 copy_wait<S::kBatches - 2>();
             } else {

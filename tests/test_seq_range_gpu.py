@@ -125,6 +125,30 @@ def test_past_32_bits():
     within(dres[-tail:], want["dres"], "dres")
 
 
+@pytest.mark.parametrize("dtype,K,C", [("f32", 4, 2048), ("bf16", 4, 2048), ("f16", 8, 2048), ("bf16", 1, 2048), ("f32", 3, 1001),
+                                       ("bf16", 2, 1001), ("bf16", 13, 2048)])
+def test_causal_conv_of_long_runs(dtype, K, C):
+    """So many positions that a thread walks its longest runs.  dx depends on a position's neighbours alone: the bits of each
+    sequence's own call, whose runs are shorter.  Without an activation dw is a sum of products, in fp32 128 in a run, 4 runs
+    to a row of partial sums, at most 160 such rows: off by 300 roundings of the sum of magnitudes at most."""
+    rng = np.random.default_rng(K)
+    T = 10001
+    x, dy = (torch.from_numpy(rng.standard_normal((2, T, C), np.float32)).to("cuda", {"f32": torch.float32, "bf16": torch.bfloat16,
+                                                                                    "f16": torch.float16}[dtype]) for _ in range(2))
+    w, b = rand(rng, (K, C), "f32"), rand(rng, C, "f32")
+    dx = dwc.causal_conv_bwd(dy, x, w, b, "silu")[0]
+    for s in range(2):
+        one = dwc.causal_conv_bwd(dy[s:s + 1], x[s:s + 1], w, b, "silu")[0]
+        assert torch.equal(dx[s], one[0])
+    _, dw, db, _ = dwc.causal_conv_bwd(dy, x, w, b)
+    x, dy = x.double(), dy.double()
+    for k in range(K):
+        back = K - 1 - k
+        terms = dy[:, back:] * x[:, :T - back]
+        assert ((dw[k].double() - terms.sum((0, 1))).abs() <= 300 * 2 ** -24 * terms.abs().sum((0, 1))).all()
+    assert ((db.double() - dy.sum((0, 1))).abs() <= 300 * 2 ** -24 * dy.abs().sum((0, 1))).all()
+
+
 @pytest.mark.parametrize("pair", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")], ids="-".join)
 @pytest.mark.parametrize("rows,C", [(64, 1000), (300, 129), (37, 1001), (257, 2048), (40, 8192), (9, 20001)])
 def test_block_norm_in_place(rows, C, pair):
