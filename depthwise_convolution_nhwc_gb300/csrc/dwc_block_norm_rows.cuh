@@ -53,17 +53,37 @@ struct GroupSum {
     }
 };
 
+// 8 parameters from column c on, zeros beside the row.  (The loads are on their way together: with a choice of the type
+// around each of them they were waited for one by one: fp16 152 x 1001 forward 3.7 us, 3.1 so.)
+template <typename T>
+__device__ __forceinline__ void params_at(float2 (&f)[4], const T* p, int c, int C) {
+    T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[min(max(c + j, 0), C - 1)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f[j] = make_float2(in_row(c + 2 * j, C) ? to_f32(v[2 * j]) : 0.f, in_row(c + 2 * j + 1, C) ? to_f32(v[2 * j + 1]) : 0.f);
+}
+
 // Parameters of a thread's vectors: one access each where the parameters are aligned and the vectors are not shifted.
 template <bool kAligned, int NV>
 __device__ __forceinline__ void params(float2 (&f)[NV][4], const void* p, int type, int C, const Columns& at) {
     const size_t align = type == kF32 ? 32 : 16;
-    if (!kAligned || p == nullptr || reinterpret_cast<uintptr_t>(p) % align != 0) {
-        load_params(f, p, type, C, at, 1.f);
-        return;
-    }
+    const bool single = !kAligned || reinterpret_cast<uintptr_t>(p) % align != 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = at.of(k);
+        if (p == nullptr) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[k][j] = make_float2(in_row(c + 2 * j, C) ? 1.f : 0.f, in_row(c + 2 * j + 1, C) ? 1.f : 0.f);
+            continue;
+        }
+        if (single && c < at.end) {
+            if (type == kF32) params_at(f[k], static_cast<const float*>(p), c, C);
+            else if (type == kBF16) params_at(f[k], static_cast<const __nv_bfloat16*>(p), c, C);
+            else params_at(f[k], static_cast<const __half*>(p), c, C);
+            continue;
+        }
         if (c >= at.end) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[k][j] = both(0.f);
