@@ -22,14 +22,15 @@ namespace block_norm {
 
 using namespace norm;
 
-constexpr int kMost = 512;                // threads of a CTA whose warps serve rows
+// Threads of a CTA whose warps serve rows, one to an SM: with 128 registers each, or 102.
+constexpr int kMost = 512, kWide = 640;
 // (lane groups of a warp: 256 threads, two or three CTAs to an SM)
-constexpr int block_threads(int G) { return G > 0 ? kWarpCta : kMost; }
+constexpr int block_threads(int G, int M) { return G > 0 ? kWarpCta : M; }
 
-// The sum of one value over the threads of a group (G lanes, or several warps).
-template <int G>
+// The sum of one value over the threads of a group (G lanes, or several warps of a CTA of up to M threads).
+template <int G, int M>
 struct GroupSum {
-    float (&e)[2][2][kMost / 32];
+    float (&e)[2][2][M / 32];
     int local, width, parity;
     // which: 0 or 1, the first or second sum of a row
     __device__ __forceinline__ float operator()(float v, int which) const {
@@ -48,7 +49,7 @@ struct GroupSum {
         }
         v = lane < warps ? e[parity][which][local * warps + lane] : 0.f;
 #pragma unroll
-        for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);    // (at most 16 warps)
+        for (int m = M > 512 ? 16 : 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);    // (of M / 32 lanes)
         return __shfl_sync(0xffffffffu, v, 0);
     }
 };
@@ -123,10 +124,10 @@ struct Place {
     }
 };
 
-template <typename TS, typename TB, bool kAligned, int G, int NV, int S>
-__global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_fwd_rows_kernel(BlockNorm p, int group_threads, int vectors) {
+template <typename TS, typename TB, bool kAligned, int G, int NV, int S, int M>
+__global__ void __launch_bounds__(block_threads(G, M), G > 0 ? 2 : 1) block_norm_fwd_rows_kernel(BlockNorm p, int group_threads, int vectors) {
     extern __shared__ __align__(16) float smem[];
-    __shared__ float exchange[2][2][kMost / 32];
+    __shared__ float exchange[2][2][M / 32];
     constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;  // granules of a slot
     const int C = p.C;
     const Place<kAligned, G, NV> me(C, vectors, group_threads);
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_fw
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[k][j] = __fmul2_rn(w[k][j], pre_w[k][j]);
     params<kAligned>(pre_w, p.gamma_pre, p.param_type, C, at);
-    GroupSum<G> sum{exchange, me.local, me.width, 0};
+    GroupSum<G, M> sum{exchange, me.local, me.width, 0};
     int stage = 0;
     const int in_warp = G > 0 ? me.local % (32 / GW) : 0;   // (the lane groups of a warp stay together)
     for (long long r = me.group; r - in_warp < p.rows; r += me.groups) {
@@ -239,10 +240,10 @@ constexpr bool params_in_registers(int NV) { return NV == 1 || sizeof(TB) == 4; 
 //     dx = rstd_post (b - xhat mean(b xhat)),  dres = alpha g,  dgate = w g xhat act'
 // and of the parameters only two sums over the rows, S = sum t xhat and sum dy zhat: dgamma_post is
 // scale S, dscale is gamma_post S.  They stay in registers; the groups of a CTA are added at its end.
-template <typename TS, typename TB, bool kAligned, int G, int NV, int S>
-__global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bwd_rows_kernel(BlockNorm p, int group_threads, int vectors) {
+template <typename TS, typename TB, bool kAligned, int G, int NV, int S, int M>
+__global__ void __launch_bounds__(block_threads(G, M), G > 0 ? 2 : 1) block_norm_bwd_rows_kernel(BlockNorm p, int group_threads, int vectors) {
     extern __shared__ __align__(16) float smem[];
-    __shared__ float exchange[2][2][kMost / 32];
+    __shared__ float exchange[2][2][M / 32];
     constexpr int kBranch = sizeof(TB) / 2, kStream = sizeof(TS) / 2;
     const int C = p.C;
     const Place<kAligned, G, NV> me(C, vectors, group_threads);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(block_threads(G), G > 0 ? 2 : 1) block_norm_bw
             }
         }
     };
-    GroupSum<G> sum{exchange, me.local, me.width, 0};
+    GroupSum<G, M> sum{exchange, me.local, me.width, 0};
     int stage = 0;
     const int in_warp = G > 0 ? me.local % (32 / GW) : 0;
     float next_post = me.group < p.rows ? p.rstd_post[me.group] : 0.f, next_pre = me.group < p.rows ? p.rstd_pre[me.group] : 0.f;
@@ -452,15 +453,15 @@ struct Plan {
 // groups to a CTA as serve its share of the rows in the fewest rounds.  Where rows are shifted the
 // number of groups is a multiple of 8, so that a group's rows all have one shift.
 template <class K>
-cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int NV, int S, size_t slot, size_t more, int vectors, int parts, Plan& l) {
+cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int NV, int S, int M, size_t slot, size_t more, int vectors, int parts, Plan& l) {
     const int sms = device_info().sm_count;
     if (G > 0) {
         l.width = G;
         l.per_cta = kWarpCta / G;
     } else {
         l.width = (vectors + NV * 32 - 1) / (NV * 32) * 32;
-        if (l.width > kMost) return cudaErrorNotSupported;
-        const long long share = (p.rows + sms - 1) / sms, most = kMost / l.width;
+        if (l.width > M) return cudaErrorNotSupported;
+        const long long share = (p.rows + sms - 1) / sms, most = M / l.width;
         const long long rounds = (share + most - 1) / most;
         l.per_cta = static_cast<int>((share + rounds - 1) / rounds);
     }
@@ -481,30 +482,42 @@ cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int
     return cudaSuccess;
 }
 
-template <typename TS, typename TB, bool kAligned, int G, int NV, int S>
+template <typename TS, typename TB, bool kAligned, int G, int NV, int S, int M = kMost>
 cudaError_t fwd_launch(const BlockNorm& p, int vectors) {
-    auto kern = block_norm_fwd_rows_kernel<TS, TB, kAligned, G, NV, S>;
+    auto kern = block_norm_fwd_rows_kernel<TS, TB, kAligned, G, NV, S, M>;
     static KernelFacts facts;
     Plan l;
     const size_t slot = 8 * (sizeof(TS) + sizeof(TB) * (p.gate != nullptr ? 2 : 1));
-    const cudaError_t err = plan_rows(kern, facts, p, G, NV, S, slot, 0, vectors, 0, l);
+    const cudaError_t err = plan_rows(kern, facts, p, G, NV, S, M, slot, 0, vectors, 0, l);
     if (err != cudaSuccess) return err;
     return launch_pdl(kern, dim3(static_cast<unsigned>(l.grid)), dim3(static_cast<unsigned>(l.threads)), l.smem, p.stream, p, l.width,
                       vectors);
 }
 
-template <typename TS, typename TB, bool kAligned, int G, int NV, int S>
+template <typename TS, typename TB, bool kAligned, int G, int NV, int S, int M = kMost>
 cudaError_t bwd_launch(const BlockNorm& p, int vectors) {
-    auto kern = block_norm_bwd_rows_kernel<TS, TB, kAligned, G, NV, S>;
+    auto kern = block_norm_bwd_rows_kernel<TS, TB, kAligned, G, NV, S, M>;
     static KernelFacts facts;
     Plan l;
     const size_t slot = 8 * (sizeof(TB) * (p.gate != nullptr ? 3 : 2) + sizeof(TS) * (p.dz != nullptr ? 2 : 1));
-    cudaError_t err = plan_rows(kern, facts, p, G, NV, S, slot, params_in_registers<TB>(NV) ? 0 : 64, vectors,
+    cudaError_t err = plan_rows(kern, facts, p, G, NV, S, M, slot, params_in_registers<TB>(NV) ? 0 : 64, vectors,
                                 p.partial != nullptr ? block_norm_partials(p.rows, p.C) : 0, l);
     if (err != cudaSuccess) return err;
     err = launch_pdl(kern, dim3(static_cast<unsigned>(l.grid)), dim3(static_cast<unsigned>(l.threads)), l.smem, p.stream, p, l.width,
                      vectors);
     return err != cudaSuccess || p.partial == nullptr ? err : launch_block_norm_params(p, l.grid);
+}
+
+// Whether CTAs of kWide threads hold so many more groups of a row than those of kMost (or one where there was none) that
+// fewer registers pay: half as many again; twice as many where rows are shifted; with fp32 branches, whose kernels
+// have room for two CTAs to an SM, only where there was none.  bf16, kWide and kMost threads: 6553 x 5120 forward 61 and 78 us,
+// backward 106 and 154; 13107 x 2560 backward 104 and 134; 21845 x 1536 105 and 116, of 1501 channels 93 and 88; fp32
+// 3276 x 5120 backward 108 and 130, 6553 x 2560 96 and 84.
+template <typename TB, bool kAligned>
+inline bool wide_cta(int vectors, int NV) {
+    const int width = (vectors + NV * 32 - 1) / (NV * 32) * 32;
+    if (width > kWide) return false;
+    return sizeof(TB) == 4 ? width > kMost : 2 * (kWide / width) >= (kAligned ? 3 : 4) * (kMost / width);
 }
 
 template <typename TS, typename TB, bool kAligned>
@@ -515,6 +528,10 @@ cudaError_t fwd_rows(const BlockNorm& p) {
     if (v <= 32) return fwd_launch<TS, TB, kAligned, 32, 1, 2>(p, v);
     // (a row to an SM: the most threads it can take)
     if (v <= kMost && p.rows <= device_info().sm_count) return fwd_launch<TS, TB, kAligned, 0, 1, 1>(p, v);
+    if (wide_cta<TB, kAligned>(v, 2)) {
+        const cudaError_t err = fwd_launch<TS, TB, kAligned, 0, 2, 2, kWide>(p, v);
+        if (err != cudaErrorNotSupported) return err;
+    }
     const cudaError_t err = fwd_launch<TS, TB, kAligned, 0, 2, 2>(p, v);
     return err == cudaErrorNotSupported ? fwd_launch<TS, TB, kAligned, 0, 2, 1>(p, v) : err;
 }
@@ -525,8 +542,9 @@ cudaError_t bwd_rows(const BlockNorm& p) {
     if (v <= 8) return bwd_launch<TS, TB, kAligned, 8, 1, 2>(p, v);
     if (v <= 16) return bwd_launch<TS, TB, kAligned, 16, 1, 2>(p, v);
     if (v <= 32) return bwd_launch<TS, TB, kAligned, 32, 1, 2>(p, v);
-    cudaError_t err = v <= kMost ? bwd_launch<TS, TB, kAligned, 0, 1, 2>(p, v) : cudaErrorNotSupported;
-    if (err == cudaErrorNotSupported) err = bwd_launch<TS, TB, kAligned, 0, 2, 2>(p, v);
+    cudaError_t err = wide_cta<TB, kAligned>(v, 1) ? bwd_launch<TS, TB, kAligned, 0, 1, 2, kWide>(p, v) : cudaErrorNotSupported;
+    if (err == cudaErrorNotSupported && v <= kMost) err = bwd_launch<TS, TB, kAligned, 0, 1, 2>(p, v);
+    // (two vectors a thread: one stage, whose kernel has registers enough; bf16 4681 x 7168 124 us, 157 with two)
     return err == cudaErrorNotSupported ? bwd_launch<TS, TB, kAligned, 0, 2, 1>(p, v) : err;
 }
 

@@ -149,6 +149,14 @@ def test_causal_conv_of_long_runs(dtype, K, C):
     assert ((db.double() - dy.sum((0, 1))).abs() <= 300 * 2 ** -24 * dy.abs().sum((0, 1))).all()
 
 
+@pytest.mark.parametrize("pair", [("f32", "f32"), ("bf16", "bf16"), ("f32", "f16")], ids="-".join)
+@pytest.mark.parametrize("rows,C", [(1000, 1536), (700, 2304), (700, 2501), (500, 2816), (340, 4104), (340, 5001), (340, 5120), (170, 6144),
+                                    (170, 7001)])
+def test_block_norm_widths_between(rows, C, pair):
+    """Rows whose groups of warps do not fill a CTA of 512 threads, several to a CTA and several rounds of them."""
+    check_norm(np.random.default_rng(C), (rows, C), *pair, dz=C % 2 == 0)
+
+
 @pytest.mark.parametrize("pair", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")], ids="-".join)
 @pytest.mark.parametrize("rows,C", [(64, 1000), (300, 129), (37, 1001), (257, 2048), (40, 8192), (9, 20001)])
 def test_block_norm_in_place(rows, C, pair):
