@@ -10,8 +10,8 @@
 //
 // Measured (bf16 branches, fp32 stream, gate, 16384 x 4096): forward 139 us, 99 % of the copy bandwidth (one CTA a row that
 // reads its row three times: 440), backward 213 us and 5.6 for the parameters (1958).  One bf16 row of 4096 channels
-// 3.0 us call to call (17.4).  fp16 4099 x 1024 backward 17.3 us; 1000 channels 18.8; of 1001, rows that no vector divides,
-// 28: masked ends of rows sit in half of the warps, 104 instructions a value.
+// 3.0 us call to call (17.4).  fp16 4190 x 1024 backward 17.7 us in a graph, 1000 channels 19.0, of 1001, rows that no vector
+// divides, 24.2: first and last vectors of a row, which are stored value by value, and parameters cut out of two vectors.
 #pragma once
 
 #include "dwc_norm_rows.cuh"
@@ -54,10 +54,33 @@ struct GroupSum {
     }
 };
 
-// 8 parameters from column c on, zeros beside the row.  (The loads are on their way together: with a choice of the type
-// around each of them they were waited for one by one: fp16 152 x 1001 forward 3.7 us, 3.1 so.)
+// 8 parameters from column c on, zeros beside the row: cut out of the two vectors they lie in (`whole`: the parameters are
+// aligned; single loads, 32 bytes apart from lane to lane, take 8 wavefronts each: fp16 4190 x 1001 forward 14.1 us,
+// 13.3 so), or
+// one by one, on their way together (with a choice of the type around each of them they were waited for in turn).
 template <typename T>
-__device__ __forceinline__ void params_at(float2 (&f)[4], const T* p, int c, int C) {
+__device__ __forceinline__ void params_at(float2 (&f)[4], const T* p, int c, int C, bool whole) {
+    const int base = c & ~7, d = c - base;
+    if (whole && base >= 0 && base + 16 <= C) {
+        Vec8<T> raw[2];
+        raw[0].load(p + base);
+        raw[1].load(p + base + 8);
+        float2 w[2][4];
+        raw[0].widen(w[0]);
+        raw[1].widen(w[1]);
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = j & 1 ? w[j / 8][j % 8 / 2].y : w[j / 8][j % 8 / 2].x;
+#pragma unroll
+        for (int j = 0; j < 12; ++j) v[j] = d & 4 ? v[j + 4] : v[j];
+#pragma unroll
+        for (int j = 0; j < 10; ++j) v[j] = d & 2 ? v[j + 2] : v[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = d & 1 ? v[j + 1] : v[j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
+        return;
+    }
     T v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = p[min(max(c + j, 0), C - 1)];
@@ -70,7 +93,7 @@ __device__ __forceinline__ void params_at(float2 (&f)[4], const T* p, int c, int
 template <bool kAligned, int NV>
 __device__ __forceinline__ void params(float2 (&f)[NV][4], const void* p, int type, int C, const Columns& at) {
     const size_t align = type == kF32 ? 32 : 16;
-    const bool single = !kAligned || reinterpret_cast<uintptr_t>(p) % align != 0;
+    const bool lines_up = reinterpret_cast<uintptr_t>(p) % align == 0, single = !kAligned || !lines_up;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = at.of(k);
@@ -80,9 +103,9 @@ __device__ __forceinline__ void params(float2 (&f)[NV][4], const void* p, int ty
             continue;
         }
         if (single && c < at.end) {
-            if (type == kF32) params_at(f[k], static_cast<const float*>(p), c, C);
-            else if (type == kBF16) params_at(f[k], static_cast<const __nv_bfloat16*>(p), c, C);
-            else params_at(f[k], static_cast<const __half*>(p), c, C);
+            if (type == kF32) params_at(f[k], static_cast<const float*>(p), c, C, lines_up);
+            else if (type == kBF16) params_at(f[k], static_cast<const __nv_bfloat16*>(p), c, C, lines_up);
+            else params_at(f[k], static_cast<const __half*>(p), c, C, lines_up);
             continue;
         }
         if (c >= at.end) {
@@ -424,19 +447,32 @@ __global__ void __launch_bounds__(block_threads(G, M), G > 0 ? 2 : 1) block_norm
     if (p.partial == nullptr) return;
     const int per_cta = threads / me.width;
     float* part = p.partial + static_cast<size_t>(blockIdx.x) * 2 * C;
-    if (per_cta == 1) {
+    if (kAligned && per_cta == 1) {
         store_sums<kAligned, NV>(part, sum_t, at, C);
         store_sums<kAligned, NV>(part + C, sum_pre, at, C);
         return;
     }
     __syncthreads();                 // no group reads its rows any more
-    float* mine_sums = smem + me.local * 2 * C;   // the groups' sums, [group][2][C]
-    store_sums<kAligned, NV>(mine_sums, sum_t, at, C);
-    store_sums<kAligned, NV>(mine_sums + C, sum_pre, at, C);
+    // the groups' sums, [group][2][vectors], each vector in its own place (a group's columns are shifted by `shift`)
+    const int room = vectors * 8;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if (at.of(k) >= at.end) continue;
+        float4* to = reinterpret_cast<float4*>(smem + me.local * 2 * room + at.of(k) + me.shift);
+        to[0] = make_float4(sum_t[k][0].x, sum_t[k][0].y, sum_t[k][1].x, sum_t[k][1].y);
+        to[1] = make_float4(sum_t[k][2].x, sum_t[k][2].y, sum_t[k][3].x, sum_t[k][3].y);
+        to += room / 4;
+        to[0] = make_float4(sum_pre[k][0].x, sum_pre[k][0].y, sum_pre[k][1].x, sum_pre[k][1].y);
+        to[1] = make_float4(sum_pre[k][2].x, sum_pre[k][2].y, sum_pre[k][3].x, sum_pre[k][3].y);
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * C; i += threads) {
+        const int from = i < C ? i : i - C + room;
         float s = 0.f;
-        for (int g = 0; g < per_cta; ++g) s += smem[g * 2 * C + i];
+        for (int g = 0; g < per_cta; ++g) {
+            const int shift = kAligned ? 0 : static_cast<int>((static_cast<long long>(blockIdx.x * per_cta + g) * C) & 7);
+            s += smem[g * 2 * room + shift + from];
+        }
         part[i] = s;
     }
 }
@@ -467,7 +503,7 @@ cudaError_t plan_rows(K kern, KernelFacts& facts, const BlockNorm& p, int G, int
     }
     l.threads = l.width * l.per_cta;
     l.smem = static_cast<size_t>(l.threads) * NV * (S * slot + more);
-    if (parts > 0 && l.per_cta > 1) l.smem = std::max(l.smem, static_cast<size_t>(l.per_cta) * 2 * p.C * sizeof(float));
+    if (parts > 0) l.smem = std::max(l.smem, static_cast<size_t>(l.per_cta) * 2 * vectors * 8 * sizeof(float));
     if (l.smem > kDynamicSmem) return cudaErrorNotSupported;
     const cudaError_t err = opt_in_smem(kern, facts.smem, kDynamicSmem);
     if (err != cudaSuccess) return err;

@@ -2,6 +2,8 @@
 element by element within the bounds that come with them: types, channel, state and group counts, lengths around the
 kernels' tiles, packed sequences (empty ones and rows beside them too), strided views, states carried on, single
 tokens, other streams, graphs, infinities and NaN."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -503,6 +505,39 @@ def test_a_prompt_and_its_tokens_are_the_whole_sequence():
         graph.replay()
         assert torch.equal(out, ys[i])
     assert torch.equal(state, state2) and torch.equal(conv, conv2)
+
+
+def test_two_threads_at_once():
+    """Two host threads on streams of their own: the bits of one after the other."""
+    rng = np.random.default_rng(8)
+    s = scan_inputs(rng, (2, 200), 48, 8, 1, "f32")
+    args, rest = [s[k] for k in ("u", "dt", "A", "B", "C")], [s[k] for k in ("D", "z", "dt_bias")]
+    w, g = rand(rng, (4, 48), "f32"), rand(rng, 48, "f32")
+
+    def passes():
+        y, saved = dwc.selective_scan_fwd(*args, *rest, save=True)
+        out = list(dwc.selective_scan_bwd(y, *args, saved, *rest)[:8])
+        out += [dwc.causal_conv_fwd(y, w, g), *dwc.causal_conv_bwd(y, s["u"], w, g, "silu")[:3]]
+        n, z, post, pre = dwc.block_norm_fwd(y, s["u"], g, g, s["z"], g, stats=True)
+        return [y, n, z, *out, *dwc.block_norm_bwd(n, y, z, post, pre, g, g, s["z"], g)]
+
+    want = passes()
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = passes()
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for side in got:
+        assert len(side) == len(want) and all(torch.equal(a, b) for a, b in zip(side, want))
 
 
 def test_streams_and_graphs_of_the_training_passes():
