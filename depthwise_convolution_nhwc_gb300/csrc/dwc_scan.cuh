@@ -150,6 +150,15 @@ struct StateRows {
     }
 };
 
+// A log2(e), kept finite: no decay is 0 times infinity.  Positions past a sequence's end, whose delta is 0, leave every state
+// alone, and a state that keeps nothing (A of minus infinity, or past -2.36e38, whose product is infinite) has derivatives of 0.
+// (A NaN stays one.)
+__device__ __forceinline__ float rate_of(float a) {
+    constexpr float kMost = 3.402823466e38f;
+    const float v = a * kLog2e;
+    return v > kMost ? kMost : v < -kMost ? -kMost : v;
+}
+
 // Values of four states in a lane's order (n ^ perm).
 struct Four {
     float2 v[2];
@@ -191,11 +200,14 @@ struct Four {
         const float4 f = *reinterpret_cast<const float4*>(from);
         v[0] = make_float2(f.x, f.y), v[1] = make_float2(f.z, f.w);
     }
-    __device__ __forceinline__ void scale(float s) { v[0] = __fmul2_rn(v[0], both(s)), v[1] = __fmul2_rn(v[1], both(s)); }
+    __device__ __forceinline__ void to_rates() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = make_float2(rate_of(v[i].x), rate_of(v[i].y));
+    }
     __device__ __forceinline__ void clear() { v[0] = v[1] = both(0.f); }
 };
 
-// exp(delta A) of two states, from A log2(e)
+// exp(delta A) of two states, from their rates
 __device__ __forceinline__ float2 decay_of(float delta, float2 a2) {
     const float2 e = __fmul2_rn(both(delta), a2);
     return make_float2(exp2_fast(e.x), exp2_fast(e.y));
@@ -261,7 +273,7 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
         const bool serves = ch[j] < k.width;
         const long long at = static_cast<long long>(k.c + ch[j]) * N;
         a2[j].get(serves ? p.A + at : nullptr, n0, 0, N);
-        a2[j].scale(kLog2e);
+        a2[j].to_rates();
         if (kStates) h[j].clear();
         else if (ends != nullptr) h[j].get(serves ? ends + slot * wide + at : nullptr, n0, 0, N);
         else h[j].get(serves && p.state != nullptr ? p.state + r.s * wide + at : nullptr, n0, 0, N);
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(Scan p, float* ends, con
         n = p.seqs.length == 0 ? 1 : (p.seqs.length + p.span - 1) / p.span;
         first = s * n;
     }
-    const float a2 = p.A[j] * kLog2e;
+    const float a2 = rate_of(p.A[j]);
     float h = from != nullptr ? from[i] : 0.f;
     constexpr int U = 8;
     for (long long k = 0; k < n; k += U) {
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         a2[j].get(ch + j < k.width ? p.A + static_cast<long long>(k.c + ch + j) * N : nullptr, n0, 0, N);
-        a2[j].scale(kLog2e);
+        a2[j].to_rates();
         carry[j].clear();
     }
     const auto row_of = [](int i) { return (static_cast<int>(threadIdx.x) + i * kThreads) / kColumns; };
@@ -651,7 +663,7 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
         const bool serves = ch[j] < k.width;
         const long long mine = static_cast<long long>(k.c + ch[j]) * N, wide = static_cast<long long>(C) * N;
         a2[j].get(serves ? p.A + mine : nullptr, n0, perm, N);
-        a2[j].scale(kLog2e);
+        a2[j].to_rates();
         da[j].clear();
         if (carries != nullptr) carry[j].get(serves && r.some ? carries + slot * wide + mine : nullptr, n0, perm, N);
         else carry[j].get(serves && r.some && p.dfinal != nullptr ? p.dfinal + r.s * wide + mine : nullptr, n0, perm, N);

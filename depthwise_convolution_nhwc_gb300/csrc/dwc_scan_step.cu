@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(Scan p, float* 
     Four h[kSeqs], b[kSeqs], c[kSeqs], a2;
     float u[kSeqs], dt[kSeqs], z[kSeqs];
     a2.get4(p.A + static_cast<long long>(ch) * N, n0, 0, N, kVec);
-    a2.scale(kLog2e);
+    a2.to_rates();
     const float bias = p.dt_bias != nullptr ? p.dt_bias[ch] : 0.f, skip = p.D != nullptr ? p.D[ch] : 0.f;
 #pragma unroll
     for (int q = 0; q < kSeqs; ++q) {

@@ -101,7 +101,9 @@ dwc_status_t dwc_causal_conv_step(const dwc_causal_conv_t* conv, void* state, lo
  *     delta[t] = dt[t] + dt_bias, or log(1 + exp(dt[t] + dt_bias)) with softplus
  *     h[t, n]  = exp(delta[t] * A[n]) * h[t-1, n] + delta[t] * u[t] * B[t, g, n]
  *     y[t]     = (sum_n C[t, g, n] * h[t, n] + D * u[t]) * silu(z[t])
- * h before a sequence's first position is its state (zero without one). */
+ * h before a sequence's first position is its state (zero without one).  A counts as at most 2.35e38
+ * either way: a state of A = minus infinity keeps nothing wherever delta is above 1e-36, and delta = 0
+ * leaves it alone, as it does every state; the gradient that reaches delta through such a state is 0. */
 typedef struct {
     dwc_seqs_t seqs;
     int C, N, G;             /* N from 1 to 128; G divides C */
