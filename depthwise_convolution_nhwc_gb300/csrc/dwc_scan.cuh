@@ -412,6 +412,17 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
     }
 }
 
+// A state behind a chunk: of what was in front of it the chunk leaves 2^x (x: the sum of delta times the rate), `end` is from
+// within.  2^x may leave fp32's range where its product with the state does not: nothing stays nothing however much it would
+// grow (A > 0, delta < 0), and past 2^+-120 the state is multiplied by 2^(x/4) four times (from the smallest state to the
+// largest are 277 powers).
+__device__ __forceinline__ float behind_chunk(float x, float h, float end) {
+    if (h == 0.f) return end;
+    if (!(fabsf(x) > 120.f)) return fmaf(exp2_fast(x), h, end);
+    const float q = exp2_fast(0.25f * x);
+    return fmaf(q, q * (q * (q * h)), end);
+}
+
 // The states in front of every chunk, in place of those at their ends: a thread per sequence, channel and state.
 // Eight chunks' values are on their way together.
 template <bool kBackward>
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(Scan p, float* ends, con
             if (k + q >= n) break;
             const long long slot = first + (kBackward ? n - 1 - k - q : k + q);
             ends[slot * width + j] = h;
-            h = fmaf(exp2_fast(d[q] * a2), h, e[q]);
+            h = behind_chunk(d[q] * a2, h, e[q]);
         }
     }
 }

@@ -1,4 +1,5 @@
-"""Sequence operators where the ordinary inputs of the other tests do not lead: decay rates past fp32's range."""
+"""Sequence operators where the ordinary inputs of the other tests do not lead: decay rates past fp32's range, states that
+grow."""
 import numpy as np
 import pytest
 import torch
@@ -81,3 +82,63 @@ def test_scan_of_positions_that_are_left_out(T):
     fwd, _ = want_scan(s, s["u"], False, None, 2, None, None)
     within(y, ref.stack([f[0] for f in fwd]), "y")
     within(last, ref.stack([f[1] for f in fwd]), "final")
+
+
+def test_scan_of_states_that_grow():
+    """A > 0, chunks over which a state grows past fp32: one of zero stays zero, forward and backward.  (The definition runs over
+    the positions behind the zeros alone, since its bounds of zero states grow as well.)"""
+    rng = np.random.default_rng(2)
+    T, C, N = 700, 16, 8
+    s = scan_inputs(rng, (1, T), C, N, 1, "f32", plus=False, bias=False)
+    s["dt"] = torch.ones_like(s["dt"])
+    s["A"][:, 1:] = 3.0
+    s["u"][:, :-20] = 0                # (exp(3 * 20) in the end)
+    args, rest = parts(s)
+    y, last = dwc.selective_scan_fwd(*args, *rest, False, final=True)
+    part = lambda a, b: {k: t[:, a:b] if k in ("u", "dt", "z", "B", "C") else t for k, t in s.items()}  # noqa: E731
+    fwd, _ = want_scan(part(-20, T), s["u"][:, -20:], False, None, 1, None, None)
+    within(y[:, -20:], ref.stack([f[0] for f in fwd]), "y")
+    within(last, ref.stack([f[1] for f in fwd]), "final")
+    assert not y[:, :-20].any()
+    s["u"] = torch.zeros_like(s["u"])
+    args, rest = parts(s)
+    dy = rand(rng, (1, T, C), "f32")
+    dy[:, 20:] = 0
+    _, saved = dwc.selective_scan_fwd(*args, *rest, False, save=True)
+    got = dwc.selective_scan_bwd(dy, *args, saved, *rest, False)
+    _, bwd = want_scan(part(0, 20), dy[:, :20], False, None, 1, None, None)
+    for k, t in zip(("du", "ddt", "dB", "dC"), (got[0], got[1], got[3], got[4])):
+        within(t[:, :20], ref.stack([f[k] for f in bwd]), k)
+        assert not t[:, 20:].any()
+
+
+def test_scan_of_large_states_that_shrink():
+    """A chunk leaves less than fp32's smallest number of a state, but the state is large."""
+    rng = np.random.default_rng(4)
+    T, C, N = 80, 16, 8
+    s = scan_inputs(rng, (1, T), C, N, 1, "f32", plus=False, bias=False)
+    s["dt"], s["u"] = torch.ones_like(s["dt"]), torch.zeros_like(s["u"])
+    s["A"][:, ::2] = -1.5              # exp(-1.5 * 64) = 2e-42
+    h0 = rand(rng, (1, C, N), "f32") * 1e30
+    args, rest = parts(s)
+    y, last = dwc.selective_scan_fwd(*args, *rest, False, h0, final=True)
+    # a decay's relative error in fp32 is 4 u of the exponential's and 2 u |delta A| of its argument's, a product u: 8 u a position;
+    # the join's: 120 * 2 u of the sum's and the product's roundings, four times 4 u, four products: 300 u beside them
+    want = h0.double() * torch.exp(s["A"].double() * T)
+    assert ((last.double() - want).abs() <= (8 * T + 300) * 2 ** -24 * want.abs() + 1e-37).all()
+    assert (want[:, :, ::2].abs() > 1e-24).any()
+
+
+def test_scan_of_small_states_that_grow():
+    """A chunk's growth is past fp32, the state that it grows is not."""
+    rng = np.random.default_rng(4)
+    T, C, N = 80, 16, 8
+    s = scan_inputs(rng, (1, T), C, N, 1, "f32", plus=False, bias=False)
+    s["dt"], s["u"] = torch.ones_like(s["dt"]), torch.zeros_like(s["u"])
+    s["A"][:, ::2] = 1.6               # exp(1.6 * 64) = 3e44
+    h0 = rand(rng, (1, C, N), "f32") * 1e-30
+    args, rest = parts(s)
+    y, last = dwc.selective_scan_fwd(*args, *rest, False, h0, final=True)
+    fwd, _ = want_scan(s, s["u"], False, None, 1, h0, None)
+    within(last, ref.stack([f[1] for f in fwd]), "final")
+    within(y, ref.stack([f[0] for f in fwd]), "y")
