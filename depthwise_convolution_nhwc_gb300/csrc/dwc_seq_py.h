@@ -108,20 +108,35 @@ struct Input {
         return v.data_ptr();
     }
 
-    // `out` must not share memory with a call's other tensors.
+    // `out` must not share memory with a call's other tensors.  Of the ranges of addresses that meet, those are apart whose
+    // entries along the first axis interleave: a sequence's state and its next input side by side in a row of one cache.
+    struct Reach {
+        int64_t entries, stride, bytes;        // of an entry: from its first element to its last
+        uintptr_t lo;
+        explicit Reach(const Tensor& v) : entries(1), stride(0), bytes(1), lo(reinterpret_cast<uintptr_t>(v.data_ptr())) {
+            const bool several = v.dim() > 0 && v.size(0) > 1 && v.stride(0) > 0;
+            for (int64_t i = several ? 1 : 0; i < v.dim(); ++i) bytes += (v.size(i) - 1) * v.stride(i);
+            bytes *= v.element_size();
+            if (several) entries = v.size(0), stride = v.stride(0) * v.element_size();
+        }
+        uintptr_t end() const { return lo + (entries - 1) * stride + bytes; }
+    };
+    static bool interleave(const Reach& a, const Reach& b) {
+        const int64_t stride = a.entries > 1 ? a.stride : b.stride;
+        if (stride <= 0 || (a.entries > 1 && b.entries > 1 && a.stride != b.stride)) return false;
+        // from the start of an entry of `a` to the next start of one of `b`, and the room behind that
+        const int64_t off = static_cast<int64_t>(b.lo - a.lo) % stride, ahead = off < 0 ? off + stride : off;
+        return ahead >= a.bytes && ahead + b.bytes <= stride;
+    }
     static void apart(const Tensor& out, const char* what, std::initializer_list<PyObject*> others) {
-        const auto end = [](const Tensor& v) {
-            int64_t n = 1;
-            for (int64_t i = 0; i < v.dim(); ++i) n += (v.size(i) - 1) * v.stride(i);
-            return reinterpret_cast<uintptr_t>(v.data_ptr()) + n * v.element_size();
-        };
         if (out.numel() == 0) return;
-        const auto lo = reinterpret_cast<uintptr_t>(out.data_ptr()), hi = end(out);
+        const Reach mine(out);
         for (PyObject* o : others) {
             if (o == nullptr || !THPVariable_Check(o)) continue;
             const Tensor& v = THPVariable_Unpack(o);
             if (v.numel() == 0) continue;
-            TORCH_CHECK_VALUE(end(v) <= lo || reinterpret_cast<uintptr_t>(v.data_ptr()) >= hi, what,
+            const Reach theirs(v);
+            TORCH_CHECK_VALUE(theirs.end() <= mine.lo || theirs.lo >= mine.end() || interleave(mine, theirs), what,
                               " overlaps another tensor of the call");
         }
     }

@@ -1,5 +1,5 @@
 """Sequence operators where the ordinary inputs of the other tests do not lead: decay rates past fp32's range, states that
-grow."""
+grow, views of one cache."""
 import numpy as np
 import pytest
 import torch
@@ -142,3 +142,32 @@ def test_scan_of_small_states_that_grow():
     fwd, _ = want_scan(s, s["u"], False, None, 1, h0, None)
     within(last, ref.stack([f[1] for f in fwd]), "final")
     within(y, ref.stack([f[0] for f in fwd]), "y")
+
+
+# ------------------------------------------------------------------------ views of one cache
+
+def test_steps_on_views_of_one_cache():
+    """A sequence's state and its next input side by side in one row of a cache: nothing is shared, whatever the range of addresses."""
+    rng = np.random.default_rng(6)
+    B, K, C, N = 3, 4, 16, 8
+    cache, w = rand(rng, (B, K, C), "f32"), rand(rng, (K, C), "f32")
+    state, x = cache[:, :K - 1], cache[:, K - 1]
+    kept, one = state.clone(), x.clone()
+    want = dwc.causal_conv_step(one, kept, w, None, "silu")
+    got = dwc.causal_conv_step(x, state, w, None, "silu")
+    assert torch.equal(got, want) and torch.equal(state, kept) and torch.equal(x, one)
+    s = scan_inputs(rng, (B, 1), C, N, 1, "f32")
+    s = {k: t[:, 0] if k in ("u", "dt", "z", "B", "C") else t for k, t in s.items()}
+    row = rand(rng, (B, C * N + 2 * C), "f32")
+    h, u, dt = row[:, C:C + C * N].view(B, C, N), row[:, :C], row[:, C + C * N:]
+    args = lambda u, dt, h: (u, dt, s["A"], s["B"], s["C"], h, s["D"], s["z"], s["dt_bias"])  # noqa: E731
+    kept = h.clone()
+    want = dwc.selective_scan_step(*args(u.clone(), dt.clone(), kept))
+    got = dwc.selective_scan_step(*args(u, dt, h))
+    assert torch.equal(got, want) and torch.equal(h, kept)
+    for call in (lambda: dwc.causal_conv_step(cache[:, K - 2], state, w), lambda: dwc.causal_conv_step(cache[:, 0], state, w),
+                 lambda: dwc.causal_conv_step(cache.view(B, -1)[:, 40:56], state, w),
+                 lambda: dwc.selective_scan_step(*args(row[:, C - 1:2 * C - 1], dt, h)),
+                 lambda: dwc.selective_scan_step(*args(u, row[:, C * N:C * N + C], h))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
