@@ -1,12 +1,12 @@
 """Sequence operators where the ordinary inputs of the other tests do not lead: decay rates past fp32's range, states that
-grow, views of one cache."""
+grow, views of one cache, calls whose sequences stay whole, many short sequences, a long backward pass."""
 import numpy as np
 import pytest
 import torch
 
 import depthwise_convolution_nhwc_gb300 as dwc
 from oracle import seq as ref
-from test_seq_gpu import added, device, inside, joined, rand, scan_inputs, want_scan, within
+from test_seq_gpu import added, check_conv, check_scan, device, inside, joined, rand, scan_inputs, want_scan, within
 
 pytestmark = pytest.mark.gpu
 
@@ -171,3 +171,78 @@ def test_steps_on_views_of_one_cache():
                  lambda: dwc.selective_scan_step(*args(u, row[:, C * N:C * N + C], h))):
         with pytest.raises(ValueError, match="overlap"):
             call()
+
+
+# ------------------------------------------------------------------ which sequences are cut
+
+def chunk_floats(count, length, C, N, offsets=None):
+    """Floats of the forward pass's workspace: none where no sequence is cut."""
+    v = dwc.Rows(1 << 16, length * C, C)
+    scan = dwc.Scan(dwc.Seqs(count, length, offsets.data_ptr() if offsets is not None else None), C, N, 1, 1, 0, v, v, v, v, v, 1 << 16, None,
+                    None)
+    return dwc.load_library().dwc_selective_scan_fwd_workspace_size(scan) // 4
+
+
+def enough(C):
+    """Sequences of C channels and 16 states (blocks of 32 channels) that fill half the CTAs of the backward pass, seven to an
+    SM, and so a third of the forward pass's ten."""
+    return -(-7 * torch.cuda.get_device_properties(0).multi_processor_count // 2 // (C // 32)) + 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scan_of_sequences_that_stay_whole(dtype):
+    """A batch that fills the GPU is not cut, although its sequences are longer than the shortest chunk."""
+    C, N, T = 1024, 16, 70
+    count = enough(C)
+    assert chunk_floats(count, T, C, N) == 0 and chunk_floats(1, T, C, N) > 0
+    check_scan(np.random.default_rng(1), (count, T), C, N, 1, dtype)
+
+
+def test_scan_of_packed_sequences_whole_and_cut():
+    """Packed sequences that fill the GPU: those past twice the mean length are cut, the others are not."""
+    C, N = 1024, 16
+    lengths = [40] * (enough(C) - 3) + [150, 300, 0]
+    offsets = [0] + [int(o) for o in np.cumsum(lengths)]
+    rows, count = offsets[-1], len(lengths)
+    span = -(-2 * (rows // count) // 16) * 16
+    assert 64 < span < 150
+    assert chunk_floats(count, rows, C, N, device(offsets)) == (rows // span + count) * C * (N + 1)
+    check_scan(np.random.default_rng(2), (rows,), C, N, 1, "f32", offsets=offsets)
+
+
+@pytest.mark.parametrize("C,K,T", [(128, 4, 5), (128, 4, 32), (33, 3, 7), (64, 1, 1), (64, 12, 3)])
+def test_causal_conv_of_many_short_sequences(C, K, T):
+    check_conv(np.random.default_rng(C), (512, T), C, K, "bf16")
+
+
+@pytest.mark.parametrize("C,N,T", [(64, 16, 3), (24, 8, 17)])
+def test_scan_of_many_short_sequences(C, N, T):
+    check_scan(np.random.default_rng(C), (300, T), C, N, 1, "bf16")
+
+
+def test_many_short_packed_sequences():
+    offsets = [int(o) for o in np.cumsum([0] + [i * i % 8 for i in range(400)])]
+    check_conv(np.random.default_rng(3), (offsets[-1] + 3,), 64, 4, "bf16", offsets=offsets)
+    check_scan(np.random.default_rng(3), (offsets[-1] + 3,), 32, 16, 1, "bf16", offsets=offsets)
+
+
+def test_scan_backward_past_32_bits():
+    """More than 2^31 elements: gradients at both ends of the sequence, the last ones from the state that was kept in front of them, the
+    first ones from a part in whose rest a state is forgotten (delta A is -0.4 a position in the mean, 500 of them)."""
+    C, T, N, tail, head = 4096, 530000, 2, 70, 600
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty(1, T, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    A = -torch.rand(C, N, device="cuda", generator=g) - 0.5
+    B, Cm = (torch.randn(1, T, 1, N, device="cuda", generator=g).bfloat16() for _ in range(2))
+    _, saved = dwc.selective_scan_fwd(x, x, A, B, Cm, save=True)
+    at = (T - tail) // 16 * 16
+    state = saved[at // 16:at // 16 + 1].clone()
+    got = dwc.selective_scan_bwd(x, x, x, A, B, Cm, saved)
+    names = ("du", "ddt", "dB", "dC")
+    got = dict(zip(names, (got[0], got[1], got[3], got[4])))
+    for a, b, keep, h in ((at, T, slice(0, T - at), state), (0, head, slice(0, 100), None)):
+        s = {"u": x[:, a:b], "dt": x[:, a:b], "z": None, "A": A, "B": B[:, a:b], "C": Cm[:, a:b], "D": None, "dt_bias": None}
+        _, bwd = want_scan(s, x[:, a:b], True, None, 1, h, None)
+        for k in names:
+            within(got[k][0, a:b][keep], bwd[0][k][keep], k)
