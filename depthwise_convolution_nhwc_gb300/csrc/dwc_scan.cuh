@@ -603,8 +603,19 @@ struct BwdShape {
     }
 };
 
+// Of the pieces those that one launch works on: the first row of each is one of `from` .. `to` - 1, their slots begin with
+// `slot`, and `rows` rows from `from` on have partial rows of dB and dC.
+struct Window {
+    long long from, to, slot, rows;
+    __device__ __forceinline__ bool has(const Seqs& q, const Piece& r) const {
+        const long long row = dense_row(q, r) + r.first;
+        return row >= from && row < to;
+    }
+};
+
 template <typename T, int L>
-__global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident) scan_bwd_kernel(Scan p, int blocks, const float* carries, float* part_bc, float* part_p) {
+__global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
+    scan_bwd_kernel(Scan p, int blocks, Window window, const float* carries, float* part_bc, float* part_p) {
     using S = BwdShape<L>;
     constexpr int kThreads = S::kThreads, kChannels = S::kChannels, kColumns = S::kColumns, NP = S::NP, W = S::kLanes;
     constexpr int kOrders = S::kOrders, kEach = S::kEach;
@@ -626,10 +637,12 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
     front += threadIdx.x;
     pdl_trigger();
     pdl_wait();
-    const long long slot = blockIdx.x / blocks;
+    const long long slot = blockIdx.x / blocks;          // (of the window's)
     const int block = static_cast<int>(blockIdx.x - slot * blocks);
-    const Block k = block_of(p, block, kChannels);
-    const Piece r = find_piece(p.seqs, slot, p.span);
+    Block k = block_of(p, block, kChannels);
+    Piece r = find_piece(p.seqs, window.slot + slot, p.span);
+    // (a piece of another launch's: nothing to walk or to write)
+    if (r.some && !window.has(p.seqs, r)) k.width = 0, r.some = false;
     const int C = p.C, N = p.N;
     const bool even = (C / p.G) % 8 == 0;
     const long long dense = r.some ? dense_row(p.seqs, r) : 0;
@@ -653,7 +666,7 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
         at_.du = static_cast<T*>(p.du) + o;
         at_.ddt = static_cast<T*>(p.ddt) + o;
         at_.dz = static_cast<T*>(p.dz) + o;
-        at_.rows = part_bc + (block * seq_rows_device(p.seqs) + dense) * 2 * N;
+        at_.rows = part_bc + (block * window.rows + dense - window.from) * 2 * N;
         at_.saved = p.saved + (saved_slot(p.seqs, r, 0) * C + k.c) * N;
     }
     __syncthreads();
@@ -959,19 +972,39 @@ __global__ void __launch_bounds__(BwdShape<L>::kThreads, BwdShape<L>::kResident)
     }
 }
 
-// dB and dC from the partial rows of a group's blocks.
+// The first row of the piece that a row belongs to.
+__device__ __forceinline__ long long piece_row(const Seqs& q, long long row, long long span) {
+    long long base;
+    if (q.offsets == nullptr) {
+        base = row / q.length * q.length;
+    } else {
+        int lo = 0, hi = q.count - 1;           // the last sequence that does not begin behind the row
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (seq_offset(q, mid) <= row) lo = mid;
+            else hi = mid - 1;
+        }
+        base = seq_offset(q, lo);
+    }
+    return base + (row - base) / span * span;
+}
+
+// dB and dC from the partial rows of a group's blocks.  (`some`: the window leaves pieces to other launches.)
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bc_kernel(Scan p, const float* part, int per_group, long long rows) {
+__global__ void __launch_bounds__(256) scan_bc_kernel(Scan p, const float* part, int per_group, Window window, bool some) {
     pdl_trigger();
     pdl_wait();
     const int N = p.N, G = p.G;
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= rows * G * 2 * N) return;
-    const long long row = i / (G * 2 * N);
-    const int j = static_cast<int>(i - row * G * 2 * N), g = j / (2 * N), which = (j - g * 2 * N) / N, n = j % N;
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, at = i / (G * 2 * N), row = window.from + at;
+    if (at >= window.rows || row >= seq_rows_device(p.seqs)) return;
+    const int j = static_cast<int>(i - at * G * 2 * N), g = j / (2 * N), which = (j - g * 2 * N) / N, n = j % N;
     if (p.seqs.offsets != nullptr && (row < seq_offset(p.seqs, 0) || row >= seq_offset(p.seqs, p.seqs.count))) return;
-    const float* from = part + (static_cast<long long>(g) * per_group * rows + row) * 2 * N + which * N + n;
-    const long long step = rows * 2 * N;
+    if (some) {
+        const long long first = piece_row(p.seqs, row, p.span);
+        if (first < window.from || first >= window.to) return;
+    }
+    const float* from = part + (static_cast<long long>(g) * per_group * window.rows + at) * 2 * N + which * N + n;
+    const long long step = window.rows * 2 * N;
     float s = 0.f;
     int k = 0;
     for (; k + 8 <= per_group; k += 8) {
@@ -1019,11 +1052,28 @@ struct FwdSpace {
         ends = sums * p.N;
     }
 };
+// Every block of channels has its own partial rows of dB and dC, 2 N floats a position, which with 33 states and more are
+// 2 N bytes a position and channel, many times the tensors themselves.  They are held to what the forward pass keeps of the
+// states, or to 8 GB where that is less: past it ranges of rows take turns, each with a launch of its own (bf16, 4096 channels:
+// 16 x 2048, 128 states 29.4 ms, with 16 GB 30.1; 8 x 8192, 64 states 32.3, with 16 GB 30.5; 1 x 65536, 64 states 38.9 and 38.2).
+constexpr long long kMostPartial = 1LL << 31;       // floats
+inline long long most_partial_rows(const Scan& p) {
+    const long long each = static_cast<long long>(channel_blocks(p, bwd_channels(p.N))) * 2 * p.N;
+    return std::max(kMostPartial, seq_slots(p.seqs, kScanTile) * p.C * p.N) / each;
+}
 struct BwdSpace {
+    long long window, rows;            // rows whose pieces one launch takes, and rows that those pieces reach
     long long bc, params, ends = 0, sums = 0;
     explicit BwdSpace(const Scan& p) {
-        const long long slots = seq_slots(p.seqs, p.span), C = p.C;
-        bc = static_cast<long long>(channel_blocks(p, bwd_channels(p.N))) * seq_rows(p.seqs) * 2 * p.N;
+        const long long slots = seq_slots(p.seqs, p.span), C = p.C, most = most_partial_rows(p);
+        window = rows = seq_rows(p.seqs);
+        if (rows > most) {
+            // (pieces that are whole sequences of a batch end where the next begins, others go past the window)
+            const bool whole = p.seqs.offsets == nullptr && p.span >= p.seqs.length;
+            window = whole ? std::max(1LL, most / p.seqs.length) * p.seqs.length : std::max(p.span, most - p.span);
+            rows = whole ? window : window + p.span;
+        }
+        bc = static_cast<long long>(channel_blocks(p, bwd_channels(p.N))) * rows * 2 * p.N;
         params = slots * C * (p.N + 2);
         if (p.span >= p.seqs.length) return;
         sums = slots * C;
@@ -1071,20 +1121,38 @@ cudaError_t bwd_t(const Scan& p) {
     using S = BwdShape<L>;
     constexpr size_t smem = S::kFloats * sizeof(float);
     const int blocks = channel_blocks(p, S::kChannels);
-    const long long slots = seq_slots(p.seqs, p.span), grid = slots * blocks, rows = seq_rows(p.seqs), C = p.C;
-    const long long sums = (rows * p.G * 2 * p.N + 255) / 256;
-    if (grid > 0x7fffffffLL || sums > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const long long slots = seq_slots(p.seqs, p.span), rows = seq_rows(p.seqs), C = p.C;
     const BwdSpace space(p);
     float *bc = p.workspace, *params = bc + space.bc, *ends = params + space.params;
+    const long long sums = (space.rows * p.G * 2 * p.N + 255) / 256;
     static DeviceOnce once;
     cudaError_t err = opt_in_smem(scan_bwd_kernel<T, L>, once, static_cast<int>(smem));
     if (err == cudaSuccess && space.ends > 0) err = adjoint_t<T, L>(p, ends, ends + space.ends);
-    if (err == cudaSuccess)
-        err = launch_pdl(scan_bwd_kernel<T, L>, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), smem, p.stream, p, blocks,
-                         static_cast<const float*>(space.ends > 0 ? ends : nullptr), bc, params);
-    if (err == cudaSuccess && sums > 0)
-        err = launch_pdl(scan_bc_kernel<T>, dim3(static_cast<unsigned>(sums)), dim3(256), 0, p.stream, p,
-                         static_cast<const float*>(bc), blocks / p.G, rows);
+    const bool some = space.window < rows;
+    // (no rows: the pieces of empty sequences)
+    for (long long from = 0; err == cudaSuccess && (from == 0 || from < rows); from += space.window) {
+        const bool last = !some || from + space.window >= rows;
+        Window w{from, last ? INT64_MAX : from + space.window, 0, space.rows};
+        long long end = slots;
+        if (some && p.seqs.offsets != nullptr) {
+            // piece k of sequence s, slot offset / span + s + k, has its first row, offset + k span, in slot - s spans
+            w.slot = from / p.span;
+            if (!last) end = (w.to - 1) / p.span + p.seqs.count;
+        } else if (some) {
+            const long long n = (p.seqs.length + p.span - 1) / p.span;         // of each sequence
+            w.slot = from / p.seqs.length * n;
+            if (!last) end = ((w.to - 1) / p.seqs.length + 1) * n;
+        }
+        const long long grid = (end - w.slot) * blocks;
+        if (grid > 0x7fffffffLL || sums > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        err = launch_pdl(scan_bwd_kernel<T, L>, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), smem, p.stream, p, blocks, w,
+                         static_cast<const float*>(space.ends > 0 ? ends + w.slot * C * p.N : nullptr), bc,
+                         params + w.slot * C * (p.N + 2));
+        if (err == cudaSuccess && sums > 0)
+            err = launch_pdl(scan_bc_kernel<T>, dim3(static_cast<unsigned>(sums)), dim3(256), 0, p.stream, p,
+                             static_cast<const float*>(bc), blocks / p.G, w, some);
+        if (!some) break;
+    }
     if (err == cudaSuccess) err = launch_row_sum(params, slots, C * (p.N + 2), {p.dA, p.dD, p.ddt_bias}, {C * p.N, C, C}, p.stream);
     return err;
 }

@@ -156,7 +156,14 @@ long long scan_fwd_span(const Scan& p) {
 }
 long long scan_bwd_span(const Scan& p) {
     const long long resident = (p.N <= 64 ? scan::BwdShape<4>::kResident : scan::BwdShape<32>::kResident) * static_cast<long long>(device_info().sm_count);
-    return span_of(p.seqs, scan::channel_blocks(p, scan::bwd_channels(p.N)), resident, resident / 2);
+    const long long blocks = scan::channel_blocks(p, scan::bwd_channels(p.N));
+    const long long span = span_of(p.seqs, blocks, resident, resident / 2), most = scan::most_partial_rows(p);
+    if (seq_rows(p.seqs) <= most) return span;
+    // Partial rows for some of the positions at a time, of pieces that fill half of the GPU then: sequences of a batch stay
+    // whole where that holds, and no piece takes more than half of them.
+    const long long fill = std::min(most, 2 * most * blocks / resident);
+    if (p.seqs.offsets == nullptr && span >= p.seqs.length && p.seqs.length <= fill) return span;
+    return std::max<long long>(64, std::min(span, fill / 2 / 16 * 16));
 }
 size_t scan_fwd_workspace_floats(const Scan& p) {
     const scan::FwdSpace s(p);

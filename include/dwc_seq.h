@@ -120,7 +120,12 @@ typedef struct {
 /* Floats of `saved`: the states in front of every 16th position of each sequence, what the
  * backward pass starts from (0 for invalid sizes). */
 size_t dwc_selective_scan_saved_floats(const dwc_scan_t* scan);
-/* Bytes of workspace of the two passes on the CURRENT device (0: none, or invalid sizes). */
+/* Bytes of workspace of the two passes on the CURRENT device (0: none, or invalid sizes).  Forward:
+ * none, or 4 C (N + 1) a chunk where sequences are few.  Backward:
+ *     8 N a position and block of channels (of one group: up to 64 of them with up to 8 states, 32 with
+ *     up to 16, 16 with up to 32, else 8) for partial rows of dB and dC, but not more than 8 GB or
+ *     what `saved` takes, the larger: past it the positions are worked on in parts of 64 and more;
+ *     and 4 C (N + 2) a sequence, 4 C (2 N + 3) a chunk where sequences are few or worked on in parts. */
 size_t dwc_selective_scan_fwd_workspace_size(const dwc_scan_t* scan);
 size_t dwc_selective_scan_bwd_workspace_size(const dwc_scan_t* scan);
 

@@ -1,5 +1,5 @@
 """Sequence operators where the ordinary inputs of the other tests do not lead: decay rates past fp32's range, states that
-grow, views of one cache, calls whose sequences stay whole, many short sequences, a long backward pass."""
+grow, views of one cache, calls whose sequences stay whole, many short sequences, long backward passes and ones of many states."""
 import numpy as np
 import pytest
 import torch
@@ -246,3 +246,112 @@ def test_scan_backward_past_32_bits():
         _, bwd = want_scan(s, x[:, a:b], True, None, 1, h, None)
         for k in names:
             within(got[k][0, a:b][keep], bwd[0][k][keep], k)
+
+
+# -------------------------------------------------- backward passes of more partial rows than fit
+
+GRADS = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dstate")
+
+
+def many_states(lead, G, dtype, seed):
+    """4096 channels of 128 states, 512 KB of partial rows a position: 8 GB are 16384 positions.  Memories are short (delta |A| is
+    0.5 and more in the mean)."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).to(dtype)  # noqa: E731
+    C, N = 4096, 128
+    s = {"u": r(*lead, C), "dt": r(*lead, C), "z": r(*lead, C), "B": r(*lead, G, N), "C": r(*lead, G, N)}
+    s["A"] = -0.5 - torch.rand(C, N, device="cuda", generator=g)
+    s["D"], s["dt_bias"] = r(C).float(), torch.full((C,), 0.5, device="cuda")
+    return s, r(*lead, C)
+
+
+def bwd_bytes(s, offsets=None):
+    """Bytes of the backward pass's workspace, and of its partial rows' bound with what the parameters take beside them."""
+    u, N = s["u"], s["A"].shape[1]
+    C = u.shape[-1]
+    seqs = dwc.Seqs(*u.shape[:2], None) if offsets is None else dwc.Seqs(offsets.numel() - 1, u.shape[0], offsets.data_ptr())
+    v = dwc.Rows(1 << 16, u.shape[-2] * C, C)
+    scan = dwc.Scan(seqs, C, N, s["B"].shape[-2], 1, 1, v, v, v, v, v, 1 << 16, None, None)
+    return dwc.load_library().dwc_selective_scan_bwd_workspace_size(scan), 2 ** 33
+
+
+def test_scan_backward_of_a_batch_in_parts():
+    """Nine sequences of which eight fit: the bits of each sequence's own call; parameters' gradients are the sums of theirs, in fp32 nine
+    terms (8 roundings)."""
+    s, dy = many_states((9, 2000), 1, torch.bfloat16, 1)
+    need, most = bwd_bytes(s)
+    assert 0.9 * most < need <= most + 9 * 4096 * 130 * 4
+    args, rest = parts(s)
+    _, saved = dwc.selective_scan_fwd(*args, *rest, save=True)
+    got = dict(zip(GRADS, dwc.selective_scan_bwd(dy, *args, saved, *rest, state_grad=True)))
+    n = saved.shape[0] // 9
+    sums = {k: [] for k in ("dA", "dD", "ddt_bias")}
+    for i in range(9):
+        one = {k: t[i:i + 1] if k in ("u", "dt", "z", "B", "C") else t for k, t in s.items()}
+        args, rest = parts(one)
+        want = dict(zip(GRADS, dwc.selective_scan_bwd(dy[i:i + 1], *args, saved[i * n:(i + 1) * n], *rest, state_grad=True)))
+        for k in GRADS:
+            if k in sums:
+                sums[k].append(want[k].double())
+            else:
+                assert torch.equal(got[k][i:i + 1], want[k]), (k, i)
+    for k, list_ in sums.items():
+        terms = torch.stack(list_)
+        assert ((got[k].double() - terms.sum(0)).abs() <= 8 * 2 ** -24 * terms.abs().sum(0) + 1e-30).all(), k
+
+
+def test_scan_backward_of_packed_sequences_in_parts():
+    """Packed sequences of which one lies across the border, empty ones and rows beside them: the bits of each one's own call."""
+    lengths = [700, 1500, 0, 1100, 900] * 4
+    offsets = [5] + [5 + int(o) for o in np.cumsum(lengths)]
+    s, dy = many_states((offsets[-1] + 3,), 1, torch.bfloat16, 2)
+    off = device(offsets)
+    need, most = bwd_bytes(s, off)
+    # (and of every piece that there may be parameters' gradients, the state behind it and a sum: 2 N + 3 values a channel)
+    assert 0.9 * most < need <= most + (len(lengths) + s["u"].shape[0] // 1500) * 4096 * 259 * 4
+    args, rest = parts(s)
+    _, saved = dwc.selective_scan_fwd(*args, *rest, offsets=off, save=True)
+    got = dict(zip(GRADS, dwc.selective_scan_bwd(dy, *args, saved, *rest, offsets=off, state_grad=True)))
+    sums = {k: 0 for k in ("dA", "dD", "ddt_bias")}
+    size = dict(sums)
+    for i, (a, b) in enumerate(zip(offsets[:-1], offsets[1:])):
+        if a == b:
+            assert not got["dstate"][i].any()
+            continue
+        one = {k: t[a:b][None] if k in ("u", "dt", "z", "B", "C") else t for k, t in s.items()}
+        args, rest = parts(one)
+        slot = a // 16 + i
+        want = dict(zip(GRADS, dwc.selective_scan_bwd(dy[a:b][None], *args, saved[slot:slot + -(-(b - a) // 16)].contiguous(), *rest,
+                                                      state_grad=True)))
+        for k in GRADS:
+            if k in sums:
+                sums[k], size[k] = sums[k] + want[k].double(), size[k] + want[k].double().abs()
+            else:
+                assert torch.equal(got[k][i] if k == "dstate" else got[k][a:b], want[k][0]), (k, i)
+    for k in sums:
+        assert ((got[k].double() - sums[k]).abs() <= len(lengths) * 2 ** -24 * size[k] + 1e-30).all(), k
+    for k in ("du", "ddt", "dz", "dB", "dC"):
+        assert not got[k][:5].any() and not got[k][-3:].any()
+
+
+def test_scan_backward_of_one_long_sequence_in_parts():
+    """A sequence that is cut for it, against a call of one group's channels, whose chunks are others: what crosses a border between
+    chunks is off by at most 16 roundings for each of the some 100 positions that it is remembered for, 1e-4 of terms of which an
+    output adds up 128 of either sign (their sum of magnitudes is a few times the largest output: 5e-4 of that).  The
+    gradients of parameters add up 20000 such terms, which err apart."""
+    s, dy = many_states((1, 20000), 64, torch.float32, 3)
+    need, most = bwd_bytes(s)
+    assert 0.9 * most < need <= most + 8 * 4096 * 259 * 4
+    args, rest = parts(s)
+    _, saved = dwc.selective_scan_fwd(*args, *rest, save=True)
+    got = dict(zip(GRADS, dwc.selective_scan_bwd(dy, *args, saved, *rest, state_grad=True)))
+    for group in (0, 37, 63):
+        c = slice(group * 64, group * 64 + 64)
+        one = {k: s[k][..., c] for k in ("u", "dt", "z", "D", "dt_bias")}
+        one.update({k: s[k][:, :, group] for k in ("B", "C")}, A=s["A"][c])
+        args, rest = parts(one)
+        want = dict(zip(GRADS, dwc.selective_scan_bwd(dy[..., c], *args, saved[:, c].contiguous(), *rest, state_grad=True)))
+        for k in GRADS:
+            mine = got[k][:, :, group] if k in ("dB", "dC") else got[k][c] if k in ("dA", "dD", "ddt_bias") else \
+                got[k][:, c] if k == "dstate" else got[k][..., c]
+            assert (mine - want[k]).abs().max() <= 5e-4 * want[k].abs().max(), (k, group)
