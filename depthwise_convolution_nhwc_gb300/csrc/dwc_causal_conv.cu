@@ -564,8 +564,17 @@ cudaError_t step_k(const CausalConv& p, void* state, long long state_stride) {
     const auto off = [](const void* t) { return reinterpret_cast<uintptr_t>(t) % (2 * sizeof(T)) != 0; };
     const bool one = p.seqs.count <= 1;
     const bool vec = p.C % 2 == 0 && !off(p.x.p) && !off(state) && !off(p.y) && (one || (p.x.seq % 2 == 0 && state_stride % 2 == 0));
-    if (p.K == 4) return vec ? step_t<T, 4, 2>(p, state, state_stride) : step_t<T, 4, 1>(p, state, state_stride);
-    return vec ? step_t<T, 16, 2>(p, state, state_stride) : step_t<T, 16, 1>(p, state, state_stride);
+    // Numbers of taps as in the other passes: rows that a kernel has registers for and the call does not have cost as if they were
+    // there (bf16, 64 sequences of 4096 channels, in a graph, this kernel and that of 16 taps: 1 tap 1.4 and 3.7 us, 2 taps 2.0
+    // and 3.8, 4 taps 2.2 and 4.0, 8 taps 4.0 and 4.4; 256 of 8192: 2 taps 8.6 and 19.1, 8 taps 12.5 and 20.5).
+    switch (p.K) {
+        case 1: return vec ? step_t<T, 1, 2>(p, state, state_stride) : step_t<T, 1, 1>(p, state, state_stride);
+        case 2: return vec ? step_t<T, 2, 2>(p, state, state_stride) : step_t<T, 2, 1>(p, state, state_stride);
+        case 3: return vec ? step_t<T, 3, 2>(p, state, state_stride) : step_t<T, 3, 1>(p, state, state_stride);
+        case 4: return vec ? step_t<T, 4, 2>(p, state, state_stride) : step_t<T, 4, 1>(p, state, state_stride);
+    }
+    if (p.K > 8) return vec ? step_t<T, 16, 2>(p, state, state_stride) : step_t<T, 16, 1>(p, state, state_stride);
+    return vec ? step_t<T, 8, 2>(p, state, state_stride) : step_t<T, 8, 1>(p, state, state_stride);
 }
 
 }  // namespace

@@ -6,7 +6,7 @@ import torch
 
 import depthwise_convolution_nhwc_gb300 as dwc
 from oracle import seq as ref
-from test_seq_gpu import added, check_conv, check_scan, device, inside, joined, rand, scan_inputs, want_scan, within
+from test_seq_gpu import added, check_conv, check_scan, d, device, inside, joined, rand, scan_inputs, want_scan, within
 
 pytestmark = pytest.mark.gpu
 
@@ -171,6 +171,19 @@ def test_steps_on_views_of_one_cache():
                  lambda: dwc.selective_scan_step(*args(u, row[:, C * N:C * N + C], h))):
         with pytest.raises(ValueError, match="overlap"):
             call()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", range(1, 17))
+def test_causal_conv_step_of_every_number_of_taps(K, dtype):
+    rng = np.random.default_rng(K)
+    for B, C in ((3, 24), (2, 33)):
+        x, w, b, state = rand(rng, (B, 3, C), dtype), rand(rng, (K, C), "f32", 0.7), rand(rng, C, "f32"), rand(rng, (B, K - 1, C), dtype)
+        start = d(state)
+        ys = torch.stack([dwc.causal_conv_step(x[:, t], state, w, b, "silu") for t in range(3)], 1)
+        want = [ref.causal_conv(d(x[i]), d(w), d(b), "silu", start[i]) for i in range(B)]
+        within(ys, ref.stack([f[0] for f in want]), "y")
+        assert torch.equal(state, torch.from_numpy(np.stack([f[1] for f in want])).to(state.dtype).cuda())
 
 
 # ------------------------------------------------------------------ which sequences are cut
