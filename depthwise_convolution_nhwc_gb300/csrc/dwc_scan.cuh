@@ -154,9 +154,9 @@ struct StateRows {
 // alone, and a state that keeps nothing (A of minus infinity, or past -2.36e38, whose product is infinite) has derivatives of 0.
 // (A NaN stays one.)
 __device__ __forceinline__ float rate_of(float a) {
-    constexpr float kMost = 3.402823466e38f;
-    const float v = a * kLog2e;
-    return v > kMost ? kMost : v < -kMost ? -kMost : v;
+    float v;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;\n\tmax.NaN.f32 %0, %0, 0fFF7FFFFF;" : "=f"(v) : "f"(a * kLog2e));
+    return v;
 }
 
 // Values of four states in a lane's order (n ^ perm).
@@ -412,15 +412,14 @@ __global__ void __launch_bounds__(FwdShape<L>::kThreads, FwdShape<L>::kResident)
     }
 }
 
-// A state behind a chunk: of what was in front of it the chunk leaves 2^x (x: the sum of delta times the rate), `end` is from
-// within.  2^x may leave fp32's range where its product with the state does not: nothing stays nothing however much it would
-// grow (A > 0, delta < 0), and past 2^+-120 the state is multiplied by 2^(x/4) four times (from the smallest state to the
-// largest are 277 powers).
-__device__ __forceinline__ float behind_chunk(float x, float h, float end) {
-    if (h == 0.f) return end;
-    if (!(fabsf(x) > 120.f)) return fmaf(exp2_fast(x), h, end);
-    const float q = exp2_fast(0.25f * x);
-    return fmaf(q, q * (q * (q * h)), end);
+// What a chunk leaves of the state in front of it, 2^x (x: the sum of delta times the rate), as two factors: 2^x may leave fp32's
+// range where its product with a state does not.  Past 2^+-120 each is the root, the growing one (A > 0, delta < 0) held to 2^127,
+// so that a state of zero stays zero however much it would grow and every other normal one is infinite past 2^254.
+// (Factors, since they do not wait for the state: a test of it in between cost packed sequences 6 us of 203.)
+__device__ __forceinline__ float2 chunk_factors(float x) {
+    const bool far = fabsf(x) > 120.f;
+    const float f = exp2_fast(far ? fminf(0.5f * x, 127.f) : x);
+    return make_float2(f, far ? f : 1.f);
 }
 
 // The states in front of every chunk, in place of those at their ends: a thread per sequence, channel and state.
@@ -447,21 +446,24 @@ __global__ void __launch_bounds__(256) scan_join_kernel(Scan p, float* ends, con
     float h = from != nullptr ? from[i] : 0.f;
     constexpr int U = 8;
     for (long long k = 0; k < n; k += U) {
-        float e[U], d[U];
+        float e[U];
+        float2 f[U];
 #pragma unroll
         for (int q = 0; q < U; ++q) {
             // (the last chunk's end is not needed, nor formed)
             const bool in = k + q < n - 1;
             const long long slot = first + (kBackward ? n - 1 - k - q : k + q);
             e[q] = in ? ends[slot * width + j] : 0.f;
-            d[q] = in ? sums[slot * C + c] : 0.f;
+            f[q].x = in ? sums[slot * C + c] : 0.f;
         }
+#pragma unroll
+        for (int q = 0; q < U; ++q) f[q] = chunk_factors(f[q].x * a2);
 #pragma unroll
         for (int q = 0; q < U; ++q) {
             if (k + q >= n) break;
             const long long slot = first + (kBackward ? n - 1 - k - q : k + q);
             ends[slot * width + j] = h;
-            h = behind_chunk(d[q] * a2, h, e[q]);
+            h = fmaf(f[q].x, f[q].y * h, e[q]);
         }
     }
 }
