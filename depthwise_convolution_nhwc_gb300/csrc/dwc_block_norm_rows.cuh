@@ -22,7 +22,7 @@ namespace block_norm {
 
 using namespace norm;
 
-// Threads of a CTA whose warps serve rows, one to an SM: with 128 registers each, or 102.
+// Threads of a CTA whose warps serve rows, one to an SM: with 128 registers each, or 96.
 constexpr int kMost = 512, kWide = 640;
 // (lane groups of a warp: 256 threads, two or three CTAs to an SM)
 constexpr int block_threads(int G, int M) { return G > 0 ? kWarpCta : M; }

@@ -10,7 +10,7 @@
 //
 // Measured (bf16, 8 sequences of 2048 positions, 4096 channels, 4 taps, SiLU): forward 44 us (89 % of the copy bandwidth),
 // with one load at a time 107; backward 85 us with 4 us for the sums of partial rows (its bytes take 59).  In fp32, whose
-// bytes bind both, 82 (96 %) and 128 (92 %).  The bf16 backward pass waits on its instructions, 26 a value, of which 16 warps
+// bytes bind both, 82 (96 %) and 128 (92 %).  The bf16 backward pass waits on its instructions, 24 a value, of which 16 warps
 // to an SM (128 registers a thread) issue one every other cycle.  fp32 packed rows of 1001 channels, one channel a thread:
 // 22 us (9).
 #include <algorithm>
@@ -516,8 +516,8 @@ cudaError_t bwd_t(CausalConv p) {
 }
 
 // Several channels a thread where every tensor allows it, else one.
-// (bf16 8 x 2048 x 2048, two channels a thread and one: 12 taps forward 75 and 89 us, backward 173 and 243, 8 taps backward
-// 96 and 138; four: 86, 8 taps backward 116.)
+// (bf16 8 x 2048 x 2048, two channels a thread and one: 12 taps forward 66 and 88 us, backward 174 and 243, 8 taps backward
+// 97 and 138; four: 12 taps forward 87, 8 taps backward 116.)
 bool vectors_of(const CausalConv& p, bool backward) {
     const size_t a = 8 * static_cast<size_t>(elem_bytes(p.type));
     const auto off = [&](const void* t) { return reinterpret_cast<uintptr_t>(t) % a != 0; };

@@ -3,8 +3,8 @@ scan of state space layers, forward, backward and for single tokens.
 
 Binding over the C ABI in ``include/dwc_seq.h``.  Sequences are a batch ``[B, T, C]``, or packed one
 behind the other as ``[rows, C]`` with ``offsets``, the int32 vector (on the device) of their first
-rows and the end of the last one; a sequence may be empty.  Tensors are on a CUDA device, fp32, bf16
-or fp16, with adjacent channels and any strides between sequences and positions (slices of a
+rows and the end of the last one; a sequence may be empty, but rows of no sequence (offsets of one
+entry) are refused.  Tensors are on a CUDA device, fp32, bf16 or fp16, with adjacent channels and any strides between sequences and positions (slices of a
 projection's output are taken as they are); outputs are dense.  Packed rows in front of the first and
 behind the last sequence are not read; an ``out`` keeps what it holds there, new outputs are zero.
 Work runs on the current CUDA stream of the tensors' device, or on ``stream``.  Nothing falls back to

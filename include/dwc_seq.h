@@ -7,11 +7,11 @@
  *
  * Sequences lie as a batch (offsets NULL): `count` sequences of `length` positions each; or packed
  * one behind the other: `length` rows in all, sequence s the rows offsets[s] .. offsets[s+1]-1
- * (count + 1 ascending 32-bit values on the device, within 0 .. length; a sequence may be empty).
- * Rows in front of the first and behind the last sequence are neither read nor written (outputs keep
- * there what they held).  The
- * offsets are read on the device; values outside 0 .. length are clamped, and descending ones give
- * undefined results but no access outside the tensors.
+ * (count + 1 ascending 32-bit values on the device, within 0 .. length; a sequence may be empty, but
+ * with a count of 0 length is 0 too: packed rows of no sequence are DWC_ERR_INVALID_ARG).  Rows in
+ * front of the first and behind the last sequence are neither read nor written (outputs keep there
+ * what they held).  The offsets are read on the device; values outside 0 .. length are clamped, and
+ * descending ones give undefined results but no access outside the tensors.
  *
  * Views: position t of sequence s of an input lies at data + s * seq_stride + t * row_stride (a
  * batch) or data + (offsets[s] + t) * row_stride (packed), strides in elements, 0 or more (0
@@ -19,9 +19,10 @@
  * one another, except where a call says that it works in place.
  *
  * Arithmetic is fp32: 16-bit inputs are widened exactly; sums, states and gradients of parameters
- * are fp32; 16-bit outputs are rounded to nearest even once, at the store.  The order of every sum
- * is fixed by the sizes, the types and the number of SMs, so results are bit-identical from run to
- * run (no atomics).  No call allocates device memory.
+ * are fp32; 16-bit outputs are rounded to nearest even once, at the store.  Exponentials (decays, SiLU,
+ * softplus) and quotients are the hardware's approximations, off by up to 2 ulp, with results below
+ * 2^-126 zero.  The order of every sum is fixed by the sizes, the types and the number of SMs, so
+ * results are bit-identical from run to run (no atomics).  No call allocates device memory.
  */
 #ifndef DWC_SEQ_GB300_H
 #define DWC_SEQ_GB300_H
